@@ -9,6 +9,8 @@ is missing, importing the binding raises.
 The entry points keep the C names (``ep_get_dispatch_layout``, ``ep_dispatch``,
 ``ep_combine``, ...). ``Config`` mirrors ``ep_config_t``; ``alloc_layout``,
 ``alloc_recv`` and ``alloc_workspace`` allocate correctly sized tensors.
+Beside them stand the router (``ep_route`` with its balance loss), the experts'
+products (``ep_expert_product``) and their gradients with the combine's.
 """
 from __future__ import annotations
 
@@ -21,8 +23,10 @@ import torch
 from . import _build
 
 EP_OK, EP_ERR_INVALID_ARG, EP_ERR_UNSUPPORTED, EP_ERR_WORKSPACE, EP_ERR_CUDA, EP_ERR_BAD_TOPK, \
-    EP_ERR_OVERFLOW, EP_ERR_TIMEOUT, EP_ERR_BOUNDS = 0, -1, -2, -3, -4, -5, -6, -7, -8
-EP_DTYPE_BF16, EP_DTYPE_FP8_E4M3 = 0, 1
+    EP_ERR_OVERFLOW, EP_ERR_TIMEOUT, EP_ERR_BOUNDS, EP_ERR_NONFINITE = 0, -1, -2, -3, -4, -5, -6, -7, -8, -9
+EP_DTYPE_BF16, EP_DTYPE_FP8_E4M3, EP_DTYPE_FP32 = 0, 1, 2
+EP_SCORE_SOFTMAX, EP_SCORE_SIGMOID = 0, 1
+EP_ACT_NONE, EP_ACT_RELU, EP_ACT_SILU, EP_ACT_GELU, EP_ACT_SWIGLU = 0, 1, 2, 3, 4
 
 __all__ = [
     "Config", "Layout", "Recv", "EpError", "lib", "ep_workspace_bytes", "ep_recv_rows",
@@ -32,6 +36,9 @@ __all__ = [
     "ep_status_string", "ep_diag_e4m3_of_bits", "ep_diag_bf16_of_bits",
     "ep_diag_copy_fanout", "ep_diag_wait_timeout", "use_checked", "alloc_layout", "alloc_recv",
     "alloc_workspace", "config_of",
+    "RouteConfig", "Route", "ProductConfig", "ep_route_workspace_bytes", "ep_product_workspace_bytes",
+    "alloc_route", "alloc_route_workspace", "alloc_product_workspace", "ep_route", "ep_route_grad",
+    "ep_combine_grad", "ep_expert_product", "ep_expert_product_grad",
 ]
 
 
@@ -163,6 +170,20 @@ def lib():
         L.ep_deterministic_sort.argtypes = [P, P, P, P, P]
         L.ep_combine.restype = I
         L.ep_combine.argtypes = [P, P, P, P, P, P, P, C.c_size_t, P]
+        L.ep_route_workspace_bytes.restype = C.c_size_t
+        L.ep_route_workspace_bytes.argtypes = [P]
+        L.ep_route.restype = I
+        L.ep_route.argtypes = [P, P, P, P, P, P, C.c_size_t, P]
+        L.ep_route_grad.restype = I
+        L.ep_route_grad.argtypes = [P, P, P, P, P, P, P, P, C.c_size_t, P]
+        L.ep_combine_grad.restype = I
+        L.ep_combine_grad.argtypes = [P, P, P, P, P, P, P, P, P, C.c_size_t, P]
+        L.ep_product_workspace_bytes.restype = C.c_size_t
+        L.ep_product_workspace_bytes.argtypes = [P, C.c_int32]
+        L.ep_expert_product.restype = I
+        L.ep_expert_product.argtypes = [P, P, P, P, P, P, P, P, P, P, C.c_size_t, P]
+        L.ep_expert_product_grad.restype = I
+        L.ep_expert_product_grad.argtypes = [P, P, P, P, P, P, P, P, P, P, C.c_size_t, P]
         L.ep_check_error.restype = I
         L.ep_check_error.argtypes = [P, P]
         L.ep_status_string.restype = C.c_char_p
@@ -370,3 +391,239 @@ def ep_diag_wait_timeout(ws: torch.Tensor, src, nbytes: int, rounds: int, stream
     `rounds` rounds with a load of `nbytes` from `src` in flight."""
     _check(lib().ep_diag_wait_timeout(_ptr(ws), _ptr(src), nbytes, rounds,
                                       _stream(stream)), "ep_diag_wait_timeout")
+
+
+# ---- router, gradient of the combine, the experts' products ---------------------
+
+
+class _RouteConfig(C.Structure):
+    _fields_ = [(n, C.c_int32) for n in (
+        "num_segments", "num_tokens", "num_experts", "num_topk", "logits_dtype", "score", "num_groups",
+        "topk_groups", "normalize")] + [("scale", C.c_float)]
+
+
+class _Route(C.Structure):
+    _fields_ = [(n, C.c_void_p) for n in (
+        "topk_idx", "topk_weights", "expert_count", "prob_sum", "num_valid", "balance_loss")]
+
+
+class _ProductConfig(C.Structure):
+    _fields_ = [("num_ranks", C.c_int32), ("num_experts", C.c_int32), ("rows", C.c_int64)] + [
+        (n, C.c_int32) for n in ("in_features", "out_features", "activation", "x_dtype", "sf_pack", "num_sms")]
+
+
+def _need(where: str, name: str, t, dtypes, numel: int, optional: bool = False):
+    """Refuse a tensor that the C ABI would misread: absent, of another type,
+    not dense, or with fewer elements than the call reads or writes."""
+    if t is None:
+        if optional:
+            return
+        raise EpError(EP_ERR_INVALID_ARG, f"{where}: {name} is missing")
+    if t.dtype not in dtypes:
+        raise EpError(EP_ERR_INVALID_ARG, f"{where}: {name} is {t.dtype}")
+    if not t.is_contiguous():
+        raise EpError(EP_ERR_INVALID_ARG, f"{where}: {name} is not contiguous")
+    if t.numel() < numel:
+        raise EpError(EP_ERR_INVALID_ARG, f"{where}: {name} has {t.numel()} elements, {numel} needed")
+    if not t.is_cuda:
+        raise EpError(EP_ERR_INVALID_ARG, f"{where}: {name} is not on the GPU")
+
+
+_BF16 = (torch.bfloat16,)
+_F32 = (torch.float32,)
+_I32 = (torch.int32,)
+_I64 = (torch.int64,)
+_CODES = (torch.uint8, torch.float8_e4m3fn)
+
+
+@dataclasses.dataclass
+class RouteConfig(_KeepsStruct):
+    num_segments: int
+    num_tokens: int  # per segment
+    num_experts: int
+    num_topk: int
+    logits_dtype: int = EP_DTYPE_FP32
+    score: int = EP_SCORE_SOFTMAX
+    num_groups: int = 1
+    topk_groups: int = 1
+    normalize: int = 1
+    scale: float = 1.0
+
+    def _build_struct(self) -> _RouteConfig:
+        return _RouteConfig(*(int(getattr(self, f[0])) for f in _RouteConfig._fields_[:-1]), float(self.scale))
+
+
+@dataclasses.dataclass
+class Route(_KeepsStruct):
+    topk_idx: torch.Tensor                      # int64 [N][K]
+    topk_weights: torch.Tensor                  # fp32 [N][K]
+    expert_count: torch.Tensor | None = None    # int32 [B][E]
+    prob_sum: torch.Tensor | None = None        # fp32 [B][E]
+    num_valid: torch.Tensor | None = None       # int32 [B]
+    balance_loss: torch.Tensor | None = None    # fp32 [1]
+
+    def _build_struct(self) -> _Route:
+        return _Route(*(_ptr(getattr(self, f[0])) for f in _Route._fields_))
+
+
+@dataclasses.dataclass
+class ProductConfig(_KeepsStruct):
+    num_ranks: int
+    num_experts: int
+    rows: int
+    in_features: int
+    out_features: int
+    activation: int = EP_ACT_NONE
+    x_dtype: int = EP_DTYPE_BF16
+    sf_pack: int = 0
+    num_sms: int = 0
+
+    @property
+    def z_features(self) -> int:
+        """Columns of z (and rows of each expert's matrix): twice out_features when gated."""
+        return self.out_features * (2 if self.activation == EP_ACT_SWIGLU else 1)
+
+    def _build_struct(self) -> _ProductConfig:
+        return _ProductConfig(*(int(getattr(self, f[0])) for f in _ProductConfig._fields_))
+
+
+def ep_route_workspace_bytes(cfg: RouteConfig) -> int:
+    c = cfg._c()
+    return int(lib().ep_route_workspace_bytes(C.byref(c)))
+
+
+def ep_product_workspace_bytes(cfg: ProductConfig, grad: bool = False) -> int:
+    c = cfg._c()
+    return int(lib().ep_product_workspace_bytes(C.byref(c), int(bool(grad))))
+
+
+def alloc_route_workspace(cfg: RouteConfig, device="cuda") -> torch.Tensor:
+    """Zero-filled workspace of ep_route_workspace_bytes(cfg) bytes."""
+    n = ep_route_workspace_bytes(cfg)
+    if n == 0:
+        raise EpError(EP_ERR_INVALID_ARG, "ep_route_workspace_bytes")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def alloc_product_workspace(cfg: ProductConfig, grad: bool = False, device="cuda") -> torch.Tensor:
+    """Workspace of ep_product_workspace_bytes(cfg, grad) bytes with a zeroed header."""
+    n = ep_product_workspace_bytes(cfg, grad)
+    if n == 0:
+        raise EpError(EP_ERR_INVALID_ARG, "ep_product_workspace_bytes")
+    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    ws[:256].zero_()
+    return ws
+
+
+def alloc_route(cfg: RouteConfig, device="cuda", stats: bool = True) -> Route:
+    N, K = cfg.num_segments * cfg.num_tokens, cfg.num_topk
+    out = Route(torch.empty(N, K, dtype=torch.int64, device=device), torch.empty(N, K, dtype=torch.float32, device=device))
+    if stats:
+        B, E = cfg.num_segments, cfg.num_experts
+        out.expert_count = torch.empty(B, E, dtype=torch.int32, device=device)
+        out.prob_sum = torch.empty(B, E, dtype=torch.float32, device=device)
+        out.num_valid = torch.empty(B, dtype=torch.int32, device=device)
+        out.balance_loss = torch.empty(1, dtype=torch.float32, device=device)
+    return out
+
+
+def _check_route(where, cfg, logits, token_mask, route):
+    N = cfg.num_segments * cfg.num_tokens
+    kind = _BF16 if cfg.logits_dtype == EP_DTYPE_BF16 else _F32
+    _need(where, "logits", logits, kind, N * cfg.num_experts)
+    _need(where, "token_mask", token_mask, (torch.uint8, torch.bool), N, True)
+    _need(where, "topk_idx", route.topk_idx, _I64, N * cfg.num_topk)
+    _need(where, "expert_count", route.expert_count, _I32, cfg.num_segments * cfg.num_experts, True)
+    _need(where, "num_valid", route.num_valid, _I32, cfg.num_segments, True)
+
+
+def ep_route(cfg: RouteConfig, logits: torch.Tensor, choice_bias, token_mask, out: Route, ws: torch.Tensor,
+             stream=None):
+    """Choose the experts of every token: logits [N][E] -> out (see Route). With
+    out.balance_loss also the counts, the probability sums and the balance loss."""
+    _check_route("ep_route", cfg, logits, token_mask, out)
+    _need("ep_route", "choice_bias", choice_bias, _F32, cfg.num_experts, True)
+    _need("ep_route", "topk_weights", out.topk_weights, _F32, cfg.num_segments * cfg.num_tokens * cfg.num_topk)
+    _need("ep_route", "prob_sum", out.prob_sum, _F32, cfg.num_segments * cfg.num_experts, True)
+    _need("ep_route", "balance_loss", out.balance_loss, _F32, 1, True)
+    c, r = cfg._c(), out._c()
+    _check(lib().ep_route(C.byref(c), _ptr(logits), _ptr(choice_bias), _ptr(token_mask), C.byref(r), _ptr(ws),
+                          ws.numel(), _stream(stream)), "ep_route")
+
+
+def ep_route_grad(cfg: RouteConfig, logits: torch.Tensor, token_mask, route: Route, d_weights, d_loss,
+                  d_logits: torch.Tensor, ws: torch.Tensor, stream=None):
+    """Gradient of the logits through the weights (d_weights [N][K] or None) and the
+    balance loss (d_loss [1] or None)."""
+    _check_route("ep_route_grad", cfg, logits, token_mask, route)
+    _need("ep_route_grad", "d_weights", d_weights, _F32, cfg.num_segments * cfg.num_tokens * cfg.num_topk, True)
+    _need("ep_route_grad", "d_loss", d_loss, _F32, 1, True)
+    _need("ep_route_grad", "d_logits", d_logits, (logits.dtype,), logits.numel())
+    c, r = cfg._c(), route._c()
+    _check(lib().ep_route_grad(C.byref(c), _ptr(logits), _ptr(token_mask), C.byref(r), _ptr(d_weights), _ptr(d_loss),
+                               _ptr(d_logits), _ptr(ws), ws.numel(), _stream(stream)), "ep_route_grad")
+
+
+def ep_combine_grad(cfg: Config, layout: Layout, y, topk_idx: torch.Tensor, topk_weights: torch.Tensor,
+                    d_out: torch.Tensor, d_y, d_weights, ws: torch.Tensor, stream=None):
+    """Gradient of ep_combine: d_y (rows of y) and d_weights [R][T][K]; either may be None."""
+    w = "ep_combine_grad"
+    N, rows = cfg.num_ranks * cfg.num_tokens, max(ep_recv_rows(cfg), 0)
+    _need(w, "y", y, _BF16, rows * cfg.hidden, d_weights is None)
+    _need(w, "topk_idx", topk_idx, _I64, N * cfg.num_topk)
+    _need(w, "topk_weights", topk_weights, _F32, N * cfg.num_topk)
+    _need(w, "d_out", d_out, _BF16, N * cfg.hidden)
+    _need(w, "d_y", d_y, _BF16, rows * cfg.hidden, True)
+    _need(w, "d_weights", d_weights, _F32, N * cfg.num_topk, True)
+    c, l = cfg._c(), layout._c()
+    _check(lib().ep_combine_grad(C.byref(c), C.byref(l), _ptr(y), _ptr(topk_idx), _ptr(topk_weights), _ptr(d_out),
+                                 _ptr(d_y), _ptr(d_weights), _ptr(ws), ws.numel(), _stream(stream)), w)
+
+
+def _check_blocks(where, cfg, layout):
+    if layout is not None:
+        R, E = cfg.num_ranks, cfg.num_experts
+        _need(where, "exp_cnt", layout.exp_cnt, _I32, E)
+        _need(where, "exp_base", layout.exp_base, _I32, E + R)
+        _need(where, "exp_region", layout.exp_region, _I32, R + 1)
+
+
+def ep_expert_product(cfg: ProductConfig, layout, x: torch.Tensor, x_sf, weight: torch.Tensor, bias, residual, z,
+                      out: torch.Tensor, ws: torch.Tensor, stream=None):
+    """out = act(x W_g^T + b_g) + residual over every expert's block of an expanded
+    layout (layout None: one group of all rows); z, if given, keeps what the activation was taken of."""
+    w = "ep_expert_product"
+    K, N, Z, E = cfg.in_features, cfg.out_features, cfg.z_features, cfg.num_experts
+    fp8 = cfg.x_dtype == EP_DTYPE_FP8_E4M3
+    _check_blocks(w, cfg, layout)
+    _need(w, "x", x, _CODES if fp8 else _BF16, cfg.rows * K)
+    groups = K // 128
+    _need(w, "x_sf", x_sf, _F32, cfg.rows * ((groups + 3) // 4 if cfg.sf_pack else groups) if fp8 else 0, not fp8)
+    _need(w, "weight", weight, _BF16, E * Z * K)
+    _need(w, "bias", bias, _BF16, E * Z, True)
+    _need(w, "residual", residual, _BF16, cfg.rows * N, True)
+    _need(w, "z", z, _BF16, cfg.rows * Z, True)
+    _need(w, "out", out, _BF16, cfg.rows * N)
+    c = cfg._c()
+    l = None if layout is None else C.byref(layout._c())
+    _check(lib().ep_expert_product(C.byref(c), l, _ptr(x), _ptr(x_sf), _ptr(weight), _ptr(bias), _ptr(residual),
+                                   _ptr(z), _ptr(out), _ptr(ws), ws.numel(), _stream(stream)), w)
+
+
+def ep_expert_product_grad(cfg: ProductConfig, layout, x, weight, z, d_out: torch.Tensor, d_x, d_weight, d_bias,
+                           ws: torch.Tensor, stream=None):
+    """Gradients of ep_expert_product's rows, matrices and biases; any of the three may be None."""
+    w = "ep_expert_product_grad"
+    K, N, Z, E = cfg.in_features, cfg.out_features, cfg.z_features, cfg.num_experts
+    _check_blocks(w, cfg, layout)
+    _need(w, "x", x, _BF16, cfg.rows * K, d_weight is None)
+    _need(w, "weight", weight, _BF16, E * Z * K, d_x is None)
+    _need(w, "z", z, _BF16, cfg.rows * Z, cfg.activation == EP_ACT_NONE)
+    _need(w, "d_out", d_out, _BF16, cfg.rows * N)
+    _need(w, "d_x", d_x, _BF16, cfg.rows * K, True)
+    _need(w, "d_weight", d_weight, _BF16, E * Z * K, True)
+    _need(w, "d_bias", d_bias, _F32, E * Z, True)
+    c = cfg._c()
+    l = None if layout is None else C.byref(layout._c())
+    _check(lib().ep_expert_product_grad(C.byref(c), l, _ptr(x), _ptr(weight), _ptr(z), _ptr(d_out), _ptr(d_x),
+                                        _ptr(d_weight), _ptr(d_bias), _ptr(ws), ws.numel(), _stream(stream)), w)

@@ -11,6 +11,7 @@
 
 #include "ep_device.cuh"
 #include "ep_internal.cuh"
+#include "moe_internal.cuh"
 
 namespace ep {
 
@@ -502,6 +503,7 @@ int ep_check_error(void* workspace, void* stream) {
   if (bits & kErrOverflow) return EP_ERR_OVERFLOW;
   if (bits & kErrTimeout) return EP_ERR_TIMEOUT;
   if (bits & kErrBounds) return EP_ERR_BOUNDS;
+  if (bits & kErrNonfinite) return EP_ERR_NONFINITE;
   return EP_OK;
 }
 
@@ -516,6 +518,7 @@ const char* ep_status_string(int status) {
     case EP_ERR_OVERFLOW: return "EP_ERR_OVERFLOW";
     case EP_ERR_TIMEOUT: return "EP_ERR_TIMEOUT";
     case EP_ERR_BOUNDS: return "EP_ERR_BOUNDS";
+    case EP_ERR_NONFINITE: return "EP_ERR_NONFINITE";
     default: return "EP_ERR_UNKNOWN";
   }
 }

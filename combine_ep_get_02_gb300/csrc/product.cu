@@ -1,0 +1,301 @@
+// The experts' products on the tensor cores: every group's rows times its matrix,
+//   acc[r][n] = sum_k A[r][k] B_g[n][k],   r in group g,
+// with bias, activation and residual applied to the fp32 sums before the one rounding
+// (forward: A = x, B = W), or plain (gradient of the rows: A = dz, B = W transposed, read
+// in place as an MN-major operand).
+//
+// A CTA per SM walks over output tiles of 128 rows x 256 columns. Warp 0 brings tiles
+// of A and B (64 of the summed index at a time) into a ring of shared-memory stages by
+// TMA, one thread of warp 1 issues tcgen05.mma into one of two TMEM accumulators, and
+// warps 2-5 take the other accumulator through the epilogue meanwhile. Row tiles start
+// at each group's first row, so a tile's last rows may belong to the next group: they are
+// computed and not stored (an output row depends on its own row of A alone). Columns past
+// the tensors read as zero.
+//
+// Every wait is bounded; one that gives up latches kErrTimeout, lets the CTA's copies
+// and products finish and returns.
+#include "product_common.cuh"
+
+namespace ep {
+
+namespace {
+
+constexpr int kThreads = 192;
+constexpr int kBM = kTileRows, kBN = 256, kBK = 64;
+constexpr int kStages = 4;
+constexpr int kABytes = kBM * kBK * 2, kBBytes = kBN * kBK * 2, kStageBytes = kABytes + kBBytes;
+constexpr int kRaster = 16;  // row tiles that share a sweep over the columns
+
+struct RowsArgs {
+  Groups groups;
+  int sum;   // length of the summed index
+  int cols;  // output columns
+  int b_rows;  // rows of B per group along the output (gated: both halves)
+  const uint16_t* bias;
+  const uint16_t* residual;
+  uint16_t* z;
+  uint16_t* out;
+  uint32_t* err;
+};
+
+struct Tile {
+  int g, begin, rows;  // group, first row of the tile, rows of the group from there on
+  int n0;
+};
+
+template <int kCols>
+struct Tiles {
+  const Groups& q;
+  const int* prefix;
+  int nt;
+  int64_t total;
+  __device__ Tiles(const Groups& groups, const int* p, int cols)
+      : q(groups), prefix(p), nt((cols + kCols - 1) / kCols), total(static_cast<int64_t>(p[groups.E]) * nt) {}
+  // Within a group: bands of kRaster row tiles, columns in turn inside a band, so that the
+  // CTAs at work share rows of A and columns of B in L2.
+  __device__ Tile at(int64_t i) const {
+    const int g = group_of_tile(prefix, q.E, static_cast<int>(i / nt));
+    const int mt = prefix[g + 1] - prefix[g];
+    int64_t r = i - static_cast<int64_t>(prefix[g]) * nt;
+    const int band = static_cast<int>(r / (static_cast<int64_t>(kRaster) * nt));
+    r -= static_cast<int64_t>(band) * kRaster * nt;
+    const int height = min(kRaster, mt - band * kRaster);
+    const int n = static_cast<int>(r) / height;
+    const int m = band * kRaster + static_cast<int>(r) - n * height;
+    const GroupRows rows = group_rows(q, g);
+    return Tile{g, rows.begin + m * kBM, rows.count - m * kBM, n * kCols};
+  }
+};
+
+template <int kAct, bool kBMn>
+__global__ void __launch_bounds__(kThreads, 1)
+    rows_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, RowsArgs a) {
+  constexpr bool kGated = kAct == EP_ACT_SWIGLU;
+  constexpr int kCols = kGated ? kBN / 2 : kBN;  // output columns of a tile
+  extern __shared__ uint8_t s_raw[];
+  __shared__ __align__(8) uint64_t s_full[kStages], s_empty[kStages], s_acc_full[2], s_acc_empty[2], s_drained;
+  __shared__ uint32_t s_tmem;
+  __shared__ volatile int s_abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t stage0 = (smem_addr(s_raw) + 1023u) & ~1023u;
+  int* prefix = reinterpret_cast<int*>(s_raw + (stage0 - smem_addr(s_raw)) + kStages * kStageBytes);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init_count(smem_addr(&s_full[s]), 1);
+      mbar_init_count(smem_addr(&s_empty[s]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init_count(smem_addr(&s_acc_full[i]), 1);
+      mbar_init_count(smem_addr(&s_acc_empty[i]), 4);
+    }
+    mbar_init_count(smem_addr(&s_drained), 1);
+    s_abort = 0;
+    fence_barrier_init();
+    tma_prefetch_map(&map_a);
+    tma_prefetch_map(&map_b);
+  }
+  if (warp == 2) {
+    tmem_alloc(smem_addr(&s_tmem), 512);
+    tmem_relinquish();
+  }
+  pdl_launch_dependents();
+  pdl_wait();
+  build_prefix<kThreads>(a.groups, kBM, prefix, blockIdx.x == 0 ? a.err : nullptr);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+  const Tiles<kCols> tiles(a.groups, prefix, a.cols);
+  const int blocks = (a.sum + kBK - 1) / kBK;
+  auto give_up = [&] {
+    s_abort = 1;
+    atomicOr(a.err, kErrTimeout);
+  };
+
+  if (warp == 0) {
+    if (elect_one()) {
+      uint32_t n = 0;  // stages filled so far
+      bool ok = true;
+      for (int64_t i = blockIdx.x; ok && i < tiles.total; i += gridDim.x) {
+        const Tile t = tiles.at(i);
+        for (int kb = 0; kb < blocks; ++kb, ++n) {
+          const uint32_t s = n % kStages, bar = smem_addr(&s_full[s]);
+          if (s_abort || !mbar_wait_timed(smem_addr(&s_empty[s]), (n / kStages & 1u) ^ 1u)) {
+            if (!s_abort) give_up();
+            ok = false;
+            break;
+          }
+          mbar_expect(bar, kStageBytes);
+          const uint32_t sa = stage0 + s * kStageBytes, sb = sa + kABytes;
+          tma_load_2d(sa, &map_a, kb * kBK, t.begin, bar);
+          if constexpr (kBMn) {
+#pragma unroll
+            for (int p = 0; p < kBN / 64; ++p)
+              tma_load_3d(sb + p * (kBK * 128), &map_b, t.n0 + p * 64, kb * kBK, t.g, bar);
+          } else {
+            tma_load_3d(sb, &map_b, kb * kBK, t.n0, t.g, bar);
+            tma_load_3d(sb + kBBytes / 2, &map_b, kb * kBK, kGated ? a.cols + t.n0 : t.n0 + kBN / 2, t.g, bar);
+          }
+        }
+      }
+      if (!ok)  // the copies in flight land before the CTA's memory goes
+        for (uint32_t back = n < kStages ? n : kStages; back > 0; --back) {
+          const uint32_t m = n - back;
+          mbar_wait_timed(smem_addr(&s_full[m % kStages]), m / kStages & 1u);
+        }
+    }
+  } else if (warp == 1) {
+    if (elect_one()) {
+      constexpr uint32_t idesc = idesc_bf16(kBM, kBN, false, kBMn);
+      uint32_t n = 0, acc = 0;
+      bool ok = true;
+      for (int64_t i = blockIdx.x; ok && i < tiles.total; i += gridDim.x, ++acc) {
+        const uint32_t b = acc & 1u;
+        if (s_abort || !mbar_wait_timed(smem_addr(&s_acc_empty[b]), (acc >> 1 & 1u) ^ 1u)) {
+          if (!s_abort) give_up();
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t d = tmem + b * kBN;
+        for (int kb = 0; kb < blocks; ++kb, ++n) {
+          const uint32_t s = n % kStages;
+          if (s_abort || !mbar_wait_timed(smem_addr(&s_full[s]), n / kStages & 1u)) {
+            if (!s_abort) give_up();
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sa = stage0 + s * kStageBytes, sb = sa + kABytes;
+          const uint64_t da = desc_k_major(sa);
+          const uint64_t db = kBMn ? desc_mn_major(sb, kBK * 128) : desc_k_major(sb);
+#pragma unroll
+          for (int k = 0; k < kBK / 16; ++k)
+            mma_bf16(d, da + k * kStepK, db + k * (kBMn ? kStepMN : kStepK), idesc, kb > 0 || k > 0);
+          mma_commit(smem_addr(&s_empty[s]));
+        }
+        if (ok) mma_commit(smem_addr(&s_acc_full[b]));
+      }
+      if (!ok) {  // the products in flight finish before the CTA's memory goes
+        mma_commit(smem_addr(&s_drained));
+        mbar_wait_timed(smem_addr(&s_drained), 0);
+      }
+    }
+  } else {
+    const int quarter = warp & 3;  // the TMEM lanes this warp may read
+    uint32_t acc = 0;
+    for (int64_t i = blockIdx.x; i < tiles.total; i += gridDim.x, ++acc) {
+      const uint32_t b = acc & 1u;
+      const Tile t = tiles.at(i);
+      bool ok = s_abort == 0 && mbar_wait_timed(smem_addr(&s_acc_full[b]), acc >> 1 & 1u);
+      ok = __all_sync(kFullMask, ok);
+      if (!ok) {
+        if (lane == 0 && !s_abort) give_up();
+        break;
+      }
+      tc_fence_after();
+      const int m = quarter * 32 + lane;
+      const bool live = m < t.rows;
+      const int64_t row = static_cast<int64_t>(t.begin) + m;
+      const uint32_t d = tmem + b * kBN + (static_cast<uint32_t>(quarter * 32) << 16);
+      const uint16_t* bias = a.bias == nullptr ? nullptr : a.bias + static_cast<int64_t>(t.g) * a.b_rows;
+      for (int c = 0; c < kCols; c += 32) {
+        const int n0 = t.n0 + c;
+        if (n0 >= a.cols) break;
+        float v[32], u[kGated ? 32 : 1];
+        tmem_ld32(d + c, v);
+        if constexpr (kGated) tmem_ld32(d + kCols + c, u);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 32; j += 8) {
+          const int n = n0 + j;
+          if (n >= a.cols) break;
+          if (bias != nullptr) {
+            float f[8];
+            unpack8(__ldg(reinterpret_cast<const uint4*>(bias + n)), f);
+#pragma unroll
+            for (int x = 0; x < 8; ++x) v[j + x] += f[x];
+            if constexpr (kGated) {
+              unpack8(__ldg(reinterpret_cast<const uint4*>(bias + a.cols + n)), f);
+#pragma unroll
+              for (int x = 0; x < 8; ++x) u[j + x] += f[x];
+            }
+          }
+          if (!live) continue;
+          if (a.z != nullptr) {
+            uint16_t* zp = a.z + row * a.b_rows + n;
+            st16(zp, pack8(v + j));
+            if constexpr (kGated) st16(zp + a.cols, pack8(u + j));
+          }
+#pragma unroll
+          for (int x = 0; x < 8; ++x) {
+            v[j + x] = activate<kAct>(v[j + x]);
+            if constexpr (kGated) v[j + x] *= u[j + x];
+          }
+          if (a.residual != nullptr) {
+            float f[8];
+            unpack8(*reinterpret_cast<const uint4*>(a.residual + row * a.cols + n), f);
+#pragma unroll
+            for (int x = 0; x < 8; ++x) v[j + x] += f[x];
+          }
+          st16(a.out + row * a.cols + n, pack8(v + j));
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(&s_acc_empty[b]));
+    }
+  }
+  __syncwarp();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 2) tmem_dealloc(tmem, 512);
+}
+
+template <int kAct, bool kBMn>
+cudaError_t launch_rows(const uint16_t* A, const uint16_t* B, const RowsArgs& a, int num_sms, cudaStream_t stream) {
+  CUtensorMap map_a, map_b;
+  const uint64_t size_a[2] = {static_cast<uint64_t>(a.sum), static_cast<uint64_t>(a.groups.rows)};
+  const uint32_t box_a[2] = {kBK, kBM};
+  cudaError_t st = make_tensor_map(&map_a, A, 2, size_a, box_a);
+  if (st != cudaSuccess) return st;
+  if (kBMn) {
+    const uint64_t size[3] = {static_cast<uint64_t>(a.cols), static_cast<uint64_t>(a.sum), static_cast<uint64_t>(a.groups.E)};
+    const uint32_t box[3] = {64, kBK, 1};
+    st = make_tensor_map(&map_b, B, 3, size, box);
+  } else {
+    const uint64_t size[3] = {static_cast<uint64_t>(a.sum), static_cast<uint64_t>(a.b_rows), static_cast<uint64_t>(a.groups.E)};
+    const uint32_t box[3] = {kBK, kBN / 2, 1};
+    st = make_tensor_map(&map_b, B, 3, size, box);
+  }
+  if (st != cudaSuccess) return st;
+  auto kern = rows_kernel<kAct, kBMn>;
+  const size_t smem = 1024 + kStages * kStageBytes + sizeof(int) * (static_cast<size_t>(a.groups.E) + 1);
+  if (resident_ctas(reinterpret_cast<const void*>(kern), kThreads, smem) < 1) return cudaErrorInvalidConfiguration;
+  const int cols = kAct == EP_ACT_SWIGLU ? kBN / 2 : kBN;
+  const int64_t most = max_row_tiles(a.groups) * ((a.cols + cols - 1) / cols);
+  const unsigned grid = static_cast<unsigned>(most < num_sms ? most : num_sms);
+  return launch_chained(kern, dim3(grid), dim3(kThreads), smem, stream, map_a, map_b, a);
+}
+
+}  // namespace
+
+cudaError_t launch_product(const ProductArgs& p, int num_sms, cudaStream_t stream) {
+  RowsArgs a = {p.g.groups, p.g.K, p.g.N, p.g.Z, p.bias, p.residual, p.z, p.out, p.err};
+  switch (p.g.act) {
+    case EP_ACT_RELU: return launch_rows<EP_ACT_RELU, false>(p.x, p.weight, a, num_sms, stream);
+    case EP_ACT_SILU: return launch_rows<EP_ACT_SILU, false>(p.x, p.weight, a, num_sms, stream);
+    case EP_ACT_GELU: return launch_rows<EP_ACT_GELU, false>(p.x, p.weight, a, num_sms, stream);
+    case EP_ACT_SWIGLU: return launch_rows<EP_ACT_SWIGLU, false>(p.x, p.weight, a, num_sms, stream);
+    default: return launch_rows<EP_ACT_NONE, false>(p.x, p.weight, a, num_sms, stream);
+  }
+}
+
+cudaError_t launch_product_dx(const ProductGradArgs& p, int num_sms, cudaStream_t stream) {
+  RowsArgs a = {p.g.groups, p.g.Z, p.g.K, 0, nullptr, nullptr, nullptr, p.d_x, p.err};
+  const uint16_t* dz = p.dz != nullptr ? p.dz : p.d_out;
+  return launch_rows<EP_ACT_NONE, true>(dz, p.weight, a, num_sms, stream);
+}
+
+}  // namespace ep

@@ -1,0 +1,235 @@
+// Gradient of the experts' matrices: dW_g[z][k] = sum over the group's rows r of
+// dz[r][z] x[r][k], for every group (zeros for an empty one).
+//
+// The same roles as the rows' products (a CTA per SM over 128 x 256 tiles of dW; one
+// warp for TMA, one for tcgen05.mma, four for the epilogue), with both operands
+// MN-major: the summed index is the row, so tiles of 64 rows are used as they lie in
+// the tensors, without a transposition. A group's last tile ends inside the next
+// group's rows (or padding): the warp that issues the products first zeroes, in shared
+// memory, the rows past the group up to the next multiple of 16 (one instruction's
+// share) in both operands, so that not even a NaN there reaches the sum.
+#include "product_common.cuh"
+
+namespace ep {
+
+namespace {
+
+constexpr int kThreads = 192;
+constexpr int kBM = 128, kBN = 256, kBK = 64;
+constexpr int kStages = 4;
+constexpr int kPanel = kBK * 128;  // bytes of 64 columns x 64 rows
+constexpr int kABytes = kBM * kBK * 2, kBBytes = kBN * kBK * 2, kStageBytes = kABytes + kBBytes;
+
+struct WeightArgs {
+  Groups groups;
+  int Z, K;
+  uint16_t* out;  // [E][Z][K]
+  uint32_t* err;
+};
+
+struct Tile {
+  int g, begin, rows, z0, k0;
+};
+
+__device__ __forceinline__ Tile tile_at(const WeightArgs& a, int64_t i, int mt, int nt) {
+  const int g = static_cast<int>(i / (static_cast<int64_t>(mt) * nt));
+  const int r = static_cast<int>(i - static_cast<int64_t>(g) * mt * nt);
+  const GroupRows rows = group_rows(a.groups, g);
+  const int n = r / mt;
+  return Tile{g, rows.begin, rows.count, (r - n * mt) * kBM, n * kBN};
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    weight_grad_kernel(const __grid_constant__ CUtensorMap map_dz, const __grid_constant__ CUtensorMap map_x, WeightArgs a) {
+  extern __shared__ uint8_t s_raw[];
+  __shared__ __align__(8) uint64_t s_full[kStages], s_empty[kStages], s_acc_full[2], s_acc_empty[2], s_drained;
+  __shared__ uint32_t s_tmem;
+  __shared__ volatile int s_abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t stage0 = (smem_addr(s_raw) + 1023u) & ~1023u;
+  uint8_t* stage_mem = s_raw + (stage0 - smem_addr(s_raw));
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init_count(smem_addr(&s_full[s]), 1);
+      mbar_init_count(smem_addr(&s_empty[s]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init_count(smem_addr(&s_acc_full[i]), 1);
+      mbar_init_count(smem_addr(&s_acc_empty[i]), 4);
+    }
+    mbar_init_count(smem_addr(&s_drained), 1);
+    s_abort = 0;
+    fence_barrier_init();
+    tma_prefetch_map(&map_dz);
+    tma_prefetch_map(&map_x);
+  }
+  if (warp == 2) {
+    tmem_alloc(smem_addr(&s_tmem), 512);
+    tmem_relinquish();
+  }
+  pdl_launch_dependents();
+  pdl_wait();
+  if (blockIdx.x == 0) {  // blocks that leave the tensors are reported once
+    bool cut = false;
+    for (int g = threadIdx.x; g < a.groups.E; g += kThreads) group_rows(a.groups, g, &cut);
+    if (cut) atomicOr(a.err, kErrOverflow);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+  const int mt = (a.Z + kBM - 1) / kBM, nt = (a.K + kBN - 1) / kBN;
+  const int64_t total = static_cast<int64_t>(a.groups.E) * mt * nt;
+  auto give_up = [&] {
+    s_abort = 1;
+    atomicOr(a.err, kErrTimeout);
+  };
+
+  if (warp == 0) {
+    if (elect_one()) {
+      uint32_t n = 0;
+      bool ok = true;
+      for (int64_t i = blockIdx.x; ok && i < total; i += gridDim.x) {
+        const Tile t = tile_at(a, i, mt, nt);
+        for (int r = 0; r < t.rows; r += kBK, ++n) {
+          const uint32_t s = n % kStages, bar = smem_addr(&s_full[s]);
+          if (s_abort || !mbar_wait_timed(smem_addr(&s_empty[s]), (n / kStages & 1u) ^ 1u)) {
+            if (!s_abort) give_up();
+            ok = false;
+            break;
+          }
+          mbar_expect(bar, kStageBytes);
+          const uint32_t sa = stage0 + s * kStageBytes, sb = sa + kABytes;
+#pragma unroll
+          for (int p = 0; p < kBM / 64; ++p) tma_load_2d(sa + p * kPanel, &map_dz, t.z0 + p * 64, t.begin + r, bar);
+#pragma unroll
+          for (int p = 0; p < kBN / 64; ++p) tma_load_2d(sb + p * kPanel, &map_x, t.k0 + p * 64, t.begin + r, bar);
+        }
+      }
+      if (!ok)
+        for (uint32_t back = n < kStages ? n : kStages; back > 0; --back) {
+          const uint32_t m = n - back;
+          mbar_wait_timed(smem_addr(&s_full[m % kStages]), m / kStages & 1u);
+        }
+    }
+  } else if (warp == 1) {
+    constexpr uint32_t idesc = idesc_bf16(kBM, kBN, true, true);
+    uint32_t n = 0, acc = 0;
+    bool ok = true;
+    for (int64_t i = blockIdx.x; ok && i < total; i += gridDim.x) {
+      const Tile t = tile_at(a, i, mt, nt);
+      if (t.rows == 0) continue;
+      const uint32_t b = acc & 1u;
+      ok = __all_sync(kFullMask, s_abort == 0 && mbar_wait_timed(smem_addr(&s_acc_empty[b]), (acc >> 1 & 1u) ^ 1u));
+      if (!ok) {
+        if (lane == 0 && !s_abort) give_up();
+        break;
+      }
+      tc_fence_after();
+      const uint32_t d = tmem + b * kBN;
+      for (int r = 0; r < t.rows; r += kBK, ++n) {
+        const uint32_t s = n % kStages;
+        ok = __all_sync(kFullMask, s_abort == 0 && mbar_wait_timed(smem_addr(&s_full[s]), n / kStages & 1u));
+        if (!ok) {
+          if (lane == 0 && !s_abort) give_up();
+          break;
+        }
+        tc_fence_after();
+        const int left = min(kBK, t.rows - r);      // rows of this tile that count
+        const int used = (left + 15) & ~15;         // rows the instructions read
+        if (used != left) {
+          // a 128-byte row of a panel holds one row's 64 columns, in whatever order
+          const int chunks = (used - left) * 8;
+          uint8_t* base = stage_mem + s * kStageBytes + left * 128;
+          for (int p = 0; p < kStageBytes / kPanel; ++p)
+            for (int c = lane; c < chunks; c += 32)
+              *reinterpret_cast<uint4*>(base + p * kPanel + c * 16) = make_uint4(0u, 0u, 0u, 0u);
+          fence_async_shared();
+          __syncwarp();
+        }
+        if (lane == 0) {
+          const uint32_t sa = stage0 + s * kStageBytes, sb = sa + kABytes;
+          const uint64_t da = desc_mn_major(sa, kPanel), db = desc_mn_major(sb, kPanel);
+          for (int k = 0; k < used / 16; ++k) mma_bf16(d, da + k * kStepMN, db + k * kStepMN, idesc, r > 0 || k > 0);
+          mma_commit(smem_addr(&s_empty[s]));
+        }
+        __syncwarp();
+      }
+      if (ok && lane == 0) mma_commit(smem_addr(&s_acc_full[b]));
+      __syncwarp();
+      ++acc;
+    }
+    if (!ok && lane == 0) {  // the products in flight finish before the CTA's memory goes
+      mma_commit(smem_addr(&s_drained));
+      mbar_wait_timed(smem_addr(&s_drained), 0);
+    }
+  } else {
+    const int quarter = warp & 3;
+    uint32_t acc = 0;
+    for (int64_t i = blockIdx.x; i < total; i += gridDim.x) {
+      const Tile t = tile_at(a, i, mt, nt);
+      const uint32_t b = acc & 1u;
+      const int zr = t.z0 + quarter * 32 + lane;
+      uint16_t* out = a.out + (static_cast<int64_t>(t.g) * a.Z + zr) * a.K + t.k0;
+      if (t.rows > 0) {
+        bool ok = s_abort == 0 && mbar_wait_timed(smem_addr(&s_acc_full[b]), acc >> 1 & 1u);
+        ok = __all_sync(kFullMask, ok);
+        if (!ok) {
+          if (lane == 0 && !s_abort) give_up();
+          break;
+        }
+        tc_fence_after();
+      }
+      const uint32_t d = tmem + b * kBN + (static_cast<uint32_t>(quarter * 32) << 16);
+      for (int c = 0; c < kBN; c += 32) {
+        if (t.k0 + c >= a.K) break;
+        float v[32];
+        if (t.rows > 0) {
+          tmem_ld32(d + c, v);
+          tmem_ld_wait();
+        } else {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = 0.f;
+        }
+        if (zr < a.Z) {
+#pragma unroll
+          for (int j = 0; j < 32; j += 8)
+            if (t.k0 + c + j < a.K) st16(out + c + j, pack8(v + j));
+        }
+      }
+      if (t.rows > 0) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&s_acc_empty[b]));
+        ++acc;
+      }
+    }
+  }
+  __syncwarp();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 2) tmem_dealloc(tmem, 512);
+}
+
+}  // namespace
+
+cudaError_t launch_product_dw(const ProductGradArgs& p, int num_sms, cudaStream_t stream) {
+  const uint16_t* dz = p.dz != nullptr ? p.dz : p.d_out;
+  WeightArgs a = {p.g.groups, p.g.Z, p.g.K, p.d_weight, p.err};
+  CUtensorMap map_dz, map_x;
+  const uint32_t box[2] = {64, kBK};
+  const uint64_t size_dz[2] = {static_cast<uint64_t>(a.Z), static_cast<uint64_t>(a.groups.rows)};
+  const uint64_t size_x[2] = {static_cast<uint64_t>(a.K), static_cast<uint64_t>(a.groups.rows)};
+  cudaError_t st = make_tensor_map(&map_dz, dz, 2, size_dz, box);
+  if (st == cudaSuccess) st = make_tensor_map(&map_x, p.x, 2, size_x, box);
+  if (st != cudaSuccess) return st;
+  const size_t smem = 1024 + kStages * kStageBytes;
+  if (resident_ctas(reinterpret_cast<const void*>(weight_grad_kernel), kThreads, smem) < 1)
+    return cudaErrorInvalidConfiguration;
+  const int64_t total =
+      static_cast<int64_t>(a.groups.E) * ((a.Z + kBM - 1) / kBM) * ((a.K + kBN - 1) / kBN);
+  const unsigned grid = static_cast<unsigned>(total < num_sms ? total : num_sms);
+  return launch_chained(weight_grad_kernel, dim3(grid), dim3(kThreads), smem, stream, map_dz, map_x, a);
+}
+
+}  // namespace ep

@@ -1,0 +1,228 @@
+// What the products need around the tensor cores: the tensor maps, FP8 rows as bf16,
+// and the gradient through the activation with the bias gradient's sums.
+#include "product_common.cuh"
+
+namespace ep {
+
+namespace {
+
+constexpr int kThreads = 256;
+
+// FP8 rows -> bf16: bf16_rn(code * scale), one scale per 128 columns (fp32, or a
+// power of two packed four to a word). A thread takes 16 columns: 16 bytes in, 32 out.
+// Rows past the last region are not part of any block and are left out.
+__global__ void __launch_bounds__(kThreads)
+    dequant_kernel(const uint8_t* x, const float* x_sf, uint16_t* out, int rows, int K, int sf_pack, const int32_t* total) {
+  pdl_launch_dependents();
+  pdl_wait();
+  if (total != nullptr) rows = max(0, min(rows, __ldg(total)));
+  const int units = K >> 4, G = K >> 7, SW = sf_pack ? (G + 3) >> 2 : G;
+  const int64_t all = static_cast<int64_t>(rows) * units;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < all;
+       i += static_cast<int64_t>(gridDim.x) * kThreads) {
+    const int64_t r = i / units;
+    const int u = static_cast<int>(i - r * units), grp = u >> 3;
+    float sf;
+    if (sf_pack) {
+      const uint32_t w = __float_as_uint(__ldg(x_sf + r * SW + (grp >> 2)));
+      const uint32_t e = w >> (8 * (grp & 3)) & 0xFFu;
+      sf = e ? __uint_as_float(e << 23) : __uint_as_float(0x00400000u);  // 2^(e-127)
+    } else {
+      sf = __ldg(x_sf + r * SW + grp);
+    }
+    const uint4 v = ld_stream16(x + r * K + u * 16);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    float f[16];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const __nv_fp8x2_storage_t p = static_cast<__nv_fp8x2_storage_t>(w[j >> 1] >> (16 * (j & 1)) & 0xFFFFu);
+      const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(p, __NV_E4M3);  // exact
+      const float2 q = __half22float2(*reinterpret_cast<const __half2*>(&h));
+      f[2 * j] = q.x * sf;
+      f[2 * j + 1] = q.y * sf;
+    }
+    st16(out + r * K + u * 16, pack8(f));
+    st16(out + r * K + u * 16 + 8, pack8(f + 8));
+  }
+}
+
+// dz = d_out * act'(z), rounded to bf16 for the products, and the column sums of the
+// unrounded dz over each row tile. A CTA takes a tile of 128 rows of one group and 512
+// output columns: 64 threads across (8 columns each), 4 down.
+constexpr int kAcross = 64, kDown = kThreads / kAcross, kSpan = kAcross * 8;
+
+struct DzArgs {
+  Groups groups;
+  int N, Z;
+  const uint16_t* z;
+  const uint16_t* d_out;
+  uint16_t* dz;  // null: only the sums
+  float* part;   // null: no sums
+  uint32_t* err;
+};
+
+template <int kAct>
+__global__ void __launch_bounds__(kThreads) dz_kernel(DzArgs a) {
+  constexpr bool kGated = kAct == EP_ACT_SWIGLU;
+  constexpr int kHalves = kGated ? 2 : 1;
+  extern __shared__ int prefix[];  // [E + 1]
+  __shared__ float s_sum[kDown][kHalves * kSpan];
+  pdl_launch_dependents();
+  pdl_wait();
+  build_prefix<kThreads>(a.groups, kTileRows, prefix, blockIdx.x == 0 ? a.err : nullptr);
+  const int across = threadIdx.x % kAcross, down = threadIdx.x / kAcross;
+  const int spans = (a.N + kSpan - 1) / kSpan;
+  const int64_t units = static_cast<int64_t>(prefix[a.groups.E]) * spans;
+  for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+    const int tile = static_cast<int>(u / spans), col = static_cast<int>(u - static_cast<int64_t>(tile) * spans) * kSpan + across * 8;
+    const int g = group_of_tile(prefix, a.groups.E, tile);
+    const GroupRows rows = group_rows(a.groups, g);
+    const int m0 = (tile - prefix[g]) * kTileRows, n = min(kTileRows, rows.count - m0);
+    const int64_t first = static_cast<int64_t>(rows.begin) + m0;
+    float sum[kHalves * 8];
+#pragma unroll
+    for (int i = 0; i < kHalves * 8; ++i) sum[i] = 0.f;
+    if (col < a.N) {
+#pragma unroll 2
+      for (int r = down; r < n; r += kDown) {
+        const int64_t row = first + r;
+        float d[8], t[kHalves * 8];
+        unpack8(ld_stream16(a.d_out + row * a.N + col), d);
+        if constexpr (kGated) {
+          float zg[8], zu[8];
+          unpack8(ld_stream16(a.z + row * a.Z + col), zg);
+          unpack8(ld_stream16(a.z + row * a.Z + a.N + col), zu);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            t[i] = d[i] * zu[i] * activate_grad<kAct>(zg[i]);
+            t[8 + i] = d[i] * activate<kAct>(zg[i]);
+          }
+        } else if constexpr (kAct == EP_ACT_NONE) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) t[i] = d[i];
+        } else {
+          float zv[8];
+          unpack8(ld_stream16(a.z + row * a.Z + col), zv);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) t[i] = d[i] * activate_grad<kAct>(zv[i]);
+        }
+        if (a.dz != nullptr) {
+#pragma unroll
+          for (int h = 0; h < kHalves; ++h) st16(a.dz + row * a.Z + h * a.N + col, pack8(t + 8 * h));
+        }
+#pragma unroll
+        for (int i = 0; i < kHalves * 8; ++i) sum[i] += t[i];
+      }
+    }
+    if (a.part != nullptr) {
+#pragma unroll
+      for (int h = 0; h < kHalves; ++h)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s_sum[down][h * kSpan + across * 8 + i] = sum[8 * h + i];
+      __syncthreads();
+      for (int i = threadIdx.x; i < kHalves * kSpan; i += kThreads) {
+        const int h = i / kSpan, c = col - across * 8 + (i - h * kSpan);
+        if (c < a.N) {
+          float s = 0.f;
+#pragma unroll
+          for (int k = 0; k < kDown; ++k) s += s_sum[k][i];
+          a.part[static_cast<int64_t>(tile) * a.Z + h * a.N + c] = s;
+        }
+      }
+      __syncthreads();
+    }
+  }
+}
+
+// d_bias_g = the sum of the group's row tiles, in order.
+__global__ void __launch_bounds__(kThreads) bias_sum_kernel(Groups q, int Z, const float* part, float* d_bias) {
+  extern __shared__ int prefix[];
+  pdl_launch_dependents();
+  pdl_wait();
+  build_prefix<kThreads>(q, kTileRows, prefix, nullptr);
+  const int64_t all = static_cast<int64_t>(q.E) * Z;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < all;
+       i += static_cast<int64_t>(gridDim.x) * kThreads) {
+    const int g = static_cast<int>(i / Z), c = static_cast<int>(i - static_cast<int64_t>(g) * Z);
+    float s = 0.f;
+#pragma unroll 8
+    for (int t = prefix[g]; t < prefix[g + 1]; ++t) s += __ldcg(part + static_cast<int64_t>(t) * Z + c);
+    d_bias[i] = s;
+  }
+}
+
+template <int kAct>
+cudaError_t launch_dz(const DzArgs& a, int num_sms, cudaStream_t stream) {
+  auto kern = dz_kernel<kAct>;
+  const size_t smem = sizeof(int) * (static_cast<size_t>(a.groups.E) + 1);
+  const int per_sm = resident_ctas(reinterpret_cast<const void*>(kern), kThreads, smem);
+  if (per_sm < 1) return cudaErrorInvalidConfiguration;
+  const int64_t most = max_row_tiles(a.groups) * ((a.N + kSpan - 1) / kSpan);
+  const int64_t ctas = static_cast<int64_t>(num_sms) * per_sm;
+  return launch_chained(kern, dim3(static_cast<unsigned>(most < ctas ? most : ctas)), dim3(kThreads), smem, stream, a);
+}
+
+}  // namespace
+
+cudaError_t make_tensor_map(CUtensorMap* map, const void* base, int dims, const uint64_t* size, const uint32_t* box) {
+  using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                              const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+  // the driver's function, looked up once per process
+  static const Encode encode = [] {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+        found != cudaDriverEntryPointSuccess)
+      fn = nullptr;
+    return reinterpret_cast<Encode>(fn);
+  }();
+  if (encode == nullptr) return cudaErrorNotSupported;
+  cuuint64_t sizes[3], strides[2];
+  cuuint32_t boxes[3], steps[3];
+  cuuint64_t stride = 2;
+  for (int i = 0; i < dims; ++i) {
+    sizes[i] = size[i];
+    boxes[i] = box[i];
+    steps[i] = 1;
+    stride *= size[i];
+    if (i + 1 < dims) strides[i] = stride;
+  }
+  const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<cuuint32_t>(dims), const_cast<void*>(base),
+                            sizes, strides, boxes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+cudaError_t launch_dequant(const ProductGeometry& g, const uint8_t* x, const float* x_sf, uint16_t* out, int num_sms,
+                           cudaStream_t stream) {
+  const int per_sm = resident_ctas(reinterpret_cast<const void*>(dequant_kernel), kThreads, 0);
+  if (per_sm < 1) return cudaErrorInvalidConfiguration;
+  const int64_t need = (static_cast<int64_t>(g.groups.rows) * (g.K >> 4) + kThreads - 1) / kThreads;
+  const int64_t ctas = static_cast<int64_t>(num_sms) * per_sm;
+  const int32_t* total = g.groups.region == nullptr ? nullptr : g.groups.region + g.groups.E / g.groups.L;
+  return launch_chained(dequant_kernel, dim3(static_cast<unsigned>(need < ctas ? need : ctas)), dim3(kThreads), 0, stream,
+                        x, x_sf, out, g.groups.rows, g.K, g.sf_pack, total);
+}
+
+cudaError_t launch_product_dz(const ProductGradArgs& p, int num_sms, cudaStream_t stream) {
+  const DzArgs a = {p.g.groups, p.g.N, p.g.Z, p.z, p.d_out, p.dz, p.part, p.err};
+  cudaError_t st;
+  switch (p.g.act) {
+    case EP_ACT_RELU: st = launch_dz<EP_ACT_RELU>(a, num_sms, stream); break;
+    case EP_ACT_SILU: st = launch_dz<EP_ACT_SILU>(a, num_sms, stream); break;
+    case EP_ACT_GELU: st = launch_dz<EP_ACT_GELU>(a, num_sms, stream); break;
+    case EP_ACT_SWIGLU: st = launch_dz<EP_ACT_SWIGLU>(a, num_sms, stream); break;
+    default: st = launch_dz<EP_ACT_NONE>(a, num_sms, stream);
+  }
+  if (st != cudaSuccess || p.part == nullptr) return st;
+  const size_t smem = sizeof(int) * (static_cast<size_t>(p.g.groups.E) + 1);
+  const int per_sm = resident_ctas(reinterpret_cast<const void*>(bias_sum_kernel), kThreads, smem);
+  if (per_sm < 1) return cudaErrorInvalidConfiguration;
+  const int64_t need = (static_cast<int64_t>(p.g.groups.E) * p.g.Z + kThreads - 1) / kThreads;
+  const int64_t ctas = static_cast<int64_t>(num_sms) * per_sm;
+  return launch_chained(bias_sum_kernel, dim3(static_cast<unsigned>(need < ctas ? need : ctas)), dim3(kThreads), smem,
+                        stream, p.g.groups, p.g.Z, static_cast<const float*>(p.part), p.d_bias);
+}
+
+}  // namespace ep

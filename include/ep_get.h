@@ -64,10 +64,13 @@ extern "C" {
                                    (libep_get_checked.so): a computed row
                                    index fell outside its buffer; that access
                                    was skipped                               */
+#define EP_ERR_NONFINITE (-9)   /* device: the router met a NaN or +inf logit or
+                                   choice score (taken as -inf: not chosen)  */
 
 /* ---- element types ------------------------------------------------------- */
 #define EP_DTYPE_BF16 0
 #define EP_DTYPE_FP8_E4M3 1 /* OCP E4M3 ("FN"), fp32 scale per 128 columns */
+#define EP_DTYPE_FP32 2     /* router logits only                          */
 
 /* ---- configuration --------------------------------------------------------
  * Ranks: R = num_scaleout_ranks * num_scaleup_ranks; global rank
@@ -302,6 +305,148 @@ int ep_dispatch_atomic(const ep_config_t* cfg, const void* x, const float* x_sf,
  * `sorted` (same shapes). num_max_tokens_per_rank <= 8192. */
 int ep_deterministic_sort(const ep_config_t* cfg, const ep_recv_t* recv,
                           const int32_t* send_counters, const ep_recv_t* sorted, void* stream);
+
+/* ---- router -------------------------------------------------------------------
+ * What stands before the dispatch (no counterpart on the DeepEP pages, which take
+ * topk_idx and topk_weights as given): the chosen experts of every token with
+ * their weights, in the form the dispatch and combine read, the lanes per expert
+ * and the balance loss; and the gradient of the logits.
+ *
+ * Tokens come in num_segments segments of num_tokens each (the source ranks, or
+ * sequences); the loss is taken over each segment. N = num_segments * num_tokens.
+ */
+#define EP_SCORE_SOFTMAX 0
+#define EP_SCORE_SIGMOID 1
+
+typedef struct ep_route_config {
+  int32_t num_segments; /* B >= 1                                                  */
+  int32_t num_tokens;   /* T >= 0 per segment; B * T * num_topk below 2^31         */
+  int32_t num_experts;  /* E, 1..4096                                              */
+  int32_t num_topk;     /* K, 1..32, at most E                                     */
+  int32_t logits_dtype; /* EP_DTYPE_FP32 or EP_DTYPE_BF16 (logits and d_logits)    */
+  int32_t score;        /* s = softmax(l) or sigmoid(l) of a token's logits l      */
+  int32_t num_groups;   /* G: 0 or 1 = none; else E in G groups of neighbours, 2 experts
+                           at least each, G <= 32                                  */
+  int32_t topk_groups;  /* groups a token may choose from, 1..G, holding K experts at
+                           least (ignored without groups)                          */
+  int32_t normalize;    /* 1: weights divided by the sum of s over the chosen      */
+  float scale;          /* every weight times this (finite)                        */
+} ep_route_config_t;
+
+/* Device outputs. The last four are the statistics: all present, or all NULL (a
+ * serving step needs none). */
+typedef struct ep_route {
+  int64_t* topk_idx;     /* [N][K]: chosen experts, best first; -1 where none is left */
+  float* topk_weights;   /* [N][K]: scale * s (/ sum); 0 where topk_idx is -1       */
+  int32_t* expert_count; /* [B][E]: lanes to each expert                            */
+  float* prob_sum;       /* [B][E]: sum over the segment's tokens of p = s (softmax)
+                            or s / sum s (sigmoid)                                  */
+  int32_t* num_valid;    /* [B]: tokens the mask leaves                             */
+  float* balance_loss;   /* [1]: mean over the segments of sum_e (E count_e / (K n))
+                            (prob_sum_e / n), n = num_valid; 0 for an empty segment */
+} ep_route_t;
+
+/* Workspace bytes of ep_route and ep_route_grad (0 for an invalid configuration).
+ * Zero-filled once before first use (ep_workspace_init), as the others; one stream
+ * at a time; errors are read by ep_check_error. */
+size_t ep_route_workspace_bytes(const ep_route_config_t* cfg);
+
+/* Router. logits: device [N][E], 16-byte aligned. choice_bias: device fp32 [E] or
+ * NULL: added to the score the choice is made by (l for softmax, s for sigmoid),
+ * not to the weights. token_mask: device uint8 [N] or NULL; 0 = padding: idx -1,
+ * weights 0, not counted, its logits are not read for anything.
+ *   - The K experts of largest choice score in order, ties to the lowest expert;
+ *     with groups, among the topk_groups groups whose two best choice scores have the
+ *     largest fp32 sum, ties to the lowest group.
+ *   - An expert whose logit or choice score is -inf is never chosen; lanes for which
+ *     no expert is left are -1. NaN and +inf are taken as -inf and latch
+ *     EP_ERR_NONFINITE.
+ *   - Results are bitwise reproducible. Without tokens the statistics are zeros. */
+int ep_route(const ep_route_config_t* cfg, const void* logits, const float* choice_bias,
+             const uint8_t* token_mask, const ep_route_t* out, void* workspace,
+             size_t workspace_bytes, void* stream);
+
+/* Gradient of the logits through the weights and the loss; the choice and the
+ * counts are constants. `route` holds ep_route's outputs (topk_idx; with d_loss
+ * also expert_count and num_valid). d_weights: device fp32 [N][K] or NULL (zero).
+ * d_loss: device fp32 [1], the gradient of balance_loss (its coefficient included),
+ * or NULL (zero). d_logits: device [N][E] of the logits' type, every element
+ * written (zero for padding tokens), 16-byte aligned. A topk_idx outside [-1, E)
+ * latches EP_ERR_BAD_TOPK and is treated as masked. */
+int ep_route_grad(const ep_route_config_t* cfg, const void* logits, const uint8_t* token_mask,
+                  const ep_route_t* route, const float* d_weights, const float* d_loss,
+                  void* d_logits, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Gradient of ep_combine: for d_out (device bf16 [R][T][H]),
+ *   d_weights[s][t][k] = <d_out[s][t], y[row of lane k]> (fp32; 0 for a masked lane),
+ *   d_y[row] = bf16_rn((sum of topk_weights over the token's lanes on that row) *
+ *              d_out[s][t]); rows that no lane reads are left untouched.
+ * Either of d_y, d_weights may be NULL; y may be NULL when d_weights is. The layout,
+ * y, topk_idx, topk_weights, workspace and errors are ep_combine's, for every
+ * receive layout. Bitwise reproducible. (Where every lane has a row of its own, the
+ * expanded layout, the gradient of the dispatch itself is ep_combine with weights 1.) */
+int ep_combine_grad(const ep_config_t* cfg, const ep_layout_t* layout, const uint16_t* y,
+                    const int64_t* topk_idx, const float* topk_weights, const uint16_t* d_out,
+                    uint16_t* d_y, float* d_weights, void* workspace, size_t workspace_bytes,
+                    void* stream);
+
+/* ---- the experts' products --------------------------------------------------------
+ * What stands between dispatch and combine: the rows of every expert's block of an
+ * expanded layout times that expert's matrix, with bias, activation and residual:
+ *   z[r] = x[r] W_g^T + b_g,   out[r] = act(z[r]) + residual[r]     for r in block g
+ * (gated: z has 2 N columns, out = silu(z[:, :N]) * z[:, N:] + residual). Products are
+ * of bf16 values, summed in fp32; the activation is taken of the fp32 sum; z and out
+ * are rounded once. Rows outside the blocks' lanes are neither read for a result nor
+ * written. layout = NULL: one group of all `rows` rows (a dense product, such as a
+ * shared expert), with num_ranks = num_experts = 1.
+ */
+#define EP_ACT_NONE 0
+#define EP_ACT_RELU 1
+#define EP_ACT_SILU 2   /* z / (1 + exp(-z))            */
+#define EP_ACT_GELU 3   /* z * (1 + erf(z / sqrt 2)) / 2 */
+#define EP_ACT_SWIGLU 4 /* gated: silu(z1) * z2          */
+
+typedef struct ep_product_config {
+  int32_t num_ranks;    /* R of the layout                                         */
+  int32_t num_experts;  /* E, a multiple of R, 1..4096                             */
+  int64_t rows;         /* rows of x, z, out, residual, 0..2^31-1 (ep_recv_rows of the
+                           dispatch); a block past them is cut and latches EP_ERR_OVERFLOW */
+  int32_t in_features;  /* K, a multiple of 8 (of 128 with FP8), up to 2^20         */
+  int32_t out_features; /* N of out, a multiple of 8, up to 2^20                    */
+  int32_t activation;   /* EP_ACT_*                                                 */
+  int32_t x_dtype;      /* EP_DTYPE_BF16, or EP_DTYPE_FP8_E4M3: the rows and x_sf of an
+                           FP8 dispatch (each element is taken as bf16_rn(code * scale);
+                           forward only)                                            */
+  int32_t sf_pack;      /* x_sf as ep_config_t.sf_pack                              */
+  int32_t num_sms;      /* SMs to use; 0 = all. Results do not depend on it.        */
+} ep_product_config_t;
+
+/* Workspace bytes of ep_expert_product (grad = 0) or ep_expert_product_grad (1); 0 for
+ * an invalid configuration. Its 256-byte header is zero-filled once before first use;
+ * one stream at a time; errors are read by ep_check_error. */
+size_t ep_product_workspace_bytes(const ep_product_config_t* cfg, int32_t grad);
+
+/* Forward. All device pointers, rows dense and 16-byte aligned: x [rows][K], weight
+ * bf16 [E][Z][K] (Z = N, or 2 N gated: the N gate rows, then the N others), bias bf16
+ * [E][Z] or NULL, residual bf16 [rows][N] or NULL (it may be out itself), z bf16
+ * [rows][Z] or NULL (kept for the gradient), out bf16 [rows][N]. x_sf: the FP8 rows'
+ * scales, else NULL. Bitwise reproducible. */
+int ep_expert_product(const ep_product_config_t* cfg, const ep_layout_t* layout, const void* x,
+                      const float* x_sf, const uint16_t* weight, const uint16_t* bias,
+                      const uint16_t* residual, uint16_t* z, uint16_t* out, void* workspace,
+                      size_t workspace_bytes, void* stream);
+
+/* Gradients for d_out (bf16 [rows][N]), with dz = d_out * act'(z) from the kept z
+ * (NULL allowed when the activation is none):
+ *   d_x[r] = dz[r] W_g (bf16), d_weight_g = sum over the block's rows of dz[r]^T x[r]
+ *   (bf16 [E][Z][K], zeros for an empty block), d_bias_g = sum of dz (fp32 [E][Z]).
+ * Any of the three may be NULL; x is needed for d_weight, weight for d_x. dz enters the
+ * products rounded to bf16 and d_bias unrounded. The gradient of the residual is
+ * d_out itself. bf16 x only. Bitwise reproducible. */
+int ep_expert_product_grad(const ep_product_config_t* cfg, const ep_layout_t* layout,
+                           const uint16_t* x, const uint16_t* weight, const uint16_t* z,
+                           const uint16_t* d_out, uint16_t* d_x, uint16_t* d_weight,
+                           float* d_bias, void* workspace, size_t workspace_bytes, void* stream);
 
 /* Synchronises `stream`, returns the first device-detected error latched in
  * the workspace since the last call (EP_OK if none) and clears it. The
