@@ -412,28 +412,41 @@ class _ProductConfig(C.Structure):
         (n, C.c_int32) for n in ("in_features", "out_features", "activation", "x_dtype", "sf_pack", "num_sms")]
 
 
-def _need(where: str, name: str, t, dtypes, numel: int, optional: bool = False):
-    """Refuse a tensor that the C ABI would misread: absent, of another type,
-    not dense, or with fewer elements than the call reads or writes."""
+def _refuse(where: str, name: str, t, dtype, numel: int):
     if t is None:
-        if optional:
-            return
-        raise EpError(EP_ERR_INVALID_ARG, f"{where}: {name} is missing")
-    if t.dtype not in dtypes:
-        raise EpError(EP_ERR_INVALID_ARG, f"{where}: {name} is {t.dtype}")
-    if not t.is_contiguous():
-        raise EpError(EP_ERR_INVALID_ARG, f"{where}: {name} is not contiguous")
-    if t.numel() < numel:
-        raise EpError(EP_ERR_INVALID_ARG, f"{where}: {name} has {t.numel()} elements, {numel} needed")
-    if not t.is_cuda:
-        raise EpError(EP_ERR_INVALID_ARG, f"{where}: {name} is not on the GPU")
+        why = "is missing"
+    elif t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
+        why = f"is {t.dtype}"
+    elif not t.is_contiguous():
+        why = "is not contiguous"
+    elif t.numel() < numel:
+        why = f"has {t.numel()} elements, {numel} needed"
+    else:
+        why = "is not on the GPU"
+    raise EpError(EP_ERR_INVALID_ARG, f"{where}: {name} {why}")
 
 
-_BF16 = (torch.bfloat16,)
-_F32 = (torch.float32,)
-_I32 = (torch.int32,)
-_I64 = (torch.int64,)
-_CODES = (torch.uint8, torch.float8_e4m3fn)
+def _at(t, dtype, numel: int, where: str, name: str):
+    """Address of a tensor that a call reads or writes `numel` elements of; refuses one that
+    the C ABI would misread: absent, of another type, not dense, too small, not on the GPU."""
+    if t is not None and t.dtype is dtype and t.is_cuda and t.is_contiguous() and t.numel() >= numel:
+        return t.data_ptr()
+    _refuse(where, name, t, dtype, numel)
+
+
+def _maybe(t, dtype, numel: int, where: str, name: str):
+    """As _at, for an argument that may be None."""
+    return None if t is None else _at(t, dtype, numel, where, name)
+
+
+def _raw_stream(stream):
+    """The stream's handle; None: the current stream, without building a Stream object."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+_BF16, _F32, _I32, _I64, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.int64, torch.uint8
 
 
 @dataclasses.dataclass
@@ -527,65 +540,67 @@ def alloc_route(cfg: RouteConfig, device="cuda", stats: bool = True) -> Route:
     return out
 
 
-def _check_route(where, cfg, logits, token_mask, route):
+def _route_args(where, cfg, logits, token_mask, r):
+    """Addresses of the logits and the mask; refuses tensors of `r` that do not fit the configuration."""
     N = cfg.num_segments * cfg.num_tokens
-    kind = _BF16 if cfg.logits_dtype == EP_DTYPE_BF16 else _F32
-    _need(where, "logits", logits, kind, N * cfg.num_experts)
-    _need(where, "token_mask", token_mask, (torch.uint8, torch.bool), N, True)
-    _need(where, "topk_idx", route.topk_idx, _I64, N * cfg.num_topk)
-    _need(where, "expert_count", route.expert_count, _I32, cfg.num_segments * cfg.num_experts, True)
-    _need(where, "num_valid", route.num_valid, _I32, cfg.num_segments, True)
+    x = _at(logits, _BF16 if cfg.logits_dtype == EP_DTYPE_BF16 else _F32, N * cfg.num_experts, where, "logits")
+    m = None if token_mask is None else _at(
+        token_mask, token_mask.dtype if token_mask.dtype in (_U8, torch.bool) else _U8, N, where, "token_mask")
+    BE = cfg.num_segments * cfg.num_experts
+    _at(r.topk_idx, _I64, N * cfg.num_topk, where, "topk_idx")
+    _maybe(r.topk_weights, _F32, N * cfg.num_topk, where, "topk_weights")
+    _maybe(r.expert_count, _I32, BE, where, "expert_count")
+    _maybe(r.prob_sum, _F32, BE, where, "prob_sum")
+    _maybe(r.num_valid, _I32, cfg.num_segments, where, "num_valid")
+    _maybe(r.balance_loss, _F32, 1, where, "balance_loss")
+    return x, m
 
 
 def ep_route(cfg: RouteConfig, logits: torch.Tensor, choice_bias, token_mask, out: Route, ws: torch.Tensor,
              stream=None):
     """Choose the experts of every token: logits [N][E] -> out (see Route). With
     out.balance_loss also the counts, the probability sums and the balance loss."""
-    _check_route("ep_route", cfg, logits, token_mask, out)
-    _need("ep_route", "choice_bias", choice_bias, _F32, cfg.num_experts, True)
-    _need("ep_route", "topk_weights", out.topk_weights, _F32, cfg.num_segments * cfg.num_tokens * cfg.num_topk)
-    _need("ep_route", "prob_sum", out.prob_sum, _F32, cfg.num_segments * cfg.num_experts, True)
-    _need("ep_route", "balance_loss", out.balance_loss, _F32, 1, True)
-    c, r = cfg._c(), out._c()
-    _check(lib().ep_route(C.byref(c), _ptr(logits), _ptr(choice_bias), _ptr(token_mask), C.byref(r), _ptr(ws),
-                          ws.numel(), _stream(stream)), "ep_route")
+    x, m = _route_args("ep_route", cfg, logits, token_mask, out)
+    b = _maybe(choice_bias, _F32, cfg.num_experts, "ep_route", "choice_bias")
+    st = lib().ep_route(C.byref(cfg._c()), x, b, m, C.byref(out._c()), ws.data_ptr(), ws.numel(), _raw_stream(stream))
+    _check(st, "ep_route")
 
 
 def ep_route_grad(cfg: RouteConfig, logits: torch.Tensor, token_mask, route: Route, d_weights, d_loss,
                   d_logits: torch.Tensor, ws: torch.Tensor, stream=None):
     """Gradient of the logits through the weights (d_weights [N][K] or None) and the
     balance loss (d_loss [1] or None)."""
-    _check_route("ep_route_grad", cfg, logits, token_mask, route)
-    _need("ep_route_grad", "d_weights", d_weights, _F32, cfg.num_segments * cfg.num_tokens * cfg.num_topk, True)
-    _need("ep_route_grad", "d_loss", d_loss, _F32, 1, True)
-    _need("ep_route_grad", "d_logits", d_logits, (logits.dtype,), logits.numel())
-    c, r = cfg._c(), route._c()
-    _check(lib().ep_route_grad(C.byref(c), _ptr(logits), _ptr(token_mask), C.byref(r), _ptr(d_weights), _ptr(d_loss),
-                               _ptr(d_logits), _ptr(ws), ws.numel(), _stream(stream)), "ep_route_grad")
+    w = "ep_route_grad"
+    x, m = _route_args(w, cfg, logits, token_mask, route)
+    dw = _maybe(d_weights, _F32, cfg.num_segments * cfg.num_tokens * cfg.num_topk, w, "d_weights")
+    dl = _maybe(d_loss, _F32, 1, w, "d_loss")
+    dx = _at(d_logits, logits.dtype, cfg.num_segments * cfg.num_tokens * cfg.num_experts, w, "d_logits")
+    _check(lib().ep_route_grad(C.byref(cfg._c()), x, m, C.byref(route._c()), dw, dl, dx, ws.data_ptr(), ws.numel(),
+                               _raw_stream(stream)), w)
 
 
 def ep_combine_grad(cfg: Config, layout: Layout, y, topk_idx: torch.Tensor, topk_weights: torch.Tensor,
                     d_out: torch.Tensor, d_y, d_weights, ws: torch.Tensor, stream=None):
     """Gradient of ep_combine: d_y (rows of y) and d_weights [R][T][K]; either may be None."""
     w = "ep_combine_grad"
-    N, rows = cfg.num_ranks * cfg.num_tokens, max(ep_recv_rows(cfg), 0)
-    _need(w, "y", y, _BF16, rows * cfg.hidden, d_weights is None)
-    _need(w, "topk_idx", topk_idx, _I64, N * cfg.num_topk)
-    _need(w, "topk_weights", topk_weights, _F32, N * cfg.num_topk)
-    _need(w, "d_out", d_out, _BF16, N * cfg.hidden)
-    _need(w, "d_y", d_y, _BF16, rows * cfg.hidden, True)
-    _need(w, "d_weights", d_weights, _F32, N * cfg.num_topk, True)
-    c, l = cfg._c(), layout._c()
-    _check(lib().ep_combine_grad(C.byref(c), C.byref(l), _ptr(y), _ptr(topk_idx), _ptr(topk_weights), _ptr(d_out),
-                                 _ptr(d_y), _ptr(d_weights), _ptr(ws), ws.numel(), _stream(stream)), w)
+    N, H = cfg.num_ranks * cfg.num_tokens, cfg.hidden
+    NK, rows = N * cfg.num_topk, max(ep_recv_rows(cfg), 0)
+    y = _at(y, _BF16, rows * H, w, "y") if d_weights is not None or y is not None else None
+    _check(lib().ep_combine_grad(
+        C.byref(cfg._c()), C.byref(layout._c()), y, _at(topk_idx, _I64, NK, w, "topk_idx"),
+        _at(topk_weights, _F32, NK, w, "topk_weights"), _at(d_out, _BF16, N * H, w, "d_out"),
+        _maybe(d_y, _BF16, rows * H, w, "d_y"), _maybe(d_weights, _F32, NK, w, "d_weights"), ws.data_ptr(), ws.numel(),
+        _raw_stream(stream)), w)
 
 
-def _check_blocks(where, cfg, layout):
-    if layout is not None:
-        R, E = cfg.num_ranks, cfg.num_experts
-        _need(where, "exp_cnt", layout.exp_cnt, _I32, E)
-        _need(where, "exp_base", layout.exp_base, _I32, E + R)
-        _need(where, "exp_region", layout.exp_region, _I32, R + 1)
+def _blocks_arg(where, cfg, layout):
+    if layout is None:
+        return None
+    R, E = cfg.num_ranks, cfg.num_experts
+    _at(layout.exp_cnt, _I32, E, where, "exp_cnt")
+    _at(layout.exp_base, _I32, E + R, where, "exp_base")
+    _at(layout.exp_region, _I32, R + 1, where, "exp_region")
+    return C.byref(layout._c())
 
 
 def ep_expert_product(cfg: ProductConfig, layout, x: torch.Tensor, x_sf, weight: torch.Tensor, bias, residual, z,
@@ -593,37 +608,30 @@ def ep_expert_product(cfg: ProductConfig, layout, x: torch.Tensor, x_sf, weight:
     """out = act(x W_g^T + b_g) + residual over every expert's block of an expanded
     layout (layout None: one group of all rows); z, if given, keeps what the activation was taken of."""
     w = "ep_expert_product"
-    K, N, Z, E = cfg.in_features, cfg.out_features, cfg.z_features, cfg.num_experts
-    fp8 = cfg.x_dtype == EP_DTYPE_FP8_E4M3
-    _check_blocks(w, cfg, layout)
-    _need(w, "x", x, _CODES if fp8 else _BF16, cfg.rows * K)
-    groups = K // 128
-    _need(w, "x_sf", x_sf, _F32, cfg.rows * ((groups + 3) // 4 if cfg.sf_pack else groups) if fp8 else 0, not fp8)
-    _need(w, "weight", weight, _BF16, E * Z * K)
-    _need(w, "bias", bias, _BF16, E * Z, True)
-    _need(w, "residual", residual, _BF16, cfg.rows * N, True)
-    _need(w, "z", z, _BF16, cfg.rows * Z, True)
-    _need(w, "out", out, _BF16, cfg.rows * N)
-    c = cfg._c()
-    l = None if layout is None else C.byref(layout._c())
-    _check(lib().ep_expert_product(C.byref(c), l, _ptr(x), _ptr(x_sf), _ptr(weight), _ptr(bias), _ptr(residual),
-                                   _ptr(z), _ptr(out), _ptr(ws), ws.numel(), _stream(stream)), w)
+    K, N, Z, E, rows = cfg.in_features, cfg.out_features, cfg.z_features, cfg.num_experts, cfg.rows
+    if cfg.x_dtype == EP_DTYPE_FP8_E4M3:
+        x = _at(x, torch.float8_e4m3fn if x is not None and x.dtype is torch.float8_e4m3fn else _U8, rows * K, w, "x")
+        groups = K // 128
+        x_sf = _at(x_sf, _F32, rows * ((groups + 3) // 4 if cfg.sf_pack else groups), w, "x_sf")
+    else:
+        x = _at(x, _BF16, rows * K, w, "x")
+        x_sf = _maybe(x_sf, _F32, 0, w, "x_sf")
+    _check(lib().ep_expert_product(
+        C.byref(cfg._c()), _blocks_arg(w, cfg, layout), x, x_sf, _at(weight, _BF16, E * Z * K, w, "weight"),
+        _maybe(bias, _BF16, E * Z, w, "bias"), _maybe(residual, _BF16, rows * N, w, "residual"),
+        _maybe(z, _BF16, rows * Z, w, "z"), _at(out, _BF16, rows * N, w, "out"), ws.data_ptr(), ws.numel(),
+        _raw_stream(stream)), w)
 
 
 def ep_expert_product_grad(cfg: ProductConfig, layout, x, weight, z, d_out: torch.Tensor, d_x, d_weight, d_bias,
                            ws: torch.Tensor, stream=None):
     """Gradients of ep_expert_product's rows, matrices and biases; any of the three may be None."""
     w = "ep_expert_product_grad"
-    K, N, Z, E = cfg.in_features, cfg.out_features, cfg.z_features, cfg.num_experts
-    _check_blocks(w, cfg, layout)
-    _need(w, "x", x, _BF16, cfg.rows * K, d_weight is None)
-    _need(w, "weight", weight, _BF16, E * Z * K, d_x is None)
-    _need(w, "z", z, _BF16, cfg.rows * Z, cfg.activation == EP_ACT_NONE)
-    _need(w, "d_out", d_out, _BF16, cfg.rows * N)
-    _need(w, "d_x", d_x, _BF16, cfg.rows * K, True)
-    _need(w, "d_weight", d_weight, _BF16, E * Z * K, True)
-    _need(w, "d_bias", d_bias, _F32, E * Z, True)
-    c = cfg._c()
-    l = None if layout is None else C.byref(layout._c())
-    _check(lib().ep_expert_product_grad(C.byref(c), l, _ptr(x), _ptr(weight), _ptr(z), _ptr(d_out), _ptr(d_x),
-                                        _ptr(d_weight), _ptr(d_bias), _ptr(ws), ws.numel(), _stream(stream)), w)
+    K, N, Z, E, rows = cfg.in_features, cfg.out_features, cfg.z_features, cfg.num_experts, cfg.rows
+    x = _at(x, _BF16, rows * K, w, "x") if d_weight is not None or x is not None else None
+    weight = _at(weight, _BF16, E * Z * K, w, "weight") if d_x is not None or weight is not None else None
+    z = _at(z, _BF16, rows * Z, w, "z") if cfg.activation != EP_ACT_NONE or z is not None else None
+    _check(lib().ep_expert_product_grad(
+        C.byref(cfg._c()), _blocks_arg(w, cfg, layout), x, weight, z, _at(d_out, _BF16, rows * N, w, "d_out"),
+        _maybe(d_x, _BF16, rows * K, w, "d_x"), _maybe(d_weight, _BF16, E * Z * K, w, "d_weight"),
+        _maybe(d_bias, _F32, E * Z, w, "d_bias"), ws.data_ptr(), ws.numel(), _raw_stream(stream)), w)

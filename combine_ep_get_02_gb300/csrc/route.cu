@@ -31,10 +31,11 @@ namespace {
 constexpr float kInf = __builtin_huge_valf();
 constexpr float kTiny = 1e-30f;  // least divisor of a sum of sigmoids
 
+// one instruction on this architecture
 __device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFullMask, v, o));
-  return v;
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xFFFFFFFF;" : "=f"(r) : "f"(v));
+  return r;
 }
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
@@ -42,11 +43,14 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// Unsigned key with the order of the floats (no NaN): -inf is 0x007FFFFF, 0 is below all.
+// Unsigned key with the order of the floats: what may be chosen lies strictly between the
+// keys of -inf and +inf; a NaN that arithmetic made is above, a negative one below.
 __device__ __forceinline__ uint32_t order_key(float f) {
   const uint32_t u = __float_as_uint(f);
   return u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
 }
+
+constexpr uint32_t kKeyNegInf = 0x007FFFFFu, kKeyPosInf = 0xFF800000u;
 
 // The sigmoid whose rounding the choice depends on: CUDA's expf, then correctly
 // rounded operations, so that equal scores tie.
@@ -97,17 +101,17 @@ __device__ __forceinline__ void load_row(const void* base, int64_t token, int E,
   }
 }
 
-// NaN and +inf count as -inf; returns whether there was one.
+// NaN and +inf count as -inf; returns whether the warp met one.
 template <int EPL>
 __device__ __forceinline__ bool clean(float (&l)[EPL]) {
-  bool bad = false;
+  bool ok = true;
+#pragma unroll
+  for (int j = 0; j < EPL; ++j) ok = ok && l[j] < kInf;
+  if (__all_sync(kFullMask, ok)) return false;
 #pragma unroll
   for (int j = 0; j < EPL; ++j)
-    if (!(l[j] < kInf)) {
-      l[j] = -kInf;
-      bad = true;
-    }
-  return bad;
+    if (!(l[j] < kInf)) l[j] = -kInf;
+  return true;
 }
 
 struct Top2 {
@@ -117,8 +121,32 @@ __device__ __forceinline__ Top2 top2_merge(Top2 x, Top2 y) {
   return Top2{fmaxf(x.a, y.a), fmaxf(fminf(x.a, y.a), fmaxf(x.b, y.b))};
 }
 
+// A lane's best two keys not yet taken: most lanes give two experts at most, and one that
+// gives a third looks for it among what comes after its last.
+struct Best {
+  uint32_t k1, k2;
+  int e1, e2;
+};
+template <int EPL>
+__device__ __forceinline__ Best best_two(const uint32_t (&key)[EPL], int lane, uint32_t below, int after) {
+  Best b{0u, 0u, 0x7FFFFFFF, 0x7FFFFFFF};
+#pragma unroll
+  for (int j = 0; j < EPL; ++j) {
+    const int e = expert_of<EPL>(j, lane);
+    const uint32_t k = key[j] < below || (key[j] == below && e > after) ? key[j] : 0u;
+    const bool first = k > b.k1, second = k > b.k2;
+    b.e2 = first ? b.e1 : second ? e : b.e2;
+    b.k2 = first ? b.k1 : second ? k : b.k2;
+    b.e1 = first ? e : b.e1;
+    b.k1 = first ? k : b.k1;
+  }
+  return b;
+}
+
+// CTAs per SM that the registers are limited for: four (what kRouteCtas counts on) while a
+// lane holds 8 experts at most.
 template <int EPL, bool kBf16, bool kVec>
-__global__ void __launch_bounds__(kRouteThreads) route_kernel(RouteArgs a) {
+__global__ void __launch_bounds__(kRouteThreads, EPL <= 8 ? 4 : EPL <= 16 ? 2 : 1) route_kernel(RouteArgs a) {
   extern __shared__ float s_mem[];
   __shared__ int s_valid[kRouteWarps];
   __shared__ float s_part[kRouteWarps];
@@ -127,14 +155,11 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(RouteArgs a) {
   const int E = g.E, K = g.K;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int seg = blockIdx.x / g.C, cta = blockIdx.x - seg * g.C;
-  float* s_prob = s_mem;                                  // [E]
-  int* s_count = reinterpret_cast<int*>(s_mem + E);       // [E]
-  float* s_row = s_mem + 2 * E + static_cast<size_t>(warp) * E;  // [E] per warp, with expert groups
+  int* s_count = reinterpret_cast<int*>(s_mem);         // [E]
+  float* s_rows = s_mem + E;                            // [kRouteWarps][E]
+  float* s_row = s_rows + static_cast<size_t>(warp) * E;  // this warp's
   const bool stats = a.count != nullptr;
-  for (int e = threadIdx.x; e < E; e += kRouteThreads) {
-    s_prob[e] = 0.f;
-    s_count[e] = 0;
-  }
+  for (int e = threadIdx.x; e < E; e += kRouteThreads) s_count[e] = 0;
   pdl_launch_dependents();
   pdl_wait();
   __syncthreads();
@@ -150,10 +175,13 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(RouteArgs a) {
 #pragma unroll
   for (int j = 0; j < EPL; ++j) prob[j] = 0.f;
   int valid = 0;
-  // group handled by this lane when groups are scored: `parts` lanes a group
+  // group that this lane helps to score: `parts` lanes a group; every group is read from its
+  // own place on, so that the lanes' banks differ
   const int per_group = E / g.G;
   int parts = 1;
   while (parts * 2 * g.G <= 32) parts *= 2;
+  const int grp = lane / parts, part = lane - grp * parts;
+  const int place = (part + grp * parts) % per_group;
 
   const int step = g.C * kRouteWarps;
   const int64_t first = static_cast<int64_t>(seg) * g.T;
@@ -185,37 +213,34 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(RouteArgs a) {
     bad |= clean<EPL>(l);
     // scores, the choice's keys, and the probabilities' sum
     uint32_t key[EPL];
-    float s[EPL];
-    float total = 0.f, top = 0.f;
-    if (g.sigmoid) {
+    float total = 0.f, top = 0.f, inv;
+    {
+      float s[EPL];
+      if (g.sigmoid) {
 #pragma unroll
-      for (int j = 0; j < EPL; ++j) {
-        s[j] = sigmoid_rn(l[j]);
-        total += s[j];
-        const float c = __fadd_rn(s[j], bias[j]);
-        const bool ok = l[j] > -kInf && c > -kInf;  // c NaN: not chosen
-        bad |= !(c < kInf);
-        key[j] = ok ? order_key(c) : 0u;
+        for (int j = 0; j < EPL; ++j) {
+          s[j] = sigmoid_rn(l[j]);
+          total += s[j];
+          key[j] = order_key(l[j] > -kInf ? __fadd_rn(s[j], bias[j]) : -kInf);
+        }
+      } else {
+        float m = -kInf;
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) m = fmaxf(m, l[j]);
+        top = warp_max(m);
+        if (top == -kInf) top = 0.f;  // no expert is available: every p is 0
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) {
+          s[j] = __expf(l[j] - top);
+          total += s[j];
+          key[j] = order_key(__fadd_rn(l[j], bias[j]));  // -0 + 0 is +0, so the two zeros tie
+        }
       }
-    } else {
-      float m = -kInf;
+      total = warp_sum(total);
+      inv = total > 0.f ? __frcp_rn(total) : 0.f;
 #pragma unroll
-      for (int j = 0; j < EPL; ++j) m = fmaxf(m, l[j]);
-      top = warp_max(m);
-      if (top == -kInf) top = 0.f;  // no expert is available: every p is 0
-#pragma unroll
-      for (int j = 0; j < EPL; ++j) {
-        s[j] = __expf(l[j] - top);
-        total += s[j];
-        const float c = __fadd_rn(l[j], bias[j]);  // -0 + 0 is +0, so the two zeros tie
-        bad |= !(c < kInf);
-        key[j] = c > -kInf ? order_key(c) : 0u;
-      }
+      for (int j = 0; j < EPL; ++j) prob[j] = fmaf(s[j], inv, prob[j]);
     }
-    total = warp_sum(total);
-    const float inv = total > 0.f ? __frcp_rn(total) : 0.f;
-#pragma unroll
-    for (int j = 0; j < EPL; ++j) prob[j] = fmaf(s[j], inv, prob[j]);
 
     if (g.G > 1) {  // keep the groups whose two best experts score highest
       __syncwarp();
@@ -223,19 +248,17 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(RouteArgs a) {
       for (int j = 0; j < EPL; ++j) {
         const int e = expert_of<EPL>(j, lane);
         const uint32_t u = key[j] & 0x80000000u ? key[j] ^ 0x80000000u : ~key[j];
-        if (e < E) s_row[e] = key[j] ? __uint_as_float(u) : -kInf;
+        if (e < E) s_row[e] = key[j] > kKeyNegInf && key[j] < kKeyPosInf ? __uint_as_float(u) : -kInf;
       }
       __syncwarp();
-      const int grp = lane / parts, part = lane - grp * parts;
       Top2 best{-kInf, -kInf};
       if (grp < g.G) {
-        // every group starts at its own place, so that the lanes' banks differ
         const float* row = s_row + grp * per_group;
-        int i = (part + grp * parts) % per_group;
+        int i = place;
         for (int n = part; n < per_group; n += parts) {
           best = top2_merge(best, Top2{row[i], -kInf});
           i += parts;
-          if (i >= per_group) i = (i - per_group) % per_group;
+          if (i >= per_group) i -= per_group;
         }
       }
       for (int o = 1; o < parts; o <<= 1) {
@@ -257,33 +280,29 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(RouteArgs a) {
       }
     }
 
-    // K rounds: the warp's best key, its lowest expert; that lane finds its next best
-    uint32_t bk = 0;
-    int be = 0x7FFFFFFF;
+    // K rounds: the warp's best key, its lowest expert; that lane goes on to its next best
+    Best b = best_two<EPL>(key, lane, 0xFFFFFFFFu, -1);
+    if (__any_sync(kFullMask, b.k1 >= kKeyPosInf)) {  // a choice score that is NaN or +inf: not chosen
+      bad = true;
 #pragma unroll
-    for (int j = 0; j < EPL; ++j)
-      if (key[j] > bk) {
-        bk = key[j];
-        be = expert_of<EPL>(j, lane);
-      }
+      for (int j = 0; j < EPL; ++j)
+        if (key[j] >= kKeyPosInf) key[j] = 0u;
+      b = best_two<EPL>(key, lane, 0xFFFFFFFFu, -1);
+    }
     int mine = -1;
     for (int r = 0; r < K; ++r) {
-      const uint32_t m = __reduce_max_sync(kFullMask, bk);
-      if (m == 0u) break;  // fewer than K experts are available: the other lanes stay -1
-      const int e = static_cast<int>(__reduce_min_sync(kFullMask, bk == m ? static_cast<uint32_t>(be) : 0xFFFFFFFFu));
+      const uint32_t m = __reduce_max_sync(kFullMask, b.k1);
+      if (m <= kKeyNegInf) break;  // fewer than K experts are available: the other lanes stay -1
+      const int e = static_cast<int>(__reduce_min_sync(kFullMask, b.k1 == m ? static_cast<uint32_t>(b.e1) : 0xFFFFFFFFu));
       if (lane == r) mine = e;
-      if (bk == m && be == e) {
-        bk = 0;
-        be = 0x7FFFFFFF;
-#pragma unroll
-        for (int j = 0; j < EPL; ++j) {
-          if (expert_of<EPL>(j, lane) == e) key[j] = 0u;
-          if (key[j] > bk) {
-            bk = key[j];
-            be = expert_of<EPL>(j, lane);
-          }
-        }
+      const bool gave = b.k1 == m && b.e1 == e;
+      if (gave) {
+        b.k1 = b.k2;
+        b.e1 = b.e2;
+        b.k2 = 0u;
+        b.e2 = 0x7FFFFFFF;
       }
+      if (EPL > 2 && gave && b.k1 == 0u) b = best_two<EPL>(key, lane, m, e);
     }
     // weights of the chosen: their logits are read again (they are in L1)
     float w = 0.f, lv = -kInf;
@@ -310,51 +329,60 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(RouteArgs a) {
   if (bad) atomicOr(a.err, kErrNonfinite);
   if (!stats) return;
 
-  // the CTA's sums, warp after warp
-  if (lane == 0) s_valid[warp] = valid;
-  for (int w = 0; w < kRouteWarps; ++w) {
-    __syncthreads();
-    if (warp == w) {
+  // the CTA's sums, in the order of the warps
 #pragma unroll
-      for (int j = 0; j < EPL; ++j) {
-        const int e = expert_of<EPL>(j, lane);
-        if (e < E) s_prob[e] += prob[j];
-      }
-    }
+  for (int j = 0; j < EPL; ++j) {
+    const int e = expert_of<EPL>(j, lane);
+    if (e < E) s_row[e] = prob[j];
   }
+  if (lane == 0) s_valid[warp] = valid;
   __syncthreads();
-  for (int e = threadIdx.x; e < E; e += kRouteThreads) {
-    a.cta_prob[static_cast<size_t>(blockIdx.x) * E + e] = s_prob[e];
-    a.cta_count[static_cast<size_t>(blockIdx.x) * E + e] = s_count[e];
-  }
-  if (threadIdx.x == 0) {
-    int n = 0;
-    for (int w = 0; w < kRouteWarps; ++w) n += s_valid[w];
-    a.cta_valid[blockIdx.x] = n;
-  }
-  __threadfence();
-  __syncthreads();
-  if (threadIdx.x == 0) s_last = atomicAdd(a.seg_done + seg, 1u) == static_cast<uint32_t>(g.C) - 1u;
-  __syncthreads();
-  if (!s_last) return;
-  __threadfence();
-
-  // the segment's last CTA adds the partial sums in CTA order
-  const size_t base = static_cast<size_t>(seg) * g.C;
   int n = 0;
-  for (int c = 0; c < g.C; ++c) n += __ldcg(a.cta_valid + base + c);
+#pragma unroll
+  for (int w = 0; w < kRouteWarps; ++w) n += s_valid[w];
   float dot = 0.f;
-  for (int e = threadIdx.x; e < E; e += kRouteThreads) {
-    float p = 0.f;
-    int cnt = 0;
-#pragma unroll 8
-    for (int c = 0; c < g.C; ++c) {
-      p += __ldcg(a.cta_prob + (base + c) * E + e);
-      cnt += __ldcg(a.cta_count + (base + c) * E + e);
+  if (g.C > 1) {
+    for (int e = threadIdx.x; e < E; e += kRouteThreads) {
+      float p = 0.f;
+#pragma unroll
+      for (int w = 0; w < kRouteWarps; ++w) p += s_rows[static_cast<size_t>(w) * E + e];
+      a.cta_prob[static_cast<size_t>(blockIdx.x) * E + e] = p;
+      a.cta_count[static_cast<size_t>(blockIdx.x) * E + e] = s_count[e];
     }
-    a.prob_sum[static_cast<size_t>(seg) * E + e] = p;
-    a.count[static_cast<size_t>(seg) * E + e] = cnt;
-    dot = fmaf(p, static_cast<float>(cnt), dot);
+    if (threadIdx.x == 0) a.cta_valid[blockIdx.x] = n;
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) s_last = atomicAdd(a.seg_done + seg, 1u) == static_cast<uint32_t>(g.C) - 1u;
+    __syncthreads();
+    if (!s_last) return;
+    __threadfence();
+    // the segment's last CTA adds the partial sums in CTA order
+    const size_t base = static_cast<size_t>(seg) * g.C;
+    n = 0;
+#pragma unroll 4
+    for (int c = 0; c < g.C; ++c) n += __ldcg(a.cta_valid + base + c);
+    for (int e = threadIdx.x; e < E; e += kRouteThreads) {
+      float p = 0.f;
+      int cnt = 0;
+#pragma unroll 16
+      for (int c = 0; c < g.C; ++c) {
+        p += __ldcg(a.cta_prob + (base + c) * E + e);
+        cnt += __ldcg(a.cta_count + (base + c) * E + e);
+      }
+      a.prob_sum[static_cast<size_t>(seg) * E + e] = p;
+      a.count[static_cast<size_t>(seg) * E + e] = cnt;
+      dot = fmaf(p, static_cast<float>(cnt), dot);
+    }
+  } else {  // the segment's only CTA
+    for (int e = threadIdx.x; e < E; e += kRouteThreads) {
+      float p = 0.f;
+#pragma unroll
+      for (int w = 0; w < kRouteWarps; ++w) p += s_rows[static_cast<size_t>(w) * E + e];
+      const int cnt = s_count[e];
+      a.prob_sum[static_cast<size_t>(seg) * E + e] = p;
+      a.count[static_cast<size_t>(seg) * E + e] = cnt;
+      dot = fmaf(p, static_cast<float>(cnt), dot);
+    }
   }
   dot = warp_sum(dot);
   if (lane == 0) s_part[warp] = dot;
@@ -363,13 +391,19 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(RouteArgs a) {
     float sum = 0.f;
     for (int w = 0; w < kRouteWarps; ++w) sum += s_part[w];
     const float nf = static_cast<float>(n > 0 ? n : 1);
+    const float seg_loss = sum * (static_cast<float>(E) / static_cast<float>(K)) / nf / nf;
     a.num_valid[seg] = n;
-    __stcg(a.seg_loss + seg, sum * (static_cast<float>(E) / static_cast<float>(K)) / nf / nf);
-    a.seg_done[seg] = 0u;
+    if (g.C > 1) a.seg_done[seg] = 0u;
+    if (g.B == 1) {
+      *a.loss = seg_loss;
+      return;
+    }
+    __stcg(a.seg_loss + seg, seg_loss);
     __threadfence();
     if (atomicAdd(a.done, 1u) == static_cast<uint32_t>(g.B) - 1u) {  // the last segment of all
       __threadfence();
       float loss = 0.f;
+#pragma unroll 16
       for (int b = 0; b < g.B; ++b) loss += __ldcg(a.seg_loss + b);
       *a.loss = loss / static_cast<float>(g.B);
       *a.done = 0u;
@@ -541,7 +575,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_grad_kernel(RouteGradArgs
 template <int EPL, bool kBf16, bool kVec>
 cudaError_t launch_fwd(const RouteArgs& a, cudaStream_t stream) {
   auto kern = route_kernel<EPL, kBf16, kVec>;
-  const size_t smem = sizeof(float) * static_cast<size_t>(a.g.E) * (2 + (a.g.G > 1 ? kRouteWarps : 0));
+  const size_t smem = sizeof(float) * static_cast<size_t>(a.g.E) * (1 + kRouteWarps);
   if (resident_ctas(reinterpret_cast<const void*>(kern), kRouteThreads, smem) < 1) return cudaErrorInvalidConfiguration;
   return launch_chained(kern, dim3(static_cast<unsigned>(a.g.B) * a.g.C), dim3(kRouteThreads), smem, stream, a);
 }
