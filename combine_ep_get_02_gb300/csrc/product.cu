@@ -7,7 +7,7 @@
 // A CTA per SM walks over output tiles of 128 rows x 256 columns. Warp 0 brings tiles
 // of A and B (64 of the summed index at a time) into a ring of shared-memory stages by
 // TMA, one thread of warp 1 issues tcgen05.mma into one of two TMEM accumulators, and
-// warps 2-5 take the other accumulator through the epilogue meanwhile. Row tiles start
+// warps 2-9 take the other accumulator through the epilogue meanwhile. Row tiles start
 // at each group's first row, so a tile's last rows may belong to the next group: they are
 // computed and not stored (an output row depends on its own row of A alone). Columns past
 // the tensors read as zero.
@@ -20,7 +20,8 @@ namespace ep {
 
 namespace {
 
-constexpr int kThreads = 192;
+constexpr int kEpilogueWarps = 8;  // two to each quarter of the TMEM lanes, each with half of the columns
+constexpr int kThreads = 64 + 32 * kEpilogueWarps;
 constexpr int kBM = kTileRows, kBN = 256, kBK = 64;
 constexpr int kStages = 4;
 constexpr int kABytes = kBM * kBK * 2, kBBytes = kBN * kBK * 2, kStageBytes = kABytes + kBBytes;
@@ -29,12 +30,7 @@ constexpr int kRaster = 16;  // row tiles that share a sweep over the columns
 struct RowsArgs {
   Groups groups;
   int sum;   // length of the summed index
-  int cols;  // output columns
-  int b_rows;  // rows of B per group along the output (gated: both halves)
-  const uint16_t* bias;
-  const uint16_t* residual;
-  uint16_t* z;
-  uint16_t* out;
+  Epilogue epi;
   uint32_t* err;
 };
 
@@ -78,7 +74,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ volatile int s_abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t stage0 = (smem_addr(s_raw) + 1023u) & ~1023u;
-  int* prefix = reinterpret_cast<int*>(s_raw + (stage0 - smem_addr(s_raw)) + kStages * kStageBytes);
+  const uint32_t patch0 = stage0 + kStages * kStageBytes;
+  int* prefix = reinterpret_cast<int*>(s_raw + (patch0 - smem_addr(s_raw)) + kEpilogueWarps * kPatchBytes);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -87,7 +84,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init_count(smem_addr(&s_acc_full[i]), 1);
-      mbar_init_count(smem_addr(&s_acc_empty[i]), 4);
+      mbar_init_count(smem_addr(&s_acc_empty[i]), kEpilogueWarps);
     }
     mbar_init_count(smem_addr(&s_drained), 1);
     s_abort = 0;
@@ -106,7 +103,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s_tmem;
-  const Tiles<kCols> tiles(a.groups, prefix, a.cols);
+  const Tiles<kCols> tiles(a.groups, prefix, a.epi.cols);
   const int blocks = (a.sum + kBK - 1) / kBK;
   auto give_up = [&] {
     s_abort = 1;
@@ -135,7 +132,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               tma_load_3d(sb + p * (kBK * 128), &map_b, t.n0 + p * 64, kb * kBK, t.g, bar);
           } else {
             tma_load_3d(sb, &map_b, kb * kBK, t.n0, t.g, bar);
-            tma_load_3d(sb + kBBytes / 2, &map_b, kb * kBK, kGated ? a.cols + t.n0 : t.n0 + kBN / 2, t.g, bar);
+            tma_load_3d(sb + kBBytes / 2, &map_b, kb * kBK, kGated ? a.epi.cols + t.n0 : t.n0 + kBN / 2, t.g, bar);
           }
         }
       }
@@ -184,6 +181,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     const int quarter = warp & 3;  // the TMEM lanes this warp may read
+    const int half = (warp - 2) >> 2;
+    const uint32_t patch = patch0 + (warp - 2) * kPatchBytes;
     uint32_t acc = 0;
     for (int64_t i = blockIdx.x; i < tiles.total; i += gridDim.x, ++acc) {
       const uint32_t b = acc & 1u;
@@ -195,52 +194,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         break;
       }
       tc_fence_after();
-      const int m = quarter * 32 + lane;
-      const bool live = m < t.rows;
+      const int m = quarter * 32;
       const int64_t row = static_cast<int64_t>(t.begin) + m;
-      const uint32_t d = tmem + b * kBN + (static_cast<uint32_t>(quarter * 32) << 16);
-      const uint16_t* bias = a.bias == nullptr ? nullptr : a.bias + static_cast<int64_t>(t.g) * a.b_rows;
-      for (int c = 0; c < kCols; c += 32) {
-        const int n0 = t.n0 + c;
-        if (n0 >= a.cols) break;
+      const int rows = t.rows - m;
+      const uint32_t d = tmem + b * kBN + (static_cast<uint32_t>(m) << 16);
+      for (int c = half * (kCols / 2); c < (half + 1) * (kCols / 2); c += 32) {
+        if (rows <= 0 || t.n0 + c >= a.epi.cols) break;
         float v[32], u[kGated ? 32 : 1];
         tmem_ld32(d + c, v);
         if constexpr (kGated) tmem_ld32(d + kCols + c, u);
         tmem_ld_wait();
-#pragma unroll
-        for (int j = 0; j < 32; j += 8) {
-          const int n = n0 + j;
-          if (n >= a.cols) break;
-          if (bias != nullptr) {
-            float f[8];
-            unpack8(__ldg(reinterpret_cast<const uint4*>(bias + n)), f);
-#pragma unroll
-            for (int x = 0; x < 8; ++x) v[j + x] += f[x];
-            if constexpr (kGated) {
-              unpack8(__ldg(reinterpret_cast<const uint4*>(bias + a.cols + n)), f);
-#pragma unroll
-              for (int x = 0; x < 8; ++x) u[j + x] += f[x];
-            }
-          }
-          if (!live) continue;
-          if (a.z != nullptr) {
-            uint16_t* zp = a.z + row * a.b_rows + n;
-            st16(zp, pack8(v + j));
-            if constexpr (kGated) st16(zp + a.cols, pack8(u + j));
-          }
-#pragma unroll
-          for (int x = 0; x < 8; ++x) {
-            v[j + x] = activate<kAct>(v[j + x]);
-            if constexpr (kGated) v[j + x] *= u[j + x];
-          }
-          if (a.residual != nullptr) {
-            float f[8];
-            unpack8(*reinterpret_cast<const uint4*>(a.residual + row * a.cols + n), f);
-#pragma unroll
-            for (int x = 0; x < 8; ++x) v[j + x] += f[x];
-          }
-          st16(a.out + row * a.cols + n, pack8(v + j));
-        }
+        finish_rows<kAct>(a.epi, patch, v, u, t.g, row, rows, t.n0 + c, lane);
       }
       tc_fence_before();
       __syncwarp();
@@ -261,20 +225,20 @@ cudaError_t launch_rows(const uint16_t* A, const uint16_t* B, const RowsArgs& a,
   cudaError_t st = make_tensor_map(&map_a, A, 2, size_a, box_a);
   if (st != cudaSuccess) return st;
   if (kBMn) {
-    const uint64_t size[3] = {static_cast<uint64_t>(a.cols), static_cast<uint64_t>(a.sum), static_cast<uint64_t>(a.groups.E)};
+    const uint64_t size[3] = {static_cast<uint64_t>(a.epi.cols), static_cast<uint64_t>(a.sum), static_cast<uint64_t>(a.groups.E)};
     const uint32_t box[3] = {64, kBK, 1};
     st = make_tensor_map(&map_b, B, 3, size, box);
   } else {
-    const uint64_t size[3] = {static_cast<uint64_t>(a.sum), static_cast<uint64_t>(a.b_rows), static_cast<uint64_t>(a.groups.E)};
+    const uint64_t size[3] = {static_cast<uint64_t>(a.sum), static_cast<uint64_t>(a.epi.z_cols), static_cast<uint64_t>(a.groups.E)};
     const uint32_t box[3] = {kBK, kBN / 2, 1};
     st = make_tensor_map(&map_b, B, 3, size, box);
   }
   if (st != cudaSuccess) return st;
   auto kern = rows_kernel<kAct, kBMn>;
-  const size_t smem = 1024 + kStages * kStageBytes + sizeof(int) * (static_cast<size_t>(a.groups.E) + 1);
+  const size_t smem = 1024 + kStages * kStageBytes + kEpilogueWarps * kPatchBytes + sizeof(int) * (static_cast<size_t>(a.groups.E) + 1);
   if (resident_ctas(reinterpret_cast<const void*>(kern), kThreads, smem) < 1) return cudaErrorInvalidConfiguration;
   const int cols = kAct == EP_ACT_SWIGLU ? kBN / 2 : kBN;
-  const int64_t most = max_row_tiles(a.groups) * ((a.cols + cols - 1) / cols);
+  const int64_t most = max_row_tiles(a.groups) * ((a.epi.cols + cols - 1) / cols);
   const unsigned grid = static_cast<unsigned>(most < num_sms ? most : num_sms);
   return launch_chained(kern, dim3(grid), dim3(kThreads), smem, stream, map_a, map_b, a);
 }
@@ -282,7 +246,7 @@ cudaError_t launch_rows(const uint16_t* A, const uint16_t* B, const RowsArgs& a,
 }  // namespace
 
 cudaError_t launch_product(const ProductArgs& p, int num_sms, cudaStream_t stream) {
-  RowsArgs a = {p.g.groups, p.g.K, p.g.N, p.g.Z, p.bias, p.residual, p.z, p.out, p.err};
+  RowsArgs a = {p.g.groups, p.g.K, {p.bias, p.residual, p.z, p.out, p.g.N, p.g.Z}, p.err};
   switch (p.g.act) {
     case EP_ACT_RELU: return launch_rows<EP_ACT_RELU, false>(p.x, p.weight, a, num_sms, stream);
     case EP_ACT_SILU: return launch_rows<EP_ACT_SILU, false>(p.x, p.weight, a, num_sms, stream);
@@ -293,7 +257,7 @@ cudaError_t launch_product(const ProductArgs& p, int num_sms, cudaStream_t strea
 }
 
 cudaError_t launch_product_dx(const ProductGradArgs& p, int num_sms, cudaStream_t stream) {
-  RowsArgs a = {p.g.groups, p.g.Z, p.g.K, 0, nullptr, nullptr, nullptr, p.d_x, p.err};
+  RowsArgs a = {p.g.groups, p.g.Z, {nullptr, nullptr, nullptr, p.d_x, p.g.K, p.g.K}, p.err};
   const uint16_t* dz = p.dz != nullptr ? p.dz : p.d_out;
   return launch_rows<EP_ACT_NONE, true>(dz, p.weight, a, num_sms, stream);
 }

@@ -86,4 +86,119 @@ __device__ __forceinline__ uint4 pack8(const float* f) {
                     f32x2_to_bf16x2(f[6], f[7]));
 }
 
+// ---- rows between registers and memory ------------------------------------------------
+//
+// An accumulator row lives in one thread, 32 columns at a time; a warp holds 32 rows. To
+// touch memory in whole 64-byte pieces of rows they pass through 2 KB of shared memory per
+// warp (16-byte chunks, XOR-permuted so that neither side has bank conflicts); a store
+// straight from the registers writes 16 bytes to each of 32 rows at once and took about
+// twice as long on the shortest sums.
+
+constexpr int kPatchBytes = 32 * 64;
+
+__device__ __forceinline__ uint32_t patch_at(uint32_t patch, int row, int chunk) {
+  return patch + row * 64 + ((chunk ^ (row >> 1 & 3)) << 4);
+}
+__device__ __forceinline__ void st_shared16(uint32_t p, const uint4& v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(p), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ __forceinline__ uint4 ld_shared16(uint32_t p) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(p) : "memory");
+  return v;
+}
+
+// The warp's 32 x 32 values to `dst` (its row 0, column 0; rows `stride` apart), rounded to
+// bf16: the first `rows` rows, the first `cols` (a multiple of 8) columns.
+__device__ __forceinline__ void store_rows(uint32_t patch, const float (&v)[32], uint16_t* dst, int64_t stride, int rows,
+                                           int cols, int lane) {
+#pragma unroll
+  for (int c = 0; c < 4; ++c) st_shared16(patch_at(patch, lane, c), pack8(v + 8 * c));
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = i * 8 + (lane >> 2), c = lane & 3;
+    const uint4 w = ld_shared16(patch_at(patch, r, c));
+    if (r < rows && c * 8 < cols) st16(dst + r * stride + c * 8, w);
+  }
+  __syncwarp();
+}
+
+// The same rows and columns of a tensor, in flight in the order they are read ...
+struct RowsInFlight {
+  uint4 v[4];
+};
+__device__ __forceinline__ RowsInFlight fetch_rows(const uint16_t* src, int64_t stride, int rows, int cols, int lane) {
+  RowsInFlight f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = i * 8 + (lane >> 2), c = lane & 3;
+    f.v[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (r < rows && c * 8 < cols) f.v[i] = *reinterpret_cast<const uint4*>(src + r * stride + c * 8);
+  }
+  return f;
+}
+// ... and added to the thread's row.
+__device__ __forceinline__ void add_rows(uint32_t patch, const RowsInFlight& f, float (&v)[32], int lane) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) st_shared16(patch_at(patch, i * 8 + (lane >> 2), lane & 3), f.v[i]);
+  __syncwarp();
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    float x[8];
+    unpack8(ld_shared16(patch_at(patch, lane, c)), x);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[8 * c + j] += x[j];
+  }
+  __syncwarp();
+}
+
+// What a product does with its sums.
+struct Epilogue {
+  const uint16_t* bias;      // [E][z_cols] or null
+  const uint16_t* residual;  // [rows][cols] or null
+  uint16_t* z;               // [rows][z_cols] or null
+  uint16_t* out;             // [rows][cols]
+  int cols, z_cols;
+};
+
+// 32 columns n0.. of a warp's 32 rows row0.. of group g, `rows` of which count: v the sums
+// (gated: u those of the other half), n0 < cols.
+template <int kAct>
+__device__ __forceinline__ void finish_rows(const Epilogue& e, uint32_t patch, float (&v)[32],
+                                            float (&u)[kAct == EP_ACT_SWIGLU ? 32 : 1], int g, int64_t row0, int rows,
+                                            int n0, int lane) {
+  constexpr bool kGated = kAct == EP_ACT_SWIGLU;
+  const int cols = min(32, e.cols - n0);
+  RowsInFlight res;
+  if (e.residual != nullptr) res = fetch_rows(e.residual + row0 * e.cols + n0, e.cols, rows, cols, lane);
+  if (e.bias != nullptr) {
+    const uint16_t* b = e.bias + static_cast<int64_t>(g) * e.z_cols + n0;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      if (c * 8 >= cols) break;
+      float f[8];
+      unpack8(__ldg(reinterpret_cast<const uint4*>(b + c * 8)), f);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[8 * c + j] += f[j];
+      if constexpr (kGated) {
+        unpack8(__ldg(reinterpret_cast<const uint4*>(b + e.cols + c * 8)), f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) u[8 * c + j] += f[j];
+      }
+    }
+  }
+  if (e.z != nullptr) {
+    store_rows(patch, v, e.z + row0 * e.z_cols + n0, e.z_cols, rows, cols, lane);
+    if constexpr (kGated) store_rows(patch, u, e.z + row0 * e.z_cols + e.cols + n0, e.z_cols, rows, cols, lane);
+  }
+#pragma unroll
+  for (int j = 0; j < 32; ++j) {
+    v[j] = activate<kAct>(v[j]);
+    if constexpr (kGated) v[j] *= u[j];
+  }
+  if (e.residual != nullptr) add_rows(patch, res, v, lane);
+  store_rows(patch, v, e.out + row0 * e.cols + n0, e.cols, rows, cols, lane);
+}
+
 }  // namespace ep

@@ -2,7 +2,7 @@
 // dz[r][z] x[r][k], for every group (zeros for an empty one).
 //
 // The same roles as the rows' products (a CTA per SM over 128 x 256 tiles of dW; one
-// warp for TMA, one for tcgen05.mma, four for the epilogue), with both operands
+// warp for TMA, one for tcgen05.mma, eight for the epilogue), with both operands
 // MN-major: the summed index is the row, so tiles of 64 rows are used as they lie in
 // the tensors, without a transposition. A group's last tile ends inside the next
 // group's rows (or padding): the warp that issues the products first zeroes, in shared
@@ -14,7 +14,8 @@ namespace ep {
 
 namespace {
 
-constexpr int kThreads = 192;
+constexpr int kEpilogueWarps = 8;
+constexpr int kThreads = 64 + 32 * kEpilogueWarps;
 constexpr int kBM = 128, kBN = 256, kBK = 64;
 constexpr int kStages = 4;
 constexpr int kPanel = kBK * 128;  // bytes of 64 columns x 64 rows
@@ -47,6 +48,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ volatile int s_abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t stage0 = (smem_addr(s_raw) + 1023u) & ~1023u;
+  const uint32_t patch0 = stage0 + kStages * kStageBytes;
   uint8_t* stage_mem = s_raw + (stage0 - smem_addr(s_raw));
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -55,7 +57,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init_count(smem_addr(&s_acc_full[i]), 1);
-      mbar_init_count(smem_addr(&s_acc_empty[i]), 4);
+      mbar_init_count(smem_addr(&s_acc_empty[i]), kEpilogueWarps);
     }
     mbar_init_count(smem_addr(&s_drained), 1);
     s_abort = 0;
@@ -164,13 +166,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_wait_timed(smem_addr(&s_drained), 0);
     }
   } else {
-    const int quarter = warp & 3;
+    const int quarter = warp & 3, half = (warp - 2) >> 2;
+    const uint32_t patch = patch0 + (warp - 2) * kPatchBytes;
     uint32_t acc = 0;
     for (int64_t i = blockIdx.x; i < total; i += gridDim.x) {
       const Tile t = tile_at(a, i, mt, nt);
       const uint32_t b = acc & 1u;
-      const int zr = t.z0 + quarter * 32 + lane;
-      uint16_t* out = a.out + (static_cast<int64_t>(t.g) * a.Z + zr) * a.K + t.k0;
+      const int z0 = t.z0 + quarter * 32;
+      uint16_t* out = a.out + (static_cast<int64_t>(t.g) * a.Z + z0) * a.K + t.k0;
       if (t.rows > 0) {
         bool ok = s_abort == 0 && mbar_wait_timed(smem_addr(&s_acc_full[b]), acc >> 1 & 1u);
         ok = __all_sync(kFullMask, ok);
@@ -181,8 +184,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
       }
       const uint32_t d = tmem + b * kBN + (static_cast<uint32_t>(quarter * 32) << 16);
-      for (int c = 0; c < kBN; c += 32) {
-        if (t.k0 + c >= a.K) break;
+      for (int c = half * (kBN / 2); c < (half + 1) * (kBN / 2); c += 32) {
+        if (z0 >= a.Z || t.k0 + c >= a.K) break;
         float v[32];
         if (t.rows > 0) {
           tmem_ld32(d + c, v);
@@ -191,11 +194,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int j = 0; j < 32; ++j) v[j] = 0.f;
         }
-        if (zr < a.Z) {
-#pragma unroll
-          for (int j = 0; j < 32; j += 8)
-            if (t.k0 + c + j < a.K) st16(out + c + j, pack8(v + j));
-        }
+        store_rows(patch, v, out + c, a.K, a.Z - z0, a.K - t.k0 - c, lane);
       }
       if (t.rows > 0) {
         tc_fence_before();
@@ -223,7 +222,7 @@ cudaError_t launch_product_dw(const ProductGradArgs& p, int num_sms, cudaStream_
   cudaError_t st = make_tensor_map(&map_dz, dz, 2, size_dz, box);
   if (st == cudaSuccess) st = make_tensor_map(&map_x, p.x, 2, size_x, box);
   if (st != cudaSuccess) return st;
-  const size_t smem = 1024 + kStages * kStageBytes;
+  const size_t smem = 1024 + kStages * kStageBytes + kEpilogueWarps * kPatchBytes;
   if (resident_ctas(reinterpret_cast<const void*>(weight_grad_kernel), kThreads, smem) < 1)
     return cudaErrorInvalidConfiguration;
   const int64_t total =
