@@ -76,6 +76,8 @@ class _KeepsStruct:
     def __setattr__(self, name, value):
         object.__setattr__(self, name, value)
         object.__setattr__(self, "_struct", None)
+        object.__setattr__(self, "_reference", None)
+        object.__setattr__(self, "_sizes", None)
 
     def _c(self):
         st = self.__dict__.get("_struct")
@@ -83,6 +85,28 @@ class _KeepsStruct:
             st = self._build_struct()
             object.__setattr__(self, "_struct", st)
         return st
+
+    def _ref(self):
+        """byref of the struct, kept as long as it is."""
+        r = self.__dict__.get("_reference")
+        if r is None:
+            r = C.byref(self._c())
+            object.__setattr__(self, "_reference", r)
+        return r
+
+    def _checked(self, where: str, fields):
+        """Element counts of the tensors named in `fields` ((name, dtype) pairs; -1 for None),
+        refused as by _at; kept, like the struct that holds their addresses."""
+        n = self.__dict__.get("_sizes")
+        if n is None:
+            n = []
+            for name, dtype in fields:
+                t = getattr(self, name)
+                if t is not None:
+                    _at(t, dtype, 0, where, name)
+                n.append(-1 if t is None else t.numel())
+            object.__setattr__(self, "_sizes", n)
+        return n
 
 
 @dataclasses.dataclass
@@ -540,20 +564,30 @@ def alloc_route(cfg: RouteConfig, device="cuda", stats: bool = True) -> Route:
     return out
 
 
+_ROUTE_FIELDS = (("topk_idx", _I64), ("topk_weights", _F32), ("expert_count", _I32), ("prob_sum", _F32),
+                 ("num_valid", _I32), ("balance_loss", _F32))
+_BLOCK_FIELDS = (("exp_cnt", _I32), ("exp_base", _I32), ("exp_region", _I32))
+
+
+def _too_small(where, obj, fields, need):
+    for (name, dtype), n in zip(fields, need):
+        t = getattr(obj, name)
+        if t is not None and t.numel() < n:
+            _refuse(where, name, t, dtype, n)
+
+
 def _route_args(where, cfg, logits, token_mask, r):
     """Addresses of the logits and the mask; refuses tensors of `r` that do not fit the configuration."""
-    N = cfg.num_segments * cfg.num_tokens
-    x = _at(logits, _BF16 if cfg.logits_dtype == EP_DTYPE_BF16 else _F32, N * cfg.num_experts, where, "logits")
-    m = None if token_mask is None else _at(
-        token_mask, token_mask.dtype if token_mask.dtype in (_U8, torch.bool) else _U8, N, where, "token_mask")
-    BE = cfg.num_segments * cfg.num_experts
-    _at(r.topk_idx, _I64, N * cfg.num_topk, where, "topk_idx")
-    _maybe(r.topk_weights, _F32, N * cfg.num_topk, where, "topk_weights")
-    _maybe(r.expert_count, _I32, BE, where, "expert_count")
-    _maybe(r.prob_sum, _F32, BE, where, "prob_sum")
-    _maybe(r.num_valid, _I32, cfg.num_segments, where, "num_valid")
-    _maybe(r.balance_loss, _F32, 1, where, "balance_loss")
-    return x, m
+    B, E = cfg.num_segments, cfg.num_experts
+    N = B * cfg.num_tokens
+    NK, BE = N * cfg.num_topk, B * E
+    i, w, c, p, v, l = r._checked(where, _ROUTE_FIELDS)
+    if i < NK or -1 < w < NK or -1 < c < BE or -1 < p < BE or -1 < v < B or l == 0:
+        _too_small(where, r, _ROUTE_FIELDS, (NK, NK, BE, BE, B, 1))
+    x = _at(logits, _BF16 if cfg.logits_dtype == EP_DTYPE_BF16 else _F32, N * E, where, "logits")
+    if token_mask is None:
+        return x, None
+    return x, _at(token_mask, torch.bool if token_mask.dtype is torch.bool else _U8, N, where, "token_mask")
 
 
 def ep_route(cfg: RouteConfig, logits: torch.Tensor, choice_bias, token_mask, out: Route, ws: torch.Tensor,
@@ -562,7 +596,7 @@ def ep_route(cfg: RouteConfig, logits: torch.Tensor, choice_bias, token_mask, ou
     out.balance_loss also the counts, the probability sums and the balance loss."""
     x, m = _route_args("ep_route", cfg, logits, token_mask, out)
     b = _maybe(choice_bias, _F32, cfg.num_experts, "ep_route", "choice_bias")
-    st = lib().ep_route(C.byref(cfg._c()), x, b, m, C.byref(out._c()), ws.data_ptr(), ws.numel(), _raw_stream(stream))
+    st = lib().ep_route(cfg._ref(), x, b, m, out._ref(), ws.data_ptr(), ws.numel(), _raw_stream(stream))
     _check(st, "ep_route")
 
 
@@ -575,7 +609,7 @@ def ep_route_grad(cfg: RouteConfig, logits: torch.Tensor, token_mask, route: Rou
     dw = _maybe(d_weights, _F32, cfg.num_segments * cfg.num_tokens * cfg.num_topk, w, "d_weights")
     dl = _maybe(d_loss, _F32, 1, w, "d_loss")
     dx = _at(d_logits, logits.dtype, cfg.num_segments * cfg.num_tokens * cfg.num_experts, w, "d_logits")
-    _check(lib().ep_route_grad(C.byref(cfg._c()), x, m, C.byref(route._c()), dw, dl, dx, ws.data_ptr(), ws.numel(),
+    _check(lib().ep_route_grad(cfg._ref(), x, m, route._ref(), dw, dl, dx, ws.data_ptr(), ws.numel(),
                                _raw_stream(stream)), w)
 
 
@@ -587,7 +621,7 @@ def ep_combine_grad(cfg: Config, layout: Layout, y, topk_idx: torch.Tensor, topk
     NK, rows = N * cfg.num_topk, max(ep_recv_rows(cfg), 0)
     y = _at(y, _BF16, rows * H, w, "y") if d_weights is not None or y is not None else None
     _check(lib().ep_combine_grad(
-        C.byref(cfg._c()), C.byref(layout._c()), y, _at(topk_idx, _I64, NK, w, "topk_idx"),
+        cfg._ref(), layout._ref(), y, _at(topk_idx, _I64, NK, w, "topk_idx"),
         _at(topk_weights, _F32, NK, w, "topk_weights"), _at(d_out, _BF16, N * H, w, "d_out"),
         _maybe(d_y, _BF16, rows * H, w, "d_y"), _maybe(d_weights, _F32, NK, w, "d_weights"), ws.data_ptr(), ws.numel(),
         _raw_stream(stream)), w)
@@ -597,10 +631,10 @@ def _blocks_arg(where, cfg, layout):
     if layout is None:
         return None
     R, E = cfg.num_ranks, cfg.num_experts
-    _at(layout.exp_cnt, _I32, E, where, "exp_cnt")
-    _at(layout.exp_base, _I32, E + R, where, "exp_base")
-    _at(layout.exp_region, _I32, R + 1, where, "exp_region")
-    return C.byref(layout._c())
+    c, b, r = layout._checked(where, _BLOCK_FIELDS)
+    if -1 < c < E or -1 < b < E + R or -1 < r < R + 1:
+        _too_small(where, layout, _BLOCK_FIELDS, (E, E + R, R + 1))
+    return layout._ref()
 
 
 def ep_expert_product(cfg: ProductConfig, layout, x: torch.Tensor, x_sf, weight: torch.Tensor, bias, residual, z,
@@ -617,7 +651,7 @@ def ep_expert_product(cfg: ProductConfig, layout, x: torch.Tensor, x_sf, weight:
         x = _at(x, _BF16, rows * K, w, "x")
         x_sf = _maybe(x_sf, _F32, 0, w, "x_sf")
     _check(lib().ep_expert_product(
-        C.byref(cfg._c()), _blocks_arg(w, cfg, layout), x, x_sf, _at(weight, _BF16, E * Z * K, w, "weight"),
+        cfg._ref(), _blocks_arg(w, cfg, layout), x, x_sf, _at(weight, _BF16, E * Z * K, w, "weight"),
         _maybe(bias, _BF16, E * Z, w, "bias"), _maybe(residual, _BF16, rows * N, w, "residual"),
         _maybe(z, _BF16, rows * Z, w, "z"), _at(out, _BF16, rows * N, w, "out"), ws.data_ptr(), ws.numel(),
         _raw_stream(stream)), w)
@@ -632,6 +666,6 @@ def ep_expert_product_grad(cfg: ProductConfig, layout, x, weight, z, d_out: torc
     weight = _at(weight, _BF16, E * Z * K, w, "weight") if d_x is not None or weight is not None else None
     z = _at(z, _BF16, rows * Z, w, "z") if cfg.activation != EP_ACT_NONE or z is not None else None
     _check(lib().ep_expert_product_grad(
-        C.byref(cfg._c()), _blocks_arg(w, cfg, layout), x, weight, z, _at(d_out, _BF16, rows * N, w, "d_out"),
+        cfg._ref(), _blocks_arg(w, cfg, layout), x, weight, z, _at(d_out, _BF16, rows * N, w, "d_out"),
         _maybe(d_x, _BF16, rows * K, w, "d_x"), _maybe(d_weight, _BF16, E * Z * K, w, "d_weight"),
         _maybe(d_bias, _F32, E * Z, w, "d_bias"), ws.data_ptr(), ws.numel(), _raw_stream(stream)), w)

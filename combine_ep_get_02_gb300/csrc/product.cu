@@ -14,54 +14,16 @@
 //
 // Every wait is bounded; one that gives up latches kErrTimeout, lets the CTA's copies
 // and products finish and returns.
-#include "product_common.cuh"
+#include "product_rows.cuh"
 
 namespace ep {
 
 namespace {
 
-constexpr int kEpilogueWarps = 8;  // two to each quarter of the TMEM lanes, each with half of the columns
-constexpr int kThreads = 64 + 32 * kEpilogueWarps;
-constexpr int kBM = kTileRows, kBN = 256, kBK = 64;
+constexpr int kThreads = kRowsThreadsTc;
+constexpr int kBM = kTileRows, kBN = 256;
 constexpr int kStages = 4;
 constexpr int kABytes = kBM * kBK * 2, kBBytes = kBN * kBK * 2, kStageBytes = kABytes + kBBytes;
-constexpr int kRaster = 16;  // row tiles that share a sweep over the columns
-
-struct RowsArgs {
-  Groups groups;
-  int sum;   // length of the summed index
-  Epilogue epi;
-  uint32_t* err;
-};
-
-struct Tile {
-  int g, begin, rows;  // group, first row of the tile, rows of the group from there on
-  int n0;
-};
-
-template <int kCols>
-struct Tiles {
-  const Groups& q;
-  const int* prefix;
-  int nt;
-  int64_t total;
-  __device__ Tiles(const Groups& groups, const int* p, int cols)
-      : q(groups), prefix(p), nt((cols + kCols - 1) / kCols), total(static_cast<int64_t>(p[groups.E]) * nt) {}
-  // Within a group: bands of kRaster row tiles, columns in turn inside a band, so that the
-  // CTAs at work share rows of A and columns of B in L2.
-  __device__ Tile at(int64_t i) const {
-    const int g = group_of_tile(prefix, q.E, static_cast<int>(i / nt));
-    const int mt = prefix[g + 1] - prefix[g];
-    int64_t r = i - static_cast<int64_t>(prefix[g]) * nt;
-    const int band = static_cast<int>(r / (static_cast<int64_t>(kRaster) * nt));
-    r -= static_cast<int64_t>(band) * kRaster * nt;
-    const int height = min(kRaster, mt - band * kRaster);
-    const int n = static_cast<int>(r) / height;
-    const int m = band * kRaster + static_cast<int>(r) - n * height;
-    const GroupRows rows = group_rows(q, g);
-    return Tile{g, rows.begin + m * kBM, rows.count - m * kBM, n * kCols};
-  }
-};
 
 template <int kAct, bool kBMn>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -103,7 +65,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s_tmem;
-  const Tiles<kCols> tiles(a.groups, prefix, a.epi.cols);
+  const Tiles<kBM, kCols> tiles(a.groups, prefix, a.epi.cols);
   const int blocks = (a.sum + kBK - 1) / kBK;
   auto give_up = [&] {
     s_abort = 1;
@@ -217,22 +179,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 2) tmem_dealloc(tmem, 512);
 }
 
+}  // namespace
+
 template <int kAct, bool kBMn>
-cudaError_t launch_rows(const uint16_t* A, const uint16_t* B, const RowsArgs& a, int num_sms, cudaStream_t stream) {
+cudaError_t launch_rows_single(const uint16_t* A, const uint16_t* B, const RowsArgs& a, int num_sms, cudaStream_t stream) {
   CUtensorMap map_a, map_b;
-  const uint64_t size_a[2] = {static_cast<uint64_t>(a.sum), static_cast<uint64_t>(a.groups.rows)};
-  const uint32_t box_a[2] = {kBK, kBM};
-  cudaError_t st = make_tensor_map(&map_a, A, 2, size_a, box_a);
-  if (st != cudaSuccess) return st;
-  if (kBMn) {
-    const uint64_t size[3] = {static_cast<uint64_t>(a.epi.cols), static_cast<uint64_t>(a.sum), static_cast<uint64_t>(a.groups.E)};
-    const uint32_t box[3] = {64, kBK, 1};
-    st = make_tensor_map(&map_b, B, 3, size, box);
-  } else {
-    const uint64_t size[3] = {static_cast<uint64_t>(a.sum), static_cast<uint64_t>(a.epi.z_cols), static_cast<uint64_t>(a.groups.E)};
-    const uint32_t box[3] = {kBK, kBN / 2, 1};
-    st = make_tensor_map(&map_b, B, 3, size, box);
-  }
+  const cudaError_t st = make_rows_maps<kBMn>(&map_a, &map_b, A, B, a, kBM, kBN / 2);
   if (st != cudaSuccess) return st;
   auto kern = rows_kernel<kAct, kBMn>;
   const size_t smem = 1024 + kStages * kStageBytes + kEpilogueWarps * kPatchBytes + sizeof(int) * (static_cast<size_t>(a.groups.E) + 1);
@@ -241,6 +193,26 @@ cudaError_t launch_rows(const uint16_t* A, const uint16_t* B, const RowsArgs& a,
   const int64_t most = max_row_tiles(a.groups) * ((a.epi.cols + cols - 1) / cols);
   const unsigned grid = static_cast<unsigned>(most < num_sms ? most : num_sms);
   return launch_chained(kern, dim3(grid), dim3(kThreads), smem, stream, map_a, map_b, a);
+}
+#define X(act, mn) \
+  template cudaError_t launch_rows_single<act, mn>(const uint16_t*, const uint16_t*, const RowsArgs&, int, cudaStream_t);
+EP_ROWS_INSTANCES(X)
+#undef X
+
+namespace {
+
+// Pairs of CTAs when the groups are long enough for tiles of 256 rows to be mostly full
+// (their average at least one and a half), a split of the summed index when the tiles
+// would leave most SMs idle, single CTAs otherwise.
+template <int kAct, bool kBMn>
+cudaError_t launch_rows(const uint16_t* A, const uint16_t* B, const RowsArgs& a, int num_sms, cudaStream_t stream) {
+  bool done = false;
+  const cudaError_t st = launch_rows_split<kAct, kBMn>(A, B, a, stream, &done);
+  if (done || st != cudaSuccess) return st;
+  const int64_t rows = a.groups.rows;
+  if (rows >= 384ll * (a.groups.count == nullptr ? 1 : a.groups.E) && num_sms >= 2)
+    return launch_rows_pair<kAct, kBMn>(A, B, a, num_sms, stream);
+  return launch_rows_single<kAct, kBMn>(A, B, a, num_sms, stream);
 }
 
 }  // namespace

@@ -163,13 +163,13 @@ struct Epilogue {
 };
 
 // 32 columns n0.. of a warp's 32 rows row0.. of group g, `rows` of which count: v the sums
-// (gated: u those of the other half), n0 < cols.
+// (gated: u those of the other half), n0 < cols; fewer than 32 with `width` (a multiple of 8).
 template <int kAct>
 __device__ __forceinline__ void finish_rows(const Epilogue& e, uint32_t patch, float (&v)[32],
                                             float (&u)[kAct == EP_ACT_SWIGLU ? 32 : 1], int g, int64_t row0, int rows,
-                                            int n0, int lane) {
+                                            int n0, int lane, int width = 32) {
   constexpr bool kGated = kAct == EP_ACT_SWIGLU;
-  const int cols = min(32, e.cols - n0);
+  const int cols = min(width, e.cols - n0);
   RowsInFlight res;
   if (e.residual != nullptr) res = fetch_rows(e.residual + row0 * e.cols + n0, e.cols, rows, cols, lane);
   if (e.bias != nullptr) {

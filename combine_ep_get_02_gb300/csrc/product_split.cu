@@ -1,0 +1,256 @@
+// The rows' products when there are few tiles (a token or a handful through a matrix):
+// reading the matrix is what counts, and too few CTAs could not read it at full rate. A
+// cluster of S CTAs takes one tile of 128 rows, each CTA 1/S of the summed index. Then
+// each CTA gets 1/S of the tile's columns: every CTA writes its partial sums of those
+// columns into that CTA's shared memory, which adds them in the order of the CTAs and
+// does the epilogue.
+//
+// The split depends on the sizes alone, not on the device, and the order of the additions
+// is fixed, so results repeat bit for bit.
+#include "product_rows.cuh"
+
+namespace ep {
+
+namespace {
+
+constexpr int kThreads = kRowsThreadsTc;
+constexpr int kBM = kTileRows;
+constexpr int kSplitCtas = 152;  // CTAs that a launch aims at: the SMs of the GPU this is written for
+
+template <int kBN>
+struct Shape {
+  static constexpr int kABytes = kBM * kBK * 2, kBBytes = kBN * kBK * 2, kStageBytes = kABytes + kBBytes;
+  static constexpr int kStages = 196608 / kStageBytes;
+};
+
+template <int kAct, bool kBMn, int kBN>
+__global__ void __launch_bounds__(kThreads, 1)
+    rows_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, RowsArgs a,
+                      int S, int a_rows) {
+  constexpr bool kGated = kAct == EP_ACT_SWIGLU;
+  constexpr int kCols = kGated ? kBN / 2 : kBN;
+  constexpr int kHalves = kGated ? 2 : 1;
+  constexpr int kStages = Shape<kBN>::kStages, kStageBytes = Shape<kBN>::kStageBytes, kABytes = Shape<kBN>::kABytes;
+  extern __shared__ uint8_t s_raw[];
+  __shared__ __align__(8) uint64_t s_full[kStages], s_empty[kStages], s_acc_full;
+  __shared__ uint32_t s_tmem;
+  __shared__ volatile int s_abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_rank());
+  const uint32_t stage0 = (smem_addr(s_raw) + 1023u) & ~1023u;
+  const uint32_t patch0 = stage0 + kStages * kStageBytes;
+  int* prefix = reinterpret_cast<int*>(s_raw + (patch0 - smem_addr(s_raw)) + kEpilogueWarps * kPatchBytes);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init_count(smem_addr(&s_full[s]), 1);
+      mbar_init_count(smem_addr(&s_empty[s]), 1);
+    }
+    mbar_init_count(smem_addr(&s_acc_full), 1);
+    s_abort = 0;
+    fence_barrier_init();
+    tma_prefetch_map(&map_a);
+    tma_prefetch_map(&map_b);
+  }
+  if (warp == 2) {
+    tmem_alloc(smem_addr(&s_tmem), kBN);
+    tmem_relinquish();
+  }
+  pdl_launch_dependents();
+  pdl_wait();
+  build_prefix<kThreads>(a.groups, kBM, prefix, blockIdx.x == 0 ? a.err : nullptr);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+  const Tiles<kBM, kCols> tiles(a.groups, prefix, a.epi.cols);
+  const int64_t tile = blockIdx.x / S;
+  const bool work = tile < tiles.total;  // the same for the whole cluster
+  const Tile t = work ? tiles.at(tile) : Tile{0, 0, 0, 0};
+  const int blocks = (a.sum + kBK - 1) / kBK, per = (blocks + S - 1) / S;
+  const int kb0 = work ? min(blocks, rank * per) : 0, kb1 = work ? min(blocks, kb0 + per) : 0;
+  auto give_up = [&] {
+    s_abort = 1;
+    atomicOr(a.err, kErrTimeout);
+  };
+
+  if (warp == 0) {
+    if (elect_one()) {
+      const uint32_t bytes = static_cast<uint32_t>(a_rows) * (kBK * 2) + kBN * (kBK * 2);
+      uint32_t n = 0;
+      bool ok = true;
+      for (int kb = kb0; kb < kb1; ++kb, ++n) {
+        const uint32_t s = n % kStages, bar = smem_addr(&s_full[s]);
+        if (s_abort || !mbar_wait_timed(smem_addr(&s_empty[s]), (n / kStages & 1u) ^ 1u)) {
+          if (!s_abort) give_up();
+          ok = false;
+          break;
+        }
+        mbar_expect(bar, bytes);
+        const uint32_t sa = stage0 + s * kStageBytes, sb = sa + kABytes;
+        tma_load_2d(sa, &map_a, kb * kBK, t.begin, bar);
+        if constexpr (kBMn) {
+#pragma unroll
+          for (int p = 0; p < kBN / 64; ++p)
+            tma_load_3d(sb + p * (kBK * 128), &map_b, t.n0 + p * 64, kb * kBK, t.g, bar);
+        } else {
+          tma_load_3d(sb, &map_b, kb * kBK, t.n0, t.g, bar);
+          tma_load_3d(sb + kBN / 2 * kBK * 2, &map_b, kb * kBK, kGated ? a.epi.cols + t.n0 : t.n0 + kBN / 2, t.g, bar);
+        }
+      }
+      if (!ok)
+        for (uint32_t back = n < kStages ? n : kStages; back > 0; --back) {
+          const uint32_t m = n - back;
+          mbar_wait_timed(smem_addr(&s_full[m % kStages]), m / kStages & 1u);
+        }
+    }
+  } else if (warp == 1) {
+    if (elect_one()) {
+      constexpr uint32_t idesc = idesc_bf16(kBM, kBN, false, kBMn);
+      uint32_t n = 0;
+      for (int kb = kb0; kb < kb1; ++kb, ++n) {
+        const uint32_t s = n % kStages;
+        if (s_abort || !mbar_wait_timed(smem_addr(&s_full[s]), n / kStages & 1u)) {
+          if (!s_abort) give_up();
+          break;
+        }
+        tc_fence_after();
+        const uint32_t sa = stage0 + s * kStageBytes, sb = sa + kABytes;
+        const uint64_t da = desc_k_major(sa);
+        const uint64_t db = kBMn ? desc_mn_major(sb, kBK * 128) : desc_k_major(sb);
+#pragma unroll
+        for (int k = 0; k < kBK / 16; ++k)
+          mma_bf16(tmem, da + k * kStepK, db + k * (kBMn ? kStepMN : kStepK), idesc, n > 0 || k > 0);
+        mma_commit(smem_addr(&s_empty[s]));
+      }
+      mma_commit(smem_addr(&s_acc_full));  // also when it gave up: what was issued has finished
+    }
+  }
+  __syncwarp();
+  // every thread: the CTA's products are done, and with them its stages are free
+  if (!mbar_wait_timed(smem_addr(&s_acc_full), 0) && lane == 0 && !s_abort) give_up();
+  __syncwarp();
+  tc_fence_after();
+  cluster_sync_all();  // all stages of the cluster are free
+
+  // partial sums [S][rows][width + 4] floats over the stages; CTA r holds columns r * slice on
+  const int slice = kCols / S, width = slice * kHalves, stride = width + 4;
+  const int quarter = warp & 3, rows = min(kBM, t.rows);
+  const int row = quarter * 32 + lane;
+  if (warp >= 2 && quarter * 32 < rows) {
+    const int half = (warp - 2) >> 2;
+    const uint32_t d = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    for (int c = half * (kBN / 2); c < (half + 1) * (kBN / 2); c += 32) {
+      float v[32];
+      if (kb1 > kb0) {
+        tmem_ld32(d + c, v);
+        tmem_ld_wait();
+      } else {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = 0.f;
+      }
+      if (row < rows) {
+#pragma unroll
+        for (int j = 0; j < 32; j += 4) {
+          const int n = c + j, h = n / kCols, col = n - h * kCols, r = col / slice;
+          const uint32_t at = stage0 + 4u * static_cast<uint32_t>((rank * kBM + row) * stride + h * slice + col - r * slice);
+          st_cluster16(cluster_addr(at, static_cast<uint32_t>(r)), v[j], v[j + 1], v[j + 2], v[j + 3]);
+        }
+      }
+    }
+  }
+  cluster_sync_all();  // the partial sums have arrived
+  if (warp >= 2 && quarter * 32 < rows) {
+    const int half = (warp - 2) >> 2;
+    const uint32_t patch = patch0 + (warp - 2) * kPatchBytes;
+    for (int c = half * 32; c < slice; c += 64) {
+      const int n0 = t.n0 + rank * slice + c, cols = min(32, slice - c);
+      if (n0 >= a.epi.cols) break;
+      float v[32], u[kGated ? 32 : 1];
+#pragma unroll
+      for (int j = 0; j < 32; ++j) {
+        v[j] = 0.f;
+        if constexpr (kGated) u[j] = 0.f;
+      }
+      for (int q = 0; q < S; ++q) {
+        const uint32_t at = stage0 + 4u * static_cast<uint32_t>((q * kBM + row) * stride + c);
+#pragma unroll
+        for (int j = 0; j < 32; j += 4) {
+          if (j >= cols) break;
+          const uint4 x = ld_shared16(at + 4u * j);
+          v[j] += __uint_as_float(x.x), v[j + 1] += __uint_as_float(x.y);
+          v[j + 2] += __uint_as_float(x.z), v[j + 3] += __uint_as_float(x.w);
+          if constexpr (kGated) {
+            const uint4 y = ld_shared16(at + 4u * static_cast<uint32_t>(slice + j));
+            u[j] += __uint_as_float(y.x), u[j + 1] += __uint_as_float(y.y);
+            u[j + 2] += __uint_as_float(y.z), u[j + 3] += __uint_as_float(y.w);
+          }
+        }
+      }
+      finish_rows<kAct>(a.epi, patch, v, u, t.g, static_cast<int64_t>(t.begin) + quarter * 32, rows - quarter * 32, n0, lane,
+                        cols);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 2) tmem_dealloc(tmem, kBN);
+}
+
+template <int kAct, bool kBMn, int kBN>
+cudaError_t launch(const uint16_t* A, const uint16_t* B, const RowsArgs& a, int64_t tiles, int S, cudaStream_t stream) {
+  // boxes of A no higher than the rows there are
+  const int a_rows = a.groups.rows < kBM ? (a.groups.rows + 7) / 8 * 8 : kBM;
+  CUtensorMap map_a, map_b;
+  const cudaError_t st = make_rows_maps<kBMn>(&map_a, &map_b, A, B, a, a_rows, kBN / 2);
+  if (st != cudaSuccess) return st;
+  auto kern = rows_split_kernel<kAct, kBMn, kBN>;
+  const size_t smem = 1024 + Shape<kBN>::kStages * Shape<kBN>::kStageBytes + kEpilogueWarps * kPatchBytes +
+                      sizeof(int) * (static_cast<size_t>(a.groups.E) + 1);
+  if (resident_ctas(reinterpret_cast<const void*>(kern), kThreads, smem) < 1) return cudaErrorInvalidConfiguration;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(tiles * S));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(S);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kern, map_a, map_b, a, S, a_rows);
+}
+
+}  // namespace
+
+// The split is taken when at least two CTAs can share a tile: tiles of 256 columns, or of
+// 128 when those, split eight ways, would still leave a quarter of the SMs idle. Every
+// CTA gets two stages of the summed index at least.
+template <int kAct, bool kBMn>
+cudaError_t launch_rows_split(const uint16_t* A, const uint16_t* B, const RowsArgs& a, cudaStream_t stream, bool* done) {
+  *done = false;
+  const int64_t rows = a.groups.rows;
+  const int64_t groups = a.groups.count == nullptr ? 1 : (rows < a.groups.E ? rows : a.groups.E);
+  const int64_t row_tiles = a.groups.count == nullptr ? (rows + kBM - 1) / kBM : rows / kBM + groups;
+  const int halves = kAct == EP_ACT_SWIGLU ? 2 : 1;
+  const int blocks = (a.sum + kBK - 1) / kBK;
+  const int64_t wide = row_tiles * ((a.epi.cols + 256 / halves - 1) / (256 / halves));
+  const int64_t narrow = row_tiles * ((a.epi.cols + 128 / halves - 1) / (128 / halves));
+  const bool use_narrow = wide * 8 < kSplitCtas * 3 / 4;
+  const int64_t tiles = use_narrow ? narrow : wide;
+  int S = 1;
+  while (S < 8 && tiles * S * 2 <= kSplitCtas && blocks >= S * 4) S *= 2;
+  if (S == 1) return cudaSuccess;
+  *done = true;
+  return use_narrow ? launch<kAct, kBMn, 128>(A, B, a, tiles, S, stream) : launch<kAct, kBMn, 256>(A, B, a, tiles, S, stream);
+}
+#define X(act, mn) \
+  template cudaError_t launch_rows_split<act, mn>(const uint16_t*, const uint16_t*, const RowsArgs&, cudaStream_t, bool*);
+EP_ROWS_INSTANCES(X)
+#undef X
+
+}  // namespace ep

@@ -144,6 +144,11 @@ SHAPES = {
     "many_experts": dict(counts=[(i * 7) % 5 for i in range(600)], K=64, N=16, R=4, act="gelu", bias=True),
     "tall": dict(counts=[2500, 10], K=256, N=328, act="silu"),
     "wide": dict(counts=[40, 300], K=2056, N=1544, act="none", bias=True),
+    "many_tiles": dict(counts=[30] * 18 + [0, 60], K=264, N=2000, R=4, act="silu", bias=True, residual=True),
+    "many_tiles_gated": dict(counts=[(i * 13) % 61 for i in range(24)], K=200, N=1000, act="swiglu", bias=True),
+    "long_groups": dict(counts=[700, 257, 900], K=392, N=264, act="gelu", bias=True, residual=True),
+    "long_groups_gated": dict(counts=[1000, 0, 513, 400], K=192, N=200, act="swiglu", R=2, align=8, bias=True),
+    "long_dense": dict(counts=[1003], K=1032, N=776, dense=True, act="relu", bias=True, residual=True),
     "few_rows_each": dict(counts=[2, 8, 1, 5, 16, 3, 9, 32], K=1024, N=640, R=2, act="swiglu"),
 }
 

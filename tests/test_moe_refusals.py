@@ -148,3 +148,17 @@ def test_tensors_that_the_abi_would_misread_are_refused(ep):
         with pytest.raises(ep.EpError, match=word) as e:
             call(**kw)
         assert e.value.status == ep.EP_ERR_INVALID_ARG
+
+
+def test_outputs_too_small_for_another_configuration_are_refused(ep):
+    """What was checked with one configuration is held against the next one's sizes."""
+    small, large = route_cfg(ep), route_cfg(ep, num_tokens=65)
+    out = ep.Route(torch.zeros(128, 4, dtype=torch.int64), torch.zeros(128, 4))
+    object.__setattr__(out, "_sizes", [512, 512, -1, -1, -1, -1])  # as a call with `small` on the GPU leaves it
+    with pytest.raises(ep.EpError, match="logits .*GPU"):
+        ep.ep_route(small, torch.zeros(128, 32), None, None, out, torch.zeros(1), stream=0)
+    with pytest.raises(ep.EpError, match="topk_idx has 512 elements, 520 needed"):
+        ep.ep_route(large, torch.zeros(130, 32), None, None, out, torch.zeros(1), stream=0)
+    with pytest.raises(ep.EpError, match="topk_idx is not on the GPU"):
+        out.topk_weights = torch.zeros(128, 4)  # an assignment: looked at again
+        ep.ep_route(small, torch.zeros(128, 32), None, None, out, torch.zeros(1), stream=0)
