@@ -64,18 +64,20 @@ int make_route(const ep_route_config_t* c, RouteGeometry* g) {
   const int most = kRouteCtas / c->num_segments;
   if (C > most) C = most;
   g->C = C < 1 ? 1 : C;
+  g->prob_shift = 62;
+  while (g->prob_shift > 0 && (int64_t{1} << (62 - g->prob_shift)) <= c->num_tokens) --g->prob_shift;
   return EP_OK;
 }
 
 RouteWorkspace route_workspace(const RouteGeometry& g) {
   RouteWorkspace w;
-  const size_t ctas = static_cast<size_t>(g.B) * g.C;
+  const size_t B = static_cast<size_t>(g.B);
   w.seg_done = 256;
-  w.seg_loss = w.seg_done + round256(4 * static_cast<size_t>(g.B));
-  w.cta_valid = w.seg_loss + round256(4 * static_cast<size_t>(g.B));
-  w.cta_count = w.cta_valid + round256(4 * ctas);
-  w.cta_prob = w.cta_count + round256(4 * ctas * g.E);
-  w.total = w.cta_prob + round256(4 * ctas * g.E);
+  w.seg_valid = w.seg_done + round256(4 * B);
+  w.seg_loss = w.seg_valid + round256(4 * B);
+  w.count = w.seg_loss + round256(4 * B);
+  w.prob = w.count + round256(4 * B * g.E);
+  w.total = w.prob + round256(8 * B * g.E);
   return w;
 }
 
@@ -177,10 +179,10 @@ int ep_route(const ep_route_config_t* cfg, const void* logits, const float* choi
   a.err = at<uint32_t>(workspace, 0);
   a.done = at<uint32_t>(workspace, 4);
   a.seg_done = at<uint32_t>(workspace, w.seg_done);
+  a.seg_valid = at<uint32_t>(workspace, w.seg_valid);
   a.seg_loss = at<float>(workspace, w.seg_loss);
-  a.cta_valid = at<int32_t>(workspace, w.cta_valid);
-  a.cta_count = at<int32_t>(workspace, w.cta_count);
-  a.cta_prob = at<float>(workspace, w.cta_prob);
+  a.ws_count = at<uint32_t>(workspace, w.count);
+  a.ws_prob = at<unsigned long long>(workspace, w.prob);
   return cuda_status(launch_route(a, static_cast<cudaStream_t>(stream)));
 }
 

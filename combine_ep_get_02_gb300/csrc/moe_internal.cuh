@@ -14,7 +14,7 @@ constexpr uint32_t kErrNonfinite = 16u;  // a NaN or +inf logit or choice bias
 
 // ---- router -------------------------------------------------------------------
 
-constexpr int kRouteThreads = 256;   // 8 warps, one token each
+constexpr int kRouteThreads = 256;  // 8 warps, a token each
 constexpr int kRouteWarps = kRouteThreads / 32;
 // CTAs of a router launch, shared evenly by the segments (at least one each): four
 // per SM on 152 SMs. A constant, so that the order in which the probabilities are
@@ -26,17 +26,18 @@ struct RouteGeometry {
   int B, T, E, K, G, keep;
   int bf16, sigmoid, normalize;
   float scale;
-  int C;  // CTAs per segment
+  int C;           // CTAs per segment
+  int prob_shift;  // 62 bits hold a segment's sum of probabilities in units of 2^-prob_shift
 };
 
 // Byte offsets of the router's workspace: the 256-byte header (error word at 0,
-// counter of finished segments at 4), then the pieces below.
+// counter of finished segments at 4), then the pieces below. Sums and counters return to 0.
 struct RouteWorkspace {
-  size_t seg_done;   // uint32 [B]: CTAs of each segment that have delivered (returns to 0)
+  size_t seg_done;   // uint32 [B]: CTAs of each segment that have delivered
+  size_t seg_valid;  // uint32 [B]: valid tokens
   size_t seg_loss;   // float [B]
-  size_t cta_valid;  // int32 [B*C]: valid tokens
-  size_t cta_count;  // int32 [B*C][E]
-  size_t cta_prob;   // float [B*C][E]
+  size_t count;      // uint32 [B][E]: lanes
+  size_t prob;       // uint64 [B][E]: probabilities in units of 2^-prob_shift
   size_t total;
 };
 
@@ -53,10 +54,10 @@ struct RouteArgs {
   uint32_t* err;
   uint32_t* done;
   uint32_t* seg_done;
+  uint32_t* seg_valid;
   float* seg_loss;
-  int32_t* cta_valid;
-  int32_t* cta_count;
-  float* cta_prob;
+  uint32_t* ws_count;
+  unsigned long long* ws_prob;
   RouteGeometry g;
 };
 

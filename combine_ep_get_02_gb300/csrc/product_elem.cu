@@ -47,9 +47,11 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 // dz = d_out * act'(z), rounded to bf16 for the products, and the column sums of the
-// unrounded dz over each row tile. A CTA takes a tile of 128 rows of one group and 512
-// output columns: 64 threads across (8 columns each), 4 down.
-constexpr int kAcross = 64, kDown = kThreads / kAcross, kSpan = kAcross * 8;
+// unrounded dz over each row tile. A CTA takes a tile of 128 rows of one group and 128
+// output columns: 16 threads across (8 columns each, 256 bytes of a row), 16 down, so that a
+// few thousand rows already occupy every SM (512 columns a CTA took 43 us for 4096 x 4096,
+// a quarter of the SMs' warps in use).
+constexpr int kAcross = 16, kDown = kThreads / kAcross, kSpan = kAcross * 8;
 
 struct DzArgs {
   Groups groups;
@@ -83,7 +85,7 @@ __global__ void __launch_bounds__(kThreads) dz_kernel(DzArgs a) {
 #pragma unroll
     for (int i = 0; i < kHalves * 8; ++i) sum[i] = 0.f;
     if (col < a.N) {
-#pragma unroll 2
+#pragma unroll 4
       for (int r = down; r < n; r += kDown) {
         const int64_t row = first + r;
         float d[8], t[kHalves * 8];

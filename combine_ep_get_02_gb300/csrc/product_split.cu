@@ -15,7 +15,9 @@ namespace {
 
 constexpr int kThreads = kRowsThreadsTc;
 constexpr int kBM = kTileRows;
-constexpr int kSplitCtas = 152;  // CTAs that a launch aims at: the SMs of the GPU this is written for
+// Clusters of S CTAs that fit on the GPU this is written for at one CTA per SM (152 SMs in
+// processing clusters of unequal size); one more would run after the others.
+constexpr int resident_clusters(int S) { return S == 8 ? 15 : S == 4 ? 36 : 76; }
 
 template <int kBN>
 struct Shape {
@@ -227,9 +229,10 @@ cudaError_t launch(const uint16_t* A, const uint16_t* B, const RowsArgs& a, int6
 
 }  // namespace
 
-// The split is taken when at least two CTAs can share a tile: tiles of 256 columns, or of
-// 128 when those, split eight ways, would still leave a quarter of the SMs idle. Every
-// CTA gets two stages of the summed index at least.
+// The split is taken when at least two CTAs can share a tile and all clusters run at once;
+// of tiles of 256 and of 128 columns and the ways to split them, the one with the most
+// CTAs at work (the wider tile when equal). Every CTA gets two blocks of the summed
+// index at least.
 template <int kAct, bool kBMn>
 cudaError_t launch_rows_split(const uint16_t* A, const uint16_t* B, const RowsArgs& a, cudaStream_t stream, bool* done) {
   *done = false;
@@ -240,11 +243,15 @@ cudaError_t launch_rows_split(const uint16_t* A, const uint16_t* B, const RowsAr
   const int blocks = (a.sum + kBK - 1) / kBK;
   const int64_t wide = row_tiles * ((a.epi.cols + 256 / halves - 1) / (256 / halves));
   const int64_t narrow = row_tiles * ((a.epi.cols + 128 / halves - 1) / (128 / halves));
-  const bool use_narrow = wide * 8 < kSplitCtas * 3 / 4;
-  const int64_t tiles = use_narrow ? narrow : wide;
   int S = 1;
-  while (S < 8 && tiles * S * 2 <= kSplitCtas && blocks >= S * 4) S *= 2;
+  bool use_narrow = false;
+  int64_t ctas = 0;
+  for (int s = 2; s <= 8 && blocks >= s * 2; s *= 2) {
+    if (wide <= resident_clusters(s) && wide * s > ctas) S = s, use_narrow = false, ctas = wide * s;
+    if (narrow <= resident_clusters(s) && narrow * s > ctas) S = s, use_narrow = true, ctas = narrow * s;
+  }
   if (S == 1) return cudaSuccess;
+  const int64_t tiles = use_narrow ? narrow : wide;
   *done = true;
   return use_narrow ? launch<kAct, kBMn, 128>(A, B, a, tiles, S, stream) : launch<kAct, kBMn, 256>(A, B, a, tiles, S, stream);
 }

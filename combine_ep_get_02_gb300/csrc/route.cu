@@ -11,13 +11,11 @@
 //   cnt_e lanes to expert e and P_e the sum of p_e: loss = sum_e (E cnt_e / (K n)) (P_e / n),
 //   and the output is its mean over the segments.
 //
-// One warp takes a token: lane i holds E/32 of its logits, loaded 16 bytes at a
-// time, and keeps the best of its own; a round of the choice is one warp-wide
-// maximum of order-preserving integer keys and one minimum of expert numbers, after
-// which the lane that lost its best looks for its next. Each lane meets the same
+// One warp takes a token: lane i holds E/32 of its logits, loaded 16 bytes at a time. The
+// choice works on order-preserving integer keys (see choose). Each lane meets the same
 // experts in every token, so the probability sums stay in its registers over all
-// the warp's tokens; warps, then CTAs, are summed in a fixed order (the last CTA of a
-// segment to arrive adds the others' partial sums), so every result repeats bit for bit.
+// the warp's tokens; a CTA's warps are summed in their order, the CTAs in fixed point, so
+// every result repeats bit for bit.
 // Reading the logits once is what the operator cannot do without.
 #include <type_traits>
 
@@ -35,6 +33,18 @@ constexpr float kTiny = 1e-30f;  // least divisor of a sum of sigmoids
 __device__ __forceinline__ float warp_max(float v) {
   float r;
   asm volatile("redux.sync.max.f32 %0, %1, 0xFFFFFFFF;" : "=f"(r) : "f"(v));
+  return r;
+}
+// e^x and 1/x by the hardware's approximations (2 ulp, and 2^-22 of x for e^x); results below
+// 2^-126 are zero
+__device__ __forceinline__ float exp_fast(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * 1.4426950408889634f));
+  return r;
+}
+__device__ __forceinline__ float rcp_fast(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
 __device__ __forceinline__ float warp_sum(float v) {
@@ -121,26 +131,89 @@ __device__ __forceinline__ Top2 top2_merge(Top2 x, Top2 y) {
   return Top2{fmaxf(x.a, y.a), fmaxf(fminf(x.a, y.a), fmaxf(x.b, y.b))};
 }
 
-// A lane's best two keys not yet taken: most lanes give two experts at most, and one that
-// gives a third looks for it among what comes after its last.
-struct Best {
-  uint32_t k1, k2;
-  int e1, e2;
+// What a warp lists the candidates of a token in.
+struct Candidates {
+  uint4 key[8];  // 32 keys
+  int expert[32];
 };
+
+// The K best keys, best first, ties to the lowest expert: the lane that returns r >= 0 has
+// the expert of place r in `mine` and its key in `mine_key`.
+//
+// The K-th largest of the lanes' best keys bounds the K-th largest of all from below, so only
+// keys that reach it can be chosen: K at least, and few more. They are listed in shared
+// memory, a lane takes one, and its place is the number of larger ones (equal keys,
+// which show as a place taken twice, are told apart by expert). More than 32 (many
+// equal keys, or K near 32) take K rounds of finding the best instead. Against K such
+// rounds for every token this halved the time of 256 experts, top 8.
 template <int EPL>
-__device__ __forceinline__ Best best_two(const uint32_t (&key)[EPL], int lane, uint32_t below, int after) {
-  Best b{0u, 0u, 0x7FFFFFFF, 0x7FFFFFFF};
+__device__ __forceinline__ int choose(uint32_t (&key)[EPL], int K, Candidates& list, int lane, int& mine, uint32_t& mine_key) {
+  mine = -1;
+  mine_key = 0u;
+  uint32_t best = 0u;
 #pragma unroll
-  for (int j = 0; j < EPL; ++j) {
-    const int e = expert_of<EPL>(j, lane);
-    const uint32_t k = key[j] < below || (key[j] == below && e > after) ? key[j] : 0u;
-    const bool first = k > b.k1, second = k > b.k2;
-    b.e2 = first ? b.e1 : second ? e : b.e2;
-    b.k2 = first ? b.k1 : second ? k : b.k2;
-    b.e1 = first ? e : b.e1;
-    b.k1 = first ? k : b.k1;
+  for (int j = 0; j < EPL; ++j) best = max(best, key[j]);
+  for (int r = 1; r < K; ++r)
+    if (best == __reduce_max_sync(kFullMask, best)) best = 0u;  // lanes that tie go together: the bound stays one
+  const uint32_t bound = max(__reduce_max_sync(kFullMask, best), kKeyNegInf + 1u);
+  int c = 0;
+#pragma unroll
+  for (int j = 0; j < EPL; ++j) c += key[j] >= bound;
+  int at = c;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(kFullMask, at, o);
+    if (lane >= o) at += v;
   }
-  return b;
+  const int n = __shfl_sync(kFullMask, at, 31);
+  if (n <= 32) {
+    at -= c;
+    uint32_t* keys = reinterpret_cast<uint32_t*>(list.key);
+#pragma unroll
+    for (int j = 0; j < EPL; ++j)
+      if (key[j] >= bound) {
+        keys[at] = key[j];
+        list.expert[at] = expert_of<EPL>(j, lane);
+        ++at;
+      }
+    if (lane >= n) keys[lane] = 0u;
+    __syncwarp();
+    mine_key = keys[lane];
+    mine = list.expert[lane];
+    int place = 0;
+    for (int i = 0; 4 * i < n; ++i) {
+      const uint4 v = list.key[i];
+      place += (v.x > mine_key) + (v.y > mine_key) + (v.z > mine_key) + (v.w > mine_key);
+    }
+    const unsigned seen = __reduce_or_sync(kFullMask, lane < n ? 1u << place : 0u);
+    if (__popc(seen) != n)
+      for (int i = 0; i < n; ++i) place += keys[i] == mine_key && list.expert[i] < mine;
+    __syncwarp();
+    return lane < n && place < K ? place : -1;
+  }
+  int place = -1;
+  for (int r = 0; r < K; ++r) {
+    uint32_t bk = 0u;
+    int be = 0x7FFFFFFF;
+#pragma unroll
+    for (int j = 0; j < EPL; ++j)
+      if (key[j] > bk) {
+        bk = key[j];
+        be = expert_of<EPL>(j, lane);
+      }
+    const uint32_t m = __reduce_max_sync(kFullMask, bk);
+    if (m <= kKeyNegInf) break;  // fewer than K experts are available
+    const int e = static_cast<int>(__reduce_min_sync(kFullMask, bk == m ? static_cast<uint32_t>(be) : 0xFFFFFFFFu));
+    if (lane == r) {
+      mine = e;
+      mine_key = m;
+      place = r;
+    }
+#pragma unroll
+    for (int j = 0; j < EPL; ++j)
+      if (expert_of<EPL>(j, lane) == e) key[j] = 0u;
+  }
+  return place;
 }
 
 // CTAs per SM that the registers are limited for: four (what kRouteCtas counts on) while a
@@ -149,6 +222,7 @@ template <int EPL, bool kBf16, bool kVec>
 __global__ void __launch_bounds__(kRouteThreads, EPL <= 8 ? 4 : EPL <= 16 ? 2 : 1) route_kernel(RouteArgs a) {
   extern __shared__ float s_mem[];
   __shared__ int s_valid[kRouteWarps];
+  __shared__ Candidates s_list[kRouteWarps];
   __shared__ float s_part[kRouteWarps];
   __shared__ bool s_last;
   const RouteGeometry& g = a.g;
@@ -185,6 +259,7 @@ __global__ void __launch_bounds__(kRouteThreads, EPL <= 8 ? 4 : EPL <= 16 ? 2 : 
 
   const int step = g.C * kRouteWarps;
   const int64_t first = static_cast<int64_t>(seg) * g.T;
+  // the next token's logits load while this one is worked on
   float next[EPL];
   int t = cta * kRouteWarps + warp;
   uint8_t next_on = 1;
@@ -231,13 +306,13 @@ __global__ void __launch_bounds__(kRouteThreads, EPL <= 8 ? 4 : EPL <= 16 ? 2 : 
         if (top == -kInf) top = 0.f;  // no expert is available: every p is 0
 #pragma unroll
         for (int j = 0; j < EPL; ++j) {
-          s[j] = __expf(l[j] - top);
+          s[j] = exp_fast(l[j] - top);
           total += s[j];
           key[j] = order_key(__fadd_rn(l[j], bias[j]));  // -0 + 0 is +0, so the two zeros tie
         }
       }
       total = warp_sum(total);
-      inv = total > 0.f ? __frcp_rn(total) : 0.f;
+      inv = total > 0.f ? rcp_fast(total) : 0.f;
 #pragma unroll
       for (int j = 0; j < EPL; ++j) prob[j] = fmaf(s[j], inv, prob[j]);
     }
@@ -280,49 +355,48 @@ __global__ void __launch_bounds__(kRouteThreads, EPL <= 8 ? 4 : EPL <= 16 ? 2 : 
       }
     }
 
-    // K rounds: the warp's best key, its lowest expert; that lane goes on to its next best
-    Best b = best_two<EPL>(key, lane, 0xFFFFFFFFu, -1);
-    if (__any_sync(kFullMask, b.k1 >= kKeyPosInf)) {  // a choice score that is NaN or +inf: not chosen
+    uint32_t most = 0u;
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) most = max(most, key[j]);
+    if (__any_sync(kFullMask, most >= kKeyPosInf)) {  // a choice score that is NaN or +inf: not chosen
       bad = true;
 #pragma unroll
       for (int j = 0; j < EPL; ++j)
         if (key[j] >= kKeyPosInf) key[j] = 0u;
-      b = best_two<EPL>(key, lane, 0xFFFFFFFFu, -1);
     }
-    int mine = -1;
-    for (int r = 0; r < K; ++r) {
-      const uint32_t m = __reduce_max_sync(kFullMask, b.k1);
-      if (m <= kKeyNegInf) break;  // fewer than K experts are available: the other lanes stay -1
-      const int e = static_cast<int>(__reduce_min_sync(kFullMask, b.k1 == m ? static_cast<uint32_t>(b.e1) : 0xFFFFFFFFu));
-      if (lane == r) mine = e;
-      const bool gave = b.k1 == m && b.e1 == e;
-      if (gave) {
-        b.k1 = b.k2;
-        b.e1 = b.e2;
-        b.k2 = 0u;
-        b.e2 = 0x7FFFFFFF;
-      }
-      if (EPL > 2 && gave && b.k1 == 0u) b = best_two<EPL>(key, lane, m, e);
-    }
-    // weights of the chosen: their logits are read again (they are in L1)
+    int mine;
+    uint32_t mine_key;
+    const int place_of = choose<EPL>(key, K, s_list[warp], lane, mine, mine_key);
+    if (place_of < 0) mine = -1;
+    // weights of the chosen: from the key if it is the logit, else the logit is read again (it is in L1)
     float w = 0.f, lv = -kInf;
-    if (mine >= 0)
-      lv = kBf16 ? __uint_as_float(static_cast<uint32_t>(__ldg(static_cast<const uint16_t*>(a.logits) + token * E + mine)) << 16)
-                 : __ldg(static_cast<const float*>(a.logits) + token * E + mine);
+    if (mine >= 0) {
+      if (!g.sigmoid && a.bias == nullptr)
+        lv = __uint_as_float(mine_key & 0x80000000u ? mine_key ^ 0x80000000u : ~mine_key);
+      else
+        lv = kBf16 ? __uint_as_float(static_cast<uint32_t>(__ldg(static_cast<const uint16_t*>(a.logits) + token * E + mine)) << 16)
+                   : __ldg(static_cast<const float*>(a.logits) + token * E + mine);
+    }
     if (g.sigmoid) {
       w = mine >= 0 ? sigmoid_rn(lv) : 0.f;
       if (g.normalize) w = __fdividef(w, fmaxf(warp_sum(w), kTiny));
     } else if (g.normalize) {
       const float m = warp_max(lv);
-      w = mine >= 0 ? __expf(lv - m) : 0.f;
+      w = mine >= 0 ? exp_fast(lv - m) : 0.f;
       const float sum = warp_sum(w);
-      w = sum > 0.f ? w / sum : 0.f;
+      w = sum > 0.f ? __fdividef(w, sum) : 0.f;
     } else {
-      w = mine >= 0 ? __expf(lv - top) * inv : 0.f;
+      w = mine >= 0 ? exp_fast(lv - top) * inv : 0.f;
     }
-    if (lane < K) {
-      a.idx[token * K + lane] = mine;
-      a.weights[token * K + lane] = w * g.scale;
+    // places that no expert took are -1
+    const int taken = __popc(__ballot_sync(kFullMask, place_of >= 0));
+    if (place_of >= 0) {
+      a.idx[token * K + place_of] = mine;
+      a.weights[token * K + place_of] = w * g.scale;
+    }
+    if (lane >= taken && lane < K) {
+      a.idx[token * K + lane] = -1;
+      a.weights[token * K + lane] = 0.f;
     }
     if (stats && mine >= 0) atomicAdd(s_count + mine, 1);
   }
@@ -341,36 +415,35 @@ __global__ void __launch_bounds__(kRouteThreads, EPL <= 8 ? 4 : EPL <= 16 ? 2 : 
 #pragma unroll
   for (int w = 0; w < kRouteWarps; ++w) n += s_valid[w];
   float dot = 0.f;
+  const size_t row = static_cast<size_t>(seg) * E;
   if (g.C > 1) {
+    // The CTAs of a segment are summed in 64-bit fixed point, in which the order of the
+    // additions does not matter: a CTA's fp32 sum is rounded to 2^-prob_shift (2^-49 for a
+    // segment of 4096 tokens). Partial sums of all CTAs, added by the last one, took 40 us
+    // with one segment of 65536 tokens.
+    const float unit = __int_as_float((127 + g.prob_shift) << 23);
     for (int e = threadIdx.x; e < E; e += kRouteThreads) {
       float p = 0.f;
 #pragma unroll
       for (int w = 0; w < kRouteWarps; ++w) p += s_rows[static_cast<size_t>(w) * E + e];
-      a.cta_prob[static_cast<size_t>(blockIdx.x) * E + e] = p;
-      a.cta_count[static_cast<size_t>(blockIdx.x) * E + e] = s_count[e];
+      atomicAdd(a.ws_prob + row + e, __float2ull_rn(p * unit));
+      if (s_count[e] != 0) atomicAdd(a.ws_count + row + e, static_cast<uint32_t>(s_count[e]));
     }
-    if (threadIdx.x == 0) a.cta_valid[blockIdx.x] = n;
+    if (threadIdx.x == 0) atomicAdd(a.seg_valid + seg, static_cast<uint32_t>(n));
     __threadfence();
     __syncthreads();
     if (threadIdx.x == 0) s_last = atomicAdd(a.seg_done + seg, 1u) == static_cast<uint32_t>(g.C) - 1u;
     __syncthreads();
     if (!s_last) return;
     __threadfence();
-    // the segment's last CTA adds the partial sums in CTA order
-    const size_t base = static_cast<size_t>(seg) * g.C;
-    n = 0;
-#pragma unroll 4
-    for (int c = 0; c < g.C; ++c) n += __ldcg(a.cta_valid + base + c);
+    n = static_cast<int>(__ldcg(a.seg_valid + seg));
     for (int e = threadIdx.x; e < E; e += kRouteThreads) {
-      float p = 0.f;
-      int cnt = 0;
-#pragma unroll 16
-      for (int c = 0; c < g.C; ++c) {
-        p += __ldcg(a.cta_prob + (base + c) * E + e);
-        cnt += __ldcg(a.cta_count + (base + c) * E + e);
-      }
-      a.prob_sum[static_cast<size_t>(seg) * E + e] = p;
-      a.count[static_cast<size_t>(seg) * E + e] = cnt;
+      const float p = __ull2float_rn(__ldcg(a.ws_prob + row + e)) / unit;
+      const int cnt = static_cast<int>(__ldcg(a.ws_count + row + e));
+      a.ws_prob[row + e] = 0ull;
+      a.ws_count[row + e] = 0u;
+      a.prob_sum[row + e] = p;
+      a.count[row + e] = cnt;
       dot = fmaf(p, static_cast<float>(cnt), dot);
     }
   } else {  // the segment's only CTA
@@ -379,8 +452,8 @@ __global__ void __launch_bounds__(kRouteThreads, EPL <= 8 ? 4 : EPL <= 16 ? 2 : 
 #pragma unroll
       for (int w = 0; w < kRouteWarps; ++w) p += s_rows[static_cast<size_t>(w) * E + e];
       const int cnt = s_count[e];
-      a.prob_sum[static_cast<size_t>(seg) * E + e] = p;
-      a.count[static_cast<size_t>(seg) * E + e] = cnt;
+      a.prob_sum[row + e] = p;
+      a.count[row + e] = cnt;
       dot = fmaf(p, static_cast<float>(cnt), dot);
     }
   }
@@ -393,7 +466,10 @@ __global__ void __launch_bounds__(kRouteThreads, EPL <= 8 ? 4 : EPL <= 16 ? 2 : 
     const float nf = static_cast<float>(n > 0 ? n : 1);
     const float seg_loss = sum * (static_cast<float>(E) / static_cast<float>(K)) / nf / nf;
     a.num_valid[seg] = n;
-    if (g.C > 1) a.seg_done[seg] = 0u;
+    if (g.C > 1) {
+      a.seg_done[seg] = 0u;
+      a.seg_valid[seg] = 0u;
+    }
     if (g.B == 1) {
       *a.loss = seg_loss;
       return;
@@ -420,7 +496,7 @@ __global__ void __launch_bounds__(kRouteThreads, EPL <= 8 ? 4 : EPL <= 16 ? 2 : 
 // A warp takes a token with the forward's lane layout; what goes to the K chosen
 // experts reaches their lanes through a row of shared memory that is zero elsewhere.
 template <int EPL, bool kBf16, bool kVec>
-__global__ void __launch_bounds__(kRouteThreads) route_grad_kernel(RouteGradArgs a) {
+__global__ void __launch_bounds__(kRouteThreads, EPL <= 8 ? 4 : EPL <= 16 ? 2 : 1) route_grad_kernel(RouteGradArgs a) {
   extern __shared__ float s_mem[];
   const RouteGeometry& g = a.g;
   const int E = g.E, K = g.K;
@@ -490,7 +566,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_grad_kernel(RouteGradArgs
     if (g.sigmoid) {
 #pragma unroll
       for (int j = 0; j < EPL; ++j) {
-        s[j] = __fdividef(1.f, 1.f + __expf(-l[j]));
+        s[j] = rcp_fast(1.f + exp_fast(-l[j]));
         total += s[j];
       }
     } else {
@@ -501,12 +577,12 @@ __global__ void __launch_bounds__(kRouteThreads) route_grad_kernel(RouteGradArgs
       if (top == -kInf) top = 0.f;
 #pragma unroll
       for (int j = 0; j < EPL; ++j) {
-        s[j] = __expf(l[j] - top);
+        s[j] = exp_fast(l[j] - top);
         total += s[j];
       }
     }
     total = warp_sum(total);
-    const float inv = total > 0.f ? __frcp_rn(total) : 0.f;
+    const float inv = total > 0.f ? rcp_fast(total) : 0.f;
     float ap = 0.f;  // sum of a p
 #pragma unroll
     for (int j = 0; j < EPL; ++j) ap = fmaf(coef[j], s[j] * inv, ap);
@@ -514,7 +590,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_grad_kernel(RouteGradArgs
     // what goes to the chosen experts
     float gl, rest = 0.f;
     if (g.sigmoid) {
-      const float sv = chosen ? __fdividef(1.f, 1.f + __expf(-lv)) : 0.f;
+      const float sv = chosen ? rcp_fast(1.f + exp_fast(-lv)) : 0.f;
       if (g.normalize) {
         const float q = __fdividef(sv, fmaxf(warp_sum(sv), kTiny));
         gl = q * (gw - warp_sum(q * gw)) * (1.f - sv);
@@ -523,12 +599,12 @@ __global__ void __launch_bounds__(kRouteThreads) route_grad_kernel(RouteGradArgs
       }
     } else if (g.normalize) {
       const float m = warp_max(lv);
-      float q = chosen && lv > -kInf ? __expf(lv - m) : 0.f;
+      float q = chosen && lv > -kInf ? exp_fast(lv - m) : 0.f;
       const float sum = warp_sum(q);
-      q = sum > 0.f ? q / sum : 0.f;
+      q = sum > 0.f ? __fdividef(q, sum) : 0.f;
       gl = q * (gw - warp_sum(q * gw));
     } else {
-      gl = chosen ? gw * __expf(lv - top) * inv : 0.f;
+      gl = chosen ? gw * exp_fast(lv - top) * inv : 0.f;
       rest = warp_sum(gl);
     }
     if (chosen) s_row[e] = gl;
