@@ -11,12 +11,12 @@
 //   cnt_e lanes to expert e and P_e the sum of p_e: loss = sum_e (E cnt_e / (K n)) (P_e / n),
 //   and the output is its mean over the segments.
 //
-// One warp takes a token: lane i holds E/32 of its logits, loaded 16 bytes at a time. The
-// choice works on order-preserving integer keys (see choose). Each lane meets the same
-// experts in every token, so the probability sums stay in its registers over all
-// the warp's tokens; a CTA's warps are summed in their order, the CTAs in fixed point, so
-// every result repeats bit for bit.
-// Reading the logits once is what the operator cannot do without.
+// One warp takes a token: lane i holds E/32 of its logits, loaded 16 bytes at a time. Each
+// lane meets the same experts in every token, so the probability sums stay in its
+// registers over all the warp's tokens; a CTA's warps are summed in their order, the CTAs
+// in fixed point, so every result repeats bit for bit.
+// Reading the logits once is what the operator cannot do without; what bounds it is the
+// arithmetic on them (comparisons run at half rate).
 #include <type_traits>
 
 #include "ep_device.cuh"
@@ -27,6 +27,7 @@ namespace ep {
 namespace {
 
 constexpr float kInf = __builtin_huge_valf();
+constexpr float kLowest = -3.402823466e38f;
 constexpr float kTiny = 1e-30f;  // least divisor of a sum of sigmoids
 
 // one instruction on this architecture
@@ -52,15 +53,6 @@ __device__ __forceinline__ float warp_sum(float v) {
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(kFullMask, v, o);
   return v;
 }
-
-// Unsigned key with the order of the floats: what may be chosen lies strictly between the
-// keys of -inf and +inf; a NaN that arithmetic made is above, a negative one below.
-__device__ __forceinline__ uint32_t order_key(float f) {
-  const uint32_t u = __float_as_uint(f);
-  return u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
-}
-
-constexpr uint32_t kKeyNegInf = 0x007FFFFFu, kKeyPosInf = 0xFF800000u;
 
 // The sigmoid whose rounding the choice depends on: CUDA's expf, then correctly
 // rounded operations, so that equal scores tie.
@@ -133,33 +125,36 @@ __device__ __forceinline__ Top2 top2_merge(Top2 x, Top2 y) {
 
 // What a warp lists the candidates of a token in.
 struct Candidates {
-  uint4 key[8];  // 32 keys
+  float4 score[8];  // 32 scores
   int expert[32];
 };
 
-// The K best keys, best first, ties to the lowest expert: the lane that returns r >= 0 has
-// the expert of place r in `mine` and its key in `mine_key`.
+// The K best scores, best first, ties to the lowest expert: the lane that returns r >= 0 has
+// the expert of place r in `mine` and its score in `mine_score`. `best` is the lane's largest
+// score; -inf and NaN are never chosen, +inf does not occur.
 //
-// The K-th largest of the lanes' best keys bounds the K-th largest of all from below, so only
-// keys that reach it can be chosen: K at least, and few more. They are listed in shared
-// memory, a lane takes one, and its place is the number of larger ones (equal keys,
+// The K-th largest of the lanes' best scores bounds the K-th largest of all from below, so only
+// scores that reach it can be chosen: K at least, and few more. They are listed in shared
+// memory, a lane takes one, and its place is the number of larger ones (equal scores,
 // which show as a place taken twice, are told apart by expert). More than 32 (many
-// equal keys, or K near 32) take K rounds of finding the best instead. Against K such
+// equal scores, or K near 32) take K rounds of finding the best instead. Against K such
 // rounds for every token this halved the time of 256 experts, top 8.
 template <int EPL>
-__device__ __forceinline__ int choose(uint32_t (&key)[EPL], int K, Candidates& list, int lane, int& mine, uint32_t& mine_key) {
+__device__ __forceinline__ int choose(float (&c)[EPL], float best, int K, Candidates& list, int lane, int& mine,
+                                      float& mine_score) {
   mine = -1;
-  mine_key = 0u;
-  uint32_t best = 0u;
-#pragma unroll
-  for (int j = 0; j < EPL; ++j) best = max(best, key[j]);
+  mine_score = 0.f;
+  // by integer keys of the same order: their warp-wide maximum takes two thirds of the floats' time
+  const uint32_t u = __float_as_uint(best);
+  uint32_t key = u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
   for (int r = 1; r < K; ++r)
-    if (best == __reduce_max_sync(kFullMask, best)) best = 0u;  // lanes that tie go together: the bound stays one
-  const uint32_t bound = max(__reduce_max_sync(kFullMask, best), kKeyNegInf + 1u);
-  int c = 0;
+    if (key == __reduce_max_sync(kFullMask, key)) key = 0u;  // lanes that tie go together: the bound stays one
+  key = __reduce_max_sync(kFullMask, key);
+  const float bound = key <= 0x007FFFFFu ? kLowest : __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key);
+  int count = 0;
 #pragma unroll
-  for (int j = 0; j < EPL; ++j) c += key[j] >= bound;
-  int at = c;
+  for (int j = 0; j < EPL; ++j) count += c[j] >= bound;
+  int at = count;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int v = __shfl_up_sync(kFullMask, at, o);
@@ -167,51 +162,51 @@ __device__ __forceinline__ int choose(uint32_t (&key)[EPL], int K, Candidates& l
   }
   const int n = __shfl_sync(kFullMask, at, 31);
   if (n <= 32) {
-    at -= c;
-    uint32_t* keys = reinterpret_cast<uint32_t*>(list.key);
+    at -= count;
+    float* scores = reinterpret_cast<float*>(list.score);
 #pragma unroll
     for (int j = 0; j < EPL; ++j)
-      if (key[j] >= bound) {
-        keys[at] = key[j];
+      if (c[j] >= bound) {
+        scores[at] = c[j];
         list.expert[at] = expert_of<EPL>(j, lane);
         ++at;
       }
-    if (lane >= n) keys[lane] = 0u;
+    if (lane >= n) scores[lane] = -kInf;
     __syncwarp();
-    mine_key = keys[lane];
+    mine_score = scores[lane];
     mine = list.expert[lane];
     int place = 0;
     for (int i = 0; 4 * i < n; ++i) {
-      const uint4 v = list.key[i];
-      place += (v.x > mine_key) + (v.y > mine_key) + (v.z > mine_key) + (v.w > mine_key);
+      const float4 v = list.score[i];
+      place += (v.x > mine_score) + (v.y > mine_score) + (v.z > mine_score) + (v.w > mine_score);
     }
     const unsigned seen = __reduce_or_sync(kFullMask, lane < n ? 1u << place : 0u);
     if (__popc(seen) != n)
-      for (int i = 0; i < n; ++i) place += keys[i] == mine_key && list.expert[i] < mine;
+      for (int i = 0; i < n; ++i) place += scores[i] == mine_score && list.expert[i] < mine;
     __syncwarp();
     return lane < n && place < K ? place : -1;
   }
   int place = -1;
   for (int r = 0; r < K; ++r) {
-    uint32_t bk = 0u;
+    float bc = -kInf;
     int be = 0x7FFFFFFF;
 #pragma unroll
     for (int j = 0; j < EPL; ++j)
-      if (key[j] > bk) {
-        bk = key[j];
+      if (c[j] > bc) {
+        bc = c[j];
         be = expert_of<EPL>(j, lane);
       }
-    const uint32_t m = __reduce_max_sync(kFullMask, bk);
-    if (m <= kKeyNegInf) break;  // fewer than K experts are available
-    const int e = static_cast<int>(__reduce_min_sync(kFullMask, bk == m ? static_cast<uint32_t>(be) : 0xFFFFFFFFu));
+    const float m = warp_max(bc);
+    if (m == -kInf) break;  // fewer than K experts are available
+    const int e = static_cast<int>(__reduce_min_sync(kFullMask, bc == m ? static_cast<uint32_t>(be) : 0xFFFFFFFFu));
     if (lane == r) {
       mine = e;
-      mine_key = m;
+      mine_score = m;
       place = r;
     }
 #pragma unroll
     for (int j = 0; j < EPL; ++j)
-      if (expert_of<EPL>(j, lane) == e) key[j] = 0u;
+      if (expert_of<EPL>(j, lane) == e) c[j] = -kInf;
   }
   return place;
 }
@@ -238,24 +233,36 @@ __global__ void __launch_bounds__(kRouteThreads, EPL <= 8 ? 4 : EPL <= 16 ? 2 : 
   pdl_wait();
   __syncthreads();
 
-  float bias[EPL];
+  // the choice bias in shared memory; one that is NaN or +inf disables its expert
   bool bad = false;
-#pragma unroll
-  for (int j = 0; j < EPL; ++j) {
-    const int e = expert_of<EPL>(j, lane);
-    bias[j] = a.bias != nullptr && e < E ? __ldg(a.bias + e) : 0.f;
+  float* s_bias = s_rows + static_cast<size_t>(kRouteWarps) * E;  // [E], with a bias
+  if (a.bias != nullptr) {
+    for (int e = threadIdx.x; e < E; e += kRouteThreads) {
+      float b = __ldg(a.bias + e);
+      if (!(b < kInf)) {
+        b = -kInf;
+        bad = true;
+      }
+      s_bias[e] = b;
+    }
+    __syncthreads();
   }
   float prob[EPL];  // the warp's sums of p
 #pragma unroll
   for (int j = 0; j < EPL; ++j) prob[j] = 0.f;
   int valid = 0;
-  // group that this lane helps to score: `parts` lanes a group; every group is read from its
-  // own place on, so that the lanes' banks differ
+  // Groups of a multiple of 4 experts are scored from the two best of every lane's 4
+  // neighbours, others from the experts one by one: `cells` of a group, `parts` lanes a group;
+  // every group is read from a place of its own on, so that the lanes' banks differ.
+  constexpr bool kQuads = EPL >= 4;
   const int per_group = E / g.G;
+  const bool quads = kQuads && per_group % 4 == 0;
+  const int cells = quads ? per_group / 4 : per_group;
   int parts = 1;
   while (parts * 2 * g.G <= 32) parts *= 2;
   const int grp = lane / parts, part = lane - grp * parts;
-  const int place = (part + grp * parts) % per_group;
+  const int place = (part + grp * parts) % cells;
+  const uint32_t group_magic = 0xFFFFFFFFu / static_cast<uint32_t>(per_group) + 1u;  // e / per_group, e < 2^16, by a high product
 
   const int step = g.C * kRouteWarps;
   const int64_t first = static_cast<int64_t>(seg) * g.T;
@@ -285,94 +292,135 @@ __global__ void __launch_bounds__(kRouteThreads, EPL <= 8 ? 4 : EPL <= 16 ? 2 : 
       continue;
     }
     ++valid;
-    bad |= clean<EPL>(l);
-    // scores, the choice's keys, and the probabilities' sum
-    uint32_t key[EPL];
-    float total = 0.f, top = 0.f, inv;
+    // choice scores (in place of the logits when these are the scores), probabilities' sum
+    float total = 0.f, top = 0.f, inv, best = -kInf;
     {
       float s[EPL];
       if (g.sigmoid) {
+        bad |= clean<EPL>(l);
 #pragma unroll
         for (int j = 0; j < EPL; ++j) {
           s[j] = sigmoid_rn(l[j]);
           total += s[j];
-          key[j] = order_key(l[j] > -kInf ? __fadd_rn(s[j], bias[j]) : -kInf);
+          l[j] = l[j] > -kInf ? s[j] : -kInf;
+          best = fmaxf(best, l[j]);
         }
+        total = warp_sum(total);
       } else {
-        float m = -kInf;
+        auto probabilities = [&] {
+          best = -kInf;
 #pragma unroll
-        for (int j = 0; j < EPL; ++j) m = fmaxf(m, l[j]);
-        top = warp_max(m);
-        if (top == -kInf) top = 0.f;  // no expert is available: every p is 0
+          for (int j = 0; j < EPL; ++j) best = fmaxf(best, l[j]);
+          top = warp_max(best);
+          if (top == -kInf) top = 0.f;  // no expert is available: every p is 0
+          total = 0.f;
 #pragma unroll
-        for (int j = 0; j < EPL; ++j) {
-          s[j] = exp_fast(l[j] - top);
-          total += s[j];
-          key[j] = order_key(__fadd_rn(l[j], bias[j]));  // -0 + 0 is +0, so the two zeros tie
+          for (int j = 0; j < EPL; ++j) {
+            s[j] = exp_fast(l[j] - top);
+            total += s[j];
+          }
+          total = warp_sum(total);
+        };
+        probabilities();
+        if (!(total < kInf)) {  // a NaN or +inf among the logits makes the sum NaN
+          bad |= clean<EPL>(l);
+          probabilities();
         }
       }
-      total = warp_sum(total);
       inv = total > 0.f ? rcp_fast(total) : 0.f;
 #pragma unroll
       for (int j = 0; j < EPL; ++j) prob[j] = fmaf(s[j], inv, prob[j]);
     }
-
-    if (g.G > 1) {  // keep the groups whose two best experts score highest
-      __syncwarp();
+    if (a.bias != nullptr) {
+      best = -kInf;
 #pragma unroll
       for (int j = 0; j < EPL; ++j) {
         const int e = expert_of<EPL>(j, lane);
-        const uint32_t u = key[j] & 0x80000000u ? key[j] ^ 0x80000000u : ~key[j];
-        if (e < E) s_row[e] = key[j] > kKeyNegInf && key[j] < kKeyPosInf ? __uint_as_float(u) : -kInf;
+        if (e < E) l[j] = __fadd_rn(l[j], s_bias[e]);
+        best = fmaxf(best, l[j]);
       }
+      if (__any_sync(kFullMask, best == kInf)) {  // a sum past the largest float: not chosen
+        bad = true;
+        best = -kInf;
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) {
+          if (l[j] == kInf) l[j] = -kInf;
+          best = fmaxf(best, l[j]);
+        }
+      }
+    }
+
+    if (g.G > 1) {  // keep the groups whose two best experts score highest
+      Top2 two{-kInf, -kInf};
       __syncwarp();
-      Top2 best{-kInf, -kInf};
-      if (grp < g.G) {
-        const float* row = s_row + grp * per_group;
-        int i = place;
-        for (int n = part; n < per_group; n += parts) {
-          best = top2_merge(best, Top2{row[i], -kInf});
-          i += parts;
-          if (i >= per_group) i -= per_group;
+      if (quads) {
+        if constexpr (kQuads) {
+#pragma unroll
+          for (int j = 0; j < EPL; j += 4) {
+            const int e = expert_of<EPL>(j, lane);
+            const Top2 q = top2_merge(top2_merge(Top2{l[j], -kInf}, Top2{l[j + 1], -kInf}),
+                                      top2_merge(Top2{l[j + 2], -kInf}, Top2{l[j + 3], -kInf}));
+            if (e < E) *reinterpret_cast<float2*>(s_row + e / 2) = make_float2(q.a, q.b);
+          }
+          __syncwarp();
+          if (grp < g.G) {
+            const float2* row = reinterpret_cast<const float2*>(s_row) + grp * cells;
+            int i = place;
+            for (int n = part; n < cells; n += parts) {
+              const float2 q = row[i];
+              two = top2_merge(two, Top2{q.x, q.y});
+              i += parts;
+              if (i >= cells) i -= cells;
+            }
+          }
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) {
+          const int e = expert_of<EPL>(j, lane);
+          if (e < E) s_row[e] = l[j];
+        }
+        __syncwarp();
+        if (grp < g.G) {
+          const float* row = s_row + grp * cells;
+          int i = place;
+          for (int n = part; n < cells; n += parts) {
+            two = top2_merge(two, Top2{row[i], -kInf});
+            i += parts;
+            if (i >= cells) i -= cells;
+          }
         }
       }
       for (int o = 1; o < parts; o <<= 1) {
-        const Top2 other{__shfl_xor_sync(kFullMask, best.a, o), __shfl_xor_sync(kFullMask, best.b, o)};
-        best = top2_merge(best, other);
+        const Top2 other{__shfl_xor_sync(kFullMask, two.a, o), __shfl_xor_sync(kFullMask, two.b, o)};
+        two = top2_merge(two, other);
       }
-      uint32_t gk = grp < g.G && part == 0 ? order_key(__fadd_rn(best.a, best.b)) : 0u;
+      // a group without two available experts goes after the others, but before what is -inf
+      // here: groups already taken, and lanes that hold none
+      float score = grp < g.G && part == 0 ? fmaxf(__fadd_rn(two.a, two.b), kLowest) : -kInf;
       uint32_t kept = 0;
       for (int r = 0; r < g.keep; ++r) {
-        const uint32_t m = __reduce_max_sync(kFullMask, gk);
-        const int src = __ffs(__ballot_sync(kFullMask, gk == m)) - 1;
+        const int src = __ffs(__ballot_sync(kFullMask, score == warp_max(score))) - 1;
         kept |= 1u << (src / parts);
-        if (lane == src) gk = 0u;
+        if (lane == src) score = -kInf;
       }
+      best = -kInf;
 #pragma unroll
       for (int j = 0; j < EPL; ++j) {
-        const int e = expert_of<EPL>(j, lane);
-        if (e < E && !(kept >> (e / per_group) & 1u)) key[j] = 0u;
+        const int e = expert_of<EPL>(kQuads && quads ? j / 4 * 4 : j, lane);
+        if (!(kept >> (__umulhi(static_cast<uint32_t>(e), group_magic) & 31u) & 1u)) l[j] = -kInf;
+        best = fmaxf(best, l[j]);
       }
     }
-
-    uint32_t most = 0u;
-#pragma unroll
-    for (int j = 0; j < EPL; ++j) most = max(most, key[j]);
-    if (__any_sync(kFullMask, most >= kKeyPosInf)) {  // a choice score that is NaN or +inf: not chosen
-      bad = true;
-#pragma unroll
-      for (int j = 0; j < EPL; ++j)
-        if (key[j] >= kKeyPosInf) key[j] = 0u;
-    }
     int mine;
-    uint32_t mine_key;
-    const int place_of = choose<EPL>(key, K, s_list[warp], lane, mine, mine_key);
+    float mine_score;
+    const int place_of = choose<EPL>(l, best, K, s_list[warp], lane, mine, mine_score);
     if (place_of < 0) mine = -1;
-    // weights of the chosen: from the key if it is the logit, else the logit is read again (it is in L1)
+    // weights of the chosen: the score is the logit, or the logit is read again (it is in L1)
     float w = 0.f, lv = -kInf;
     if (mine >= 0) {
       if (!g.sigmoid && a.bias == nullptr)
-        lv = __uint_as_float(mine_key & 0x80000000u ? mine_key ^ 0x80000000u : ~mine_key);
+        lv = mine_score;
       else
         lv = kBf16 ? __uint_as_float(static_cast<uint32_t>(__ldg(static_cast<const uint16_t*>(a.logits) + token * E + mine)) << 16)
                    : __ldg(static_cast<const float*>(a.logits) + token * E + mine);
@@ -651,7 +699,7 @@ __global__ void __launch_bounds__(kRouteThreads, EPL <= 8 ? 4 : EPL <= 16 ? 2 : 
 template <int EPL, bool kBf16, bool kVec>
 cudaError_t launch_fwd(const RouteArgs& a, cudaStream_t stream) {
   auto kern = route_kernel<EPL, kBf16, kVec>;
-  const size_t smem = sizeof(float) * static_cast<size_t>(a.g.E) * (1 + kRouteWarps);
+  const size_t smem = sizeof(float) * static_cast<size_t>(a.g.E) * (1 + kRouteWarps + (a.bias != nullptr));
   if (resident_ctas(reinterpret_cast<const void*>(kern), kRouteThreads, smem) < 1) return cudaErrorInvalidConfiguration;
   return launch_chained(kern, dim3(static_cast<unsigned>(a.g.B) * a.g.C), dim3(kRouteThreads), smem, stream, a);
 }
