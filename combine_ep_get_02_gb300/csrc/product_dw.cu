@@ -1,13 +1,21 @@
 // Gradient of the experts' matrices: dW_g[z][k] = sum over the group's rows r of
 // dz[r][z] x[r][k], for every group (zeros for an empty one).
 //
-// The same roles as the rows' products (a CTA per SM over 128 x 256 tiles of dW; one
-// warp for TMA, one for tcgen05.mma, eight for the epilogue), with both operands
-// MN-major: the summed index is the row, so tiles of 64 rows are used as they lie in
-// the tensors, without a transposition. A group's last tile ends inside the next
-// group's rows (or padding): the warp that issues the products first zeroes, in shared
-// memory, the rows past the group up to the next multiple of 16 (one instruction's
-// share) in both operands, so that not even a NaN there reaches the sum.
+// Tiles of 256 x 256 of dW, one to a pair of CTAs (a cluster of two) with one tcgen05.mma
+// over both SMs, as in the rows' products; roles as there (a warp for TMA, one for the
+// products, eight for the epilogue). Both operands are MN-major: the summed index is the
+// row, so tiles of 64 rows are used as they lie in the tensors, without a transposition.
+//
+// A group's last tile ends inside the next group's rows (or padding). The rows past the
+// group, up to the next multiple of 16 (one instruction's share), are zeroed in shared memory
+// in both operands, so that not even a NaN there reaches the sum; the rest is left out by
+// issuing fewer instructions. Since each CTA must have mended its own half before the
+// pair's product reads it, the loads of such a tile count on the CTA's own barrier; the second
+// CTA's product warp waits for that, mends, and then arrives on a barrier of the first. (All
+// tiles' loads taking that way more than doubled the kernel's time: 285 us against 119 for
+// single CTAs at 4096 x 4096 x 4096.)
+// (Single CTAs with tiles of 128 x 256 reached 48% of the tensor cores' time: they want
+// 96 bytes a cycle from L2 where an SM gets about 64.)
 #include "product_common.cuh"
 
 namespace ep {
@@ -16,10 +24,10 @@ namespace {
 
 constexpr int kEpilogueWarps = 8;
 constexpr int kThreads = 64 + 32 * kEpilogueWarps;
-constexpr int kBM = 128, kBN = 256, kBK = 64;
-constexpr int kStages = 4;
+constexpr int kBM = 128, kBN = 256, kBK = 64;  // rows of dW a CTA, columns a pair, rows of x and dz a stage
+constexpr int kStages = 6;
 constexpr int kPanel = kBK * 128;  // bytes of 64 columns x 64 rows
-constexpr int kABytes = kBM * kBK * 2, kBBytes = kBN * kBK * 2, kStageBytes = kABytes + kBBytes;
+constexpr int kABytes = kBM * kBK * 2, kBBytes = kBN / 2 * kBK * 2, kStageBytes = kABytes + kBBytes;
 
 struct WeightArgs {
   Groups groups;
@@ -27,6 +35,9 @@ struct WeightArgs {
   uint16_t* out;  // [E][Z][K]
   uint32_t* err;
 };
+
+// Rows of a stage that count, and whether the tile ends inside an instruction's 16.
+__device__ __forceinline__ bool to_mend(int left) { return left < kBK && (left & 15) != 0; }
 
 struct Tile {
   int g, begin, rows, z0, k0;
@@ -37,16 +48,17 @@ __device__ __forceinline__ Tile tile_at(const WeightArgs& a, int64_t i, int mt, 
   const int r = static_cast<int>(i - static_cast<int64_t>(g) * mt * nt);
   const GroupRows rows = group_rows(a.groups, g);
   const int n = r / mt;
-  return Tile{g, rows.begin, rows.count, (r - n * mt) * kBM, n * kBN};
+  return Tile{g, rows.begin, rows.count, (r - n * mt) * 2 * kBM, n * kBN};
 }
 
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     weight_grad_kernel(const __grid_constant__ CUtensorMap map_dz, const __grid_constant__ CUtensorMap map_x, WeightArgs a) {
   extern __shared__ uint8_t s_raw[];
-  __shared__ __align__(8) uint64_t s_full[kStages], s_empty[kStages], s_acc_full[2], s_acc_empty[2], s_drained;
+  __shared__ __align__(8) uint64_t s_full[kStages], s_empty[kStages], s_part[kStages], s_other[kStages], s_acc_full[2], s_acc_empty[2], s_drained;
   __shared__ uint32_t s_tmem;
   __shared__ volatile int s_abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_rank());
   const uint32_t stage0 = (smem_addr(s_raw) + 1023u) & ~1023u;
   const uint32_t patch0 = stage0 + kStages * kStageBytes;
   uint8_t* stage_mem = s_raw + (stage0 - smem_addr(s_raw));
@@ -54,10 +66,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int s = 0; s < kStages; ++s) {
       mbar_init_count(smem_addr(&s_full[s]), 1);
       mbar_init_count(smem_addr(&s_empty[s]), 1);
+      mbar_init_count(smem_addr(&s_part[s]), 1);
+      mbar_init_count(smem_addr(&s_other[s]), 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init_count(smem_addr(&s_acc_full[i]), 1);
-      mbar_init_count(smem_addr(&s_acc_empty[i]), kEpilogueWarps);
+      mbar_init_count(smem_addr(&s_acc_empty[i]), 2 * kEpilogueWarps);
     }
     mbar_init_count(smem_addr(&s_drained), 1);
     s_abort = 0;
@@ -66,8 +80,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_map(&map_x);
   }
   if (warp == 2) {
-    tmem_alloc(smem_addr(&s_tmem), 512);
-    tmem_relinquish();
+    tmem_alloc_pair(smem_addr(&s_tmem), 512);
+    tmem_relinquish_pair();
   }
   pdl_launch_dependents();
   pdl_wait();
@@ -78,10 +92,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
+  cluster_sync_all();  // both CTAs' barriers and accumulators exist
   tc_fence_after();
   const uint32_t tmem = s_tmem;
-  const int mt = (a.Z + kBM - 1) / kBM, nt = (a.K + kBN - 1) / kBN;
+  const int mt = (a.Z + 2 * kBM - 1) / (2 * kBM), nt = (a.K + kBN - 1) / kBN;
   const int64_t total = static_cast<int64_t>(a.groups.E) * mt * nt;
+  const int64_t first = blockIdx.x >> 1, step = gridDim.x >> 1;
   auto give_up = [&] {
     s_abort = 1;
     atomicOr(a.err, kErrTimeout);
@@ -90,56 +106,68 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0) {
     if (elect_one()) {
       uint32_t n = 0;
+      uint32_t part = 0, full_phase = 0, part_phase = 0;  // bit s: stage s's last use, phases of its barriers
       bool ok = true;
-      for (int64_t i = blockIdx.x; ok && i < total; i += gridDim.x) {
+      for (int64_t i = first; ok && i < total; i += step) {
         const Tile t = tile_at(a, i, mt, nt);
         for (int r = 0; r < t.rows; r += kBK, ++n) {
-          const uint32_t s = n % kStages, bar = smem_addr(&s_full[s]);
+          const uint32_t s = n % kStages, bit = 1u << s;
           if (s_abort || !mbar_wait_timed(smem_addr(&s_empty[s]), (n / kStages & 1u) ^ 1u)) {
             if (!s_abort) give_up();
             ok = false;
             break;
           }
-          mbar_expect(bar, kStageBytes);
           const uint32_t sa = stage0 + s * kStageBytes, sb = sa + kABytes;
+          const int z = t.z0 + rank * kBM, k = t.k0 + rank * (kBN / 2);
+          uint32_t bar;
+          if (to_mend(t.rows - r)) {
+            bar = smem_addr(&s_part[s]);
+            mbar_expect(bar, kStageBytes);
+            part |= bit;
+            part_phase ^= bit;
+          } else {
+            bar = cluster_addr(smem_addr(&s_full[s]), 0);
+            if (rank == 0) mbar_expect(smem_addr(&s_full[s]), 2 * kStageBytes);
+            part &= ~bit;
+            full_phase ^= bit;
+          }
 #pragma unroll
-          for (int p = 0; p < kBM / 64; ++p) tma_load_2d(sa + p * kPanel, &map_dz, t.z0 + p * 64, t.begin + r, bar);
+          for (int p = 0; p < kBM / 64; ++p) tma_load_2d_pair(sa + p * kPanel, &map_dz, z + p * 64, t.begin + r, bar);
 #pragma unroll
-          for (int p = 0; p < kBN / 64; ++p) tma_load_2d(sb + p * kPanel, &map_x, t.k0 + p * 64, t.begin + r, bar);
+          for (int p = 0; p < kBN / 128; ++p) tma_load_2d_pair(sb + p * kPanel, &map_x, k + p * 64, t.begin + r, bar);
         }
       }
-      if (!ok)
-        for (uint32_t back = n < kStages ? n : kStages; back > 0; --back) {
-          const uint32_t m = n - back;
-          mbar_wait_timed(smem_addr(&s_full[m % kStages]), m / kStages & 1u);
+      if (!ok)  // the copies in flight land before the CTAs' memory goes
+        for (uint32_t s = 0; s < kStages && s < n; ++s) {
+          if (part >> s & 1u) mbar_wait_timed(smem_addr(&s_part[s]), (part_phase >> s & 1u) ^ 1u);
+          else if (rank == 0) mbar_wait_timed(smem_addr(&s_full[s]), (full_phase >> s & 1u) ^ 1u);
         }
     }
   } else if (warp == 1) {
-    constexpr uint32_t idesc = idesc_bf16(kBM, kBN, true, true);
+    constexpr uint32_t idesc = idesc_bf16(2 * kBM, kBN, true, true);
     uint32_t n = 0, acc = 0;
+    uint32_t full_phase = 0, part_phase = 0;  // bit s: phase of stage s's barriers
     bool ok = true;
-    for (int64_t i = blockIdx.x; ok && i < total; i += gridDim.x) {
+    auto wait_all = [&](uint32_t bar, uint32_t parity) {  // the whole warp
+      ok = __all_sync(kFullMask, s_abort == 0 && mbar_wait_timed(bar, parity));
+      if (!ok && lane == 0 && !s_abort) give_up();
+      return ok;
+    };
+    for (int64_t i = first; ok && i < total; i += step) {
       const Tile t = tile_at(a, i, mt, nt);
       if (t.rows == 0) continue;
       const uint32_t b = acc & 1u;
-      ok = __all_sync(kFullMask, s_abort == 0 && mbar_wait_timed(smem_addr(&s_acc_empty[b]), (acc >> 1 & 1u) ^ 1u));
-      if (!ok) {
-        if (lane == 0 && !s_abort) give_up();
-        break;
-      }
+      if (rank == 0 && !wait_all(smem_addr(&s_acc_empty[b]), (acc >> 1 & 1u) ^ 1u)) break;
       tc_fence_after();
       const uint32_t d = tmem + b * kBN;
       for (int r = 0; r < t.rows; r += kBK, ++n) {
-        const uint32_t s = n % kStages;
-        ok = __all_sync(kFullMask, s_abort == 0 && mbar_wait_timed(smem_addr(&s_full[s]), n / kStages & 1u));
-        if (!ok) {
-          if (lane == 0 && !s_abort) give_up();
-          break;
-        }
-        tc_fence_after();
-        const int left = min(kBK, t.rows - r);      // rows of this tile that count
-        const int used = (left + 15) & ~15;         // rows the instructions read
-        if (used != left) {
+        const uint32_t s = n % kStages, bit = 1u << s;
+        const int left = min(kBK, t.rows - r);  // rows of this tile that count
+        const int used = (left + 15) & ~15;     // rows the instructions read
+        if (to_mend(t.rows - r)) {
+          const uint32_t phase = part_phase >> s & 1u;
+          part_phase ^= bit;
+          if (!wait_all(smem_addr(&s_part[s]), phase)) break;
           // a 128-byte row of a panel holds one row's 64 columns, in whatever order
           const int chunks = (used - left) * 8;
           uint8_t* base = stage_mem + s * kStageBytes + left * 128;
@@ -148,31 +176,44 @@ __global__ void __launch_bounds__(kThreads, 1)
               *reinterpret_cast<uint4*>(base + p * kPanel + c * 16) = make_uint4(0u, 0u, 0u, 0u);
           fence_async_shared();
           __syncwarp();
+          if (rank != 0) {
+            if (lane == 0) mbar_arrive_cluster(cluster_addr(smem_addr(&s_other[s]), 0));
+            __syncwarp();
+            continue;
+          }
+          if (!wait_all(smem_addr(&s_other[s]), phase)) break;
+        } else {
+          if (rank != 0) continue;
+          const uint32_t phase = full_phase >> s & 1u;
+          full_phase ^= bit;
+          if (!wait_all(smem_addr(&s_full[s]), phase)) break;
         }
-        if (lane == 0) {
+        tc_fence_after();
+        if (elect_one()) {  // the same lane each time
           const uint32_t sa = stage0 + s * kStageBytes, sb = sa + kABytes;
           const uint64_t da = desc_mn_major(sa, kPanel), db = desc_mn_major(sb, kPanel);
-          for (int k = 0; k < used / 16; ++k) mma_bf16(d, da + k * kStepMN, db + k * kStepMN, idesc, r > 0 || k > 0);
-          mma_commit(smem_addr(&s_empty[s]));
+#pragma unroll
+          for (int k = 0; k < kBK / 16; ++k)
+            if (k * 16 < used) mma_bf16_pair(d, da + k * kStepMN, db + k * kStepMN, idesc, r > 0 || k > 0);
+          mma_commit_pair(smem_addr(&s_empty[s]));
+          if (r + kBK >= t.rows) mma_commit_pair(smem_addr(&s_acc_full[b]));
         }
         __syncwarp();
       }
-      if (ok && lane == 0) mma_commit(smem_addr(&s_acc_full[b]));
-      __syncwarp();
       ++acc;
     }
-    if (!ok && lane == 0) {  // the products in flight finish before the CTA's memory goes
-      mma_commit(smem_addr(&s_drained));
+    if (!ok && rank == 0 && elect_one()) {  // the products in flight finish before the CTAs' memory goes
+      mma_commit_pair(smem_addr(&s_drained));
       mbar_wait_timed(smem_addr(&s_drained), 0);
     }
   } else {
     const int quarter = warp & 3, half = (warp - 2) >> 2;
     const uint32_t patch = patch0 + (warp - 2) * kPatchBytes;
     uint32_t acc = 0;
-    for (int64_t i = blockIdx.x; i < total; i += gridDim.x) {
+    for (int64_t i = first; i < total; i += step) {
       const Tile t = tile_at(a, i, mt, nt);
       const uint32_t b = acc & 1u;
-      const int z0 = t.z0 + quarter * 32;
+      const int z0 = t.z0 + rank * kBM + quarter * 32;
       uint16_t* out = a.out + (static_cast<int64_t>(t.g) * a.Z + z0) * a.K + t.k0;
       if (t.rows > 0) {
         bool ok = s_abort == 0 && mbar_wait_timed(smem_addr(&s_acc_full[b]), acc >> 1 & 1u);
@@ -199,15 +240,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (t.rows > 0) {
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_addr(&s_acc_empty[b]));
+        if (lane == 0) mbar_arrive_cluster(cluster_addr(smem_addr(&s_acc_empty[b]), 0));
         ++acc;
       }
     }
   }
   __syncwarp();
   __syncthreads();
+  cluster_sync_all();  // neither CTA's memory goes while the other may still use it
   tc_fence_after();
-  if (warp == 2) tmem_dealloc(tmem, 512);
+  if (warp == 2) tmem_dealloc_pair(tmem, 512);
 }
 
 }  // namespace
@@ -226,8 +268,9 @@ cudaError_t launch_product_dw(const ProductGradArgs& p, int num_sms, cudaStream_
   if (resident_ctas(reinterpret_cast<const void*>(weight_grad_kernel), kThreads, smem) < 1)
     return cudaErrorInvalidConfiguration;
   const int64_t total =
-      static_cast<int64_t>(a.groups.E) * ((a.Z + kBM - 1) / kBM) * ((a.K + kBN - 1) / kBN);
-  const unsigned grid = static_cast<unsigned>(total < num_sms ? total : num_sms);
+      static_cast<int64_t>(a.groups.E) * ((a.Z + 2 * kBM - 1) / (2 * kBM)) * ((a.K + kBN - 1) / kBN);
+  const int64_t pairs = num_sms < 4 ? 1 : num_sms / 2;
+  const unsigned grid = static_cast<unsigned>(2 * (total < pairs ? total : pairs));
   return launch_chained(weight_grad_kernel, dim3(grid), dim3(kThreads), smem, stream, map_dz, map_x, a);
 }
 

@@ -190,7 +190,7 @@ cudaError_t launch_rows_pair(const uint16_t* A, const uint16_t* B, const RowsArg
   const int cols = kAct == EP_ACT_SWIGLU ? kBN / 2 : kBN;
   const int64_t row_tiles = a.groups.rows / (2 * kBM) + (a.groups.count == nullptr ? 1 : a.groups.E);
   const int64_t most = row_tiles * ((a.epi.cols + cols - 1) / cols);
-  const int64_t pairs = most < num_sms / 2 ? most : num_sms / 2;
+  const int64_t pairs = most < num_sms / 2 ? most : num_sms / 2;  // num_sms >= 2
   return launch_chained(kern, dim3(static_cast<unsigned>(2 * pairs)), dim3(kThreads), smem, stream, map_a, map_b, a);
 }
 #define X(act, mn) \
