@@ -618,7 +618,11 @@ def ep_combine_grad(cfg: Config, layout: Layout, y, topk_idx: torch.Tensor, topk
     """Gradient of ep_combine: d_y (rows of y) and d_weights [R][T][K]; either may be None."""
     w = "ep_combine_grad"
     N, H = cfg.num_ranks * cfg.num_tokens, cfg.hidden
-    NK, rows = N * cfg.num_topk, max(ep_recv_rows(cfg), 0)
+    rows = cfg.__dict__.get("_sizes")  # kept until a field of cfg is assigned
+    if rows is None:
+        rows = max(ep_recv_rows(cfg), 0)
+        object.__setattr__(cfg, "_sizes", rows)
+    NK = N * cfg.num_topk
     y = _at(y, _BF16, rows * H, w, "y") if d_weights is not None or y is not None else None
     _check(lib().ep_combine_grad(
         cfg._ref(), layout._ref(), y, _at(topk_idx, _I64, NK, w, "topk_idx"),

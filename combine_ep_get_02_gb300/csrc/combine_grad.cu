@@ -6,10 +6,12 @@
 // across units. Reading g and the rows of y and writing the rows of dy is what it
 // cannot do without; the multiply-adds are 3 per column and row.
 //
-// One warp takes a token; lane k finds the row of top-k lane k, and the lowest lane of
-// those that share a row stands for it. Each lane holds 8 columns of g per step and
-// streams the distinct rows past them; the K dot products stay in registers in 32
-// bits to the end of the token and are summed across the warp once.
+// `ways` warps take a token (one, when there are tokens for every warp of the GPU; up to the
+// eight of a CTA when there are few, so that a token's columns load at once); lane k finds
+// the row of top-k lane k, and the lowest lane of those that share a row stands for it.
+// Each lane holds 8 columns of g per step and streams the distinct rows past them; the K
+// dot products stay in registers in 32 bits to the end of the token and are summed across
+// the warp once, then over the token's warps in their order.
 #include "ep_device.cuh"
 #include "moe_internal.cuh"
 
@@ -20,20 +22,24 @@ namespace {
 constexpr int kWarps = kCopyThreads / 32;
 
 template <bool kExpand, int kMaxK>
-__global__ void __launch_bounds__(kCopyThreads) combine_grad_kernel(CombineGradArgs ga) {
+__global__ void __launch_bounds__(kCopyThreads) combine_grad_kernel(CombineGradArgs ga, int ways) {
   const CombineArgs& a = ga.c;
   __shared__ int64_t s_row[kWarps][kMaxK];
   __shared__ float s_w[kWarps][kMaxK];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t nwarps = static_cast<int64_t>(gridDim.x) * kWarps;
+  __shared__ float s_dot[kWarps][kMaxK];
   const int nchunk = a.H >> 3;  // 8 bf16 per chunk
+  const int per_cta = kWarps / ways, way = warp % ways;
   pdl_launch_dependents();
   pdl_wait();
 
-  for (int64_t tok = static_cast<int64_t>(blockIdx.x) * kWarps + warp; tok < a.num_tokens; tok += nwarps) {
+  // the CTA's warps go round together: they meet where a token's dot products are joined
+  for (int64_t base = static_cast<int64_t>(blockIdx.x) * per_cta; base < a.num_tokens;
+       base += static_cast<int64_t>(gridDim.x) * per_cta) {
+    const int64_t tok = base + warp / ways;
     int64_t row = -1;
     float w = 0.f;
-    if (lane < a.K) {
+    if (lane < a.K && tok < a.num_tokens) {
       const int64_t i = tok * a.K + lane;
       const int64_t e = __ldg(a.topk_idx + i);
       const int r = __ldg((kExpand ? a.exp_pos : a.slot_map) + i);
@@ -66,7 +72,7 @@ __global__ void __launch_bounds__(kCopyThreads) combine_grad_kernel(CombineGradA
       dot[k] = 0.f;
     }
     const uint16_t* grow = ga.d_out + tok * a.H;
-    for (int c = lane; c < nchunk; c += 32) {
+    for (int c = way * 32 + lane; tok < a.num_tokens && c < nchunk; c += 32 * ways) {
       const size_t col = static_cast<size_t>(c) << 3;
       const uint4 gv = ld_stream16(grow + col);
       uint4 yv[kMaxK];
@@ -113,8 +119,16 @@ __global__ void __launch_bounds__(kCopyThreads) combine_grad_kernel(CombineGradA
         for (int o = 16; o; o >>= 1) dot[k] += __shfl_xor_sync(kFullMask, dot[k], o);
         if (lane == k) mine = dot[k];
       }
+      if (ways > 1) {
+        if (lane < kMaxK) s_dot[warp][lane] = mine;
+        __syncthreads();
+        mine = 0.f;
+        if (lane < kMaxK)
+          for (int i = 0; i < ways; ++i) mine += s_dot[warp - way + i][lane];
+        __syncthreads();
+      }
       mine = __shfl_sync(kFullMask, mine, leader);
-      if (lane < a.K) ga.d_w[tok * a.K + lane] = row >= 0 ? mine : 0.f;
+      if (way == 0 && lane < a.K && tok < a.num_tokens) ga.d_w[tok * a.K + lane] = row >= 0 ? mine : 0.f;
     }
     __syncwarp();  // s_row / s_w are rewritten by the next token
   }
@@ -125,11 +139,16 @@ cudaError_t launch_one(const CombineGradArgs& a, int num_sms, cudaStream_t strea
   auto kern = combine_grad_kernel<kExpand, kMaxK>;
   int per_sm = resident_ctas(reinterpret_cast<const void*>(kern), kCopyThreads, 0);
   if (per_sm < 1) return cudaErrorInvalidConfiguration;
+  // warps a token: enough for the warps of 152 SMs at two CTAs each (a constant, so that results
+  // do not depend on the device), and no more than sweeps of 32 chunks in a row
+  int ways = 1;
+  while (ways < kWarps && a.c.num_tokens * ways * 2 <= 152 * 2 * kWarps && a.c.H / 8 >= ways * 32 * 2) ways *= 2;
+  const int64_t per_cta = kWarps / ways;
   int64_t ctas = static_cast<int64_t>(num_sms) * per_sm;
-  const int64_t need = (a.c.num_tokens + kWarps - 1) / kWarps;
+  const int64_t need = (a.c.num_tokens + per_cta - 1) / per_cta;
   if (ctas > need) ctas = need;
   if (ctas < 1) return cudaSuccess;
-  return launch_chained(kern, dim3(static_cast<unsigned>(ctas)), dim3(kCopyThreads), 0, stream, a);
+  return launch_chained(kern, dim3(static_cast<unsigned>(ctas)), dim3(kCopyThreads), 0, stream, a, ways);
 }
 
 }  // namespace
