@@ -95,6 +95,11 @@ int make_product(const ep_product_config_t* c, ProductGeometry* g) {
   if (c->sf_pack != 0 && c->sf_pack != 1) return EP_ERR_INVALID_ARG;
   if (c->x_dtype == EP_DTYPE_FP8_E4M3 && c->in_features % 128 != 0) return EP_ERR_INVALID_ARG;
   if (c->sf_pack && c->x_dtype != EP_DTYPE_FP8_E4M3) return EP_ERR_UNSUPPORTED;
+  // output tiles are numbered in 32 bits (more would not fit any GPU's memory)
+  const int64_t width = 2ll * (c->in_features > c->out_features ? c->in_features : c->out_features) / 64 + 2;
+  if ((c->rows / kDzRows + c->num_experts) * width > INT32_MAX ||
+      (c->in_features / 256 + 1ll) * (c->out_features / 128 + 1ll) * c->num_experts > INT32_MAX)
+    return EP_ERR_UNSUPPORTED;
   g->K = c->in_features;
   g->N = c->out_features;
   g->Z = c->activation == EP_ACT_SWIGLU ? 2 * c->out_features : c->out_features;
@@ -107,7 +112,7 @@ int make_product(const ep_product_config_t* c, ProductGeometry* g) {
 
 struct ProductWorkspace {
   size_t rows;  // bf16 rows of FP8 x [rows][K], or dz [rows][Z]
-  size_t part;  // float [row tiles][Z]
+  size_t part;  // float [tiles of kDzRows rows][Z]
   size_t total;
 };
 
@@ -118,8 +123,7 @@ ProductWorkspace product_workspace(const ProductGeometry& g, bool grad) {
   if (grad) bytes = g.act == EP_ACT_NONE ? 0 : 2 * static_cast<size_t>(g.groups.rows) * g.Z;
   else if (g.x_fp8) bytes = 2 * static_cast<size_t>(g.groups.rows) * g.K;
   w.part = w.rows + round256(bytes);
-  Groups q = g.groups;
-  const int64_t tiles = q.rows / kTileRows + q.E;
+  const int64_t tiles = g.groups.rows / kDzRows + g.groups.E;
   w.total = w.part + (grad ? round256(4 * static_cast<size_t>(tiles) * g.Z) : 0);
   return w;
 }

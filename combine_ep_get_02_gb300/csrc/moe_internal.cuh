@@ -140,17 +140,20 @@ struct ProductGradArgs {
   const uint16_t* z;
   const uint16_t* d_out;
   uint16_t* dz;       // workspace [rows][Z]; null when the activation is none (dz = d_out)
-  float* part;        // workspace [row tiles][Z]: column sums of dz; null without d_bias
+  float* part;        // workspace [tiles of kDzRows rows][Z]: column sums of dz; null without d_bias
   uint16_t* d_x;      // may be null
   uint16_t* d_weight; // may be null
   float* d_bias;      // may be null
   uint32_t* err;
 };
 
-constexpr int kTileRows = 128;
-// Row tiles of all groups together, at most.
-inline int64_t max_row_tiles(const Groups& q) {
-  return static_cast<int64_t>(q.rows) / kTileRows + (q.count == nullptr ? 1 : q.E);
+constexpr int kTileRows = 128;  // rows a CTA's products take at once
+constexpr int kDzRows = 64;     // rows whose dz is summed to one partial bias gradient
+// Row tiles of all groups together, at most: whole ones and one part of every group that
+// has a row.
+inline int64_t max_row_tiles(const Groups& q, int tile_rows = kTileRows) {
+  const int64_t groups = q.count == nullptr ? 1 : q.E < q.rows ? q.E : q.rows;
+  return q.rows / tile_rows + groups;
 }
 
 cudaError_t launch_dequant(const ProductGeometry& g, const uint8_t* x, const float* x_sf, uint16_t* out, int num_sms,

@@ -65,7 +65,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s_tmem;
-  const Tiles<kBM, kCols> tiles(a.groups, prefix, a.epi.cols);
+  const Tiles<kBM> tiles(a.groups, prefix, a.epi.cols, kCols);
   const int blocks = (a.sum + kBK - 1) / kBK;
   auto give_up = [&] {
     s_abort = 1;
@@ -76,7 +76,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (elect_one()) {
       uint32_t n = 0;  // stages filled so far
       bool ok = true;
-      for (int64_t i = blockIdx.x; ok && i < tiles.total; i += gridDim.x) {
+      for (int i = blockIdx.x; ok && i < tiles.total; i += gridDim.x) {
         const Tile t = tiles.at(i);
         for (int kb = 0; kb < blocks; ++kb, ++n) {
           const uint32_t s = n % kStages, bar = smem_addr(&s_full[s]);
@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr uint32_t idesc = idesc_bf16(kBM, kBN, false, kBMn);
       uint32_t n = 0, acc = 0;
       bool ok = true;
-      for (int64_t i = blockIdx.x; ok && i < tiles.total; i += gridDim.x, ++acc) {
+      for (int i = blockIdx.x; ok && i < tiles.total; i += gridDim.x, ++acc) {
         const uint32_t b = acc & 1u;
         if (s_abort || !mbar_wait_timed(smem_addr(&s_acc_empty[b]), (acc >> 1 & 1u) ^ 1u)) {
           if (!s_abort) give_up();
@@ -146,7 +146,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int half = (warp - 2) >> 2;
     const uint32_t patch = patch0 + (warp - 2) * kPatchBytes;
     uint32_t acc = 0;
-    for (int64_t i = blockIdx.x; i < tiles.total; i += gridDim.x, ++acc) {
+    for (int i = blockIdx.x; i < tiles.total; i += gridDim.x, ++acc) {
       const uint32_t b = acc & 1u;
       const Tile t = tiles.at(i);
       bool ok = s_abort == 0 && mbar_wait_timed(smem_addr(&s_acc_full[b]), acc >> 1 & 1u);

@@ -43,9 +43,9 @@ struct Tile {
   int g, begin, rows, z0, k0;
 };
 
-__device__ __forceinline__ Tile tile_at(const WeightArgs& a, int64_t i, int mt, int nt) {
-  const int g = static_cast<int>(i / (static_cast<int64_t>(mt) * nt));
-  const int r = static_cast<int>(i - static_cast<int64_t>(g) * mt * nt);
+__device__ __forceinline__ Tile tile_at(const WeightArgs& a, int i, int total, int mt, int nt) {
+  if (i >= total) return Tile{0, 0, 0, 0, 0};
+  const int g = i / (mt * nt), r = i - g * (mt * nt);
   const GroupRows rows = group_rows(a.groups, g);
   const int n = r / mt;
   return Tile{g, rows.begin, rows.count, (r - n * mt) * 2 * kBM, n * kBN};
@@ -96,8 +96,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = s_tmem;
   const int mt = (a.Z + 2 * kBM - 1) / (2 * kBM), nt = (a.K + kBN - 1) / kBN;
-  const int64_t total = static_cast<int64_t>(a.groups.E) * mt * nt;
-  const int64_t first = blockIdx.x >> 1, step = gridDim.x >> 1;
+  const int total = a.groups.E * mt * nt;
+  const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
+  // the next tile's group is looked up while the current one is worked on: a short group's
+  // products take less time than the lookup
+  Tile ahead = tile_at(a, first, total, mt, nt);
   auto give_up = [&] {
     s_abort = 1;
     atomicOr(a.err, kErrTimeout);
@@ -108,8 +111,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       uint32_t n = 0;
       uint32_t part = 0, full_phase = 0, part_phase = 0;  // bit s: stage s's last use, phases of its barriers
       bool ok = true;
-      for (int64_t i = first; ok && i < total; i += step) {
-        const Tile t = tile_at(a, i, mt, nt);
+      for (int i = first; ok && i < total; i += step) {
+        const Tile t = ahead;
+        ahead = tile_at(a, i + step, total, mt, nt);
         for (int r = 0; r < t.rows; r += kBK, ++n) {
           const uint32_t s = n % kStages, bit = 1u << s;
           if (s_abort || !mbar_wait_timed(smem_addr(&s_empty[s]), (n / kStages & 1u) ^ 1u)) {
@@ -153,8 +157,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (!ok && lane == 0 && !s_abort) give_up();
       return ok;
     };
-    for (int64_t i = first; ok && i < total; i += step) {
-      const Tile t = tile_at(a, i, mt, nt);
+    for (int i = first; ok && i < total; i += step) {
+      const Tile t = ahead;
+      ahead = tile_at(a, i + step, total, mt, nt);
       if (t.rows == 0) continue;
       const uint32_t b = acc & 1u;
       if (rank == 0 && !wait_all(smem_addr(&s_acc_empty[b]), (acc >> 1 & 1u) ^ 1u)) break;
@@ -210,8 +215,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int quarter = warp & 3, half = (warp - 2) >> 2;
     const uint32_t patch = patch0 + (warp - 2) * kPatchBytes;
     uint32_t acc = 0;
-    for (int64_t i = first; i < total; i += step) {
-      const Tile t = tile_at(a, i, mt, nt);
+    for (int i = first; i < total; i += step) {
+      const Tile t = ahead;
+      ahead = tile_at(a, i + step, total, mt, nt);
       const uint32_t b = acc & 1u;
       const int z0 = t.z0 + rank * kBM + quarter * 32;
       uint16_t* out = a.out + (static_cast<int64_t>(t.g) * a.Z + z0) * a.K + t.k0;

@@ -47,10 +47,9 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 // dz = d_out * act'(z), rounded to bf16 for the products, and the column sums of the
-// unrounded dz over each row tile. A CTA takes a tile of 128 rows of one group and 128
+// unrounded dz over each tile of kDzRows rows. A CTA takes such a tile of one group and 128
 // output columns: 16 threads across (8 columns each, 256 bytes of a row), 16 down, so that a
-// few thousand rows already occupy every SM (512 columns a CTA took 43 us for 4096 x 4096,
-// a quarter of the SMs' warps in use).
+// few thousand rows already occupy every SM evenly.
 constexpr int kAcross = 16, kDown = kThreads / kAcross, kSpan = kAcross * 8;
 
 struct DzArgs {
@@ -71,7 +70,7 @@ __global__ void __launch_bounds__(kThreads) dz_kernel(DzArgs a) {
   __shared__ float s_sum[kDown][kHalves * kSpan];
   pdl_launch_dependents();
   pdl_wait();
-  build_prefix<kThreads>(a.groups, kTileRows, prefix, blockIdx.x == 0 ? a.err : nullptr);
+  build_prefix<kThreads>(a.groups, kDzRows, prefix, blockIdx.x == 0 ? a.err : nullptr);
   const int across = threadIdx.x % kAcross, down = threadIdx.x / kAcross;
   const int spans = (a.N + kSpan - 1) / kSpan;
   const int64_t units = static_cast<int64_t>(prefix[a.groups.E]) * spans;
@@ -79,7 +78,7 @@ __global__ void __launch_bounds__(kThreads) dz_kernel(DzArgs a) {
     const int tile = static_cast<int>(u / spans), col = static_cast<int>(u - static_cast<int64_t>(tile) * spans) * kSpan + across * 8;
     const int g = group_of_tile(prefix, a.groups.E, tile);
     const GroupRows rows = group_rows(a.groups, g);
-    const int m0 = (tile - prefix[g]) * kTileRows, n = min(kTileRows, rows.count - m0);
+    const int m0 = (tile - prefix[g]) * kDzRows, n = min(kDzRows, rows.count - m0);
     const int64_t first = static_cast<int64_t>(rows.begin) + m0;
     float sum[kHalves * 8];
 #pragma unroll
@@ -136,20 +135,33 @@ __global__ void __launch_bounds__(kThreads) dz_kernel(DzArgs a) {
   }
 }
 
-// d_bias_g = the sum of the group's row tiles, in order.
+// d_bias_g = the sum over the group's row tiles: 32 columns a CTA, 8 ways of every 8th tile,
+// then the ways in order. (A thread for all tiles of a column took 18 us at 4096 rows.)
 __global__ void __launch_bounds__(kThreads) bias_sum_kernel(Groups q, int Z, const float* part, float* d_bias) {
+  constexpr int kWays = kThreads / 32;
   extern __shared__ int prefix[];
+  __shared__ float s_sum[kWays][32];
   pdl_launch_dependents();
   pdl_wait();
-  build_prefix<kThreads>(q, kTileRows, prefix, nullptr);
-  const int64_t all = static_cast<int64_t>(q.E) * Z;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < all;
-       i += static_cast<int64_t>(gridDim.x) * kThreads) {
-    const int g = static_cast<int>(i / Z), c = static_cast<int>(i - static_cast<int64_t>(g) * Z);
+  build_prefix<kThreads>(q, kDzRows, prefix, nullptr);
+  const int way = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int spans = (Z + 31) / 32;
+  const int64_t units = static_cast<int64_t>(q.E) * spans;
+  for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+    const int g = static_cast<int>(u / spans), c = static_cast<int>(u - static_cast<int64_t>(g) * spans) * 32 + lane;
     float s = 0.f;
+    if (c < Z) {
 #pragma unroll 8
-    for (int t = prefix[g]; t < prefix[g + 1]; ++t) s += __ldcg(part + static_cast<int64_t>(t) * Z + c);
-    d_bias[i] = s;
+      for (int t = prefix[g] + way; t < prefix[g + 1]; t += kWays) s += __ldcg(part + static_cast<int64_t>(t) * Z + c);
+    }
+    s_sum[way][lane] = s;
+    __syncthreads();
+    if (way == 0 && c < Z) {
+#pragma unroll
+      for (int w = 1; w < kWays; ++w) s += s_sum[w][lane];
+      d_bias[static_cast<int64_t>(g) * Z + c] = s;
+    }
+    __syncthreads();
   }
 }
 
@@ -159,7 +171,7 @@ cudaError_t launch_dz(const DzArgs& a, int num_sms, cudaStream_t stream) {
   const size_t smem = sizeof(int) * (static_cast<size_t>(a.groups.E) + 1);
   const int per_sm = resident_ctas(reinterpret_cast<const void*>(kern), kThreads, smem);
   if (per_sm < 1) return cudaErrorInvalidConfiguration;
-  const int64_t most = max_row_tiles(a.groups) * ((a.N + kSpan - 1) / kSpan);
+  const int64_t most = max_row_tiles(a.groups, kDzRows) * ((a.N + kSpan - 1) / kSpan);
   const int64_t ctas = static_cast<int64_t>(num_sms) * per_sm;
   return launch_chained(kern, dim3(static_cast<unsigned>(most < ctas ? most : ctas)), dim3(kThreads), smem, stream, a);
 }
@@ -221,7 +233,7 @@ cudaError_t launch_product_dz(const ProductGradArgs& p, int num_sms, cudaStream_
   const size_t smem = sizeof(int) * (static_cast<size_t>(p.g.groups.E) + 1);
   const int per_sm = resident_ctas(reinterpret_cast<const void*>(bias_sum_kernel), kThreads, smem);
   if (per_sm < 1) return cudaErrorInvalidConfiguration;
-  const int64_t need = (static_cast<int64_t>(p.g.groups.E) * p.g.Z + kThreads - 1) / kThreads;
+  const int64_t need = static_cast<int64_t>(p.g.groups.E) * ((p.g.Z + 31) / 32);
   const int64_t ctas = static_cast<int64_t>(num_sms) * per_sm;
   return launch_chained(bias_sum_kernel, dim3(static_cast<unsigned>(need < ctas ? need : ctas)), dim3(kThreads), smem,
                         stream, p.g.groups, p.g.Z, static_cast<const float*>(p.part), p.d_bias);

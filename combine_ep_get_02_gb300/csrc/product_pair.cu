@@ -60,9 +60,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   cluster_sync_all();  // both CTAs' barriers and accumulators exist
   tc_fence_after();
   const uint32_t tmem = s_tmem;
-  const Tiles<2 * kBM, kCols> tiles(a.groups, prefix, a.epi.cols);
+  const Tiles<2 * kBM> tiles(a.groups, prefix, a.epi.cols, kCols);
   const int blocks = (a.sum + kBK - 1) / kBK;
-  const int64_t first = blockIdx.x >> 1, step = gridDim.x >> 1;
+  const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
   auto give_up = [&] {
     s_abort = 1;
     atomicOr(a.err, kErrTimeout);
@@ -72,7 +72,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (elect_one()) {
       uint32_t n = 0;  // stages filled so far
       bool ok = true;
-      for (int64_t i = first; ok && i < tiles.total; i += step) {
+      for (int i = first; ok && i < tiles.total; i += step) {
         const Tile t = tiles.at(i);
         for (int kb = 0; kb < blocks; ++kb, ++n) {
           const uint32_t s = n % kStages, bar = cluster_addr(smem_addr(&s_full[s]), 0);
@@ -106,7 +106,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       constexpr uint32_t idesc = idesc_bf16(2 * kBM, kBN, false, kBMn);
       uint32_t n = 0, acc = 0;
       bool ok = true;
-      for (int64_t i = first; ok && i < tiles.total; i += step, ++acc) {
+      for (int i = first; ok && i < tiles.total; i += step, ++acc) {
         const uint32_t b = acc & 1u;
         if (s_abort || !mbar_wait_timed(smem_addr(&s_acc_empty[b]), (acc >> 1 & 1u) ^ 1u)) {
           if (!s_abort) give_up();
@@ -143,7 +143,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int half = (warp - 2) >> 2;
     const uint32_t patch = patch0 + (warp - 2) * kPatchBytes;
     uint32_t acc = 0;
-    for (int64_t i = first; i < tiles.total; i += step, ++acc) {
+    for (int i = first; i < tiles.total; i += step, ++acc) {
       const uint32_t b = acc & 1u;
       const Tile t = tiles.at(i);
       bool ok = s_abort == 0 && mbar_wait_timed(smem_addr(&s_acc_full[b]), acc >> 1 & 1u);
@@ -188,7 +188,7 @@ cudaError_t launch_rows_pair(const uint16_t* A, const uint16_t* B, const RowsArg
   const size_t smem = 1024 + kStages * kStageBytes + kEpilogueWarps * kPatchBytes + sizeof(int) * (static_cast<size_t>(a.groups.E) + 1);
   if (resident_ctas(reinterpret_cast<const void*>(kern), kThreads, smem) < 1) return cudaErrorInvalidConfiguration;
   const int cols = kAct == EP_ACT_SWIGLU ? kBN / 2 : kBN;
-  const int64_t row_tiles = a.groups.rows / (2 * kBM) + (a.groups.count == nullptr ? 1 : a.groups.E);
+  const int64_t row_tiles = max_row_tiles(a.groups, 2 * kBM);
   const int64_t most = row_tiles * ((a.epi.cols + cols - 1) / cols);
   const int64_t pairs = most < num_sms / 2 ? most : num_sms / 2;  // num_sms >= 2
   return launch_chained(kern, dim3(static_cast<unsigned>(2 * pairs)), dim3(kThreads), smem, stream, map_a, map_b, a);

@@ -22,28 +22,27 @@ struct Tile {
   int n0;
 };
 
-// Output tiles of kRows x kCols.
-template <int kRows, int kCols>
+// Output tiles of kRows rows x `width` columns, numbered in 32 bits.
+template <int kRows>
 struct Tiles {
   const Groups& q;
   const int* prefix;  // row tiles (of kRows) before each group
-  int nt;
-  int64_t total;
-  __device__ Tiles(const Groups& groups, const int* p, int cols)
-      : q(groups), prefix(p), nt((cols + kCols - 1) / kCols), total(static_cast<int64_t>(p[groups.E]) * nt) {}
+  int width, nt, total;
+  __device__ Tiles(const Groups& groups, const int* p, int cols, int w)
+      : q(groups), prefix(p), width(w), nt((cols + w - 1) / w), total(p[groups.E] * nt) {}
   // Within a group: bands of kRaster row tiles, columns in turn inside a band, so that the
   // CTAs at work share rows of A and columns of B in L2.
-  __device__ Tile at(int64_t i) const {
-    const int g = group_of_tile(prefix, q.E, static_cast<int>(i / nt));
-    const int mt = prefix[g + 1] - prefix[g];
-    int64_t r = i - static_cast<int64_t>(prefix[g]) * nt;
-    const int band = static_cast<int>(r / (static_cast<int64_t>(kRaster) * nt));
-    r -= static_cast<int64_t>(band) * kRaster * nt;
-    const int height = min(kRaster, mt - band * kRaster);
-    const int n = static_cast<int>(r) / height;
-    const int m = band * kRaster + static_cast<int>(r) - n * height;
+  __device__ Tile at(int i) const {
+    const int g = group_of_tile(prefix, q.E, i / nt);
     const GroupRows rows = group_rows(q, g);
-    return Tile{g, rows.begin + m * kRows, rows.count - m * kRows, n * kCols};
+    const int mt = prefix[g + 1] - prefix[g];
+    int r = i - prefix[g] * nt;
+    const int band = r / (kRaster * nt);
+    r -= band * kRaster * nt;
+    const int height = min(kRaster, mt - band * kRaster);
+    const int n = r / height;
+    const int m = band * kRaster + r - n * height;
+    return Tile{g, rows.begin + m * kRows, rows.count - m * kRows, n * width};
   }
 };
 

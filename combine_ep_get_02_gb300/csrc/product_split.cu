@@ -65,8 +65,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s_tmem;
-  const Tiles<kBM, kCols> tiles(a.groups, prefix, a.epi.cols);
-  const int64_t tile = blockIdx.x / S;
+  const Tiles<kBM> tiles(a.groups, prefix, a.epi.cols, kCols);
+  const int tile = blockIdx.x / S;
   const bool work = tile < tiles.total;  // the same for the whole cluster
   const Tile t = work ? tiles.at(tile) : Tile{0, 0, 0, 0};
   const int blocks = (a.sum + kBK - 1) / kBK, per = (blocks + S - 1) / S;
@@ -237,8 +237,7 @@ template <int kAct, bool kBMn>
 cudaError_t launch_rows_split(const uint16_t* A, const uint16_t* B, const RowsArgs& a, cudaStream_t stream, bool* done) {
   *done = false;
   const int64_t rows = a.groups.rows;
-  const int64_t groups = a.groups.count == nullptr ? 1 : (rows < a.groups.E ? rows : a.groups.E);
-  const int64_t row_tiles = a.groups.count == nullptr ? (rows + kBM - 1) / kBM : rows / kBM + groups;
+  const int64_t row_tiles = a.groups.count == nullptr ? (rows + kBM - 1) / kBM : max_row_tiles(a.groups);
   const int halves = kAct == EP_ACT_SWIGLU ? 2 : 1;
   const int blocks = (a.sum + kBK - 1) / kBK;
   const int64_t wide = row_tiles * ((a.epi.cols + 256 / halves - 1) / (256 / halves));

@@ -101,7 +101,7 @@ def test_product_workspace_closed_forms(ep):
     up = lambda n: (n + 255) // 256 * 256  # noqa: E731
     assert ep.ep_product_workspace_bytes(product_cfg(ep)) == 256
     assert ep.ep_product_workspace_bytes(product_cfg(ep, x_dtype=1)) == 256 + up(100 * 128 * 2)
-    tiles = 100 // 128 + 8
+    tiles = 100 // 64 + 8
     assert ep.ep_product_workspace_bytes(product_cfg(ep), True) == 256 + up(4 * tiles * 64)
     assert ep.ep_product_workspace_bytes(product_cfg(ep, activation=4), True) == 256 + up(100 * 128 * 2) + up(4 * tiles * 128)
 
