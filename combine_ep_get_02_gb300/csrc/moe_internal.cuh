@@ -105,15 +105,19 @@ struct GroupRows {
 };
 
 // A block that leaves the tensor (a layout of another configuration) is cut to it.
-__device__ __forceinline__ GroupRows group_rows(const Groups& q, int g, bool* cut = nullptr) {
-  if (q.count == nullptr) return GroupRows{0, q.rows};
-  const int d = g / q.L, j = g - d * q.L;
-  const int64_t begin = static_cast<int64_t>(__ldg(q.region + d)) + __ldg(q.base + d * (q.L + 1) + j);
-  const int64_t n = __ldg(q.count + g);
-  if (n >= 0 && begin >= 0 && begin + n <= q.rows) return GroupRows{static_cast<int>(begin), static_cast<int>(n)};
-  if (cut != nullptr) *cut = true;
+__device__ __forceinline__ GroupRows clip_rows(const Groups& q, int64_t begin, int n, bool* cut) {
+  if (n >= 0 && begin >= 0 && begin + n <= q.rows) return GroupRows{static_cast<int>(begin), n};
+  *cut = true;
   if (n <= 0 || begin < 0 || begin >= q.rows) return GroupRows{0, 0};
   return GroupRows{static_cast<int>(begin), static_cast<int>(q.rows - begin)};
+}
+__device__ __forceinline__ GroupRows group_rows(const Groups& q, int g, bool* cut = nullptr) {
+  if (q.count == nullptr) return GroupRows{0, q.rows};
+  const int d = g / q.L;  // block g starts at entry g + d of the [R][L+1] block starts
+  bool over = false;
+  const GroupRows r = clip_rows(q, static_cast<int64_t>(__ldg(q.region + d)) + __ldg(q.base + g + d), __ldg(q.count + g), &over);
+  if (over && cut != nullptr) *cut = true;
+  return r;
 }
 
 struct ProductGeometry {

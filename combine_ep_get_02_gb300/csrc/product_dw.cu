@@ -3,17 +3,18 @@
 //
 // Tiles of 256 x 256 of dW, one to a pair of CTAs (a cluster of two) with one tcgen05.mma
 // over both SMs, as in the rows' products; roles as there (a warp for TMA, one for the
-// products, eight for the epilogue). Both operands are MN-major: the summed index is the
+// products, eight for the epilogue), and one that mends the tiles below. Both operands are MN-major: the summed index is the
 // row, so tiles of 64 rows are used as they lie in the tensors, without a transposition.
 //
 // A group's last tile ends inside the next group's rows (or padding). The rows past the
 // group, up to the next multiple of 16 (one instruction's share), are zeroed in shared memory
 // in both operands, so that not even a NaN there reaches the sum; the rest is left out by
 // issuing fewer instructions. Since each CTA must have mended its own half before the
-// pair's product reads it, the loads of such a tile count on the CTA's own barrier; the second
-// CTA's product warp waits for that, mends, and then arrives on a barrier of the first. (All
-// tiles' loads taking that way more than doubled the kernel's time: 285 us against 119 for
-// single CTAs at 4096 x 4096 x 4096.)
+// pair's product reads it, the loads of such a tile count on the CTA's own barrier; a warp of
+// each CTA waits for that, mends, and arrives on a barrier of the first CTA, which its
+// product thread waits for. (All tiles' loads taking that way more than doubled the
+// kernel's time; the product warp mending itself, all its lanes waiting for every tile, cost
+// a fifth: 97 us against 80 at 4096 x 4096 x 4096.)
 // (Single CTAs with tiles of 128 x 256 reached 48% of the tensor cores' time: they want
 // 96 bytes a cycle from L2 where an SM gets about 64.)
 #include "product_common.cuh"
@@ -23,7 +24,7 @@ namespace ep {
 namespace {
 
 constexpr int kEpilogueWarps = 8;
-constexpr int kThreads = 64 + 32 * kEpilogueWarps;
+constexpr int kThreads = 64 + 32 * kEpilogueWarps + 32;
 constexpr int kBM = 128, kBN = 256, kBK = 64;  // rows of dW a CTA, columns a pair, rows of x and dz a stage
 constexpr int kStages = 6;
 constexpr int kPanel = kBK * 128;  // bytes of 64 columns x 64 rows
@@ -43,18 +44,38 @@ struct Tile {
   int g, begin, rows, z0, k0;
 };
 
-__device__ __forceinline__ Tile tile_at(const WeightArgs& a, int i, int total, int mt, int nt) {
-  if (i >= total) return Tile{0, 0, 0, 0, 0};
-  const int g = i / (mt * nt), r = i - g * (mt * nt);
-  const GroupRows rows = group_rows(a.groups, g);
-  const int n = r / mt;
-  return Tile{g, rows.begin, rows.count, (r - n * mt) * 2 * kBM, n * kBN};
+// A tile whose group's place is still on its way from memory: the next one is looked up
+// (and nothing computed from it) while the current one is worked on.
+struct Ahead {
+  int g, r, region, base, count;
+};
+__device__ __forceinline__ Ahead look_up(const WeightArgs& a, int i, int total, int mt, int nt) {
+  Ahead t{0, 0, 0, 0, 0};
+  if (i >= total) return t;
+  t.g = i / (mt * nt);
+  t.r = i - t.g * (mt * nt);
+  const Groups& q = a.groups;
+  if (q.count == nullptr) {
+    t.count = q.rows;
+  } else {
+    const int d = t.g / q.L;
+    t.region = __ldg(q.region + d);
+    t.base = __ldg(q.base + t.g + d);
+    t.count = __ldg(q.count + t.g);
+  }
+  return t;
+}
+__device__ __forceinline__ Tile resolve(const WeightArgs& a, const Ahead& t, int mt) {
+  bool cut = false;
+  const GroupRows rows = clip_rows(a.groups, static_cast<int64_t>(t.region) + t.base, t.count, &cut);
+  const int n = t.r / mt;
+  return Tile{t.g, rows.begin, rows.count, (t.r - n * mt) * 2 * kBM, n * kBN};
 }
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     weight_grad_kernel(const __grid_constant__ CUtensorMap map_dz, const __grid_constant__ CUtensorMap map_x, WeightArgs a) {
   extern __shared__ uint8_t s_raw[];
-  __shared__ __align__(8) uint64_t s_full[kStages], s_empty[kStages], s_part[kStages], s_other[kStages], s_acc_full[2], s_acc_empty[2], s_drained;
+  __shared__ __align__(8) uint64_t s_full[kStages], s_empty[kStages], s_part[kStages], s_mended[kStages], s_acc_full[2], s_acc_empty[2], s_drained;
   __shared__ uint32_t s_tmem;
   __shared__ volatile int s_abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -67,7 +88,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init_count(smem_addr(&s_full[s]), 1);
       mbar_init_count(smem_addr(&s_empty[s]), 1);
       mbar_init_count(smem_addr(&s_part[s]), 1);
-      mbar_init_count(smem_addr(&s_other[s]), 1);
+      mbar_init_count(smem_addr(&s_mended[s]), 2);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init_count(smem_addr(&s_acc_full[i]), 1);
@@ -98,9 +119,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int mt = (a.Z + 2 * kBM - 1) / (2 * kBM), nt = (a.K + kBN - 1) / kBN;
   const int total = a.groups.E * mt * nt;
   const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
-  // the next tile's group is looked up while the current one is worked on: a short group's
-  // products take less time than the lookup
-  Tile ahead = tile_at(a, first, total, mt, nt);
+  Ahead ahead = look_up(a, first, total, mt, nt);
   auto give_up = [&] {
     s_abort = 1;
     atomicOr(a.err, kErrTimeout);
@@ -112,8 +131,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       uint32_t part = 0, full_phase = 0, part_phase = 0;  // bit s: stage s's last use, phases of its barriers
       bool ok = true;
       for (int i = first; ok && i < total; i += step) {
-        const Tile t = ahead;
-        ahead = tile_at(a, i + step, total, mt, nt);
+        const Tile t = resolve(a, ahead, mt);
+        ahead = look_up(a, i + step, total, mt, nt);
         for (int r = 0; r < t.rows; r += kBK, ++n) {
           const uint32_t s = n % kStages, bit = 1u << s;
           if (s_abort || !mbar_wait_timed(smem_addr(&s_empty[s]), (n / kStages & 1u) ^ 1u)) {
@@ -148,76 +167,91 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
     }
   } else if (warp == 1) {
-    constexpr uint32_t idesc = idesc_bf16(2 * kBM, kBN, true, true);
-    uint32_t n = 0, acc = 0;
-    uint32_t full_phase = 0, part_phase = 0;  // bit s: phase of stage s's barriers
-    bool ok = true;
-    auto wait_all = [&](uint32_t bar, uint32_t parity) {  // the whole warp
-      ok = __all_sync(kFullMask, s_abort == 0 && mbar_wait_timed(bar, parity));
-      if (!ok && lane == 0 && !s_abort) give_up();
-      return ok;
-    };
-    for (int i = first; ok && i < total; i += step) {
-      const Tile t = ahead;
-      ahead = tile_at(a, i + step, total, mt, nt);
-      if (t.rows == 0) continue;
-      const uint32_t b = acc & 1u;
-      if (rank == 0 && !wait_all(smem_addr(&s_acc_empty[b]), (acc >> 1 & 1u) ^ 1u)) break;
-      tc_fence_after();
-      const uint32_t d = tmem + b * kBN;
-      for (int r = 0; r < t.rows; r += kBK, ++n) {
-        const uint32_t s = n % kStages, bit = 1u << s;
-        const int left = min(kBK, t.rows - r);  // rows of this tile that count
-        const int used = (left + 15) & ~15;     // rows the instructions read
-        if (to_mend(t.rows - r)) {
-          const uint32_t phase = part_phase >> s & 1u;
-          part_phase ^= bit;
-          if (!wait_all(smem_addr(&s_part[s]), phase)) break;
-          // a 128-byte row of a panel holds one row's 64 columns, in whatever order
-          const int chunks = (used - left) * 8;
-          uint8_t* base = stage_mem + s * kStageBytes + left * 128;
-          for (int p = 0; p < kStageBytes / kPanel; ++p)
-            for (int c = lane; c < chunks; c += 32)
-              *reinterpret_cast<uint4*>(base + p * kPanel + c * 16) = make_uint4(0u, 0u, 0u, 0u);
-          fence_async_shared();
-          __syncwarp();
-          if (rank != 0) {
-            if (lane == 0) mbar_arrive_cluster(cluster_addr(smem_addr(&s_other[s]), 0));
-            __syncwarp();
-            continue;
-          }
-          if (!wait_all(smem_addr(&s_other[s]), phase)) break;
-        } else {
-          if (rank != 0) continue;
-          const uint32_t phase = full_phase >> s & 1u;
-          full_phase ^= bit;
-          if (!wait_all(smem_addr(&s_full[s]), phase)) break;
+    if (rank == 0 && elect_one()) {
+      constexpr uint32_t idesc = idesc_bf16(2 * kBM, kBN, true, true);
+      uint32_t n = 0, acc = 0;
+      uint32_t full_phase = 0, mended_phase = 0;  // bit s: phase of stage s's barriers
+      bool ok = true;
+      for (int i = first; ok && i < total; i += step) {
+        const Tile t = resolve(a, ahead, mt);
+        ahead = look_up(a, i + step, total, mt, nt);
+        if (t.rows == 0) continue;
+        const uint32_t b = acc & 1u;
+        if (s_abort || !mbar_wait_timed(smem_addr(&s_acc_empty[b]), (acc >> 1 & 1u) ^ 1u)) {
+          if (!s_abort) give_up();
+          ok = false;
+          break;
         }
         tc_fence_after();
-        if (elect_one()) {  // the same lane each time
+        const uint32_t d = tmem + b * kBN;
+        for (int r = 0; r < t.rows; r += kBK, ++n) {
+          const uint32_t s = n % kStages, bit = 1u << s;
+          uint32_t bar, phase;
+          if (to_mend(t.rows - r)) {
+            bar = smem_addr(&s_mended[s]);
+            phase = mended_phase >> s & 1u;
+            mended_phase ^= bit;
+          } else {
+            bar = smem_addr(&s_full[s]);
+            phase = full_phase >> s & 1u;
+            full_phase ^= bit;
+          }
+          if (s_abort || !mbar_wait_timed(bar, phase)) {
+            if (!s_abort) give_up();
+            ok = false;
+            break;
+          }
+          tc_fence_after();
           const uint32_t sa = stage0 + s * kStageBytes, sb = sa + kABytes;
           const uint64_t da = desc_mn_major(sa, kPanel), db = desc_mn_major(sb, kPanel);
+          const int left = t.rows - r;
 #pragma unroll
           for (int k = 0; k < kBK / 16; ++k)
-            if (k * 16 < used) mma_bf16_pair(d, da + k * kStepMN, db + k * kStepMN, idesc, r > 0 || k > 0);
+            if (k * 16 < left) mma_bf16_pair(d, da + k * kStepMN, db + k * kStepMN, idesc, r > 0 || k > 0);
           mma_commit_pair(smem_addr(&s_empty[s]));
-          if (r + kBK >= t.rows) mma_commit_pair(smem_addr(&s_acc_full[b]));
         }
-        __syncwarp();
+        if (ok) mma_commit_pair(smem_addr(&s_acc_full[b]));
+        ++acc;
       }
-      ++acc;
+      if (!ok) {  // the products in flight finish before the CTAs' memory goes
+        mma_commit_pair(smem_addr(&s_drained));
+        mbar_wait_timed(smem_addr(&s_drained), 0);
+      }
     }
-    if (!ok && rank == 0 && elect_one()) {  // the products in flight finish before the CTAs' memory goes
-      mma_commit_pair(smem_addr(&s_drained));
-      mbar_wait_timed(smem_addr(&s_drained), 0);
+  } else if (warp == 2 + kEpilogueWarps) {
+    uint32_t n = 0, part_phase = 0;
+    bool ok = true;
+    for (int i = first; ok && i < total; i += step) {
+      const Tile t = resolve(a, ahead, mt);
+      ahead = look_up(a, i + step, total, mt, nt);
+      const int stages = (t.rows + kBK - 1) / kBK;
+      n += static_cast<uint32_t>(stages);
+      const int left = t.rows - (stages - 1) * kBK;  // rows of the last stage that count
+      if (stages == 0 || !to_mend(left)) continue;
+      const uint32_t s = (n - 1) % kStages;
+      ok = __all_sync(kFullMask, s_abort == 0 && mbar_wait_timed(smem_addr(&s_part[s]), part_phase >> s & 1u));
+      if (!ok) {
+        if (lane == 0 && !s_abort) give_up();
+        break;
+      }
+      part_phase ^= 1u << s;
+      // a 128-byte row of a panel holds one row's 64 columns, in whatever order
+      const int chunks = (((left + 15) & ~15) - left) * 8;
+      uint8_t* base = stage_mem + s * kStageBytes + left * 128;
+      for (int p = 0; p < kStageBytes / kPanel; ++p)
+        for (int c = lane; c < chunks; c += 32)
+          *reinterpret_cast<uint4*>(base + p * kPanel + c * 16) = make_uint4(0u, 0u, 0u, 0u);
+      fence_async_shared();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(cluster_addr(smem_addr(&s_mended[s]), 0));
     }
   } else {
     const int quarter = warp & 3, half = (warp - 2) >> 2;
     const uint32_t patch = patch0 + (warp - 2) * kPatchBytes;
     uint32_t acc = 0;
     for (int i = first; i < total; i += step) {
-      const Tile t = ahead;
-      ahead = tile_at(a, i + step, total, mt, nt);
+      const Tile t = resolve(a, ahead, mt);
+      ahead = look_up(a, i + step, total, mt, nt);
       const uint32_t b = acc & 1u;
       const int z0 = t.z0 + rank * kBM + quarter * 32;
       uint16_t* out = a.out + (static_cast<int64_t>(t.g) * a.Z + z0) * a.K + t.k0;
