@@ -33,7 +33,6 @@ constexpr int kABytes = kBM * kBK * 2, kBBytes = kBN / 2 * kBK * 2, kStageBytes 
 struct WeightArgs {
   Groups groups;
   int Z, K;
-  uint16_t* out;  // [E][Z][K]
   uint32_t* err;
 };
 
@@ -73,7 +72,8 @@ __device__ __forceinline__ Tile resolve(const WeightArgs& a, const Ahead& t, int
 }
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-    weight_grad_kernel(const __grid_constant__ CUtensorMap map_dz, const __grid_constant__ CUtensorMap map_x, WeightArgs a) {
+    weight_grad_kernel(const __grid_constant__ CUtensorMap map_dz, const __grid_constant__ CUtensorMap map_x,
+                       const __grid_constant__ CUtensorMap map_out, WeightArgs a) {
   extern __shared__ uint8_t s_raw[];
   __shared__ __align__(8) uint64_t s_full[kStages], s_empty[kStages], s_part[kStages], s_mended[kStages], s_acc_full[2], s_acc_empty[2], s_drained;
   __shared__ uint32_t s_tmem;
@@ -99,6 +99,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     fence_barrier_init();
     tma_prefetch_map(&map_dz);
     tma_prefetch_map(&map_x);
+    tma_prefetch_map(&map_out);
   }
   if (warp == 2) {
     tmem_alloc_pair(smem_addr(&s_tmem), 512);
@@ -247,14 +248,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
   } else {
     const int quarter = warp & 3, half = (warp - 2) >> 2;
-    const uint32_t patch = patch0 + (warp - 2) * kPatchBytes;
+    const uint32_t patch = patch0 + (warp - 2) * 2 * kPatchBytes;
+    uint32_t stored = 0;  // chunks handed to TMA; two patches in turn
     uint32_t acc = 0;
     for (int i = first; i < total; i += step) {
       const Tile t = resolve(a, ahead, mt);
       ahead = look_up(a, i + step, total, mt, nt);
       const uint32_t b = acc & 1u;
       const int z0 = t.z0 + rank * kBM + quarter * 32;
-      uint16_t* out = a.out + (static_cast<int64_t>(t.g) * a.Z + z0) * a.K + t.k0;
       if (t.rows > 0) {
         bool ok = s_abort == 0 && mbar_wait_timed(smem_addr(&s_acc_full[b]), acc >> 1 & 1u);
         ok = __all_sync(kFullMask, ok);
@@ -275,7 +276,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int j = 0; j < 32; ++j) v[j] = 0.f;
         }
-        store_rows(patch, v, out + c, a.K, a.Z - z0, a.K - t.k0 - c, lane);
+        // the last but one store from this patch has been read by now, or is waited for
+        if (lane == 0) tma_store_wait_reads<1>();
+        __syncwarp();
+        const uint32_t at = patch + (stored++ & 1u) * kPatchBytes;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) st_shared16(patch_at(at, lane, j), pack8(v + 8 * j));
+        fence_async_shared();
+        __syncwarp();
+        if (lane == 0) {  // what lies past Z or K is not written
+          tma_store_3d(&map_out, t.k0 + c, z0, t.g, at);
+          bulk_commit();
+        }
       }
       if (t.rows > 0) {
         tc_fence_before();
@@ -284,6 +296,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         ++acc;
       }
     }
+    if (lane == 0) bulk_wait_all();
   }
   __syncwarp();
   __syncthreads();
@@ -296,22 +309,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
 cudaError_t launch_product_dw(const ProductGradArgs& p, int num_sms, cudaStream_t stream) {
   const uint16_t* dz = p.dz != nullptr ? p.dz : p.d_out;
-  WeightArgs a = {p.g.groups, p.g.Z, p.g.K, p.d_weight, p.err};
-  CUtensorMap map_dz, map_x;
+  WeightArgs a = {p.g.groups, p.g.Z, p.g.K, p.err};
+  CUtensorMap map_dz, map_x, map_out;
   const uint32_t box[2] = {64, kBK};
   const uint64_t size_dz[2] = {static_cast<uint64_t>(a.Z), static_cast<uint64_t>(a.groups.rows)};
   const uint64_t size_x[2] = {static_cast<uint64_t>(a.K), static_cast<uint64_t>(a.groups.rows)};
   cudaError_t st = make_tensor_map(&map_dz, dz, 2, size_dz, box);
   if (st == cudaSuccess) st = make_tensor_map(&map_x, p.x, 2, size_x, box);
+  const uint64_t size_out[3] = {static_cast<uint64_t>(a.K), static_cast<uint64_t>(a.Z), static_cast<uint64_t>(a.groups.E)};
+  const uint32_t box_out[3] = {32, 32, 1};
+  if (st == cudaSuccess) st = make_tensor_map(&map_out, p.d_weight, 3, size_out, box_out);
   if (st != cudaSuccess) return st;
-  const size_t smem = 1024 + kStages * kStageBytes + kEpilogueWarps * kPatchBytes;
+  const size_t smem = 1024 + kStages * kStageBytes + 2 * kEpilogueWarps * kPatchBytes;
   if (resident_ctas(reinterpret_cast<const void*>(weight_grad_kernel), kThreads, smem) < 1)
     return cudaErrorInvalidConfiguration;
   const int64_t total =
       static_cast<int64_t>(a.groups.E) * ((a.Z + 2 * kBM - 1) / (2 * kBM)) * ((a.K + kBN - 1) / kBN);
   const int64_t pairs = num_sms < 4 ? 1 : num_sms / 2;
   const unsigned grid = static_cast<unsigned>(2 * (total < pairs ? total : pairs));
-  return launch_chained(weight_grad_kernel, dim3(grid), dim3(kThreads), smem, stream, map_dz, map_x, a);
+  return launch_chained(weight_grad_kernel, dim3(grid), dim3(kThreads), smem, stream, map_dz, map_x,
+                        map_out, a);
 }
 
 }  // namespace ep

@@ -77,6 +77,22 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
       "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
       : "memory");
 }
+// stores of tiles in shared memory; the issuing thread's groups as for bulk copies
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, int x, int y, uint32_t src) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(map), "r"(x), "r"(y),
+               "r"(src)
+               : "memory");
+}
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, int x, int y, int z, uint32_t src) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map), "r"(x),
+               "r"(y), "r"(z), "r"(src)
+               : "memory");
+}
+// all but the last N committed stores have finished reading shared memory
+template <int N>
+__device__ __forceinline__ void tma_store_wait_reads() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
 __device__ __forceinline__ void tma_prefetch_map(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
@@ -220,8 +236,9 @@ constexpr uint32_t idesc_bf16(int m, int n, bool a_mn, bool b_mn) {
 
 // ---- tensor maps (host) -----------------------------------------------------------
 
-// A bf16 tensor of `dims` dimensions (innermost first, dense), read in boxes with the
-// 128-byte swizzle; elements outside read as zero.
+// A bf16 tensor of `dims` dimensions (innermost first, dense), moved in boxes whose rows
+// are 128 bytes with the 128-byte swizzle, or 64 with the 64-byte one; elements outside
+// read as zero and are not written.
 cudaError_t make_tensor_map(CUtensorMap* map, const void* base, int dims, const uint64_t* size, const uint32_t* box);
 
 }  // namespace ep
