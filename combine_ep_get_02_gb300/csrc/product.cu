@@ -4,7 +4,7 @@
 // (forward: A = x, B = W), or plain (gradient of the rows: A = dz, B = W transposed, read
 // in place as an MN-major operand).
 //
-// A CTA per SM walks over output tiles of 128 rows x 256 columns. Warp 0 brings tiles
+// A CTA per SM walks over output tiles of 128 rows x 256 columns (128 or 64 when there are few). Warp 0 brings tiles
 // of A and B (64 of the summed index at a time) into a ring of shared-memory stages by
 // TMA, one thread of warp 1 issues tcgen05.mma into one of two TMEM accumulators, and
 // warps 2-9 take the other accumulator through the epilogue meanwhile. Row tiles start
@@ -21,26 +21,35 @@ namespace ep {
 namespace {
 
 constexpr int kThreads = kRowsThreadsTc;
-constexpr int kBM = kTileRows, kBN = 256;
-constexpr int kStages = 4;
-constexpr int kABytes = kBM * kBK * 2, kBBytes = kBN * kBK * 2, kStageBytes = kABytes + kBBytes;
+constexpr int kBM = kTileRows, kMaxBN = 256;
+constexpr int kLowRows = 32;  // tiles with no more rows read that many of A
+constexpr int kABytes = kBM * kBK * 2;
+constexpr int kRingBytes = 196608, kMaxStages = 8;
+
+__host__ __device__ constexpr int stage_bytes(int bn) { return kABytes + bn * kBK * 2; }
+__host__ __device__ constexpr int stage_count(int bn) {
+  return kRingBytes / stage_bytes(bn) < kMaxStages ? kRingBytes / stage_bytes(bn) : kMaxStages;
+}
 
 template <int kAct, bool kBMn>
 __global__ void __launch_bounds__(kThreads, 1)
-    rows_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, RowsArgs a) {
+    rows_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_low,
+                const __grid_constant__ CUtensorMap map_b, RowsArgs a, int bn) {
   constexpr bool kGated = kAct == EP_ACT_SWIGLU;
-  constexpr int kCols = kGated ? kBN / 2 : kBN;  // output columns of a tile
+  const int cols = kGated ? bn / 2 : bn;  // output columns of a tile
+  const int b_bytes = bn * kBK * 2;
+  const uint32_t kStages = static_cast<uint32_t>(stage_count(bn)), kStageBytes = static_cast<uint32_t>(stage_bytes(bn));
   extern __shared__ uint8_t s_raw[];
-  __shared__ __align__(8) uint64_t s_full[kStages], s_empty[kStages], s_acc_full[2], s_acc_empty[2], s_drained;
+  __shared__ __align__(8) uint64_t s_full[kMaxStages], s_empty[kMaxStages], s_acc_full[2], s_acc_empty[2], s_drained;
   __shared__ uint32_t s_tmem;
   __shared__ volatile int s_abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t stage0 = (smem_addr(s_raw) + 1023u) & ~1023u;
-  const uint32_t patch0 = stage0 + kStages * kStageBytes;
+  const uint32_t patch0 = stage0 + kRingBytes;
   int* prefix = reinterpret_cast<int*>(s_raw + (patch0 - smem_addr(s_raw)) + kEpilogueWarps * kPatchBytes);
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
+    for (int s = 0; s < kMaxStages; ++s) {
       mbar_init_count(smem_addr(&s_full[s]), 1);
       mbar_init_count(smem_addr(&s_empty[s]), 1);
     }
@@ -52,6 +61,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     s_abort = 0;
     fence_barrier_init();
     tma_prefetch_map(&map_a);
+    tma_prefetch_map(&map_low);
     tma_prefetch_map(&map_b);
   }
   if (warp == 2) {
@@ -65,7 +75,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s_tmem;
-  const Tiles<kBM> tiles(a.groups, prefix, a.epi.cols, kCols);
+  const Tiles<kBM> tiles(a.groups, prefix, a.epi.cols, cols);
   const int blocks = (a.sum + kBK - 1) / kBK;
   auto give_up = [&] {
     s_abort = 1;
@@ -78,6 +88,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       for (int i = blockIdx.x; ok && i < tiles.total; i += gridDim.x) {
         const Tile t = tiles.at(i);
+        const bool low = t.rows <= kLowRows;
+        const uint32_t bytes = static_cast<uint32_t>(b_bytes + (low ? kLowRows * kBK * 2 : kABytes));
         for (int kb = 0; kb < blocks; ++kb, ++n) {
           const uint32_t s = n % kStages, bar = smem_addr(&s_full[s]);
           if (s_abort || !mbar_wait_timed(smem_addr(&s_empty[s]), (n / kStages & 1u) ^ 1u)) {
@@ -85,16 +97,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = false;
             break;
           }
-          mbar_expect(bar, kStageBytes);
+          mbar_expect(bar, bytes);
           const uint32_t sa = stage0 + s * kStageBytes, sb = sa + kABytes;
-          tma_load_2d(sa, &map_a, kb * kBK, t.begin, bar);
+          tma_load_2d(sa, low ? &map_low : &map_a, kb * kBK, t.begin, bar);
           if constexpr (kBMn) {
-#pragma unroll
-            for (int p = 0; p < kBN / 64; ++p)
+            for (int p = 0; p < bn / 64; ++p)
               tma_load_3d(sb + p * (kBK * 128), &map_b, t.n0 + p * 64, kb * kBK, t.g, bar);
           } else {
             tma_load_3d(sb, &map_b, kb * kBK, t.n0, t.g, bar);
-            tma_load_3d(sb + kBBytes / 2, &map_b, kb * kBK, kGated ? a.epi.cols + t.n0 : t.n0 + kBN / 2, t.g, bar);
+            tma_load_3d(sb + b_bytes / 2, &map_b, kb * kBK, kGated ? a.epi.cols + t.n0 : t.n0 + bn / 2, t.g, bar);
           }
         }
       }
@@ -106,7 +117,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 1) {
     if (elect_one()) {
-      constexpr uint32_t idesc = idesc_bf16(kBM, kBN, false, kBMn);
+      const uint32_t idesc = idesc_bf16(kBM, bn, false, kBMn);
       uint32_t n = 0, acc = 0;
       bool ok = true;
       for (int i = blockIdx.x; ok && i < tiles.total; i += gridDim.x, ++acc) {
@@ -117,7 +128,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         tc_fence_after();
-        const uint32_t d = tmem + b * kBN;
+        const uint32_t d = tmem + b * kMaxBN;
         for (int kb = 0; kb < blocks; ++kb, ++n) {
           const uint32_t s = n % kStages;
           if (s_abort || !mbar_wait_timed(smem_addr(&s_full[s]), n / kStages & 1u)) {
@@ -159,12 +170,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int m = quarter * 32;
       const int64_t row = static_cast<int64_t>(t.begin) + m;
       const int rows = t.rows - m;
-      const uint32_t d = tmem + b * kBN + (static_cast<uint32_t>(m) << 16);
-      for (int c = half * (kCols / 2); c < (half + 1) * (kCols / 2); c += 32) {
+      const uint32_t d = tmem + b * kMaxBN + (static_cast<uint32_t>(m) << 16);
+      for (int c = half * 32; c < cols; c += 64) {
         if (rows <= 0 || t.n0 + c >= a.epi.cols) break;
         float v[32], u[kGated ? 32 : 1];
         tmem_ld32(d + c, v);
-        if constexpr (kGated) tmem_ld32(d + kCols + c, u);
+        if constexpr (kGated) tmem_ld32(d + cols + c, u);
         tmem_ld_wait();
         finish_rows<kAct>(a.epi, patch, v, u, t.g, row, rows, t.n0 + c, lane);
       }
@@ -183,16 +194,25 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 template <int kAct, bool kBMn>
 cudaError_t launch_rows_single(const uint16_t* A, const uint16_t* B, const RowsArgs& a, int num_sms, cudaStream_t stream) {
-  CUtensorMap map_a, map_b;
-  const cudaError_t st = make_rows_maps<kBMn>(&map_a, &map_b, A, B, a, kBM, kBN / 2);
+  // The widest tile that still gives every SM one: with fewer tiles than SMs it is reading B
+  // that counts, and more CTAs read it faster (48 experts with a few rows each, 4376 -> 256:
+  // 256 columns 50 us).
+  const int halves = kAct == EP_ACT_SWIGLU ? 2 : 1;
+  auto tiles = [&](int bn) { return max_row_tiles(a.groups) * ((a.epi.cols + bn / halves - 1) / (bn / halves)); };
+  int bn = kMaxBN;
+  while (bn > 64 && tiles(bn) < num_sms) bn /= 2;
+  CUtensorMap map_a, map_low, map_b;
+  cudaError_t st = make_rows_maps<kBMn>(&map_a, &map_b, A, B, a, kBM, bn / 2);
+  if (st != cudaSuccess) return st;
+  const uint64_t size[2] = {static_cast<uint64_t>(a.sum), static_cast<uint64_t>(a.groups.rows)};
+  const uint32_t box[2] = {kBK, kLowRows};
+  st = make_tensor_map(&map_low, A, 2, size, box);
   if (st != cudaSuccess) return st;
   auto kern = rows_kernel<kAct, kBMn>;
-  const size_t smem = 1024 + kStages * kStageBytes + kEpilogueWarps * kPatchBytes + sizeof(int) * (static_cast<size_t>(a.groups.E) + 1);
+  const size_t smem = 1024 + kRingBytes + kEpilogueWarps * kPatchBytes + sizeof(int) * (static_cast<size_t>(a.groups.E) + 1);
   if (resident_ctas(reinterpret_cast<const void*>(kern), kThreads, smem) < 1) return cudaErrorInvalidConfiguration;
-  const int cols = kAct == EP_ACT_SWIGLU ? kBN / 2 : kBN;
-  const int64_t most = max_row_tiles(a.groups) * ((a.epi.cols + cols - 1) / cols);
-  const unsigned grid = static_cast<unsigned>(most < num_sms ? most : num_sms);
-  return launch_chained(kern, dim3(grid), dim3(kThreads), smem, stream, map_a, map_b, a);
+  const unsigned grid = static_cast<unsigned>(tiles(bn) < num_sms ? tiles(bn) : num_sms);
+  return launch_chained(kern, dim3(grid), dim3(kThreads), smem, stream, map_a, map_low, map_b, a, bn);
 }
 #define X(act, mn) \
   template cudaError_t launch_rows_single<act, mn>(const uint16_t*, const uint16_t*, const RowsArgs&, int, cudaStream_t);

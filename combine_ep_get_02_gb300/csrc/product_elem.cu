@@ -8,41 +8,51 @@ namespace {
 
 constexpr int kThreads = 256;
 
+__device__ __forceinline__ void st32(void* p, const uint4& a, const uint4& b) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w),
+               "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+               : "memory");
+}
+
 // FP8 rows -> bf16: bf16_rn(code * scale), one scale per 128 columns (fp32, or a
-// power of two packed four to a word). A thread takes 16 columns: 16 bytes in, 32 out.
-// Rows past the last region are not part of any block and are left out.
+// power of two packed four to a word). A warp takes 2048 columns of a row, a lane 16 at a
+// time: 16 bytes in, 32 out. Rows past the last region are not part of any block and are left out.
 __global__ void __launch_bounds__(kThreads)
     dequant_kernel(const uint8_t* x, const float* x_sf, uint16_t* out, int rows, int K, int sf_pack, const int32_t* total) {
   pdl_launch_dependents();
   pdl_wait();
   if (total != nullptr) rows = max(0, min(rows, __ldg(total)));
-  const int units = K >> 4, G = K >> 7, SW = sf_pack ? (G + 3) >> 2 : G;
-  const int64_t all = static_cast<int64_t>(rows) * units;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < all;
-       i += static_cast<int64_t>(gridDim.x) * kThreads) {
-    const int64_t r = i / units;
-    const int u = static_cast<int>(i - r * units), grp = u >> 3;
-    float sf;
-    if (sf_pack) {
-      const uint32_t w = __float_as_uint(__ldg(x_sf + r * SW + (grp >> 2)));
-      const uint32_t e = w >> (8 * (grp & 3)) & 0xFFu;
-      sf = e ? __uint_as_float(e << 23) : __uint_as_float(0x00400000u);  // 2^(e-127)
-    } else {
-      sf = __ldg(x_sf + r * SW + grp);
-    }
-    const uint4 v = ld_stream16(x + r * K + u * 16);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    float f[16];
+  const int G = K >> 7, SW = sf_pack ? (G + 3) >> 2 : G, lane = threadIdx.x & 31;
+  const int warps = gridDim.x * (kThreads / 32), spans = (K + 2047) / 2048;
+  const int units = rows * spans;  // their bytes fit memory, so their number fits 32 bits
+  for (int u = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); u < units; u += warps) {
+    const int r = u / spans, c0 = (u - r * spans) * 2048;
+    const uint8_t* in = x + static_cast<int64_t>(r) * K;
+    uint16_t* to = out + static_cast<int64_t>(r) * K;
+    const float* sfs = x_sf + static_cast<int64_t>(r) * SW;
+#pragma unroll 4
+    for (int c = c0 + lane * 16; c < min(K, c0 + 2048); c += 512) {
+      const int grp = c >> 7;
+      float sf;
+      if (sf_pack) {
+        const uint32_t e = __float_as_uint(__ldg(sfs + (grp >> 2))) >> (8 * (grp & 3)) & 0xFFu;
+        sf = e ? __uint_as_float(e << 23) : __uint_as_float(0x00400000u);  // 2^(e-127)
+      } else {
+        sf = __ldg(sfs + grp);
+      }
+      const uint4 v = ld_stream16(in + c);
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+      float f[16];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const __nv_fp8x2_storage_t p = static_cast<__nv_fp8x2_storage_t>(w[j >> 1] >> (16 * (j & 1)) & 0xFFFFu);
-      const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(p, __NV_E4M3);  // exact
-      const float2 q = __half22float2(*reinterpret_cast<const __half2*>(&h));
-      f[2 * j] = q.x * sf;
-      f[2 * j + 1] = q.y * sf;
+      for (int j = 0; j < 8; ++j) {
+        const __nv_fp8x2_storage_t p = static_cast<__nv_fp8x2_storage_t>(w[j >> 1] >> (16 * (j & 1)) & 0xFFFFu);
+        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(p, __NV_E4M3);  // exact
+        const float2 q = __half22float2(*reinterpret_cast<const __half2*>(&h));
+        f[2 * j] = q.x * sf;
+        f[2 * j + 1] = q.y * sf;
+      }
+      st32(to + c, pack8(f), pack8(f + 8));  // a whole sector: two 16-byte stores took half as long again
     }
-    st16(out + r * K + u * 16, pack8(f));
-    st16(out + r * K + u * 16 + 8, pack8(f + 8));
   }
 }
 
@@ -213,7 +223,7 @@ cudaError_t launch_dequant(const ProductGeometry& g, const uint8_t* x, const flo
                            cudaStream_t stream) {
   const int per_sm = resident_ctas(reinterpret_cast<const void*>(dequant_kernel), kThreads, 0);
   if (per_sm < 1) return cudaErrorInvalidConfiguration;
-  const int64_t need = (static_cast<int64_t>(g.groups.rows) * (g.K >> 4) + kThreads - 1) / kThreads;
+  const int64_t need = (static_cast<int64_t>(g.groups.rows) * ((g.K + 2047) / 2048) + kThreads / 32 - 1) / (kThreads / 32);
   const int64_t ctas = static_cast<int64_t>(num_sms) * per_sm;
   const int32_t* total = g.groups.region == nullptr ? nullptr : g.groups.region + g.groups.E / g.groups.L;
   return launch_chained(dequant_kernel, dim3(static_cast<unsigned>(need < ctas ? need : ctas)), dim3(kThreads), 0, stream,

@@ -1,4 +1,4 @@
-// The rows' products with pairs of CTAs: tiles of 256 rows x 256 columns, one tcgen05.mma
+// The rows' products with pairs of CTAs: tiles of 256 rows x up to 256 columns, one tcgen05.mma
 // over both SMs of a cluster of two. Each CTA brings its 128 rows of A and its half of B's
 // columns, so B crosses from L2 once for 256 rows instead of once for 128, and a
 // stage is 32 KB instead of 48, which makes room for six. (L2 gives an SM about 64 bytes a
@@ -14,15 +14,17 @@ namespace ep {
 namespace {
 
 constexpr int kThreads = kRowsThreadsTc;
-constexpr int kBM = kTileRows, kBN = 256;  // rows a CTA, columns a pair
+constexpr int kBM = kTileRows, kBN = 256;  // rows a CTA, columns a pair at most
 constexpr int kStages = 6;
 constexpr int kABytes = kBM * kBK * 2, kBBytes = kBN / 2 * kBK * 2, kStageBytes = kABytes + kBBytes;
 
 template <int kAct, bool kBMn>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-    rows_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, RowsArgs a) {
+    rows_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, RowsArgs a, int bn) {
   constexpr bool kGated = kAct == EP_ACT_SWIGLU;
-  constexpr int kCols = kGated ? kBN / 2 : kBN;  // output columns of a tile
+  const int cols = kGated ? bn / 2 : bn;  // output columns of a tile
+  const int panels = (bn / 2 + 63) / 64;  // of B's half, MN-major
+  const uint32_t bytes = static_cast<uint32_t>(kABytes + (kBMn ? panels * (kBK * 128) : bn / 2 * kBK * 2));
   extern __shared__ uint8_t s_raw[];
   __shared__ __align__(8) uint64_t s_full[kStages], s_empty[kStages], s_acc_full[2], s_acc_empty[2], s_drained;
   __shared__ uint32_t s_tmem;
@@ -60,7 +62,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   cluster_sync_all();  // both CTAs' barriers and accumulators exist
   tc_fence_after();
   const uint32_t tmem = s_tmem;
-  const Tiles<2 * kBM> tiles(a.groups, prefix, a.epi.cols, kCols);
+  const Tiles<2 * kBM> tiles(a.groups, prefix, a.epi.cols, cols);
   const int blocks = (a.sum + kBK - 1) / kBK;
   const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
   auto give_up = [&] {
@@ -81,16 +83,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             ok = false;
             break;
           }
-          if (rank == 0) mbar_expect(smem_addr(&s_full[s]), 2 * kStageBytes);
+          if (rank == 0) mbar_expect(smem_addr(&s_full[s]), 2 * bytes);
           const uint32_t sa = stage0 + s * kStageBytes, sb = sa + kABytes;
           tma_load_2d_pair(sa, &map_a, kb * kBK, t.begin + static_cast<int>(rank) * kBM, bar);
           if constexpr (kBMn) {
-#pragma unroll
-            for (int p = 0; p < kBN / 128; ++p)
-              tma_load_3d_pair(sb + p * (kBK * 128), &map_b, t.n0 + static_cast<int>(rank) * (kBN / 2) + p * 64, kb * kBK,
+            for (int p = 0; p < panels; ++p)
+              tma_load_3d_pair(sb + p * (kBK * 128), &map_b, t.n0 + static_cast<int>(rank) * (bn / 2) + p * 64, kb * kBK,
                                t.g, bar);
           } else {
-            const int second = kGated ? a.epi.cols : kBN / 2;
+            const int second = kGated ? a.epi.cols : bn / 2;
             tma_load_3d_pair(sb, &map_b, kb * kBK, t.n0 + (rank ? second : 0), t.g, bar);
           }
         }
@@ -103,7 +104,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 1) {
     if (rank == 0 && elect_one()) {
-      constexpr uint32_t idesc = idesc_bf16(2 * kBM, kBN, false, kBMn);
+      const uint32_t idesc = idesc_bf16(2 * kBM, bn, false, kBMn);
       uint32_t n = 0, acc = 0;
       bool ok = true;
       for (int i = first; ok && i < tiles.total; i += step, ++acc) {
@@ -157,13 +158,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int rows = t.rows - static_cast<int>(rank) * kBM - m;
       const int64_t row = static_cast<int64_t>(t.begin) + static_cast<int>(rank) * kBM + m;
       const uint32_t d = tmem + b * kBN + (static_cast<uint32_t>(m) << 16);
-      for (int c = half * (kCols / 2); c < (half + 1) * (kCols / 2); c += 32) {
+      for (int c = half * 32; c < cols; c += 64) {
         if (rows <= 0 || t.n0 + c >= a.epi.cols) break;
         float v[32], u[kGated ? 32 : 1];
         tmem_ld32(d + c, v);
-        if constexpr (kGated) tmem_ld32(d + kCols + c, u);
+        if constexpr (kGated) tmem_ld32(d + cols + c, u);
         tmem_ld_wait();
-        finish_rows<kAct>(a.epi, patch, v, u, t.g, row, rows, t.n0 + c, lane);
+        finish_rows<kAct>(a.epi, patch, v, u, t.g, row, rows, t.n0 + c, lane, min(32, cols - c));
       }
       tc_fence_before();
       __syncwarp();
@@ -181,17 +182,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
 template <int kAct, bool kBMn>
 cudaError_t launch_rows_pair(const uint16_t* A, const uint16_t* B, const RowsArgs& a, int num_sms, cudaStream_t stream) {
+  // Tile width: a narrower tile can fill the last round of tiles better. The time of a width is
+  // taken as rounds x cycles of a block of the summed index: 2 a column, or its bytes at the
+  // 64 a cycle that L2 gives. (1613 rows, 1152 -> 3064: 256 columns 21.7 us, the 192 taken here
+  // 18.2. MN-major tiles load whole panels of 64, so 224 columns of them gain nothing.)
+  const int halves = kAct == EP_ACT_SWIGLU ? 2 : 1;
+  const int64_t row_tiles = a.groups.count == nullptr ? (a.groups.rows + 2 * kBM - 1) / (2 * kBM)
+                                                      : a.groups.rows / (2 * kBM) + (a.groups.E + 1) / 2;
+  int bn = kBN;
+  int64_t least = INT64_MAX;
+  for (int w = kBN; w >= 128; w -= 32) {
+    const int64_t rounds = (row_tiles * ((a.epi.cols + w / halves - 1) / (w / halves)) + num_sms / 2 - 1) / (num_sms / 2);
+    const int loaded = kBMn ? (w / 2 + 63) / 64 * 64 : w / 2;
+    const int64_t cycles = 2 * w > (kABytes + 128 * loaded) / 64 ? 2 * w : (kABytes + 128 * loaded) / 64;
+    if (rounds * cycles < least) least = rounds * cycles, bn = w;
+  }
   CUtensorMap map_a, map_b;
-  const cudaError_t st = make_rows_maps<kBMn>(&map_a, &map_b, A, B, a, kBM, kBN / 2);
+  const cudaError_t st = make_rows_maps<kBMn>(&map_a, &map_b, A, B, a, kBM, bn / 2);
   if (st != cudaSuccess) return st;
   auto kern = rows_pair_kernel<kAct, kBMn>;
   const size_t smem = 1024 + kStages * kStageBytes + kEpilogueWarps * kPatchBytes + sizeof(int) * (static_cast<size_t>(a.groups.E) + 1);
   if (resident_ctas(reinterpret_cast<const void*>(kern), kThreads, smem) < 1) return cudaErrorInvalidConfiguration;
-  const int cols = kAct == EP_ACT_SWIGLU ? kBN / 2 : kBN;
-  const int64_t row_tiles = max_row_tiles(a.groups, 2 * kBM);
-  const int64_t most = row_tiles * ((a.epi.cols + cols - 1) / cols);
+  const int cols = bn / halves;
+  const int64_t most = max_row_tiles(a.groups, 2 * kBM) * ((a.epi.cols + cols - 1) / cols);
   const int64_t pairs = most < num_sms / 2 ? most : num_sms / 2;  // num_sms >= 2
-  return launch_chained(kern, dim3(static_cast<unsigned>(2 * pairs)), dim3(kThreads), smem, stream, map_a, map_b, a);
+  return launch_chained(kern, dim3(static_cast<unsigned>(2 * pairs)), dim3(kThreads), smem, stream, map_a, map_b, a, bn);
 }
 #define X(act, mn) \
   template cudaError_t launch_rows_pair<act, mn>(const uint16_t*, const uint16_t*, const RowsArgs&, int, cudaStream_t);
