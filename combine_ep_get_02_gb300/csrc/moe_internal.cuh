@@ -31,7 +31,8 @@ struct RouteGeometry {
 };
 
 // Byte offsets of the router's workspace: the 256-byte header (error word at 0,
-// counter of finished segments at 4), then the pieces below. Sums and counters return to 0.
+// counter of finished segments at 4), then the pieces below, all of which return to 0, so that
+// a workspace serves calls of other sizes too.
 struct RouteWorkspace {
   size_t seg_done;   // uint32 [B]: CTAs of each segment that have delivered
   size_t seg_valid;  // uint32 [B]: valid tokens

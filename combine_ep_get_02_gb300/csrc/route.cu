@@ -528,7 +528,10 @@ __global__ void __launch_bounds__(kRouteThreads, EPL <= 8 ? 4 : EPL <= 16 ? 2 : 
       __threadfence();
       float loss = 0.f;
 #pragma unroll 16
-      for (int b = 0; b < g.B; ++b) loss += __ldcg(a.seg_loss + b);
+      for (int b = 0; b < g.B; ++b) {
+        loss += __ldcg(a.seg_loss + b);
+        a.seg_loss[b] = 0.f;
+      }
       *a.loss = loss / static_cast<float>(g.B);
       *a.done = 0u;
     }

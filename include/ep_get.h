@@ -347,8 +347,9 @@ typedef struct ep_route {
 } ep_route_t;
 
 /* Workspace bytes of ep_route and ep_route_grad (0 for an invalid configuration).
- * Zero-filled once before first use (ep_workspace_init), as the others; one stream
- * at a time; errors are read by ep_check_error. */
+ * Zero-filled once before first use (ep_workspace_init), as the others (it may then
+ * serve any configuration that fits it); one stream at a time; errors are read by
+ * ep_check_error. */
 size_t ep_route_workspace_bytes(const ep_route_config_t* cfg);
 
 /* Router. logits: device [N][E], 16-byte aligned. choice_bias: device fp32 [E] or
@@ -398,7 +399,8 @@ int ep_combine_grad(const ep_config_t* cfg, const ep_layout_t* layout, const uin
  * of bf16 values, summed in fp32; the activation is taken of the fp32 sum; z and out
  * are rounded once. Rows outside the blocks' lanes are neither read for a result nor
  * written. layout = NULL: one group of all `rows` rows (a dense product, such as a
- * shared expert), with num_ranks = num_experts = 1.
+ * shared expert), with num_ranks = num_experts = 1. Every wait in the kernels is
+ * bounded; one that gives up latches EP_ERR_TIMEOUT and leaves outputs incomplete.
  */
 #define EP_ACT_NONE 0
 #define EP_ACT_RELU 1

@@ -275,3 +275,40 @@ def test_blocks_past_the_rows_are_cut_and_reported():
     assert ep.ep_check_error(ws) == ep.EP_ERR_OVERFLOW
     want, _ = c.forward()
     assert torch.equal(guard[:70], want[:70]) and (guard[70:] == 9.0).all()
+
+
+def test_offsets_past_32_bits():
+    """Outputs of more than 2^31 elements: the last block against the definition, forward and gradients."""
+    rows, K, N = 300_000, 64, 8192
+    lay, blocks, _ = blocks_of([rows - 300, 300], 1)
+    g = torch.Generator(device="cuda").manual_seed(4)
+    x = torch.randn(rows, K, device="cuda", generator=g).bfloat16()
+    w = (torch.randn(2, N, K, device="cuda", generator=g) / 8).bfloat16()
+    out = torch.empty(rows, N, dtype=torch.bfloat16, device="cuda")
+    cfg = ep.ProductConfig(1, 2, rows, K, N, ep.EP_ACT_RELU)
+    ws = ep.alloc_product_workspace(cfg, grad=True)
+    z = torch.empty_like(out)
+    ep.ep_expert_product(cfg, lay, x, None, w, None, None, z, out, ws)
+    want, want_z = ref.product([(0, 300)], x[-300:], w[1:], None, None, "relu")
+    near(out[-300:], want, 2 ** -8, 1e-4)
+    near(z[-300:], want_z, 2 ** -8, 1e-4)
+    first, _ = ref.product([(0, 200)], x[:200], w[:1], None, None, "relu")
+    near(out[:200], first, 2 ** -8, 1e-4)
+    out.normal_(generator=g)  # now the gradient of the output
+    dx, dw, db = torch.empty_like(x), torch.empty_like(w), torch.empty(2, N, device="cuda")
+    ep.ep_expert_product_grad(cfg, lay, x, w, z, out, dx, dw, db, ws)
+    assert ep.ep_check_error(ws) == ep.EP_OK
+    wx, ww, wb = ref.product_grad([(0, 300)], x[-300:], w[1:], z[-300:], out[-300:], "relu")
+    # relu's dz is exact in bf16: one rounding of the result, and fp32 sums of thousands of products
+    near(dx[-300:], wx, 2 ** -8, 1e-3 * rms(wx))
+    near(dw[1:], ww, 2 ** -8, 1e-3 * rms(ww))
+    near(db[1:], wb, 1e-5, 1e-4 * rms(wb))
+
+
+def test_row_strides_that_do_not_fill_a_tile():
+    """Every multiple of 8 around the tile widths, in both features."""
+    for K, N in ((8, 264), (56, 8), (64, 72), (72, 120), (120, 136), (136, 248), (248, 256), (264, 56)):
+        for act in ("none", "swiglu"):
+            c = Case([37, 129, 5], K, N, act=act, bias=True)
+            c.check()
+            c.check_grads()

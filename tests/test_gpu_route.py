@@ -210,6 +210,42 @@ def test_no_tokens():
     c.grad(out)
 
 
+def test_a_workspace_serves_other_sizes():
+    cases = [Case(5, 300, 64, 4), Case(1, 700, 200, 8, score="sigmoid", bias=True), Case(40, 20, 24, 2, dtype="bf16"),
+             Case(2, 90, 512, 6)]
+    ws = ep.alloc_route_workspace(max((c.cfg for c in cases), key=ep.ep_route_workspace_bytes))
+    for c in cases + cases[::-1]:
+        c.ws = ws
+        c.check()
+    assert not ws.any()
+
+
+def test_offsets_past_32_bits():
+    """More than 2^31 logits: the last tokens against the definition, the counts against the choice."""
+    T, E, K = 8_400_000, 256, 8
+    logits = torch.empty(T, E, device="cuda")
+    for i in range(0, T, 1 << 20):
+        logits[i:i + (1 << 20)].normal_(generator=torch.Generator(device="cuda").manual_seed(i))
+    cfg = ep.RouteConfig(1, T, E, K)
+    out, ws = ep.alloc_route(cfg), ep.alloc_route_workspace(cfg)
+    ep.ep_route(cfg, logits, None, None, out, ws)
+    assert ep.ep_check_error(ws) == ep.EP_OK
+    last = slice(T - 1000, T)
+    want = ref.route(logits[last], None, None, 1, 1000, K)
+    assert torch.equal(out.topk_idx[last], want[0])
+    close(out.topk_weights[last], want[1])
+    assert int(out.num_valid) == T
+    assert torch.equal(out.expert_count[0].long(), torch.bincount(out.topk_idx.reshape(-1), minlength=E))
+    close(out.prob_sum.sum(1), torch.full((1,), float(T), device="cuda"))
+    d = torch.empty_like(logits)
+    g = torch.randn(T, K, device="cuda")
+    ep.ep_route_grad(cfg, logits, None, out, g, None, d, ws)
+    l = logits[last].double().requires_grad_(True)
+    w = torch.softmax(l.gather(1, want[0]), -1)
+    exact = torch.autograd.grad((w * g[last].double()).sum(), l)[0]
+    assert ((d[last].double() - exact).abs() <= RTOL * 2 * g[last].abs().amax(1, keepdim=True)).all()
+
+
 def test_without_statistics_and_repeatable():
     c = Case(4, 1111, 256, 8)
     a, b = c.run(), c.run()
