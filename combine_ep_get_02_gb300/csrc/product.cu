@@ -193,14 +193,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 }  // namespace
 
 template <int kAct, bool kBMn>
-cudaError_t launch_rows_single(const uint16_t* A, const uint16_t* B, const RowsArgs& a, int num_sms, cudaStream_t stream) {
-  // The widest tile that still gives every SM one: with fewer tiles than SMs it is reading B
-  // that counts, and more CTAs read it faster (48 experts with a few rows each, 4376 -> 256:
-  // 256 columns 50 us).
+cudaError_t launch_rows_single(const uint16_t* A, const uint16_t* B, const RowsArgs& a, int bn, int num_sms, cudaStream_t stream) {
   const int halves = kAct == EP_ACT_SWIGLU ? 2 : 1;
-  auto tiles = [&](int bn) { return max_row_tiles(a.groups) * ((a.epi.cols + bn / halves - 1) / (bn / halves)); };
-  int bn = kMaxBN;
-  while (bn > 64 && tiles(bn) < num_sms) bn /= 2;
   CUtensorMap map_a, map_low, map_b;
   cudaError_t st = make_rows_maps<kBMn>(&map_a, &map_b, A, B, a, kBM, bn / 2);
   if (st != cudaSuccess) return st;
@@ -211,28 +205,53 @@ cudaError_t launch_rows_single(const uint16_t* A, const uint16_t* B, const RowsA
   auto kern = rows_kernel<kAct, kBMn>;
   const size_t smem = 1024 + kRingBytes + kEpilogueWarps * kPatchBytes + sizeof(int) * (static_cast<size_t>(a.groups.E) + 1);
   if (resident_ctas(reinterpret_cast<const void*>(kern), kThreads, smem) < 1) return cudaErrorInvalidConfiguration;
-  const unsigned grid = static_cast<unsigned>(tiles(bn) < num_sms ? tiles(bn) : num_sms);
+  const int64_t tiles = max_row_tiles(a.groups) * ((a.epi.cols + bn / halves - 1) / (bn / halves));
+  const unsigned grid = static_cast<unsigned>(tiles < num_sms ? tiles : num_sms);
   return launch_chained(kern, dim3(grid), dim3(kThreads), smem, stream, map_a, map_low, map_b, a, bn);
 }
 #define X(act, mn) \
-  template cudaError_t launch_rows_single<act, mn>(const uint16_t*, const uint16_t*, const RowsArgs&, int, cudaStream_t);
+  template cudaError_t launch_rows_single<act, mn>(const uint16_t*, const uint16_t*, const RowsArgs&, int, int, cudaStream_t);
 EP_ROWS_INSTANCES(X)
 #undef X
 
 namespace {
 
-// Pairs of CTAs when the groups are long enough for tiles of 256 rows to be mostly full
-// (their average at least one and a half), a split of the summed index when the tiles
-// would leave most SMs idle, single CTAs otherwise.
+// Which kernel and tile width. A split of the summed index when the tiles would leave most
+// SMs idle. Pairs when their tiles of 256 rows are mostly full: groups of 384 rows on average
+// (8 groups of about 350 rows, 3336 -> 2408: pairs 77 us, single CTAs 66). The width is
+// the one with the least rounds of tiles x cycles of a 64-block of the summed index,
+// which are 2 a column of the tile (the tensor cores) or the tile's bytes at the 64 a
+// cycle that L2 gives an SM, whichever is more. How the rows lie in the groups is not known
+// here: half a tile of every group is taken to be empty. So narrow tiles come where wide
+// ones leave SMs idle or a last round short:
+//   1613 rows 1152 -> 3064 (pairs): 256 columns 21.7 us, the 192 taken 18.2;
+//   48 experts with a few rows, 4376 -> 256: 256 columns 50 us, the 128 taken 32.
+// (MN-major tiles load whole panels of 64 columns, so the widths between gain nothing there.)
 template <int kAct, bool kBMn>
 cudaError_t launch_rows(const uint16_t* A, const uint16_t* B, const RowsArgs& a, int num_sms, cudaStream_t stream) {
   bool done = false;
   const cudaError_t st = launch_rows_split<kAct, kBMn>(A, B, a, stream, &done);
   if (done || st != cudaSuccess) return st;
-  const int64_t rows = a.groups.rows;
-  if (rows >= 384ll * (a.groups.count == nullptr ? 1 : a.groups.E) && num_sms >= 2)
-    return launch_rows_pair<kAct, kBMn>(A, B, a, num_sms, stream);
-  return launch_rows_single<kAct, kBMn>(A, B, a, num_sms, stream);
+  const int halves = kAct == EP_ACT_SWIGLU ? 2 : 1;
+  const int64_t rows = a.groups.rows, groups = a.groups.count == nullptr ? 1 : a.groups.E < rows ? a.groups.E : rows;
+  auto cost = [&](int tile_rows, int bn, int at_once) {
+    int64_t row_tiles = a.groups.count == nullptr ? (rows + tile_rows - 1) / tile_rows : rows / tile_rows + groups / 2;
+    if (row_tiles < groups) row_tiles = groups;
+    const int64_t tiles = row_tiles * ((a.epi.cols + bn / halves - 1) / (bn / halves));
+    const bool pair = tile_rows > kBM;
+    const int b_rows = pair ? bn / 2 : bn;  // of B, loaded by a CTA
+    const int64_t bytes = kABytes + 128 * (kBMn ? (b_rows + 63) / 64 * 64 : b_rows);
+    return (tiles + at_once - 1) / at_once * (2 * bn > bytes / 64 ? 2 * bn : bytes / 64);
+  };
+  const bool pair = rows >= 384 * groups && num_sms >= 2;
+  int bn = kMaxBN;
+  int64_t least = INT64_MAX;
+  for (int w = kMaxBN; w >= (pair ? 128 : 64); w = pair ? w - 32 : w / 2) {
+    const int64_t c = pair ? cost(2 * kBM, w, num_sms / 2) : cost(kBM, w, num_sms);
+    if (c < least) least = c, bn = w;
+  }
+  return pair ? launch_rows_pair<kAct, kBMn>(A, B, a, bn, num_sms, stream)
+              : launch_rows_single<kAct, kBMn>(A, B, a, bn, num_sms, stream);
 }
 
 }  // namespace

@@ -181,22 +181,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 }  // namespace
 
 template <int kAct, bool kBMn>
-cudaError_t launch_rows_pair(const uint16_t* A, const uint16_t* B, const RowsArgs& a, int num_sms, cudaStream_t stream) {
-  // Tile width: a narrower tile can fill the last round of tiles better. The time of a width is
-  // taken as rounds x cycles of a block of the summed index: 2 a column, or its bytes at the
-  // 64 a cycle that L2 gives. (1613 rows, 1152 -> 3064: 256 columns 21.7 us, the 192 taken here
-  // 18.2. MN-major tiles load whole panels of 64, so 224 columns of them gain nothing.)
+cudaError_t launch_rows_pair(const uint16_t* A, const uint16_t* B, const RowsArgs& a, int bn, int num_sms, cudaStream_t stream) {
   const int halves = kAct == EP_ACT_SWIGLU ? 2 : 1;
-  const int64_t row_tiles = a.groups.count == nullptr ? (a.groups.rows + 2 * kBM - 1) / (2 * kBM)
-                                                      : a.groups.rows / (2 * kBM) + (a.groups.E + 1) / 2;
-  int bn = kBN;
-  int64_t least = INT64_MAX;
-  for (int w = kBN; w >= 128; w -= 32) {
-    const int64_t rounds = (row_tiles * ((a.epi.cols + w / halves - 1) / (w / halves)) + num_sms / 2 - 1) / (num_sms / 2);
-    const int loaded = kBMn ? (w / 2 + 63) / 64 * 64 : w / 2;
-    const int64_t cycles = 2 * w > (kABytes + 128 * loaded) / 64 ? 2 * w : (kABytes + 128 * loaded) / 64;
-    if (rounds * cycles < least) least = rounds * cycles, bn = w;
-  }
   CUtensorMap map_a, map_b;
   const cudaError_t st = make_rows_maps<kBMn>(&map_a, &map_b, A, B, a, kBM, bn / 2);
   if (st != cudaSuccess) return st;
@@ -209,7 +195,7 @@ cudaError_t launch_rows_pair(const uint16_t* A, const uint16_t* B, const RowsArg
   return launch_chained(kern, dim3(static_cast<unsigned>(2 * pairs)), dim3(kThreads), smem, stream, map_a, map_b, a, bn);
 }
 #define X(act, mn) \
-  template cudaError_t launch_rows_pair<act, mn>(const uint16_t*, const uint16_t*, const RowsArgs&, int, cudaStream_t);
+  template cudaError_t launch_rows_pair<act, mn>(const uint16_t*, const uint16_t*, const RowsArgs&, int, int, cudaStream_t);
 EP_ROWS_INSTANCES(X)
 #undef X
 

@@ -66,12 +66,12 @@ cudaError_t make_rows_maps(CUtensorMap* map_a, CUtensorMap* map_b, const uint16_
   return make_tensor_map(map_b, B, 3, size, box);
 }
 
-// The three kernels: a CTA per tile of 128 rows, CTA pairs on tiles of 256 rows, and
-// clusters that split the summed index of a few tiles.
+// The three kernels: a CTA per tile of 128 rows, CTA pairs on tiles of 256 rows (both with
+// tiles of `bn` rows of B), and clusters that split the summed index of a few tiles.
 template <int kAct, bool kBMn>
-cudaError_t launch_rows_single(const uint16_t* A, const uint16_t* B, const RowsArgs& a, int num_sms, cudaStream_t stream);
+cudaError_t launch_rows_single(const uint16_t* A, const uint16_t* B, const RowsArgs& a, int bn, int num_sms, cudaStream_t stream);
 template <int kAct, bool kBMn>
-cudaError_t launch_rows_pair(const uint16_t* A, const uint16_t* B, const RowsArgs& a, int num_sms, cudaStream_t stream);
+cudaError_t launch_rows_pair(const uint16_t* A, const uint16_t* B, const RowsArgs& a, int bn, int num_sms, cudaStream_t stream);
 // *done says whether the rule took the call (see there).
 template <int kAct, bool kBMn>
 cudaError_t launch_rows_split(const uint16_t* A, const uint16_t* B, const RowsArgs& a, cudaStream_t stream, bool* done);

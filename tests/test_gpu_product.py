@@ -219,6 +219,16 @@ def test_each_gradient_alone_and_sms():
     assert torch.equal(c.forward(keep=False)[0], c.forward()[0])
 
 
+def test_pairs_and_single_ctas_agree():
+    """Long groups run on pairs of CTAs; one SM cannot: the same sums in the same order."""
+    kw = dict(counts=[700, 257, 900], K=392, N=264, act="gelu", bias=True, residual=True)
+    a, b = Case(**kw), Case(**kw, num_sms=1)
+    for x, y in zip(a.forward(), b.forward()):
+        assert torch.equal(x[a.live], y[a.live])
+    for x, y in zip(a.grads(), b.grads()):
+        assert torch.equal(x, y)
+
+
 def test_residual_in_place():
     c = Case([100], 64, 128, dense=True, residual=True)
     want, _ = c.forward()
