@@ -12,6 +12,10 @@
 // computed and not stored (an output row depends on its own row of A alone). Columns past
 // the tensors read as zero.
 //
+// It serves groups too short for pairs of CTAs (product_pair.cu); there reading B bounds it.
+// Measured: 64 experts with 8 rows on average, 4096 -> 2 x 2048, 305-316 us (2.15 GB of
+// matrices, 6.8-7.0 TB/s); 48 experts with a few rows, 4376 -> 256, 31 us.
+//
 // Every wait is bounded; one that gives up latches kErrTimeout, lets the CTA's copies
 // and products finish and returns.
 #include "product_rows.cuh"

@@ -16,7 +16,11 @@ __device__ __forceinline__ void st32(void* p, const uint4& a, const uint4& b) {
 
 // FP8 rows -> bf16: bf16_rn(code * scale), one scale per 128 columns (fp32, or a
 // power of two packed four to a word). A warp takes 2048 columns of a row, a lane 16 at a
-// time: 16 bytes in, 32 out. Rows past the last region are not part of any block and are left out.
+// time: 16 bytes in, 32 out. Rows past the last region are not part of any block and are left
+// out. This rounding puts the result's error at 2.8e-3 of its norm, where its own rounding
+// alone would leave 1.7e-3; scaling fp32 sums over every 128 columns instead was that exact
+// and took 5.1 ms instead of 2.5 for 65536 x 7168 -> 2 x 2048. Measured: 65536 x 7168 in
+// 226 us (1.4 GB, 6.2 TB/s).
 __global__ void __launch_bounds__(kThreads)
     dequant_kernel(const uint8_t* x, const float* x_sf, uint16_t* out, int rows, int K, int sf_pack, const int32_t* total) {
   pdl_launch_dependents();
@@ -51,7 +55,7 @@ __global__ void __launch_bounds__(kThreads)
         f[2 * j] = q.x * sf;
         f[2 * j + 1] = q.y * sf;
       }
-      st32(to + c, pack8(f), pack8(f + 8));  // a whole sector: two 16-byte stores took half as long again
+      st32(to + c, pack8(f), pack8(f + 8));  // a whole sector: with two 16-byte stores 285 us instead of 226
     }
   }
 }
@@ -59,7 +63,8 @@ __global__ void __launch_bounds__(kThreads)
 // dz = d_out * act'(z), rounded to bf16 for the products, and the column sums of the
 // unrounded dz over each tile of kDzRows rows. A CTA takes such a tile of one group and 128
 // output columns: 16 threads across (8 columns each, 256 bytes of a row), 16 down, so that a
-// few thousand rows already occupy every SM evenly.
+// few thousand rows already occupy every SM evenly. Memory bounds it, with GELU the arithmetic:
+// 4096 x 4096 GELU 30 us (100 MB), 16384 x 1024 gated 29 us (168 MB, 5.8 TB/s).
 constexpr int kAcross = 16, kDown = kThreads / kAcross, kSpan = kAcross * 8;
 
 struct DzArgs {

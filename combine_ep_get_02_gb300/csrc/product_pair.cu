@@ -4,6 +4,11 @@
 // stage is 32 KB instead of 48, which makes room for six. (L2 gives an SM about 64 bytes a
 // cycle; a 128 x 256 tile of its own wants 96 at the tensor cores' full rate, a pair's tile 64.)
 //
+// The tensor cores bound it (70 to 90% of their time busy; the rest is the first loads, the last
+// epilogue and the last round of tiles). Measured: 4096 x 2048 -> 7168 with bias and residual
+// 70-82 us (1.5-1.7 PFLOP/s, by the clock that the power limit leaves; single CTAs 94 us);
+// 65536 x 7168 -> 2 x 2048 over 64 experts 2.26 ms (1.70 PFLOP/s).
+//
 // The pair's first CTA issues the products for both. Its "full" barriers count the bytes
 // that land in both CTAs; the commits arrive on both CTAs' "empty" and "accumulator full"
 // barriers; the epilogue warps of both arrive on its "accumulator empty" ones.

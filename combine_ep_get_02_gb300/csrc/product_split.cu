@@ -5,6 +5,10 @@
 // columns into that CTA's shared memory, which adds them in the order of the CTAs and
 // does the epilogue.
 //
+// Measured: one row, 7168 -> 2 x 2048: 15.6 us (58.7 MB; 16 CTAs without the split 42 us, and
+// 29 us with 16 clusters of 8, of which 15 fit at once). 9 us of it are the matrix at 6.5 TB/s;
+// the rest is start-up, the first loads and the exchange, which bound the smaller calls.
+//
 // The split depends on the sizes alone, not on the device, and the order of the additions
 // is fixed, so results repeat bit for bit.
 #include "product_rows.cuh"

@@ -16,7 +16,11 @@
 // registers over all the warp's tokens; a CTA's warps are summed in their order, the CTAs
 // in fixed point, so every result repeats bit for bit.
 // Reading the logits once is what the operator cannot do without; what bounds it is the
-// arithmetic on them (comparisons run at half rate).
+// instructions on them, about 560 a token at 256 experts, top 8, half of them the choice
+// (comparisons run at half rate). Measured: 16 x 4096 tokens, 256 experts, top 8, softmax
+// 45 us (67 MB of logits, 1.6 TB/s; 84 us with sigmoid scores and 8 groups), one segment of
+// 65536 tokens 43 us; 64 tokens 7 us, of which 3.5 are the statistics' chain of one atomic
+// and one load across the CTAs; the gradient of 16 x 4096 tokens 30 us (141 MB, 4.7 TB/s).
 #include <type_traits>
 
 #include "ep_device.cuh"
@@ -137,8 +141,9 @@ struct Candidates {
 // scores that reach it can be chosen: K at least, and few more. They are listed in shared
 // memory, a lane takes one, and its place is the number of larger ones (equal scores,
 // which show as a place taken twice, are told apart by expert). More than 32 (many
-// equal scores, or K near 32) take K rounds of finding the best instead. Against K such
-// rounds for every token this halved the time of 256 experts, top 8.
+// equal scores, or K near 32) take K rounds of finding the best instead (such rounds for
+// every token: 68 us for 16 x 4096 tokens, 256 experts, top 8; with the list 52, and 45
+// after its bound came from integer maxima).
 template <int EPL>
 __device__ __forceinline__ int choose(float (&c)[EPL], float best, int K, Candidates& list, int lane, int& mine,
                                       float& mine_score) {
