@@ -543,12 +543,12 @@ def alloc_route_workspace(cfg: RouteConfig, device="cuda") -> torch.Tensor:
 
 
 def alloc_product_workspace(cfg: ProductConfig, grad: bool = False, device="cuda") -> torch.Tensor:
-    """Workspace of ep_product_workspace_bytes(cfg, grad) bytes with a zeroed header."""
+    """Workspace of ep_product_workspace_bytes(cfg, grad) bytes, zeroed where that is needed."""
     n = ep_product_workspace_bytes(cfg, grad)
     if n == 0:
         raise EpError(EP_ERR_INVALID_ARG, "ep_product_workspace_bytes")
     ws = torch.empty(n, dtype=torch.uint8, device=device)
-    ws[:256].zero_()
+    ws[:ep_product_workspace_bytes(dataclasses.replace(cfg, rows=0), grad)].zero_()
     return ws
 
 

@@ -111,6 +111,7 @@ int make_product(const ep_product_config_t* c, ProductGeometry* g) {
 }
 
 struct ProductWorkspace {
+  size_t done;  // uint32 [E][spans of output columns], gradient: follows the header, zeroed with it
   size_t rows;  // bf16 rows of FP8 x [rows][K], or dz [rows][Z]
   size_t part;  // float [tiles of kDzRows rows][Z]
   size_t total;
@@ -118,7 +119,9 @@ struct ProductWorkspace {
 
 ProductWorkspace product_workspace(const ProductGeometry& g, bool grad) {
   ProductWorkspace w;
-  w.rows = 256;
+  w.done = 256;
+  const size_t spans = (g.N + kDzColumns - 1) / kDzColumns;
+  w.rows = w.done + (grad ? round256(4 * spans * g.groups.E) : 0);
   size_t bytes = 0;
   if (grad) bytes = g.act == EP_ACT_NONE ? 0 : 2 * static_cast<size_t>(g.groups.rows) * g.Z;
   else if (g.x_fp8) bytes = 2 * static_cast<size_t>(g.groups.rows) * g.K;
@@ -334,6 +337,7 @@ int ep_expert_product_grad(const ep_product_config_t* cfg, const ep_layout_t* la
   const bool products = d_x != nullptr || d_weight != nullptr;
   a.dz = a.g.act == EP_ACT_NONE || !products ? nullptr : at<uint16_t>(workspace, w.rows);
   a.part = d_bias != nullptr ? at<float>(workspace, w.part) : nullptr;
+  a.done = at<uint32_t>(workspace, w.done);
   a.d_x = d_x;
   a.d_weight = d_weight;
   a.d_bias = d_bias;

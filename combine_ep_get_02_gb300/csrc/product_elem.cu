@@ -60,12 +60,14 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-// dz = d_out * act'(z), rounded to bf16 for the products, and the column sums of the
-// unrounded dz over each tile of kDzRows rows. A CTA takes such a tile of one group and 128
+// dz = d_out * act'(z), rounded to bf16 for the products, and the bias gradient: the column
+// sums of the unrounded dz over each tile of kDzRows rows, which the last CTA to finish of
+// a group's tiles adds up in their order (a kernel of its own for that took 4 to 18 us). A CTA takes such a tile of one group and 128
 // output columns: 16 threads across (8 columns each, 256 bytes of a row), 16 down, so that a
 // few thousand rows already occupy every SM evenly. Memory bounds it, with GELU the arithmetic:
 // 4096 x 4096 GELU 30 us (100 MB), 16384 x 1024 gated 29 us (168 MB, 5.8 TB/s).
-constexpr int kAcross = 16, kDown = kThreads / kAcross, kSpan = kAcross * 8;
+constexpr int kSpan = kDzColumns, kAcross = kSpan / 8, kDown = kThreads / kAcross;
+constexpr int kBiasWays = 8;  // orders the bias gradients' sums, here and in bias_sum_kernel
 
 struct DzArgs {
   Groups groups;
@@ -74,6 +76,8 @@ struct DzArgs {
   const uint16_t* d_out;
   uint16_t* dz;  // null: only the sums
   float* part;   // null: no sums
+  float* d_bias;
+  uint32_t* done;  // [E][spans]: tiles finished (returns to 0); null: the sums stay in part
   uint32_t* err;
 };
 
@@ -86,8 +90,13 @@ __global__ void __launch_bounds__(kThreads) dz_kernel(DzArgs a) {
   pdl_launch_dependents();
   pdl_wait();
   build_prefix<kThreads>(a.groups, kDzRows, prefix, blockIdx.x == 0 ? a.err : nullptr);
+  __shared__ bool s_last;
   const int across = threadIdx.x % kAcross, down = threadIdx.x / kAcross;
   const int spans = (a.N + kSpan - 1) / kSpan;
+  if (a.done != nullptr)  // groups without a row
+    for (int g = blockIdx.x; g < a.groups.E; g += gridDim.x)
+      if (prefix[g] == prefix[g + 1])
+        for (int c = threadIdx.x; c < a.Z; c += kThreads) a.d_bias[static_cast<int64_t>(g) * a.Z + c] = 0.f;
   const int64_t units = static_cast<int64_t>(prefix[a.groups.E]) * spans;
   for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
     const int tile = static_cast<int>(u / spans), col = static_cast<int>(u - static_cast<int64_t>(tile) * spans) * kSpan + across * 8;
@@ -131,18 +140,52 @@ __global__ void __launch_bounds__(kThreads) dz_kernel(DzArgs a) {
       }
     }
     if (a.part != nullptr) {
+      constexpr int kColumns = kHalves * kSpan;
+      float* sums = &s_sum[0][0];
+      const int tiles = prefix[g + 1] - prefix[g], span = col / kSpan;
+      // column i of the CTA's, in z and in d_bias; past N: none
+      auto column = [&](int i) {
+        const int h = i / kSpan, c = span * kSpan + i - h * kSpan;
+        return c < a.N ? h * a.N + c : -1;
+      };
 #pragma unroll
       for (int h = 0; h < kHalves; ++h)
 #pragma unroll
         for (int i = 0; i < 8; ++i) s_sum[down][h * kSpan + across * 8 + i] = sum[8 * h + i];
       __syncthreads();
-      for (int i = threadIdx.x; i < kHalves * kSpan; i += kThreads) {
-        const int h = i / kSpan, c = col - across * 8 + (i - h * kSpan);
-        if (c < a.N) {
-          float s = 0.f;
+      float* to = tiles == 1 && a.done != nullptr ? a.d_bias + static_cast<int64_t>(g) * a.Z : a.part + static_cast<int64_t>(tile) * a.Z;
+      for (int i = threadIdx.x; i < kColumns; i += kThreads) {
+        float s = 0.f;
 #pragma unroll
-          for (int k = 0; k < kDown; ++k) s += s_sum[k][i];
-          a.part[static_cast<int64_t>(tile) * a.Z + h * a.N + c] = s;
+        for (int k = 0; k < kDown; ++k) s += s_sum[k][i];
+        if (const int c = column(i); c >= 0) to[c] = s;
+      }
+      if (tiles > 1 && a.done != nullptr) {
+        __threadfence();
+        __syncthreads();
+        uint32_t* done = a.done + static_cast<int64_t>(g) * spans + span;
+        if (threadIdx.x == 0) s_last = atomicAdd(done, 1u) == static_cast<uint32_t>(tiles) - 1u;
+        __syncthreads();
+        if (s_last) {  // every kBiasWays-th tile, then the ways in order, as bias_sum_kernel
+          __threadfence();
+          for (int i = threadIdx.x; i < kBiasWays * kColumns; i += kThreads) {
+            const int way = i / kColumns, c = column(i - way * kColumns);
+            float s = 0.f;
+            if (c >= 0) {
+#pragma unroll 8
+              for (int t = prefix[g] + way; t < prefix[g + 1]; t += kBiasWays)
+                s += __ldcg(a.part + static_cast<int64_t>(t) * a.Z + c);
+            }
+            sums[i] = s;
+          }
+          __syncthreads();
+          for (int i = threadIdx.x; i < kColumns; i += kThreads) {
+            float s = sums[i];
+#pragma unroll
+            for (int w = 1; w < kBiasWays; ++w) s += sums[w * kColumns + i];
+            if (const int c = column(i); c >= 0) a.d_bias[static_cast<int64_t>(g) * a.Z + c] = s;
+          }
+          if (threadIdx.x == 0) *done = 0u;
         }
       }
       __syncthreads();
@@ -153,7 +196,8 @@ __global__ void __launch_bounds__(kThreads) dz_kernel(DzArgs a) {
 // d_bias_g = the sum over the group's row tiles: 32 columns a CTA, 8 ways of every 8th tile,
 // then the ways in order. (A thread for all tiles of a column took 18 us at 4096 rows.)
 __global__ void __launch_bounds__(kThreads) bias_sum_kernel(Groups q, int Z, const float* part, float* d_bias) {
-  constexpr int kWays = kThreads / 32;
+  constexpr int kWays = kBiasWays;
+  static_assert(kWays == kThreads / 32, "a warp a way");
   extern __shared__ int prefix[];
   __shared__ float s_sum[kWays][32];
   pdl_launch_dependents();
@@ -181,14 +225,22 @@ __global__ void __launch_bounds__(kThreads) bias_sum_kernel(Groups q, int Z, con
 }
 
 template <int kAct>
-cudaError_t launch_dz(const DzArgs& a, int num_sms, cudaStream_t stream) {
+cudaError_t launch_dz(DzArgs a, int num_sms, cudaStream_t stream) {
   auto kern = dz_kernel<kAct>;
   const size_t smem = sizeof(int) * (static_cast<size_t>(a.groups.E) + 1);
   const int per_sm = resident_ctas(reinterpret_cast<const void*>(kern), kThreads, smem);
   if (per_sm < 1) return cudaErrorInvalidConfiguration;
   const int64_t most = max_row_tiles(a.groups, kDzRows) * ((a.N + kSpan - 1) / kSpan);
   const int64_t ctas = static_cast<int64_t>(num_sms) * per_sm;
-  return launch_chained(kern, dim3(static_cast<unsigned>(most < ctas ? most : ctas)), dim3(kThreads), smem, stream, a);
+  if (a.part == nullptr || most > ctas) a.done = nullptr;
+  const cudaError_t st = launch_chained(kern, dim3(static_cast<unsigned>(most < ctas ? most : ctas)), dim3(kThreads), smem, stream, a);
+  if (st != cudaSuccess || a.part == nullptr || a.done != nullptr) return st;
+  const int sum_per_sm = resident_ctas(reinterpret_cast<const void*>(bias_sum_kernel), kThreads, smem);
+  if (sum_per_sm < 1) return cudaErrorInvalidConfiguration;
+  const int64_t need = static_cast<int64_t>(a.groups.E) * ((a.Z + 31) / 32);
+  const int64_t sum_ctas = static_cast<int64_t>(num_sms) * sum_per_sm;
+  return launch_chained(bias_sum_kernel, dim3(static_cast<unsigned>(need < sum_ctas ? need : sum_ctas)), dim3(kThreads),
+                        smem, stream, a.groups, a.Z, static_cast<const float*>(a.part), a.d_bias);
 }
 
 }  // namespace
@@ -236,23 +288,14 @@ cudaError_t launch_dequant(const ProductGeometry& g, const uint8_t* x, const flo
 }
 
 cudaError_t launch_product_dz(const ProductGradArgs& p, int num_sms, cudaStream_t stream) {
-  const DzArgs a = {p.g.groups, p.g.N, p.g.Z, p.z, p.d_out, p.dz, p.part, p.err};
-  cudaError_t st;
+  const DzArgs a = {p.g.groups, p.g.N, p.g.Z, p.z, p.d_out, p.dz, p.part, p.d_bias, p.done, p.err};
   switch (p.g.act) {
-    case EP_ACT_RELU: st = launch_dz<EP_ACT_RELU>(a, num_sms, stream); break;
-    case EP_ACT_SILU: st = launch_dz<EP_ACT_SILU>(a, num_sms, stream); break;
-    case EP_ACT_GELU: st = launch_dz<EP_ACT_GELU>(a, num_sms, stream); break;
-    case EP_ACT_SWIGLU: st = launch_dz<EP_ACT_SWIGLU>(a, num_sms, stream); break;
-    default: st = launch_dz<EP_ACT_NONE>(a, num_sms, stream);
+    case EP_ACT_RELU: return launch_dz<EP_ACT_RELU>(a, num_sms, stream);
+    case EP_ACT_SILU: return launch_dz<EP_ACT_SILU>(a, num_sms, stream);
+    case EP_ACT_GELU: return launch_dz<EP_ACT_GELU>(a, num_sms, stream);
+    case EP_ACT_SWIGLU: return launch_dz<EP_ACT_SWIGLU>(a, num_sms, stream);
+    default: return launch_dz<EP_ACT_NONE>(a, num_sms, stream);
   }
-  if (st != cudaSuccess || p.part == nullptr) return st;
-  const size_t smem = sizeof(int) * (static_cast<size_t>(p.g.groups.E) + 1);
-  const int per_sm = resident_ctas(reinterpret_cast<const void*>(bias_sum_kernel), kThreads, smem);
-  if (per_sm < 1) return cudaErrorInvalidConfiguration;
-  const int64_t need = static_cast<int64_t>(p.g.groups.E) * ((p.g.Z + 31) / 32);
-  const int64_t ctas = static_cast<int64_t>(num_sms) * per_sm;
-  return launch_chained(bias_sum_kernel, dim3(static_cast<unsigned>(need < ctas ? need : ctas)), dim3(kThreads), smem,
-                        stream, p.g.groups, p.g.Z, static_cast<const float*>(p.part), p.d_bias);
 }
 
 }  // namespace ep

@@ -1,4 +1,5 @@
 """The experts' products and their gradients against the 64-bit definitions."""
+import dataclasses
 import math
 
 import pytest
@@ -76,7 +77,7 @@ class Case:
         dw = torch.full_like(self.w, 33.0) if d_w else None
         db = torch.full((self.E, self.Z), 33.0, device="cuda") if d_b else None
         ws = ep.alloc_product_workspace(cfg, grad=True)
-        ws[256:].fill_(0xFF)  # NaN wherever the workspace is read without being written
+        ws[ep.ep_product_workspace_bytes(dataclasses.replace(cfg, rows=0), True):].fill_(0xFF)  # NaN where nothing was written
         ep.ep_expert_product_grad(cfg, self.lay, self.x, self.w, self.z_in, self.d_out, dx, dw, db, ws)
         assert ep.ep_check_error(ws) == ep.EP_OK
         if d_x:
@@ -217,6 +218,27 @@ def test_each_gradient_alone_and_sms():
         assert torch.equal(a, b)
     assert torch.equal(few.forward()[0], c.forward()[0])
     assert torch.equal(c.forward(keep=False)[0], c.forward()[0])
+
+
+def test_bias_gradients_repeat_on_one_workspace():
+    """The counters of finished tiles return to zero: the same call again, and from a graph."""
+    c = Case([700, 0, 65, 64, 900], 40, 264, act="swiglu", bias=True)
+    ws = ep.alloc_product_workspace(c.cfg, grad=True)
+    want = c.grads(False, False, True)[2]
+    got = [torch.empty_like(want) for _ in range(4)]
+    call = lambda out: ep.ep_expert_product_grad(c.cfg, c.lay, None, None, c.z_in, c.d_out, None, None, out, ws)  # noqa: E731
+    for t in got[:3]:
+        call(t)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(got[3])
+    for _ in range(2):
+        got[3].fill_(7)
+        graph.replay()
+        for t in got:
+            assert torch.equal(t, want)
+    assert ep.ep_check_error(ws) == ep.EP_OK
 
 
 def test_pairs_and_single_ctas_agree():
