@@ -463,10 +463,13 @@ def _maybe(t, dtype, numel: int, where: str, name: str):
     return None if t is None else _at(t, dtype, numel, where, name)
 
 
+_current_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+
+
 def _raw_stream(stream):
     """The stream's handle; None: the current stream, without building a Stream object."""
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        return _current_stream(_current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -485,6 +488,13 @@ class RouteConfig(_KeepsStruct):
     topk_groups: int = 1
     normalize: int = 1
     scale: float = 1.0
+
+    def _needs(self):
+        """(logits' type, logits, lanes, statistics, segments, tokens) of a call, kept as the struct is."""
+        N, B, E = self.num_segments * self.num_tokens, self.num_segments, self.num_experts
+        n = (_BF16 if self.logits_dtype == EP_DTYPE_BF16 else _F32, N * E, N * self.num_topk, B * E, B, N)
+        object.__setattr__(self, "_sizes", n)
+        return n
 
     def _build_struct(self) -> _RouteConfig:
         return _RouteConfig(*(int(getattr(self, f[0])) for f in _RouteConfig._fields_[:-1]), float(self.scale))
@@ -520,6 +530,14 @@ class ProductConfig(_KeepsStruct):
         """Columns of z (and rows of each expert's matrix): twice out_features when gated."""
         return self.out_features * (2 if self.activation == EP_ACT_SWIGLU else 1)
 
+    def _needs(self):
+        """(x, x_sf, weight, bias, out, z) elements and (blocks' counts, starts, regions) of a call."""
+        K, N, Z, E, rows = self.in_features, self.out_features, self.z_features, self.num_experts, self.rows
+        sf = rows * ((K // 128 + 3) // 4 if self.sf_pack else K // 128)
+        n = (rows * K, sf, E * Z * K, E * Z, rows * N, rows * Z, E, E + self.num_ranks, self.num_ranks + 1)
+        object.__setattr__(self, "_sizes", n)
+        return n
+
     def _build_struct(self) -> _ProductConfig:
         return _ProductConfig(*(int(getattr(self, f[0])) for f in _ProductConfig._fields_))
 
@@ -543,12 +561,12 @@ def alloc_route_workspace(cfg: RouteConfig, device="cuda") -> torch.Tensor:
 
 
 def alloc_product_workspace(cfg: ProductConfig, grad: bool = False, device="cuda") -> torch.Tensor:
-    """Workspace of ep_product_workspace_bytes(cfg, grad) bytes, zeroed where that is needed."""
+    """Workspace of ep_product_workspace_bytes(cfg, grad) bytes with a zeroed header."""
     n = ep_product_workspace_bytes(cfg, grad)
     if n == 0:
         raise EpError(EP_ERR_INVALID_ARG, "ep_product_workspace_bytes")
     ws = torch.empty(n, dtype=torch.uint8, device=device)
-    ws[:ep_product_workspace_bytes(dataclasses.replace(cfg, rows=0), grad)].zero_()
+    ws[:256].zero_()
     return ws
 
 
@@ -577,27 +595,29 @@ def _too_small(where, obj, fields, need):
 
 
 def _route_args(where, cfg, logits, token_mask, r):
-    """Addresses of the logits and the mask; refuses tensors of `r` that do not fit the configuration."""
-    B, E = cfg.num_segments, cfg.num_experts
-    N = B * cfg.num_tokens
-    NK, BE = N * cfg.num_topk, B * E
-    i, w, c, p, v, l = r._checked(where, _ROUTE_FIELDS)
+    """What a call needs, and the addresses of the logits and the mask; refuses tensors of `r`
+    that do not fit the configuration."""
+    needs = cfg._sizes or cfg._needs()
+    kind, NE, NK, BE, B, N = needs
+    i, w, c, p, v, l = r._sizes or r._checked(where, _ROUTE_FIELDS)
     if i < NK or -1 < w < NK or -1 < c < BE or -1 < p < BE or -1 < v < B or l == 0:
         _too_small(where, r, _ROUTE_FIELDS, (NK, NK, BE, BE, B, 1))
-    x = _at(logits, _BF16 if cfg.logits_dtype == EP_DTYPE_BF16 else _F32, N * E, where, "logits")
-    if token_mask is None:
-        return x, None
-    return x, _at(token_mask, torch.bool if token_mask.dtype is torch.bool else _U8, N, where, "token_mask")
+    x = _at(logits, kind, NE, where, "logits")
+    if token_mask is not None:
+        token_mask = _at(token_mask, torch.bool if token_mask.dtype is torch.bool else _U8, N, where, "token_mask")
+    return needs, x, token_mask
 
 
 def ep_route(cfg: RouteConfig, logits: torch.Tensor, choice_bias, token_mask, out: Route, ws: torch.Tensor,
              stream=None):
     """Choose the experts of every token: logits [N][E] -> out (see Route). With
     out.balance_loss also the counts, the probability sums and the balance loss."""
-    x, m = _route_args("ep_route", cfg, logits, token_mask, out)
-    b = _maybe(choice_bias, _F32, cfg.num_experts, "ep_route", "choice_bias")
-    st = lib().ep_route(cfg._ref(), x, b, m, out._ref(), ws.data_ptr(), ws.numel(), _raw_stream(stream))
-    _check(st, "ep_route")
+    _, x, m = _route_args("ep_route", cfg, logits, token_mask, out)
+    b = None if choice_bias is None else _at(choice_bias, _F32, cfg.num_experts, "ep_route", "choice_bias")
+    st = (_lib or lib()).ep_route(cfg._reference or cfg._ref(), x, b, m, out._reference or out._ref(), ws.data_ptr(),
+                                  ws.numel(), _raw_stream(stream))
+    if st:
+        raise EpError(st, "ep_route")
 
 
 def ep_route_grad(cfg: RouteConfig, logits: torch.Tensor, token_mask, route: Route, d_weights, d_loss,
@@ -605,12 +625,14 @@ def ep_route_grad(cfg: RouteConfig, logits: torch.Tensor, token_mask, route: Rou
     """Gradient of the logits through the weights (d_weights [N][K] or None) and the
     balance loss (d_loss [1] or None)."""
     w = "ep_route_grad"
-    x, m = _route_args(w, cfg, logits, token_mask, route)
-    dw = _maybe(d_weights, _F32, cfg.num_segments * cfg.num_tokens * cfg.num_topk, w, "d_weights")
-    dl = _maybe(d_loss, _F32, 1, w, "d_loss")
-    dx = _at(d_logits, logits.dtype, cfg.num_segments * cfg.num_tokens * cfg.num_experts, w, "d_logits")
-    _check(lib().ep_route_grad(cfg._ref(), x, m, route._ref(), dw, dl, dx, ws.data_ptr(), ws.numel(),
-                               _raw_stream(stream)), w)
+    needs, x, m = _route_args(w, cfg, logits, token_mask, route)
+    dw = None if d_weights is None else _at(d_weights, _F32, needs[2], w, "d_weights")
+    dl = None if d_loss is None else _at(d_loss, _F32, 1, w, "d_loss")
+    st = (_lib or lib()).ep_route_grad(cfg._reference or cfg._ref(), x, m, route._reference or route._ref(), dw, dl,
+                                       _at(d_logits, needs[0], needs[1], w, "d_logits"), ws.data_ptr(), ws.numel(),
+                                       _raw_stream(stream))
+    if st:
+        raise EpError(st, w)
 
 
 def ep_combine_grad(cfg: Config, layout: Layout, y, topk_idx: torch.Tensor, topk_weights: torch.Tensor,
@@ -618,27 +640,26 @@ def ep_combine_grad(cfg: Config, layout: Layout, y, topk_idx: torch.Tensor, topk
     """Gradient of ep_combine: d_y (rows of y) and d_weights [R][T][K]; either may be None."""
     w = "ep_combine_grad"
     N, H = cfg.num_ranks * cfg.num_tokens, cfg.hidden
-    rows = cfg.__dict__.get("_sizes")  # kept until a field of cfg is assigned
+    rows = cfg._sizes  # kept until a field of cfg is assigned
     if rows is None:
         rows = max(ep_recv_rows(cfg), 0)
         object.__setattr__(cfg, "_sizes", rows)
     NK = N * cfg.num_topk
     y = _at(y, _BF16, rows * H, w, "y") if d_weights is not None or y is not None else None
-    _check(lib().ep_combine_grad(
-        cfg._ref(), layout._ref(), y, _at(topk_idx, _I64, NK, w, "topk_idx"),
+    _check((_lib or lib()).ep_combine_grad(
+        cfg._reference or cfg._ref(), layout._reference or layout._ref(), y, _at(topk_idx, _I64, NK, w, "topk_idx"),
         _at(topk_weights, _F32, NK, w, "topk_weights"), _at(d_out, _BF16, N * H, w, "d_out"),
         _maybe(d_y, _BF16, rows * H, w, "d_y"), _maybe(d_weights, _F32, NK, w, "d_weights"), ws.data_ptr(), ws.numel(),
         _raw_stream(stream)), w)
 
 
-def _blocks_arg(where, cfg, layout):
+def _blocks_arg(where, needs, layout):
     if layout is None:
         return None
-    R, E = cfg.num_ranks, cfg.num_experts
-    c, b, r = layout._checked(where, _BLOCK_FIELDS)
-    if -1 < c < E or -1 < b < E + R or -1 < r < R + 1:
-        _too_small(where, layout, _BLOCK_FIELDS, (E, E + R, R + 1))
-    return layout._ref()
+    c, b, r = layout._sizes or layout._checked(where, _BLOCK_FIELDS)
+    if -1 < c < needs[6] or -1 < b < needs[7] or -1 < r < needs[8]:
+        _too_small(where, layout, _BLOCK_FIELDS, needs[6:])
+    return layout._reference or layout._ref()
 
 
 def ep_expert_product(cfg: ProductConfig, layout, x: torch.Tensor, x_sf, weight: torch.Tensor, bias, residual, z,
@@ -646,30 +667,37 @@ def ep_expert_product(cfg: ProductConfig, layout, x: torch.Tensor, x_sf, weight:
     """out = act(x W_g^T + b_g) + residual over every expert's block of an expanded
     layout (layout None: one group of all rows); z, if given, keeps what the activation was taken of."""
     w = "ep_expert_product"
-    K, N, Z, E, rows = cfg.in_features, cfg.out_features, cfg.z_features, cfg.num_experts, cfg.rows
+    needs = cfg._sizes or cfg._needs()
+    n_x, n_sf, n_w, n_b, n_out, n_z = needs[:6]
     if cfg.x_dtype == EP_DTYPE_FP8_E4M3:
-        x = _at(x, torch.float8_e4m3fn if x is not None and x.dtype is torch.float8_e4m3fn else _U8, rows * K, w, "x")
-        groups = K // 128
-        x_sf = _at(x_sf, _F32, rows * ((groups + 3) // 4 if cfg.sf_pack else groups), w, "x_sf")
+        x = _at(x, torch.float8_e4m3fn if x is not None and x.dtype is torch.float8_e4m3fn else _U8, n_x, w, "x")
+        x_sf = _at(x_sf, _F32, n_sf, w, "x_sf")
     else:
-        x = _at(x, _BF16, rows * K, w, "x")
+        x = _at(x, _BF16, n_x, w, "x")
         x_sf = _maybe(x_sf, _F32, 0, w, "x_sf")
-    _check(lib().ep_expert_product(
-        cfg._ref(), _blocks_arg(w, cfg, layout), x, x_sf, _at(weight, _BF16, E * Z * K, w, "weight"),
-        _maybe(bias, _BF16, E * Z, w, "bias"), _maybe(residual, _BF16, rows * N, w, "residual"),
-        _maybe(z, _BF16, rows * Z, w, "z"), _at(out, _BF16, rows * N, w, "out"), ws.data_ptr(), ws.numel(),
-        _raw_stream(stream)), w)
+    st = (_lib or lib()).ep_expert_product(
+        cfg._reference or cfg._ref(), _blocks_arg(w, needs, layout), x, x_sf, _at(weight, _BF16, n_w, w, "weight"),
+        None if bias is None else _at(bias, _BF16, n_b, w, "bias"),
+        None if residual is None else _at(residual, _BF16, n_out, w, "residual"),
+        None if z is None else _at(z, _BF16, n_z, w, "z"), _at(out, _BF16, n_out, w, "out"), ws.data_ptr(), ws.numel(),
+        _raw_stream(stream))
+    if st:
+        raise EpError(st, w)
 
 
 def ep_expert_product_grad(cfg: ProductConfig, layout, x, weight, z, d_out: torch.Tensor, d_x, d_weight, d_bias,
                            ws: torch.Tensor, stream=None):
     """Gradients of ep_expert_product's rows, matrices and biases; any of the three may be None."""
     w = "ep_expert_product_grad"
-    K, N, Z, E, rows = cfg.in_features, cfg.out_features, cfg.z_features, cfg.num_experts, cfg.rows
-    x = _at(x, _BF16, rows * K, w, "x") if d_weight is not None or x is not None else None
-    weight = _at(weight, _BF16, E * Z * K, w, "weight") if d_x is not None or weight is not None else None
-    z = _at(z, _BF16, rows * Z, w, "z") if cfg.activation != EP_ACT_NONE or z is not None else None
-    _check(lib().ep_expert_product_grad(
-        cfg._ref(), _blocks_arg(w, cfg, layout), x, weight, z, _at(d_out, _BF16, rows * N, w, "d_out"),
-        _maybe(d_x, _BF16, rows * K, w, "d_x"), _maybe(d_weight, _BF16, E * Z * K, w, "d_weight"),
-        _maybe(d_bias, _F32, E * Z, w, "d_bias"), ws.data_ptr(), ws.numel(), _raw_stream(stream)), w)
+    needs = cfg._sizes or cfg._needs()
+    n_x, _, n_w, n_b, n_out, n_z = needs[:6]
+    x = _at(x, _BF16, n_x, w, "x") if d_weight is not None or x is not None else None
+    weight = _at(weight, _BF16, n_w, w, "weight") if d_x is not None or weight is not None else None
+    z = _at(z, _BF16, n_z, w, "z") if cfg.activation != EP_ACT_NONE or z is not None else None
+    st = (_lib or lib()).ep_expert_product_grad(
+        cfg._reference or cfg._ref(), _blocks_arg(w, needs, layout), x, weight, z, _at(d_out, _BF16, n_out, w, "d_out"),
+        None if d_x is None else _at(d_x, _BF16, n_x, w, "d_x"),
+        None if d_weight is None else _at(d_weight, _BF16, n_w, w, "d_weight"),
+        None if d_bias is None else _at(d_bias, _F32, n_b, w, "d_bias"), ws.data_ptr(), ws.numel(), _raw_stream(stream))
+    if st:
+        raise EpError(st, w)

@@ -111,7 +111,7 @@ int make_product(const ep_product_config_t* c, ProductGeometry* g) {
 }
 
 struct ProductWorkspace {
-  size_t done;  // uint32 [E][spans of output columns], gradient: follows the header, zeroed with it
+  size_t done;  // uint32 [kDzCounters] in the header: tiles finished (return to 0)
   size_t rows;  // bf16 rows of FP8 x [rows][K], or dz [rows][Z]
   size_t part;  // float [tiles of kDzRows rows][Z]
   size_t total;
@@ -119,9 +119,8 @@ struct ProductWorkspace {
 
 ProductWorkspace product_workspace(const ProductGeometry& g, bool grad) {
   ProductWorkspace w;
-  w.done = 256;
-  const size_t spans = (g.N + kDzColumns - 1) / kDzColumns;
-  w.rows = w.done + (grad ? round256(4 * spans * g.groups.E) : 0);
+  w.done = 64;
+  w.rows = 256;
   size_t bytes = 0;
   if (grad) bytes = g.act == EP_ACT_NONE ? 0 : 2 * static_cast<size_t>(g.groups.rows) * g.Z;
   else if (g.x_fp8) bytes = 2 * static_cast<size_t>(g.groups.rows) * g.K;

@@ -146,7 +146,7 @@ struct ProductGradArgs {
   const uint16_t* d_out;
   uint16_t* dz;       // workspace [rows][Z]; null when the activation is none (dz = d_out)
   float* part;        // workspace [tiles of kDzRows rows][Z]: column sums of dz; null without d_bias
-  uint32_t* done;     // workspace [E][spans of kDzColumns]: tiles whose sums are in part (returns to 0)
+  uint32_t* done;     // workspace [kDzCounters]: tiles whose sums are in part (return to 0)
   uint16_t* d_x;      // may be null
   uint16_t* d_weight; // may be null
   float* d_bias;      // may be null
@@ -156,6 +156,7 @@ struct ProductGradArgs {
 constexpr int kTileRows = 128;  // rows a CTA's products take at once
 constexpr int kDzRows = 64;     // rows whose dz is summed to one partial bias gradient
 constexpr int kDzColumns = 128; // output columns a CTA takes there
+constexpr int kDzCounters = 48; // of finished tiles, in the last 192 bytes of the workspace's header
 // Row tiles of all groups together, at most: whole ones and one part of every group that
 // has a row.
 inline int64_t max_row_tiles(const Groups& q, int tile_rows = kTileRows) {

@@ -232,7 +232,7 @@ cudaError_t launch_dz(DzArgs a, int num_sms, cudaStream_t stream) {
   if (per_sm < 1) return cudaErrorInvalidConfiguration;
   const int64_t most = max_row_tiles(a.groups, kDzRows) * ((a.N + kSpan - 1) / kSpan);
   const int64_t ctas = static_cast<int64_t>(num_sms) * per_sm;
-  if (a.part == nullptr || most > ctas) a.done = nullptr;
+  if (a.part == nullptr || most > ctas || a.groups.E * ((a.N + kSpan - 1) / kSpan) > kDzCounters) a.done = nullptr;
   const cudaError_t st = launch_chained(kern, dim3(static_cast<unsigned>(most < ctas ? most : ctas)), dim3(kThreads), smem, stream, a);
   if (st != cudaSuccess || a.part == nullptr || a.done != nullptr) return st;
   const int sum_per_sm = resident_ctas(reinterpret_cast<const void*>(bias_sum_kernel), kThreads, smem);

@@ -424,9 +424,9 @@ typedef struct ep_product_config {
 } ep_product_config_t;
 
 /* Workspace bytes of ep_expert_product (grad = 0) or ep_expert_product_grad (1); 0 for
- * an invalid configuration. Zero-filled once before first use (ep_workspace_init; the
- * bytes that the same configuration with rows = 0 needs are enough, and a workspace used with
- * other sizes is zero-filled again); one stream at a time; errors are read by ep_check_error. */
+ * an invalid configuration. Its 256-byte header is zero-filled once before first use
+ * (every call leaves its counters zero); one stream at a time; errors are read by
+ * ep_check_error. */
 size_t ep_product_workspace_bytes(const ep_product_config_t* cfg, int32_t grad);
 
 /* Forward. All device pointers, rows dense and 16-byte aligned: x [rows][K], weight

@@ -1,5 +1,4 @@
 """The experts' products and their gradients against the 64-bit definitions."""
-import dataclasses
 import math
 
 import pytest
@@ -77,7 +76,7 @@ class Case:
         dw = torch.full_like(self.w, 33.0) if d_w else None
         db = torch.full((self.E, self.Z), 33.0, device="cuda") if d_b else None
         ws = ep.alloc_product_workspace(cfg, grad=True)
-        ws[ep.ep_product_workspace_bytes(dataclasses.replace(cfg, rows=0), True):].fill_(0xFF)  # NaN where nothing was written
+        ws[256:].fill_(0xFF)  # NaN wherever the workspace is read without being written
         ep.ep_expert_product_grad(cfg, self.lay, self.x, self.w, self.z_in, self.d_out, dx, dw, db, ws)
         assert ep.ep_check_error(ws) == ep.EP_OK
         if d_x:
@@ -221,9 +220,14 @@ def test_each_gradient_alone_and_sms():
 
 
 def test_bias_gradients_repeat_on_one_workspace():
-    """The counters of finished tiles return to zero: the same call again, and from a graph."""
+    """The counters of finished tiles return to zero: the same call again, from a graph, and other sizes."""
     c = Case([700, 0, 65, 64, 900], 40, 264, act="swiglu", bias=True)
     ws = ep.alloc_product_workspace(c.cfg, grad=True)
+    for other in (Case([200], 8, 1000, dense=True, act="silu"), Case([5, 130, 64], 16, 8)):  # they fit the same workspace
+        want = other.grads(False, False, True)[2]
+        got = torch.empty_like(want)
+        ep.ep_expert_product_grad(other.cfg, other.lay, None, None, other.z_in, other.d_out, None, None, got, ws)
+        assert torch.equal(got, want) and not ws[:256].any()
     want = c.grads(False, False, True)[2]
     got = [torch.empty_like(want) for _ in range(4)]
     call = lambda out: ep.ep_expert_product_grad(c.cfg, c.lay, None, None, c.z_in, c.d_out, None, None, out, ws)  # noqa: E731

@@ -101,11 +101,9 @@ def test_product_workspace_closed_forms(ep):
     up = lambda n: (n + 255) // 256 * 256  # noqa: E731
     assert ep.ep_product_workspace_bytes(product_cfg(ep)) == 256
     assert ep.ep_product_workspace_bytes(product_cfg(ep, x_dtype=1)) == 256 + up(100 * 128 * 2)
-    tiles, done = 100 // 64 + 8, up(4 * 8 * 1)
-    assert ep.ep_product_workspace_bytes(product_cfg(ep), True) == 256 + done + up(4 * tiles * 64)
-    assert ep.ep_product_workspace_bytes(product_cfg(ep, activation=4), True) == \
-        256 + done + up(100 * 128 * 2) + up(4 * tiles * 128)
-    assert ep.ep_product_workspace_bytes(product_cfg(ep, out_features=1032), True) == 256 + up(4 * 8 * 9) + up(4 * tiles * 1032)
+    tiles = 100 // 64 + 8
+    assert ep.ep_product_workspace_bytes(product_cfg(ep), True) == 256 + up(4 * tiles * 64)
+    assert ep.ep_product_workspace_bytes(product_cfg(ep, activation=4), True) == 256 + up(100 * 128 * 2) + up(4 * tiles * 128)
 
 
 def test_product_arguments(ep):
