@@ -235,8 +235,10 @@ cudaError_t launch(const uint16_t* A, const uint16_t* B, const RowsArgs& a, int6
 
 // The split is taken when at least two CTAs can share a tile and all clusters run at once;
 // of tiles of 256 and of 128 columns and the ways to split them, the one with the most
-// CTAs at work (the wider tile when equal). Every CTA gets two blocks of the summed
-// index at least.
+// CTAs at work (the wider tile when equal). A single tile of a few rows takes 3.4 us and 0.27
+// a block of 64 of the summed index, the exchange 2.5 us (5 with 100 rows): one row, 512 ->
+// 2048, 6.6 us split and 5.7 not, 1024 -> 2048 7.0 and 7.7; 100 rows, 1024 -> 2048 9.6 and
+// 8.0, 2048 -> 2048 10.5 and 12.3. So it needs 16 blocks, or 32 with more than 32 rows.
 template <int kAct, bool kBMn>
 cudaError_t launch_rows_split(const uint16_t* A, const uint16_t* B, const RowsArgs& a, cudaStream_t stream, bool* done) {
   *done = false;
@@ -249,6 +251,7 @@ cudaError_t launch_rows_split(const uint16_t* A, const uint16_t* B, const RowsAr
   int S = 1;
   bool use_narrow = false;
   int64_t ctas = 0;
+  if (blocks < (rows <= 32 ? 16 : 32)) return cudaSuccess;
   for (int s = 2; s <= 8 && blocks >= s * 2; s *= 2) {
     if (wide <= resident_clusters(s) && wide * s > ctas) S = s, use_narrow = false, ctas = wide * s;
     if (narrow <= resident_clusters(s) && narrow * s > ctas) S = s, use_narrow = true, ctas = narrow * s;

@@ -149,6 +149,8 @@ SHAPES = {
     "long_groups": dict(counts=[700, 257, 900], K=392, N=264, act="gelu", bias=True, residual=True),
     "long_groups_gated": dict(counts=[1000, 0, 513, 400], K=192, N=200, act="swiglu", R=2, align=8, bias=True),
     "long_dense": dict(counts=[1003], K=1032, N=776, dense=True, act="relu", bias=True, residual=True),
+    "split_groups": dict(counts=[5, 0, 20], K=1096, N=200, act="gelu", bias=True, residual=True),
+    "split_gated_rows": dict(counts=[90], K=2120, N=1104, dense=True, act="swiglu", bias=True, residual=True),
     "few_rows_each": dict(counts=[2, 8, 1, 5, 16, 3, 9, 32], K=1024, N=640, R=2, act="swiglu"),
 }
 
