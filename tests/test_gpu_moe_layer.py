@@ -57,7 +57,8 @@ def test_training_step(size):
     # forward, then the gradients of y, h, z and the rows; eight of them are allowed
     tol = 8 * 2 ** -9
     assert off(out, want) <= tol
-    assert abs(float(layer.route.balance_loss) - float(loss)) <= 1e-5 * float(loss)
+    loss = float(loss.detach())
+    assert abs(float(layer.route.balance_loss) - loss) <= 1e-5 * loss
     assert off(d_up, gup) <= tol and off(d_down, gdown) <= tol
     assert off(layer.d_logits, gl) <= tol
     gx = gx + gl @ layer.router.double()
