@@ -60,7 +60,7 @@ int make_route(const ep_route_config_t* c, RouteGeometry* g) {
   g->normalize = c->normalize;
   g->scale = c->scale;
   // one token per warp at least, and no more CTAs in all than kRouteCtas (one per segment at least)
-  int C = (c->num_tokens + kRouteWarps - 1) / kRouteWarps;
+  int C = c->num_tokens / kRouteWarps + (c->num_tokens % kRouteWarps != 0);
   const int most = kRouteCtas / c->num_segments;
   if (C > most) C = most;
   g->C = C < 1 ? 1 : C;

@@ -269,23 +269,24 @@ __global__ void __launch_bounds__(kRouteThreads, EPL <= 8 ? 4 : EPL <= 16 ? 2 : 
   const int place = (part + grp * parts) % cells;
   const uint32_t group_magic = 0xFFFFFFFFu / static_cast<uint32_t>(per_group) + 1u;  // e / per_group, e < 2^16, by a high product
 
-  const int step = g.C * kRouteWarps;
+  // unsigned: T is below 2^31, so t + step does not wrap
+  const uint32_t T = static_cast<uint32_t>(g.T), step = static_cast<uint32_t>(g.C * kRouteWarps);
   const int64_t first = static_cast<int64_t>(seg) * g.T;
   // the next token's logits load while this one is worked on
   float next[EPL];
-  int t = cta * kRouteWarps + warp;
+  uint32_t t = static_cast<uint32_t>(cta * kRouteWarps + warp);
   uint8_t next_on = 1;
-  if (t < g.T) {
+  if (t < T) {
     load_row<EPL, kBf16, kVec>(a.logits, first + t, E, lane, next);
     if (a.mask != nullptr) next_on = __ldg(a.mask + first + t);
   }
-  for (; t < g.T; t += step) {
+  for (; t < T; t += step) {
     float l[EPL];
 #pragma unroll
     for (int j = 0; j < EPL; ++j) l[j] = next[j];
     const bool on = next_on != 0;
     const int64_t token = first + t;
-    if (t + step < g.T) {
+    if (t + step < T) {
       load_row<EPL, kBf16, kVec>(a.logits, token + step, E, lane, next);
       if (a.mask != nullptr) next_on = __ldg(a.mask + token + step);
     }
@@ -579,7 +580,8 @@ __global__ void __launch_bounds__(kRouteThreads, EPL <= 8 ? 4 : EPL <= 16 ? 2 : 
       coef[j] = a.d_loss != nullptr && e < E ? f * static_cast<float>(__ldg(a.count + static_cast<size_t>(seg) * E + e)) : 0.f;
     }
   }
-  const int step = g.C * kRouteWarps;
+  // unsigned: T is below 2^31, so t + step does not wrap
+  const uint32_t T = static_cast<uint32_t>(g.T), step = static_cast<uint32_t>(g.C * kRouteWarps);
   const int64_t first = static_cast<int64_t>(seg) * g.T;
   float next[EPL];
   int64_t next_e = -1;
@@ -595,10 +597,10 @@ __global__ void __launch_bounds__(kRouteThreads, EPL <= 8 ? 4 : EPL <= 16 ? 2 : 
     }
     if (a.mask != nullptr) next_on = __ldg(a.mask + token);
   };
-  int t = cta * kRouteWarps + warp;
-  if (t < g.T) fetch(first + t);
+  uint32_t t = static_cast<uint32_t>(cta * kRouteWarps + warp);
+  if (t < T) fetch(first + t);
   bool bad = false;
-  for (; t < g.T; t += step) {
+  for (; t < T; t += step) {
     const int64_t token = first + t;
     float l[EPL];
 #pragma unroll
@@ -606,7 +608,7 @@ __global__ void __launch_bounds__(kRouteThreads, EPL <= 8 ? 4 : EPL <= 16 ? 2 : 
     const int64_t e64 = next_e;
     const float gw = next_g * g.scale;
     const bool on = next_on != 0;
-    if (t + step < g.T) fetch(token + step);
+    if (t + step < T) fetch(token + step);
     clean<EPL>(l);
     const bool chosen = on && e64 >= 0 && e64 < E;
     bad |= e64 < -1 || e64 >= E;
