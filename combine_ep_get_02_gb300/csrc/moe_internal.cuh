@@ -159,7 +159,7 @@ constexpr int kDzColumns = 128; // output columns a CTA takes there
 constexpr int kDzCounters = 48; // of finished tiles, in the last 192 bytes of the workspace's header
 // Row tiles of all groups together, at most: whole ones and one part of every group that
 // has a row.
-inline int64_t max_row_tiles(const Groups& q, int tile_rows = kTileRows) {
+__host__ __device__ inline int64_t max_row_tiles(const Groups& q, int tile_rows = kTileRows) {
   const int64_t groups = q.count == nullptr ? 1 : q.E < q.rows ? q.E : q.rows;
   return q.rows / tile_rows + groups;
 }

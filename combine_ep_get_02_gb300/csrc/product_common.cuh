@@ -8,32 +8,40 @@ namespace ep {
 
 // prefix[g] = row tiles of the groups before g, prefix[E] = of all. Called by every
 // thread of the CTA (a multiple of 32, at most 1024); ends with a CTA barrier. Cut
-// groups latch kErrOverflow.
+// groups latch kErrOverflow. Blocks that lie apart never need more than max_row_tiles, which
+// the workspace and the tiles' numbering count on; of blocks that overlap (a layout of
+// another configuration) the tiles past that are left out and latch it too.
 template <int kThreads>
 __device__ __forceinline__ void build_prefix(const Groups& q, int tile_rows, int* prefix, uint32_t* err) {
   __shared__ int s_warp[kThreads / 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int per = (q.E + kThreads - 1) / kThreads;
   const int g0 = min(q.E, static_cast<int>(threadIdx.x) * per), g1 = min(q.E, g0 + per);
+  const int most = static_cast<int>(max_row_tiles(q, tile_rows));  // below 2^26, as tiles have 64 rows at least
   bool cut = false;
+  auto add = [&](int a, int b) {
+    cut = cut || a + b > most;
+    return min(a + b, most);
+  };
   int sum = 0;
-  for (int g = g0; g < g1; ++g) sum += (group_rows(q, g, &cut).count + tile_rows - 1) / tile_rows;
-  if (cut && err != nullptr) atomicOr(err, kErrOverflow);
+  for (int g = g0; g < g1; ++g) sum = add(sum, (group_rows(q, g, &cut).count + tile_rows - 1) / tile_rows);
   int incl = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int v = __shfl_up_sync(kFullMask, incl, o);
-    if (lane >= o) incl += v;
+    if (lane >= o) incl = add(incl, v);
   }
   if (lane == 31) s_warp[warp] = incl;
+  int before = __shfl_up_sync(kFullMask, incl, 1);
+  if (lane == 0) before = 0;
   __syncthreads();
-  int before = incl - sum;
-  for (int w = 0; w < warp; ++w) before += s_warp[w];
+  for (int w = 0; w < warp; ++w) before = add(before, s_warp[w]);
   for (int g = g0; g < g1; ++g) {
     prefix[g] = before;
-    before += (group_rows(q, g).count + tile_rows - 1) / tile_rows;
+    before = add(before, (group_rows(q, g).count + tile_rows - 1) / tile_rows);
     if (g == q.E - 1) prefix[q.E] = before;
   }
+  if (cut && err != nullptr) atomicOr(err, kErrOverflow);
   __syncthreads();
 }
 

@@ -412,7 +412,8 @@ typedef struct ep_product_config {
   int32_t num_ranks;    /* R of the layout                                         */
   int32_t num_experts;  /* E, a multiple of R, 1..4096                             */
   int64_t rows;         /* rows of x, z, out, residual, 0..2^31-1 (ep_recv_rows of the
-                           dispatch); a block past them is cut and latches EP_ERR_OVERFLOW */
+                           dispatch); a block past them is cut and latches EP_ERR_OVERFLOW,
+                           as do blocks that overlap (some of their rows are left out)  */
   int32_t in_features;  /* K, a multiple of 8 (of 128 with FP8), up to 2^20         */
   int32_t out_features; /* N of out, a multiple of 8, up to 2^20                    */
   int32_t activation;   /* EP_ACT_*                                                 */
