@@ -463,6 +463,14 @@ def _maybe(t, dtype, numel: int, where: str, name: str):
     return None if t is None else _at(t, dtype, numel, where, name)
 
 
+def _space(ws, where: str):
+    """Address and bytes of a workspace; refuses one that is not dense GPU memory."""
+    if ws is not None and ws.is_cuda and ws.is_contiguous():
+        return ws.data_ptr(), ws.nbytes
+    why = "is missing" if ws is None else "is not on the GPU" if not ws.is_cuda else "is not contiguous"
+    raise EpError(EP_ERR_WORKSPACE, f"{where}: the workspace {why}")
+
+
 _current_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 
 
@@ -614,8 +622,8 @@ def ep_route(cfg: RouteConfig, logits: torch.Tensor, choice_bias, token_mask, ou
     out.balance_loss also the counts, the probability sums and the balance loss."""
     _, x, m = _route_args("ep_route", cfg, logits, token_mask, out)
     b = None if choice_bias is None else _at(choice_bias, _F32, cfg.num_experts, "ep_route", "choice_bias")
-    st = (_lib or lib()).ep_route(cfg._reference or cfg._ref(), x, b, m, out._reference or out._ref(), ws.data_ptr(),
-                                  ws.numel(), _raw_stream(stream))
+    st = (_lib or lib()).ep_route(cfg._reference or cfg._ref(), x, b, m, out._reference or out._ref(),
+                                  *_space(ws, "ep_route"), _raw_stream(stream))
     if st:
         raise EpError(st, "ep_route")
 
@@ -629,7 +637,7 @@ def ep_route_grad(cfg: RouteConfig, logits: torch.Tensor, token_mask, route: Rou
     dw = None if d_weights is None else _at(d_weights, _F32, needs[2], w, "d_weights")
     dl = None if d_loss is None else _at(d_loss, _F32, 1, w, "d_loss")
     st = (_lib or lib()).ep_route_grad(cfg._reference or cfg._ref(), x, m, route._reference or route._ref(), dw, dl,
-                                       _at(d_logits, needs[0], needs[1], w, "d_logits"), ws.data_ptr(), ws.numel(),
+                                       _at(d_logits, needs[0], needs[1], w, "d_logits"), *_space(ws, w),
                                        _raw_stream(stream))
     if st:
         raise EpError(st, w)
@@ -649,7 +657,7 @@ def ep_combine_grad(cfg: Config, layout: Layout, y, topk_idx: torch.Tensor, topk
     _check((_lib or lib()).ep_combine_grad(
         cfg._reference or cfg._ref(), layout._reference or layout._ref(), y, _at(topk_idx, _I64, NK, w, "topk_idx"),
         _at(topk_weights, _F32, NK, w, "topk_weights"), _at(d_out, _BF16, N * H, w, "d_out"),
-        _maybe(d_y, _BF16, rows * H, w, "d_y"), _maybe(d_weights, _F32, NK, w, "d_weights"), ws.data_ptr(), ws.numel(),
+        _maybe(d_y, _BF16, rows * H, w, "d_y"), _maybe(d_weights, _F32, NK, w, "d_weights"), *_space(ws, w),
         _raw_stream(stream)), w)
 
 
@@ -679,7 +687,7 @@ def ep_expert_product(cfg: ProductConfig, layout, x: torch.Tensor, x_sf, weight:
         cfg._reference or cfg._ref(), _blocks_arg(w, needs, layout), x, x_sf, _at(weight, _BF16, n_w, w, "weight"),
         None if bias is None else _at(bias, _BF16, n_b, w, "bias"),
         None if residual is None else _at(residual, _BF16, n_out, w, "residual"),
-        None if z is None else _at(z, _BF16, n_z, w, "z"), _at(out, _BF16, n_out, w, "out"), ws.data_ptr(), ws.numel(),
+        None if z is None else _at(z, _BF16, n_z, w, "z"), _at(out, _BF16, n_out, w, "out"), *_space(ws, w),
         _raw_stream(stream))
     if st:
         raise EpError(st, w)
@@ -698,6 +706,6 @@ def ep_expert_product_grad(cfg: ProductConfig, layout, x, weight, z, d_out: torc
         cfg._reference or cfg._ref(), _blocks_arg(w, needs, layout), x, weight, z, _at(d_out, _BF16, n_out, w, "d_out"),
         None if d_x is None else _at(d_x, _BF16, n_x, w, "d_x"),
         None if d_weight is None else _at(d_weight, _BF16, n_w, w, "d_weight"),
-        None if d_bias is None else _at(d_bias, _F32, n_b, w, "d_bias"), ws.data_ptr(), ws.numel(), _raw_stream(stream))
+        None if d_bias is None else _at(d_bias, _F32, n_b, w, "d_bias"), *_space(ws, w), _raw_stream(stream))
     if st:
         raise EpError(st, w)
