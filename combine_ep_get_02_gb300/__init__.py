@@ -78,6 +78,7 @@ class _KeepsStruct:
         object.__setattr__(self, "_struct", None)
         object.__setattr__(self, "_reference", None)
         object.__setattr__(self, "_sizes", None)
+        object.__setattr__(self, "_lanes", None)
 
     def _c(self):
         st = self.__dict__.get("_struct")
@@ -94,17 +95,22 @@ class _KeepsStruct:
             object.__setattr__(self, "_reference", r)
         return r
 
-    def _checked(self, where: str, fields):
+    def _count(self, where: str, fields):
         """Element counts of the tensors named in `fields` ((name, dtype) pairs; -1 for None),
-        refused as by _at; kept, like the struct that holds their addresses."""
+        refused as by _at."""
+        n = []
+        for name, dtype in fields:
+            t = getattr(self, name)
+            if t is not None:
+                _at(t, dtype, 0, where, name)
+            n.append(-1 if t is None else t.numel())
+        return n
+
+    def _checked(self, where: str, fields):
+        """_count, kept like the struct that holds the tensors' addresses."""
         n = self.__dict__.get("_sizes")
         if n is None:
-            n = []
-            for name, dtype in fields:
-                t = getattr(self, name)
-                if t is not None:
-                    _at(t, dtype, 0, where, name)
-                n.append(-1 if t is None else t.numel())
+            n = self._count(where, fields)
             object.__setattr__(self, "_sizes", n)
         return n
 
@@ -595,6 +601,11 @@ _ROUTE_FIELDS = (("topk_idx", _I64), ("topk_weights", _F32), ("expert_count", _I
 _BLOCK_FIELDS = (("exp_cnt", _I32), ("exp_base", _I32), ("exp_region", _I32))
 
 
+# what leads the combine's gradient to a lane's row: slots, compact, packed, per-expert blocks
+_LANE_FIELDS = (("slot_map", _I32), ("recv_psum", _I32), ("recv_region", _I32))
+_LANE_FIELDS = (*(_LANE_FIELDS[:i] for i in (1, 2, 3)), (("exp_pos", _I32), ("exp_region", _I32)))
+
+
 def _too_small(where, obj, fields, need):
     for (name, dtype), n in zip(fields, need):
         t = getattr(obj, name)
@@ -652,7 +663,16 @@ def ep_combine_grad(cfg: Config, layout: Layout, y, topk_idx: torch.Tensor, topk
     if rows is None:
         rows = max(ep_recv_rows(cfg), 0)
         object.__setattr__(cfg, "_sizes", rows)
-    NK = N * cfg.num_topk
+    NK, R = N * cfg.num_topk, cfg.num_ranks
+    fields = _LANE_FIELDS[3 if cfg.expand else min(max(cfg.compact_recv, 0), 2)]
+    kept = layout._lanes
+    if kept is None or kept[0] is not fields:
+        kept = (fields, layout._count(w, fields))
+        object.__setattr__(layout, "_lanes", kept)
+    need = (NK, R) if cfg.expand else (NK, R * R, R)
+    for n, least in zip(kept[1], need):
+        if -1 < n < least:
+            _too_small(w, layout, fields, need)
     y = _at(y, _BF16, rows * H, w, "y") if d_weights is not None or y is not None else None
     _check((_lib or lib()).ep_combine_grad(
         cfg._reference or cfg._ref(), layout._reference or layout._ref(), y, _at(topk_idx, _I64, NK, w, "topk_idx"),

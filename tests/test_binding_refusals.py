@@ -91,3 +91,38 @@ def test_workspaces_outside_the_gpu(stub, name):
     assert stub.calls == 0
     call(Device(1 << 20, dtype=U8))
     assert stub.calls == 1
+
+
+@pytest.mark.parametrize("mode,names", [
+    (dict(), ("slot_map",)), (dict(compact_recv=1), ("slot_map", "recv_psum")),
+    (dict(compact_recv=2), ("slot_map", "recv_psum", "recv_region")), (dict(expand=1), ("exp_pos", "exp_region"))])
+def test_layouts_of_a_smaller_configuration(stub, mode, names):
+    """The combine's gradient reads a row's place from these and writes there."""
+    R, T, K, H = 4, 8, 4, 64
+    cfg = ep.Config(1, R, 16, K, T, T, H, **mode)
+    full = dict(slot_map=R * T * K, exp_pos=R * T * K, recv_psum=R * R, recv_region=R, exp_region=R)
+    lay = ep.Layout(*[None] * 6)
+    for name in names:
+        setattr(lay, name, Device(full[name], dtype=I32))
+    y, tok = Device(ep.ep_recv_rows(cfg), H, dtype=BF), Device(R, T, H, dtype=BF)
+    idx, wt, ws = Device(R, T, K, dtype=I64), Device(R, T, K), Device(1 << 20, dtype=U8)
+    call = lambda: ep.ep_combine_grad(cfg, lay, y, idx, wt, tok, y, wt, ws, stream=0)  # noqa: E731
+    call()
+    assert stub.calls == 1
+    for name in names:
+        for t, why in ((Device(full[name] - 1, dtype=I32), f"{full[name] - 1} elements, {full[name]} needed"),
+                       (Device(full[name], dtype=I64), "int64"), (torch.zeros(full[name], dtype=I32), "not on the GPU")):
+            setattr(lay, name, t)
+            with pytest.raises(ep.EpError, match=f"{name} .*{why}") as e:
+                call()
+            assert e.value.status == ep.EP_ERR_INVALID_ARG
+        setattr(lay, name, Device(full[name], dtype=I32))
+    assert stub.calls == 1
+    call()
+    assert stub.calls == 2
+    cfg.num_tokens = T + 1  # the layout was looked at with the smaller configuration
+    more = dict(y=Device(ep.ep_recv_rows(cfg), H, dtype=BF), tok=Device(R, T + 1, H, dtype=BF),
+                idx=Device(R, T + 1, K, dtype=I64), wt=Device(R, T + 1, K))
+    with pytest.raises(ep.EpError, match=f"{names[0]} has"):
+        ep.ep_combine_grad(cfg, lay, more["y"], more["idx"], more["wt"], more["tok"], more["y"], more["wt"], ws, stream=0)
+    assert stub.calls == 2
