@@ -606,13 +606,14 @@ __global__ void __launch_bounds__(kRouteThreads, EPL <= 8 ? 4 : EPL <= 16 ? 2 : 
 #pragma unroll
     for (int j = 0; j < EPL; ++j) l[j] = next[j];
     const int64_t e64 = next_e;
-    const float gw = next_g * g.scale;
+    const float given = next_g;
     const bool on = next_on != 0;
     if (t + step < T) fetch(token + step);
     clean<EPL>(l);
     const bool chosen = on && e64 >= 0 && e64 < E;
     bad |= e64 < -1 || e64 >= E;
     const int e = chosen ? static_cast<int>(e64) : 0;
+    const float gw = chosen ? given * g.scale : 0.f;  // what stands at an absent lane may be a NaN
 
     float lv = -kInf;
     if (chosen)

@@ -369,7 +369,8 @@ int ep_route(const ep_route_config_t* cfg, const void* logits, const float* choi
 
 /* Gradient of the logits through the weights and the loss; the choice and the
  * counts are constants. `route` holds ep_route's outputs (topk_idx; with d_loss
- * also expert_count and num_valid). d_weights: device fp32 [N][K] or NULL (zero).
+ * also expert_count and num_valid). d_weights: device fp32 [N][K] or NULL (zero); what
+ * stands where topk_idx is -1 is not used.
  * d_loss: device fp32 [1], the gradient of balance_loss (its coefficient included),
  * or NULL (zero). d_logits: device [N][E] of the logits' type, every element
  * written (zero for padding tokens), 16-byte aligned. A topk_idx outside [-1, E)
