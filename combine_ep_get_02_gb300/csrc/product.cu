@@ -35,10 +35,30 @@ __host__ __device__ constexpr int stage_count(int bn) {
   return kRingBytes / stage_bytes(bn) < kMaxStages ? kRingBytes / stage_bytes(bn) : kMaxStages;
 }
 
-template <int kAct, bool kBMn>
+// kParts: a tile's sum is taken `part` blocks at a time, as the clusters of product_split.cu do
+// it. The epilogue warps add each part to the sum of those before, which lies in the half of TMEM
+// that accumulators of 128 columns leave, and finish the tile after the last. It runs
+// the calls that are allowed fewer SMs than those clusters take.
+constexpr int kSumColumn = 128;
+// v += the sum kept at `at` (0 before the first part), which goes back there unless v is the last
+__device__ __forceinline__ void add_part(uint32_t at, float (&v)[32], bool first, bool last) {
+  float sum[32];
+  if (!first) {
+    tmem_ld32(at, sum);
+    tmem_ld_wait();
+  }
+#pragma unroll
+  for (int j = 0; j < 32; ++j) v[j] = (first ? 0.f : sum[j]) + v[j];
+  if (!last) {
+    tmem_st32(at, v);
+    tmem_st_wait();
+  }
+}
+
+template <int kAct, bool kBMn, bool kParts>
 __global__ void __launch_bounds__(kThreads, 1)
     rows_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_low,
-                const __grid_constant__ CUtensorMap map_b, RowsArgs a, int bn) {
+                const __grid_constant__ CUtensorMap map_b, RowsArgs a, int bn, int part) {
   constexpr bool kGated = kAct == EP_ACT_SWIGLU;
   const int cols = kGated ? bn / 2 : bn;  // output columns of a tile
   const int b_bytes = bn * kBK * 2;
@@ -81,6 +101,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = s_tmem;
   const Tiles<kBM> tiles(a.groups, prefix, a.epi.cols, cols);
   const int blocks = (a.sum + kBK - 1) / kBK;
+  const int parts = kParts ? (blocks + part - 1) / part : 1;
   auto give_up = [&] {
     s_abort = 1;
     atomicOr(a.err, kErrTimeout);
@@ -124,32 +145,35 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t idesc = idesc_bf16(kBM, bn, false, kBMn);
       uint32_t n = 0, acc = 0;
       bool ok = true;
-      for (int i = blockIdx.x; ok && i < tiles.total; i += gridDim.x, ++acc) {
-        const uint32_t b = acc & 1u;
-        if (s_abort || !mbar_wait_timed(smem_addr(&s_acc_empty[b]), (acc >> 1 & 1u) ^ 1u)) {
-          if (!s_abort) give_up();
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const uint32_t d = tmem + b * kMaxBN;
-        for (int kb = 0; kb < blocks; ++kb, ++n) {
-          const uint32_t s = n % kStages;
-          if (s_abort || !mbar_wait_timed(smem_addr(&s_full[s]), n / kStages & 1u)) {
+      for (int i = blockIdx.x; ok && i < tiles.total; i += gridDim.x) {
+        for (int p = 0; ok && p < parts; ++p, ++acc) {
+          const uint32_t b = acc & 1u;
+          if (s_abort || !mbar_wait_timed(smem_addr(&s_acc_empty[b]), (acc >> 1 & 1u) ^ 1u)) {
             if (!s_abort) give_up();
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t sa = stage0 + s * kStageBytes, sb = sa + kABytes;
-          const uint64_t da = desc_k_major(sa);
-          const uint64_t db = kBMn ? desc_mn_major(sb, kBK * 128) : desc_k_major(sb);
+          const uint32_t d = tmem + b * kMaxBN;
+          const int k0 = kParts ? p * part : 0, k1 = kParts ? min(blocks, k0 + part) : blocks;
+          for (int kb = k0; kb < k1; ++kb, ++n) {
+            const uint32_t s = n % kStages;
+            if (s_abort || !mbar_wait_timed(smem_addr(&s_full[s]), n / kStages & 1u)) {
+              if (!s_abort) give_up();
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t sa = stage0 + s * kStageBytes, sb = sa + kABytes;
+            const uint64_t da = desc_k_major(sa);
+            const uint64_t db = kBMn ? desc_mn_major(sb, kBK * 128) : desc_k_major(sb);
 #pragma unroll
-          for (int k = 0; k < kBK / 16; ++k)
-            mma_bf16(d, da + k * kStepK, db + k * (kBMn ? kStepMN : kStepK), idesc, kb > 0 || k > 0);
-          mma_commit(smem_addr(&s_empty[s]));
+            for (int k = 0; k < kBK / 16; ++k)
+              mma_bf16(d, da + k * kStepK, db + k * (kBMn ? kStepMN : kStepK), idesc, kb > k0 || k > 0);
+            mma_commit(smem_addr(&s_empty[s]));
+          }
+          if (ok) mma_commit(smem_addr(&s_acc_full[b]));
         }
-        if (ok) mma_commit(smem_addr(&s_acc_full[b]));
       }
       if (!ok) {  // the products in flight finish before the CTA's memory goes
         mma_commit(smem_addr(&s_drained));
@@ -161,31 +185,40 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int half = (warp - 2) >> 2;
     const uint32_t patch = patch0 + (warp - 2) * kPatchBytes;
     uint32_t acc = 0;
-    for (int i = blockIdx.x; i < tiles.total; i += gridDim.x, ++acc) {
-      const uint32_t b = acc & 1u;
+    bool ok = true;
+    for (int i = blockIdx.x; ok && i < tiles.total; i += gridDim.x) {
       const Tile t = tiles.at(i);
-      bool ok = s_abort == 0 && mbar_wait_timed(smem_addr(&s_acc_full[b]), acc >> 1 & 1u);
-      ok = __all_sync(kFullMask, ok);
-      if (!ok) {
-        if (lane == 0 && !s_abort) give_up();
-        break;
-      }
-      tc_fence_after();
       const int m = quarter * 32;
       const int64_t row = static_cast<int64_t>(t.begin) + m;
       const int rows = t.rows - m;
-      const uint32_t d = tmem + b * kMaxBN + (static_cast<uint32_t>(m) << 16);
-      for (int c = half * 32; c < cols; c += 64) {
-        if (rows <= 0 || t.n0 + c >= a.epi.cols) break;
-        float v[32], u[kGated ? 32 : 1];
-        tmem_ld32(d + c, v);
-        if constexpr (kGated) tmem_ld32(d + cols + c, u);
-        tmem_ld_wait();
-        finish_rows<kAct>(a.epi, patch, v, u, t.g, row, rows, t.n0 + c, lane);
+      for (int p = 0; p < parts; ++p, ++acc) {
+        const uint32_t b = acc & 1u;
+        ok = s_abort == 0 && mbar_wait_timed(smem_addr(&s_acc_full[b]), acc >> 1 & 1u);
+        ok = __all_sync(kFullMask, ok);
+        if (!ok) {
+          if (lane == 0 && !s_abort) give_up();
+          break;
+        }
+        tc_fence_after();
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(m) << 16), d = lanes + b * kMaxBN;
+        for (int c = half * 32; c < cols; c += 64) {
+          if (rows <= 0 || t.n0 + c >= a.epi.cols) break;
+          float v[32], u[kGated ? 32 : 1];
+          tmem_ld32(d + c, v);
+          if constexpr (kGated) tmem_ld32(d + cols + c, u);
+          tmem_ld_wait();
+          if constexpr (kParts) {
+            const bool last = p + 1 == parts;
+            add_part(lanes + kSumColumn + c, v, p == 0, last);
+            if constexpr (kGated) add_part(lanes + kSumColumn + cols + c, u, p == 0, last);
+            if (!last) continue;
+          }
+          finish_rows<kAct>(a.epi, patch, v, u, t.g, row, rows, t.n0 + c, lane);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&s_acc_empty[b]));
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_addr(&s_acc_empty[b]));
     }
   }
   __syncwarp();
@@ -197,7 +230,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 }  // namespace
 
 template <int kAct, bool kBMn>
-cudaError_t launch_rows_single(const uint16_t* A, const uint16_t* B, const RowsArgs& a, int bn, int num_sms, cudaStream_t stream) {
+cudaError_t launch_rows_single(const uint16_t* A, const uint16_t* B, const RowsArgs& a, int bn, int part, int num_sms,
+                               cudaStream_t stream) {
   const int halves = kAct == EP_ACT_SWIGLU ? 2 : 1;
   CUtensorMap map_a, map_low, map_b;
   cudaError_t st = make_rows_maps<kBMn>(&map_a, &map_b, A, B, a, kBM, bn / 2);
@@ -206,22 +240,23 @@ cudaError_t launch_rows_single(const uint16_t* A, const uint16_t* B, const RowsA
   const uint32_t box[2] = {kBK, kLowRows};
   st = make_tensor_map(&map_low, A, 2, size, box);
   if (st != cudaSuccess) return st;
-  auto kern = rows_kernel<kAct, kBMn>;
+  auto kern = part > 0 ? rows_kernel<kAct, kBMn, true> : rows_kernel<kAct, kBMn, false>;
   const size_t smem = 1024 + kRingBytes + kEpilogueWarps * kPatchBytes + sizeof(int) * (static_cast<size_t>(a.groups.E) + 1);
   if (resident_ctas(reinterpret_cast<const void*>(kern), kThreads, smem) < 1) return cudaErrorInvalidConfiguration;
   const int64_t tiles = max_row_tiles(a.groups) * ((a.epi.cols + bn / halves - 1) / (bn / halves));
   const unsigned grid = static_cast<unsigned>(tiles < num_sms ? tiles : num_sms);
-  return launch_chained(kern, dim3(grid), dim3(kThreads), smem, stream, map_a, map_low, map_b, a, bn);
+  return launch_chained(kern, dim3(grid), dim3(kThreads), smem, stream, map_a, map_low, map_b, a, bn, part);
 }
 #define X(act, mn) \
-  template cudaError_t launch_rows_single<act, mn>(const uint16_t*, const uint16_t*, const RowsArgs&, int, int, cudaStream_t);
+  template cudaError_t launch_rows_single<act, mn>(const uint16_t*, const uint16_t*, const RowsArgs&, int, int, int, cudaStream_t);
 EP_ROWS_INSTANCES(X)
 #undef X
 
 namespace {
 
 // Which kernel and tile width. A split of the summed index when the tiles would leave most
-// SMs idle. Pairs when their tiles of 256 rows are mostly full: groups of 384 rows on average
+// SMs idle; if its clusters want more SMs than are allowed, single CTAs sum the same parts.
+// Pairs when their tiles of 256 rows are mostly full: groups of 384 rows on average
 // (8 groups of about 350 rows, 3336 -> 2408: pairs 77 us, single CTAs 66). The width is
 // the one with the least rounds of tiles x cycles of a 64-block of the summed index,
 // which are 2 a column of the tile (the tensor cores) or the tile's bytes at the 64 a
@@ -233,9 +268,8 @@ namespace {
 // (MN-major tiles load whole panels of 64 columns, so the widths between gain nothing there.)
 template <int kAct, bool kBMn>
 cudaError_t launch_rows(const uint16_t* A, const uint16_t* B, const RowsArgs& a, int num_sms, cudaStream_t stream) {
-  bool done = false;
-  const cudaError_t st = launch_rows_split<kAct, kBMn>(A, B, a, stream, &done);
-  if (done || st != cudaSuccess) return st;
+  const SplitPlan split = plan_rows_split(a, kAct == EP_ACT_SWIGLU);
+  if (split.S > 1 && split.tiles * split.S <= num_sms) return launch_rows_split<kAct, kBMn>(A, B, a, split, stream);
   const int halves = kAct == EP_ACT_SWIGLU ? 2 : 1;
   const int64_t rows = a.groups.rows, groups = a.groups.count == nullptr ? 1 : a.groups.E < rows ? a.groups.E : rows;
   auto cost = [&](int tile_rows, int bn, int at_once) {
@@ -247,15 +281,16 @@ cudaError_t launch_rows(const uint16_t* A, const uint16_t* B, const RowsArgs& a,
     const int64_t bytes = kABytes + 128 * (kBMn ? (b_rows + 63) / 64 * 64 : b_rows);
     return (tiles + at_once - 1) / at_once * (2 * bn > bytes / 64 ? 2 * bn : bytes / 64);
   };
-  const bool pair = rows >= 384 * groups && num_sms >= 2;
+  const bool by_parts = split.S > 1;
+  const bool pair = !by_parts && rows >= 384 * groups && num_sms >= 2;
   int bn = kMaxBN;
   int64_t least = INT64_MAX;
-  for (int w = kMaxBN; w >= (pair ? 128 : 64); w = pair ? w - 32 : w / 2) {
+  for (int w = by_parts ? kMaxBN / 2 : kMaxBN; w >= (pair ? 128 : 64); w = pair ? w - 32 : w / 2) {
     const int64_t c = pair ? cost(2 * kBM, w, num_sms / 2) : cost(kBM, w, num_sms);
     if (c < least) least = c, bn = w;
   }
   return pair ? launch_rows_pair<kAct, kBMn>(A, B, a, bn, num_sms, stream)
-              : launch_rows_single<kAct, kBMn>(A, B, a, bn, num_sms, stream);
+              : launch_rows_single<kAct, kBMn>(A, B, a, bn, by_parts ? split.part : 0, num_sms, stream);
 }
 
 }  // namespace

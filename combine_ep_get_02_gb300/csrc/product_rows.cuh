@@ -66,15 +66,26 @@ cudaError_t make_rows_maps(CUtensorMap* map_a, CUtensorMap* map_b, const uint16_
   return make_tensor_map(map_b, B, 3, size, box);
 }
 
+// How a call with few tiles is shared out (product_split.cu), from its sizes alone: S CTAs to a
+// tile, each `part` blocks of the summed index; S = 1: not at all. The parts are summed apart
+// and added in their order, whatever runs them, so that results do not depend on the SMs.
+struct SplitPlan {
+  int S, part;
+  bool narrow;  // tiles of 128 rows of B instead of 256
+  int64_t tiles;
+};
+SplitPlan plan_rows_split(const RowsArgs& a, bool gated);
+
 // The three kernels: a CTA per tile of 128 rows, CTA pairs on tiles of 256 rows (both with
 // tiles of `bn` rows of B), and clusters that split the summed index of a few tiles.
+// The first also sums by parts of `part` blocks (0: all at once), on tiles of 128 rows of B at most.
 template <int kAct, bool kBMn>
-cudaError_t launch_rows_single(const uint16_t* A, const uint16_t* B, const RowsArgs& a, int bn, int num_sms, cudaStream_t stream);
+cudaError_t launch_rows_single(const uint16_t* A, const uint16_t* B, const RowsArgs& a, int bn, int part, int num_sms,
+                               cudaStream_t stream);
 template <int kAct, bool kBMn>
 cudaError_t launch_rows_pair(const uint16_t* A, const uint16_t* B, const RowsArgs& a, int bn, int num_sms, cudaStream_t stream);
-// *done says whether the rule took the call (see there).
 template <int kAct, bool kBMn>
-cudaError_t launch_rows_split(const uint16_t* A, const uint16_t* B, const RowsArgs& a, cudaStream_t stream, bool* done);
+cudaError_t launch_rows_split(const uint16_t* A, const uint16_t* B, const RowsArgs& a, const SplitPlan& plan, cudaStream_t stream);
 
 #define EP_ROWS_INSTANCES(X) \
   X(EP_ACT_NONE, false) X(EP_ACT_RELU, false) X(EP_ACT_SILU, false) X(EP_ACT_GELU, false) X(EP_ACT_SWIGLU, false) X(EP_ACT_NONE, true)

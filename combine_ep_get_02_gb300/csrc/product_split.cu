@@ -239,30 +239,31 @@ cudaError_t launch(const uint16_t* A, const uint16_t* B, const RowsArgs& a, int6
 // a block of 64 of the summed index, the exchange 2.5 us (5 with 100 rows): one row, 512 ->
 // 2048, 6.6 us split and 5.7 not, 1024 -> 2048 7.0 and 7.7; 100 rows, 1024 -> 2048 9.6 and
 // 8.0, 2048 -> 2048 10.5 and 12.3. So it needs 16 blocks, or 32 with more than 32 rows.
-template <int kAct, bool kBMn>
-cudaError_t launch_rows_split(const uint16_t* A, const uint16_t* B, const RowsArgs& a, cudaStream_t stream, bool* done) {
-  *done = false;
+SplitPlan plan_rows_split(const RowsArgs& a, bool gated) {
   const int64_t rows = a.groups.rows;
   const int64_t row_tiles = a.groups.count == nullptr ? (rows + kBM - 1) / kBM : max_row_tiles(a.groups);
-  const int halves = kAct == EP_ACT_SWIGLU ? 2 : 1;
+  const int halves = gated ? 2 : 1;
   const int blocks = (a.sum + kBK - 1) / kBK;
   const int64_t wide = row_tiles * ((a.epi.cols + 256 / halves - 1) / (256 / halves));
   const int64_t narrow = row_tiles * ((a.epi.cols + 128 / halves - 1) / (128 / halves));
-  int S = 1;
-  bool use_narrow = false;
+  SplitPlan plan = {1, blocks, false, 0};
+  if (blocks < (rows <= 32 ? 16 : 32)) return plan;
   int64_t ctas = 0;
-  if (blocks < (rows <= 32 ? 16 : 32)) return cudaSuccess;
   for (int s = 2; s <= 8 && blocks >= s * 2; s *= 2) {
-    if (wide <= resident_clusters(s) && wide * s > ctas) S = s, use_narrow = false, ctas = wide * s;
-    if (narrow <= resident_clusters(s) && narrow * s > ctas) S = s, use_narrow = true, ctas = narrow * s;
+    const int part = (blocks + s - 1) / s;
+    if (wide <= resident_clusters(s) && wide * s > ctas) plan = {s, part, false, wide}, ctas = wide * s;
+    if (narrow <= resident_clusters(s) && narrow * s > ctas) plan = {s, part, true, narrow}, ctas = narrow * s;
   }
-  if (S == 1) return cudaSuccess;
-  const int64_t tiles = use_narrow ? narrow : wide;
-  *done = true;
-  return use_narrow ? launch<kAct, kBMn, 128>(A, B, a, tiles, S, stream) : launch<kAct, kBMn, 256>(A, B, a, tiles, S, stream);
+  return plan;
+}
+
+template <int kAct, bool kBMn>
+cudaError_t launch_rows_split(const uint16_t* A, const uint16_t* B, const RowsArgs& a, const SplitPlan& plan, cudaStream_t stream) {
+  return plan.narrow ? launch<kAct, kBMn, 128>(A, B, a, plan.tiles, plan.S, stream)
+                     : launch<kAct, kBMn, 256>(A, B, a, plan.tiles, plan.S, stream);
 }
 #define X(act, mn) \
-  template cudaError_t launch_rows_split<act, mn>(const uint16_t*, const uint16_t*, const RowsArgs&, cudaStream_t, bool*);
+  template cudaError_t launch_rows_split<act, mn>(const uint16_t*, const uint16_t*, const RowsArgs&, const SplitPlan&, cudaStream_t);
 EP_ROWS_INSTANCES(X)
 #undef X
 

@@ -422,7 +422,8 @@ typedef struct ep_product_config {
                            FP8 dispatch (each element is taken as bf16_rn(code * scale);
                            forward only)                                            */
   int32_t sf_pack;      /* x_sf as ep_config_t.sf_pack                              */
-  int32_t num_sms;      /* SMs to use; 0 = all. Results do not depend on it.        */
+  int32_t num_sms;      /* SMs to use; 0 = all. Results do not depend on it. (d_weight
+                           is computed by pairs of SMs: it takes two for 1)         */
 } ep_product_config_t;
 
 /* Workspace bytes of ep_expert_product (grad = 0) or ep_expert_product_grad (1); 0 for
