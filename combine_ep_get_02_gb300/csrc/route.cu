@@ -33,6 +33,12 @@ namespace {
 constexpr float kInf = __builtin_huge_valf();
 constexpr float kLowest = -3.402823466e38f;
 constexpr float kTiny = 1e-30f;  // least divisor of a sum of sigmoids
+// A sum of sigmoids below this: every one of them is e^l to 2^-60, and quotients are taken of
+// e^(l - largest l) instead, which does not leave the floats' range.
+constexpr float kSmallSum = 0x1p-60f;
+// Below this logit e^l is 0 even in 64 bits, and so is the score: tokens that have no other
+// (the type's lowest value, say) have weights and probabilities of 0.
+constexpr float kLeastLogit = -745.f;
 
 // one instruction on this architecture
 __device__ __forceinline__ float warp_max(float v) {
@@ -312,6 +318,22 @@ __global__ void __launch_bounds__(kRouteThreads, EPL <= 8 ? 4 : EPL <= 16 ? 2 : 
           best = fmaxf(best, l[j]);
         }
         total = warp_sum(total);
+        if (total < kSmallSum) {
+          load_row<EPL, kBf16, kVec>(a.logits, token, E, lane, s);
+          clean<EPL>(s);
+          float most = -kInf;
+#pragma unroll
+          for (int j = 0; j < EPL; ++j) most = fmaxf(most, s[j]);
+          most = warp_max(most);
+          if (most < kLeastLogit) most = 0.f;  // every p is 0
+          total = 0.f;
+#pragma unroll
+          for (int j = 0; j < EPL; ++j) {
+            s[j] = exp_fast(s[j] - most);
+            total += s[j];
+          }
+          total = warp_sum(total);
+        }
       } else {
         auto probabilities = [&] {
           best = -kInf;
@@ -433,7 +455,15 @@ __global__ void __launch_bounds__(kRouteThreads, EPL <= 8 ? 4 : EPL <= 16 ? 2 : 
     }
     if (g.sigmoid) {
       w = mine >= 0 ? sigmoid_rn(lv) : 0.f;
-      if (g.normalize) w = __fdividef(w, fmaxf(warp_sum(w), kTiny));
+      if (g.normalize) {
+        float sum = warp_sum(w);
+        if (sum < kSmallSum) {
+          const float m = warp_max(lv);
+          w = mine >= 0 && m >= kLeastLogit ? exp_fast(lv - m) : 0.f;
+          sum = warp_sum(w);
+        }
+        w = sum > 0.f ? __fdividef(w, sum) : 0.f;
+      }
     } else if (g.normalize) {
       const float m = warp_max(lv);
       w = mine >= 0 ? exp_fast(lv - m) : 0.f;

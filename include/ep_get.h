@@ -329,7 +329,9 @@ typedef struct ep_route_config {
                            at least each, G <= 32                                  */
   int32_t topk_groups;  /* groups a token may choose from, 1..G, holding K experts at
                            least (ignored without groups)                          */
-  int32_t normalize;    /* 1: weights divided by the sum of s over the chosen      */
+  int32_t normalize;    /* 1: weights divided by the sum of s over the chosen (taken
+                           of logarithms where sigmoids are tiny; 0 where the chosen s
+                           are all 0 in 64 bits: logits below -745)                */
   float scale;          /* every weight times this (finite)                        */
 } ep_route_config_t;
 
