@@ -20,7 +20,7 @@
 // (comparisons run at half rate). Measured: 16 x 4096 tokens, 256 experts, top 8, softmax
 // 45 us (67 MB of logits, 1.6 TB/s; 84 us with sigmoid scores and 8 groups), one segment of
 // 65536 tokens 43 us; 64 tokens 7 us, of which 3.5 are the statistics' chain of one atomic
-// and one load across the CTAs; the gradient of 16 x 4096 tokens 30 us (141 MB, 4.7 TB/s).
+// and one load across the CTAs; the gradient of 16 x 4096 tokens 32 us (sigmoid; 141 MB, 4.4 TB/s).
 #include <type_traits>
 
 #include "ep_device.cuh"
@@ -32,7 +32,6 @@ namespace {
 
 constexpr float kInf = __builtin_huge_valf();
 constexpr float kLowest = -3.402823466e38f;
-constexpr float kTiny = 1e-30f;  // least divisor of a sum of sigmoids
 // A sum of sigmoids below this: every one of them is e^l to 2^-60, and quotients are taken of
 // e^(l - largest l) instead, which does not leave the floats' range.
 constexpr float kSmallSum = 0x1p-60f;
@@ -67,6 +66,16 @@ __device__ __forceinline__ float warp_sum(float v) {
 // The sigmoid whose rounding the choice depends on: CUDA's expf, then correctly
 // rounded operations, so that equal scores tie.
 __device__ __forceinline__ float sigmoid_rn(float x) { return __frcp_rn(__fadd_rn(1.f, expf(-x))); }
+
+// The sigmoid s and 1 - s, each from the smaller of e^x and e^-x, so that neither loses digits at
+// its small end.
+struct Sigmoids {
+  float s, c;
+};
+__device__ __forceinline__ Sigmoids sigmoids_fast(float x) {
+  const float t = exp_fast(-fabsf(x)), r = rcp_fast(1.f + t), q = t * r;
+  return x >= 0.f ? Sigmoids{r, q} : Sigmoids{q, r};
+}
 
 // Expert of register j of a lane: 4 (or EPL, if less) consecutive experts per lane
 // and step, so that a lane reads 16 bytes of fp32 at once.
@@ -124,6 +133,23 @@ __device__ __forceinline__ bool clean(float (&l)[EPL]) {
   for (int j = 0; j < EPL; ++j)
     if (!(l[j] < kInf)) l[j] = -kInf;
   return true;
+}
+
+// A token's logits, all of them far below zero, become its scores up to a common factor; returns
+// the lane's sum.
+template <int EPL>
+__device__ __forceinline__ float small_scores(float (&s)[EPL]) {
+  float most = -kInf, total = 0.f;
+#pragma unroll
+  for (int j = 0; j < EPL; ++j) most = fmaxf(most, s[j]);
+  most = warp_max(most);
+  if (most < kLeastLogit) most = 0.f;  // every score is 0
+#pragma unroll
+  for (int j = 0; j < EPL; ++j) {
+    s[j] = exp_fast(s[j] - most);
+    total += s[j];
+  }
+  return total;
 }
 
 struct Top2 {
@@ -321,18 +347,7 @@ __global__ void __launch_bounds__(kRouteThreads, EPL <= 8 ? 4 : EPL <= 16 ? 2 : 
         if (total < kSmallSum) {
           load_row<EPL, kBf16, kVec>(a.logits, token, E, lane, s);
           clean<EPL>(s);
-          float most = -kInf;
-#pragma unroll
-          for (int j = 0; j < EPL; ++j) most = fmaxf(most, s[j]);
-          most = warp_max(most);
-          if (most < kLeastLogit) most = 0.f;  // every p is 0
-          total = 0.f;
-#pragma unroll
-          for (int j = 0; j < EPL; ++j) {
-            s[j] = exp_fast(s[j] - most);
-            total += s[j];
-          }
-          total = warp_sum(total);
+          total = warp_sum(small_scores<EPL>(s));
         }
       } else {
         auto probabilities = [&] {
@@ -650,13 +665,37 @@ __global__ void __launch_bounds__(kRouteThreads, EPL <= 8 ? 4 : EPL <= 16 ? 2 : 
       lv = kBf16 ? __uint_as_float(static_cast<uint32_t>(__ldg(static_cast<const uint16_t*>(a.logits) + token * E + e)) << 16)
                  : __ldg(static_cast<const float*>(a.logits) + token * E + e);
     if (!(lv < kInf)) lv = -kInf;
+    // softmax: s[j] = e^(l - top), p = s / sum s. Sigmoid: s[j] = e^-l, of which both the score
+    // 1 / (1 + s[j]) and one minus it, s[j] / (1 + s[j]), keep all their digits.
     float s[EPL];
-    float total = 0.f, top = 0.f;
+    float total = 0.f, ap = 0.f, top = 0.f;  // ap: the sum of a p
     if (g.sigmoid) {
+      auto sums = [&](int j) {
+        const float v = rcp_fast(1.f + s[j]);
+        total += v;
+        ap = fmaf(coef[j], v, ap);
+      };
 #pragma unroll
       for (int j = 0; j < EPL; ++j) {
-        s[j] = rcp_fast(1.f + exp_fast(-l[j]));
-        total += s[j];
+        s[j] = exp_fast(-l[j]);
+        sums(j);
+      }
+      total = warp_sum(total);
+      if (total < kSmallSum) {  // the quotients of logits that are shifted up to -42 at the largest
+        load_row<EPL, kBf16, kVec>(a.logits, token, E, lane, s);
+        clean<EPL>(s);
+        float m = -kInf;
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) m = fmaxf(m, s[j]);
+        m = warp_max(m);
+        if (m < kLeastLogit) m = kInf;  // every score is 0
+        total = ap = 0.f;
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) {
+          s[j] = exp_fast(42.f - (s[j] - m));
+          sums(j);
+        }
+        total = warp_sum(total);
       }
     } else {
       float m = -kInf;
@@ -668,23 +707,27 @@ __global__ void __launch_bounds__(kRouteThreads, EPL <= 8 ? 4 : EPL <= 16 ? 2 : 
       for (int j = 0; j < EPL; ++j) {
         s[j] = exp_fast(l[j] - top);
         total += s[j];
+        ap = fmaf(coef[j], s[j], ap);
       }
+      total = warp_sum(total);
     }
-    total = warp_sum(total);
     const float inv = total > 0.f ? rcp_fast(total) : 0.f;
-    float ap = 0.f;  // sum of a p
-#pragma unroll
-    for (int j = 0; j < EPL; ++j) ap = fmaf(coef[j], s[j] * inv, ap);
-    ap = warp_sum(ap);
+    ap = warp_sum(ap) * inv;
     // what goes to the chosen experts
     float gl, rest = 0.f;
     if (g.sigmoid) {
-      const float sv = chosen ? rcp_fast(1.f + exp_fast(-lv)) : 0.f;
+      const Sigmoids v = sigmoids_fast(lv);  // s = 0 where no expert is chosen
       if (g.normalize) {
-        const float q = __fdividef(sv, fmaxf(warp_sum(sv), kTiny));
-        gl = q * (gw - warp_sum(q * gw)) * (1.f - sv);
+        float q = v.s, sum = warp_sum(q);
+        if (sum < kSmallSum) {
+          const float m = warp_max(lv);
+          q = lv > -kInf && m >= kLeastLogit ? exp_fast(lv - m) : 0.f;
+          sum = warp_sum(q);
+        }
+        q = sum > 0.f ? __fdividef(q, sum) : 0.f;
+        gl = q * (gw - warp_sum(q * gw)) * v.c;
       } else {
-        gl = gw * sv * (1.f - sv);
+        gl = gw * v.s * v.c;
       }
     } else if (g.normalize) {
       const float m = warp_max(lv);
@@ -704,9 +747,13 @@ __global__ void __launch_bounds__(kRouteThreads, EPL <= 8 ? 4 : EPL <= 16 ? 2 : 
       float d[V];
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        const float p = s[j + i] * inv;
-        float v = p * (coef[j + i] - ap - rest);
-        if (g.sigmoid) v *= 1.f - s[j + i];
+        float p = s[j + i] * inv, v = coef[j + i] - ap - rest;
+        if (g.sigmoid) {
+          const float score = rcp_fast(1.f + s[j + i]);
+          p = score * inv;
+          v *= fminf(score * s[j + i], 1.f);  // 0 * inf becomes 1
+        }
+        v *= p;
         if (e0 + i < E) v += s_row[e0 + i];
         d[i] = on ? v : 0.f;
       }

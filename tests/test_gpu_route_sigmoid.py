@@ -1,5 +1,5 @@
 """Sigmoid scores far from zero: weights and probabilities are quotients of scores, which stay
-of ordinary size when the scores themselves are tiny."""
+of ordinary size when the scores themselves are tiny, and 1 - s stays exact when s is near 1."""
 import pytest
 import torch
 
@@ -57,3 +57,38 @@ def test_quotients_of_tiny_scores(dtype, E, K):
     N = len(logits)
     loss = float((E * out.expert_count[0].double() / (K * N) * p / N).sum())
     assert abs(float(out.balance_loss) - loss) <= QUOTIENT * loss
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("normalize", [0, 1])
+@pytest.mark.parametrize("E,K", [(24, 4), (200, 8), (1500, 5)])
+def test_gradients_at_both_ends(dtype, normalize, E, K):
+    """Each gradient against its own terms, of which 1 - s is a factor."""
+    logits = logits_of(dtype, E, seed=1)
+    cfg, out, ws = run(logits, K, normalize, scale=1.5)
+    N = len(logits)
+    g = torch.Generator().manual_seed(2)
+    d_weights, d_loss = torch.randn(N, K, generator=g).cuda(), torch.full((1,), 3.0 * N, device="cuda")
+    d = torch.empty_like(logits)
+    ep.ep_route_grad(cfg, logits, None, out, d_weights, d_loss, d, ws)
+    assert ep.ep_check_error(ws) == ep.EP_OK
+    l, idx, gw = logits.double(), out.topk_idx, 1.5 * d_weights.double()
+    s, c = torch.sigmoid(l), torch.sigmoid(-l)  # c = 1 - s
+    p = quotient(log_scores(logits))
+    a = float(d_loss) * E / (K * N * N) * out.expert_count[0].double()
+    ap = (a * p).sum(-1, keepdim=True)
+    sk = s.gather(1, idx)
+    if normalize:
+        q = quotient(log_scores(logits).gather(1, idx))
+        gl = q * (gw - (q * gw).sum(-1, keepdim=True))
+        size = q * (gw.abs() + (q * gw.abs()).sum(-1, keepdim=True))
+    else:
+        gl, size = gw * sk, gw.abs() * sk
+    want = c * (p * (a - ap)).scatter_add(1, idx, gl)
+    terms = c * (p * (a + ap)).scatter_add(1, idx, size)
+    # two quotients and 1 - s multiply in each term
+    tol = 3 * QUOTIENT * terms + 1e-35  # what is below the least normal number may be 0
+    if dtype == torch.bfloat16:
+        tol = tol + 2 ** -8 * want.abs()  # one rounding of the result
+    off = (d.double() - want).abs() - tol
+    assert torch.isfinite(d.float()).all() and float(off.max()) <= 0, (float(off.max()), int((off > 0).sum()))
