@@ -58,19 +58,26 @@ __device__ __forceinline__ int group_of_tile(const int* prefix, int E, int t) {
 
 __device__ __forceinline__ float sigmoid_fast(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
 
-// act(z)
+// the larger; NaN if either is
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// act(z); a NaN stays one
 template <int kAct>
 __device__ __forceinline__ float activate(float z) {
-  if constexpr (kAct == EP_ACT_RELU) return fmaxf(z, 0.f);
+  if constexpr (kAct == EP_ACT_RELU) return max_nan(z, 0.f);
   if constexpr (kAct == EP_ACT_SILU || kAct == EP_ACT_SWIGLU) return z * sigmoid_fast(z);
   if constexpr (kAct == EP_ACT_GELU) return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
   return z;
 }
 
-// act'(z)
+// act'(z); NaN of a NaN
 template <int kAct>
 __device__ __forceinline__ float activate_grad(float z) {
-  if constexpr (kAct == EP_ACT_RELU) return z > 0.f ? 1.f : 0.f;
+  if constexpr (kAct == EP_ACT_RELU) return z > 0.f ? 1.f : z <= 0.f ? 0.f : z;
   if constexpr (kAct == EP_ACT_SILU || kAct == EP_ACT_SWIGLU) {
     const float s = sigmoid_fast(z);
     return s * fmaf(z, 1.f - s, 1.f);

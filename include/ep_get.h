@@ -406,7 +406,7 @@ int ep_combine_grad(const ep_config_t* cfg, const ep_layout_t* layout, const uin
  * bounded; one that gives up latches EP_ERR_TIMEOUT and leaves outputs incomplete.
  */
 #define EP_ACT_NONE 0
-#define EP_ACT_RELU 1
+#define EP_ACT_RELU 1   /* max(z, 0); NaN stays NaN, as under the others */
 #define EP_ACT_SILU 2   /* z / (1 + exp(-z))            */
 #define EP_ACT_GELU 3   /* z * (1 + erf(z / sqrt 2)) / 2 */
 #define EP_ACT_SWIGLU 4 /* gated: silu(z1) * z2          */
