@@ -71,7 +71,13 @@ class _Recv(C.Structure):
 class _KeepsStruct:
     """Keeps the ctypes struct built by _c() until a field is assigned again, so
     a call reuses it instead of marshalling every field (the struct holds the
-    values, and for tensors their data pointers, as of that build)."""
+    values, and for tensors their data pointers, as of that build). Copies and
+    pickles start without what is kept."""
+
+    _struct = _reference = _sizes = _lanes = None
+
+    def __getstate__(self):
+        return {k: v for k, v in self.__dict__.items() if k not in ("_struct", "_reference", "_sizes", "_lanes")}
 
     def __setattr__(self, name, value):
         object.__setattr__(self, name, value)
