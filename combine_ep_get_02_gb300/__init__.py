@@ -483,12 +483,16 @@ def _space(ws, where: str):
     raise EpError(EP_ERR_WORKSPACE, f"{where}: the workspace {why}")
 
 
-_current_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+# the current stream's handle without building a Stream object; builds of torch without CUDA lack it
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
 
 
 def _raw_stream(stream):
-    """The stream's handle; None: the current stream, without building a Stream object."""
+    """The stream's handle; None: the current stream."""
     if stream is None:
+        if _current_stream is None or _current_device is None:
+            return torch.cuda.current_stream().cuda_stream
         return _current_stream(_current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 

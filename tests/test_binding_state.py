@@ -2,7 +2,10 @@
 copied, pickled or sent to another process."""
 import copy
 import dataclasses
+import os
 import pickle
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -40,3 +43,16 @@ def test_tensors_after_a_call(twin):
     assert torch.equal(other.slot_map, lay.slot_map)
     assert other._c().slot_map == other.slot_map.data_ptr() != lay.slot_map.data_ptr()
     assert other._sizes is None and other._lanes is None
+
+
+def test_import_without_the_cuda_part_of_torch():
+    """A build of torch for the CPU has no current stream; the package still imports there."""
+    code = ("import torch\n"
+            "for name in ('_cuda_getCurrentRawStream', '_cuda_getDevice'):\n"
+            "    if hasattr(torch._C, name): delattr(torch._C, name)\n"
+            "import combine_ep_get_02_gb300 as ep\n"
+            "assert ep._raw_stream(7) == 7\n"
+            "assert ep.RouteConfig(1, 1, 8, 2).num_topk == 2\n")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
