@@ -29,7 +29,7 @@ class MoELayer:
                  grad=True):
         g = torch.Generator(device="cuda").manual_seed(seed)
         rnd = lambda *s: (torch.randn(*s, generator=g, device="cuda") * s[-1] ** -0.5).bfloat16()  # noqa: E731
-        self.ranks, self.tokens, self.hidden, self.topk = ranks, tokens, hidden, topk
+        self.ranks, self.tokens, self.hidden, self.topk, self.grad = ranks, tokens, hidden, topk, grad
         self.router = rnd(experts, hidden)
         self.up, self.down = rnd(experts, 2 * inner, hidden), rnd(experts, hidden, inner)
         self.cfg = ep.Config(1, ranks, experts, topk, tokens, tokens, hidden, expand=1,
@@ -88,8 +88,11 @@ class MoELayer:
         return d_x, self.d_logits.t() @ self.x.reshape(-1, self.hidden), self.d_up, self.d_down
 
     def check(self):
-        """First error that the device found since the last call."""
-        for ws in (self.ws, self.route_ws, self.up_ws, self.down_ws):
+        """First error that the device found since the last call, in the forward or the backward."""
+        spaces = [self.ws, self.route_ws, self.up_ws, self.down_ws]
+        if self.grad:
+            spaces += [self.up_grad_ws, self.down_grad_ws]
+        for ws in spaces:
             status = ep.ep_check_error(ws)
             if status != ep.EP_OK:
                 return status
