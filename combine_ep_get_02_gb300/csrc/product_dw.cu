@@ -223,7 +223,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp == 2 + kEpilogueWarps) {
-    uint32_t n = 0, part_phase = 0;
+    uint32_t n = 0, part_phase = 0, waited = 0;  // waited: stages up to the last tile that was mended
     bool ok = true;
     for (int i = first; ok && i < total; i += step) {
       const Tile t = resolve(a, ahead, mt);
@@ -233,7 +233,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int left = t.rows - (stages - 1) * kBK;  // rows of the last stage that count
       if (stages == 0 || !to_mend(left)) continue;
       const uint32_t s = (n - 1) % kStages;
-      ok = __all_sync(kFullMask, s_abort == 0 && mbar_wait_timed(smem_addr(&s_part[s]), part_phase >> s & 1u));
+      ok = __all_sync(kFullMask, s_abort == 0 && mbar_wait_stages(smem_addr(&s_part[s]), part_phase >> s & 1u, n - waited, &s_abort));
+      waited = n;
       if (!ok) {
         if (lane == 0 && !s_abort) give_up();
         break;
@@ -260,7 +261,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const uint32_t b = acc & 1u;
       const int z0 = t.z0 + rank * kBM + quarter * 32;
       if (t.rows > 0) {
-        bool ok = s_abort == 0 && mbar_wait_timed(smem_addr(&s_acc_full[b]), acc >> 1 & 1u);
+        bool ok = s_abort == 0 && mbar_wait_stages(smem_addr(&s_acc_full[b]), acc >> 1 & 1u,
+                                                   static_cast<uint32_t>(t.rows) / kBK, &s_abort);
         ok = __all_sync(kFullMask, ok);
         if (!ok) {
           if (lane == 0 && !s_abort) give_up();

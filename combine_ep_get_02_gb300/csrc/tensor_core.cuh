@@ -56,6 +56,16 @@ __device__ __forceinline__ bool mbar_wait_timed(uint32_t bar, uint32_t parity) {
   return false;
 }
 
+// A wait that may rightly last as long as `stages` stages of the products take (about 0.3 us
+// each): the bound above for every 2^18 of them; it also ends once *abort is set.
+__device__ __forceinline__ bool mbar_wait_stages(uint32_t bar, uint32_t parity, uint32_t stages, const volatile int* abort) {
+  for (uint32_t i = 0; i <= stages >> 18; ++i) {
+    if (mbar_wait_timed(bar, parity)) return true;
+    if (*abort != 0) return false;
+  }
+  return false;
+}
+
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
   asm volatile("{ .reg .pred p; elect.sync _|p, 0xFFFFFFFF; selp.u32 %0, 1, 0, p; }" : "=r"(p));
