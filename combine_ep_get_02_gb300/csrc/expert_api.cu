@@ -289,9 +289,13 @@ int ep_expert_product(const ep_product_config_t* cfg, const ep_layout_t* layout,
   if (sms < 0) return EP_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   a.x = static_cast<const uint16_t*>(x);
+  a.x_sf = nullptr;
   if (a.g.x_fp8) {
+    // a code times a power of two is exact in bf16; other scales are applied to the fp32 sums
+    if (!a.g.sf_pack) a.x_sf = x_sf;
     uint16_t* rows = at<uint16_t>(workspace, w.rows);
-    const cudaError_t e = launch_dequant(a.g, static_cast<const uint8_t*>(x), x_sf, rows, sms, s);
+    const cudaError_t e =
+        launch_dequant(a.g, static_cast<const uint8_t*>(x), a.g.sf_pack ? x_sf : nullptr, rows, sms, s);
     if (e != cudaSuccess) return EP_ERR_CUDA;
     a.x = rows;
   }

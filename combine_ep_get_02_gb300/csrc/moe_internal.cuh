@@ -129,7 +129,8 @@ struct ProductGeometry {
 
 struct ProductArgs {
   ProductGeometry g;
-  const uint16_t* x;        // bf16 rows (after any FP8 conversion)
+  const uint16_t* x;        // bf16 rows (of an FP8 dispatch: its values, or its codes if x_sf is set)
+  const float* x_sf;        // [rows][K / 128] scales of the codes' sums; null: none
   const uint16_t* weight;   // [E][Z][K]
   const uint16_t* bias;     // [E][Z] or null
   const uint16_t* residual; // [rows][N] or null
@@ -164,6 +165,7 @@ __host__ __device__ inline int64_t max_row_tiles(const Groups& q, int tile_rows 
   return q.rows / tile_rows + groups;
 }
 
+// x_sf: packed powers of two; null: the codes alone
 cudaError_t launch_dequant(const ProductGeometry& g, const uint8_t* x, const float* x_sf, uint16_t* out, int num_sms,
                            cudaStream_t stream);
 cudaError_t launch_product(const ProductArgs& a, int num_sms, cudaStream_t stream);

@@ -24,15 +24,15 @@ namespace ep {
 
 namespace {
 
-constexpr int kThreads = kRowsThreadsTc;
-constexpr int kBM = kTileRows, kMaxBN = 256;
+constexpr int kBM = kTileRows, kMaxBN = kAccColumns;
 constexpr int kLowRows = 32;  // tiles with no more rows read that many of A
 constexpr int kABytes = kBM * kBK * 2;
-constexpr int kRingBytes = 196608, kMaxStages = 8;
+constexpr int kMaxStages = 8;
+constexpr int ring_bytes(bool scaled) { return scaled ? 180224 : 196608; }  // the more warps, the more patches
 
 __host__ __device__ constexpr int stage_bytes(int bn) { return kABytes + bn * kBK * 2; }
-__host__ __device__ constexpr int stage_count(int bn) {
-  return kRingBytes / stage_bytes(bn) < kMaxStages ? kRingBytes / stage_bytes(bn) : kMaxStages;
+__host__ __device__ constexpr int stage_count(int ring, int bn) {
+  return ring / stage_bytes(bn) < kMaxStages ? ring / stage_bytes(bn) : kMaxStages;
 }
 
 // kParts: a tile's sum is taken `part` blocks at a time, as the clusters of product_split.cu do
@@ -55,14 +55,16 @@ __device__ __forceinline__ void add_part(uint32_t at, float (&v)[32], bool first
   }
 }
 
-template <int kAct, bool kBMn, bool kParts>
-__global__ void __launch_bounds__(kThreads, 1)
+// kScaled: scaled sums (product_rows.cuh), an accumulator per scale.
+template <int kAct, bool kBMn, bool kParts, bool kScaled>
+__global__ void __launch_bounds__(rows_threads(kScaled), 1)
     rows_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_low,
                 const __grid_constant__ CUtensorMap map_b, RowsArgs a, int bn, int part) {
   constexpr bool kGated = kAct == EP_ACT_SWIGLU;
+  constexpr int kThreads = rows_threads(kScaled), kEpilogueWarps = epilogue_warps(kScaled), kRingBytes = ring_bytes(kScaled);
   const int cols = kGated ? bn / 2 : bn;  // output columns of a tile
   const int b_bytes = bn * kBK * 2;
-  const uint32_t kStages = static_cast<uint32_t>(stage_count(bn)), kStageBytes = static_cast<uint32_t>(stage_bytes(bn));
+  const uint32_t kStages = static_cast<uint32_t>(stage_count(kRingBytes, bn)), kStageBytes = static_cast<uint32_t>(stage_bytes(bn));
   extern __shared__ uint8_t s_raw[];
   __shared__ __align__(8) uint64_t s_full[kMaxStages], s_empty[kMaxStages], s_acc_full[2], s_acc_empty[2], s_drained;
   __shared__ uint32_t s_tmem;
@@ -146,7 +148,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t n = 0, acc = 0;
       bool ok = true;
       for (int i = blockIdx.x; ok && i < tiles.total; i += gridDim.x) {
-        for (int p = 0; ok && p < parts; ++p, ++acc) {
+        for (int p = 0; ok && p < (kScaled ? blocks / kScaledBlocks : parts); ++p, ++acc) {
           const uint32_t b = acc & 1u;
           if (s_abort || !mbar_wait_timed(smem_addr(&s_acc_empty[b]), (acc >> 1 & 1u) ^ 1u)) {
             if (!s_abort) give_up();
@@ -155,7 +157,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           tc_fence_after();
           const uint32_t d = tmem + b * kMaxBN;
-          const int k0 = kParts ? p * part : 0, k1 = kParts ? min(blocks, k0 + part) : blocks;
+          const int each = kScaled ? kScaledBlocks : part;  // blocks of an accumulator
+          const int k0 = kScaled || kParts ? p * each : 0, k1 = kScaled || kParts ? min(blocks, k0 + each) : blocks;
           for (int kb = k0; kb < k1; ++kb, ++n) {
             const uint32_t s = n % kStages;
             if (s_abort || !mbar_wait_timed(smem_addr(&s_full[s]), n / kStages & 1u)) {
@@ -191,33 +194,66 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int m = quarter * 32;
       const int64_t row = static_cast<int64_t>(t.begin) + m;
       const int rows = t.rows - m;
-      for (int p = 0; p < parts; ++p, ++acc) {
-        const uint32_t b = acc & 1u;
-        ok = s_abort == 0 && mbar_wait_timed(smem_addr(&s_acc_full[b]), acc >> 1 & 1u);
-        ok = __all_sync(kFullMask, ok);
-        if (!ok) {
-          if (lane == 0 && !s_abort) give_up();
-          break;
-        }
-        tc_fence_after();
-        const uint32_t lanes = tmem + (static_cast<uint32_t>(m) << 16), d = lanes + b * kMaxBN;
-        for (int c = half * 32; c < cols; c += 64) {
-          if (rows <= 0 || t.n0 + c >= a.epi.cols) break;
-          float v[32], u[kGated ? 32 : 1];
-          tmem_ld32(d + c, v);
-          if constexpr (kGated) tmem_ld32(d + cols + c, u);
-          tmem_ld_wait();
+      if constexpr (kScaled) {
+        const bool valid = lane < rows;
+        const int h = (warp - 2) >> 2, c0 = h * 32 < cols ? h * 32 : -1;
+        const int c1 = kGated ? (c0 >= 0 ? cols + c0 : -1) : (h + 4) * 32 < cols ? (h + 4) * 32 : -1;
+        const int each = part / kScaledBlocks, all = blocks / kScaledBlocks;  // scales
+        const float* sf = valid ? a.a_sf + (row + lane) * all : nullptr;
+        for (int p = 0; p < parts; ++p) {
+          float v[32], u[32];
+          const int g0 = kParts ? p * each : 0, n = kParts ? min(each, all - g0) : all;
+          ok = sum_scaled(s_acc_full, tmem + (static_cast<uint32_t>(m) << 16), c0, c1, valid ? sf + g0 : nullptr, n, acc, v, u,
+                          &s_abort, [&](uint32_t b) { mbar_arrive(smem_addr(&s_acc_empty[b])); });
+          if (!ok) {
+            if (lane == 0 && !s_abort) give_up();
+            break;
+          }
+          if (rows <= 0) continue;
           if constexpr (kParts) {
             const bool last = p + 1 == parts;
-            add_part(lanes + kSumColumn + c, v, p == 0, last);
-            if constexpr (kGated) add_part(lanes + kSumColumn + cols + c, u, p == 0, last);
+            const uint32_t sum = tmem + (static_cast<uint32_t>(m) << 16) + kSumColumn;
+            if (c0 >= 0) add_part(sum + c0, v, p == 0, last);
+            if (c1 >= 0) add_part(sum + c1, u, p == 0, last);
             if (!last) continue;
           }
-          finish_rows<kAct>(a.epi, patch, v, u, t.g, row, rows, t.n0 + c, lane);
+          if constexpr (kGated) {
+            if (c0 >= 0 && t.n0 + c0 < a.epi.cols) finish_rows<kAct>(a.epi, patch, v, u, t.g, row, rows, t.n0 + c0, lane);
+          } else {
+            float none[1];
+            if (c0 >= 0 && t.n0 + c0 < a.epi.cols) finish_rows<kAct>(a.epi, patch, v, none, t.g, row, rows, t.n0 + c0, lane);
+            if (c1 >= 0 && t.n0 + c1 < a.epi.cols) finish_rows<kAct>(a.epi, patch, u, none, t.g, row, rows, t.n0 + c1, lane);
+          }
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_addr(&s_acc_empty[b]));
+      } else {
+        for (int p = 0; p < parts; ++p, ++acc) {
+          const uint32_t b = acc & 1u;
+          ok = s_abort == 0 && mbar_wait_timed(smem_addr(&s_acc_full[b]), acc >> 1 & 1u);
+          ok = __all_sync(kFullMask, ok);
+          if (!ok) {
+            if (lane == 0 && !s_abort) give_up();
+            break;
+          }
+          tc_fence_after();
+          const uint32_t lanes = tmem + (static_cast<uint32_t>(m) << 16), d = lanes + b * kMaxBN;
+          for (int c = half * 32; c < cols; c += 64) {
+            if (rows <= 0 || t.n0 + c >= a.epi.cols) break;
+            float v[32], u[kGated ? 32 : 1];
+            tmem_ld32(d + c, v);
+            if constexpr (kGated) tmem_ld32(d + cols + c, u);
+            tmem_ld_wait();
+            if constexpr (kParts) {
+              const bool last = p + 1 == parts;
+              add_part(lanes + kSumColumn + c, v, p == 0, last);
+              if constexpr (kGated) add_part(lanes + kSumColumn + cols + c, u, p == 0, last);
+              if (!last) continue;
+            }
+            finish_rows<kAct>(a.epi, patch, v, u, t.g, row, rows, t.n0 + c, lane);
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_addr(&s_acc_empty[b]));
+        }
       }
     }
   }
@@ -229,7 +265,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 }  // namespace
 
-template <int kAct, bool kBMn>
+template <int kAct, bool kBMn, bool kScaled>
 cudaError_t launch_rows_single(const uint16_t* A, const uint16_t* B, const RowsArgs& a, int bn, int part, int num_sms,
                                cudaStream_t stream) {
   const int halves = kAct == EP_ACT_SWIGLU ? 2 : 1;
@@ -240,15 +276,16 @@ cudaError_t launch_rows_single(const uint16_t* A, const uint16_t* B, const RowsA
   const uint32_t box[2] = {kBK, kLowRows};
   st = make_tensor_map(&map_low, A, 2, size, box);
   if (st != cudaSuccess) return st;
-  auto kern = part > 0 ? rows_kernel<kAct, kBMn, true> : rows_kernel<kAct, kBMn, false>;
-  const size_t smem = 1024 + kRingBytes + kEpilogueWarps * kPatchBytes + sizeof(int) * (static_cast<size_t>(a.groups.E) + 1);
+  auto kern = part > 0 ? rows_kernel<kAct, kBMn, true, kScaled> : rows_kernel<kAct, kBMn, false, kScaled>;
+  constexpr int kThreads = rows_threads(kScaled);
+  const size_t smem = 1024 + ring_bytes(kScaled) + epilogue_warps(kScaled) * kPatchBytes + sizeof(int) * (static_cast<size_t>(a.groups.E) + 1);
   if (resident_ctas(reinterpret_cast<const void*>(kern), kThreads, smem) < 1) return cudaErrorInvalidConfiguration;
   const int64_t tiles = max_row_tiles(a.groups) * ((a.epi.cols + bn / halves - 1) / (bn / halves));
   const unsigned grid = static_cast<unsigned>(tiles < num_sms ? tiles : num_sms);
   return launch_chained(kern, dim3(grid), dim3(kThreads), smem, stream, map_a, map_low, map_b, a, bn, part);
 }
-#define X(act, mn) \
-  template cudaError_t launch_rows_single<act, mn>(const uint16_t*, const uint16_t*, const RowsArgs&, int, int, int, cudaStream_t);
+#define X(act, mn, scaled) \
+  template cudaError_t launch_rows_single<act, mn, scaled>(const uint16_t*, const uint16_t*, const RowsArgs&, int, int, int, cudaStream_t);
 EP_ROWS_INSTANCES(X)
 #undef X
 
@@ -266,10 +303,10 @@ namespace {
 //   1613 rows 1152 -> 3064 (pairs): 256 columns 21.7 us, the 192 taken 18.2;
 //   48 experts with a few rows, 4376 -> 256: 256 columns 50 us, the 128 taken 32.
 // (MN-major tiles load whole panels of 64 columns, so the widths between gain nothing there.)
-template <int kAct, bool kBMn>
+template <int kAct, bool kBMn, bool kScaled>
 cudaError_t launch_rows(const uint16_t* A, const uint16_t* B, const RowsArgs& a, int num_sms, cudaStream_t stream) {
   const SplitPlan split = plan_rows_split(a, kAct == EP_ACT_SWIGLU);
-  if (split.S > 1 && split.tiles * split.S <= num_sms) return launch_rows_split<kAct, kBMn>(A, B, a, split, stream);
+  if (split.S > 1 && split.tiles * split.S <= num_sms) return launch_rows_split<kAct, kBMn, kScaled>(A, B, a, split, stream);
   const int halves = kAct == EP_ACT_SWIGLU ? 2 : 1;
   const int64_t rows = a.groups.rows, groups = a.groups.count == nullptr ? 1 : a.groups.E < rows ? a.groups.E : rows;
   auto cost = [&](int tile_rows, int bn, int at_once) {
@@ -289,27 +326,33 @@ cudaError_t launch_rows(const uint16_t* A, const uint16_t* B, const RowsArgs& a,
     const int64_t c = pair ? cost(2 * kBM, w, num_sms / 2) : cost(kBM, w, num_sms);
     if (c < least) least = c, bn = w;
   }
-  return pair ? launch_rows_pair<kAct, kBMn>(A, B, a, bn, num_sms, stream)
-              : launch_rows_single<kAct, kBMn>(A, B, a, bn, by_parts ? split.part : 0, num_sms, stream);
+  return pair ? launch_rows_pair<kAct, kBMn, kScaled>(A, B, a, bn, num_sms, stream)
+              : launch_rows_single<kAct, kBMn, kScaled>(A, B, a, bn, by_parts ? split.part : 0, num_sms, stream);
+}
+
+template <int kAct>
+cudaError_t launch_forward(const ProductArgs& p, const RowsArgs& a, int num_sms, cudaStream_t stream) {
+  return a.a_sf != nullptr ? launch_rows<kAct, false, true>(p.x, p.weight, a, num_sms, stream)
+                           : launch_rows<kAct, false, false>(p.x, p.weight, a, num_sms, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_product(const ProductArgs& p, int num_sms, cudaStream_t stream) {
-  RowsArgs a = {p.g.groups, p.g.K, {p.bias, p.residual, p.z, p.out, p.g.N, p.g.Z}, p.err};
+  RowsArgs a = {p.g.groups, p.g.K, {p.bias, p.residual, p.z, p.out, p.g.N, p.g.Z}, p.err, p.x_sf};
   switch (p.g.act) {
-    case EP_ACT_RELU: return launch_rows<EP_ACT_RELU, false>(p.x, p.weight, a, num_sms, stream);
-    case EP_ACT_SILU: return launch_rows<EP_ACT_SILU, false>(p.x, p.weight, a, num_sms, stream);
-    case EP_ACT_GELU: return launch_rows<EP_ACT_GELU, false>(p.x, p.weight, a, num_sms, stream);
-    case EP_ACT_SWIGLU: return launch_rows<EP_ACT_SWIGLU, false>(p.x, p.weight, a, num_sms, stream);
-    default: return launch_rows<EP_ACT_NONE, false>(p.x, p.weight, a, num_sms, stream);
+    case EP_ACT_RELU: return launch_forward<EP_ACT_RELU>(p, a, num_sms, stream);
+    case EP_ACT_SILU: return launch_forward<EP_ACT_SILU>(p, a, num_sms, stream);
+    case EP_ACT_GELU: return launch_forward<EP_ACT_GELU>(p, a, num_sms, stream);
+    case EP_ACT_SWIGLU: return launch_forward<EP_ACT_SWIGLU>(p, a, num_sms, stream);
+    default: return launch_forward<EP_ACT_NONE>(p, a, num_sms, stream);
   }
 }
 
 cudaError_t launch_product_dx(const ProductGradArgs& p, int num_sms, cudaStream_t stream) {
-  RowsArgs a = {p.g.groups, p.g.Z, {nullptr, nullptr, nullptr, p.d_x, p.g.K, p.g.K}, p.err};
+  RowsArgs a = {p.g.groups, p.g.Z, {nullptr, nullptr, nullptr, p.d_x, p.g.K, p.g.K}, p.err, nullptr};
   const uint16_t* dz = p.dz != nullptr ? p.dz : p.d_out;
-  return launch_rows<EP_ACT_NONE, true>(dz, p.weight, a, num_sms, stream);
+  return launch_rows<EP_ACT_NONE, true, false>(dz, p.weight, a, num_sms, stream);
 }
 
 }  // namespace ep

@@ -14,19 +14,18 @@ __device__ __forceinline__ void st32(void* p, const uint4& a, const uint4& b) {
                : "memory");
 }
 
-// FP8 rows -> bf16: bf16_rn(code * scale), one scale per 128 columns (fp32, or a
-// power of two packed four to a word). A warp takes 2048 columns of a row, a lane 16 at a
-// time: 16 bytes in, 32 out. Rows past the last region are not part of any block and are left
-// out. This rounding puts the result's error at 2.8e-3 of its norm, where its own rounding
-// alone would leave 1.7e-3; scaling fp32 sums over every 128 columns instead was that exact
-// and took 5.1 ms instead of 2.5 for 65536 x 7168 -> 2 x 2048. Measured: 65536 x 7168 in
-// 226 us (1.4 GB, 6.2 TB/s).
+// FP8 rows -> bf16, exactly: the codes (fp32 scales are applied to the products' sums), or codes
+// times a power of two, one per 128 columns, packed four to a word (exact down to bf16's
+// least numbers). A warp takes 2048 columns of a row, a lane 16 at a time: 16 bytes in, 32
+// out. Rows past the last region are not part of any block and are left out. (Codes times fp32
+// scales rounded to bf16 put the products' error at 2.8e-3 of their norm instead of the 1.7e-3 of
+// their own rounding.) Measured: 65536 x 7168 in 226 us (1.4 GB, 6.2 TB/s).
 __global__ void __launch_bounds__(kThreads)
-    dequant_kernel(const uint8_t* x, const float* x_sf, uint16_t* out, int rows, int K, int sf_pack, const int32_t* total) {
+    dequant_kernel(const uint8_t* x, const float* x_sf, uint16_t* out, int rows, int K, const int32_t* total) {
   pdl_launch_dependents();
   pdl_wait();
   if (total != nullptr) rows = max(0, min(rows, __ldg(total)));
-  const int G = K >> 7, SW = sf_pack ? (G + 3) >> 2 : G, lane = threadIdx.x & 31;
+  const int SW = ((K >> 7) + 3) >> 2, lane = threadIdx.x & 31;
   const int warps = gridDim.x * (kThreads / 32), spans = (K + 2047) / 2048;
   const int units = rows * spans;  // their bytes fit memory, so their number fits 32 bits
   for (int u = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); u < units; u += warps) {
@@ -37,12 +36,10 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll 4
     for (int c = c0 + lane * 16; c < min(K, c0 + 2048); c += 512) {
       const int grp = c >> 7;
-      float sf;
-      if (sf_pack) {
+      float sf = 1.f;
+      if (x_sf != nullptr) {
         const uint32_t e = __float_as_uint(__ldg(sfs + (grp >> 2))) >> (8 * (grp & 3)) & 0xFFu;
         sf = e ? __uint_as_float(e << 23) : __uint_as_float(0x00400000u);  // 2^(e-127)
-      } else {
-        sf = __ldg(sfs + grp);
       }
       const uint4 v = ld_stream16(in + c);
       const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -284,7 +281,7 @@ cudaError_t launch_dequant(const ProductGeometry& g, const uint8_t* x, const flo
   const int64_t ctas = static_cast<int64_t>(num_sms) * per_sm;
   const int32_t* total = g.groups.region == nullptr ? nullptr : g.groups.region + g.groups.E / g.groups.L;
   return launch_chained(dequant_kernel, dim3(static_cast<unsigned>(need < ctas ? need : ctas)), dim3(kThreads), 0, stream,
-                        x, x_sf, out, g.groups.rows, g.K, g.sf_pack, total);
+                        x, x_sf, out, g.groups.rows, g.K, total);
 }
 
 cudaError_t launch_product_dz(const ProductGradArgs& p, int num_sms, cudaStream_t stream) {

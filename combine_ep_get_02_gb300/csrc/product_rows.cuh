@@ -5,9 +5,13 @@
 
 namespace ep {
 
-constexpr int kEpilogueWarps = 8;  // two to each quarter of the TMEM lanes, each with half of the columns
-constexpr int kRowsThreadsTc = 64 + 32 * kEpilogueWarps;
+// Warps of the epilogue, two to each quarter of the TMEM lanes, each with half of the columns. With
+// scaled sums (below) four, so that a thread's 64 sums stay in registers.
+constexpr int epilogue_warps(bool scaled) { return scaled ? 16 : 8; }
+constexpr int rows_threads(bool scaled) { return 64 + 32 * epilogue_warps(scaled); }
 constexpr int kBK = 64;       // summed index per stage: 128 bytes of bf16, one swizzle row
+constexpr int kScaledBlocks = 2;  // blocks of kBK that one scale of the rows covers
+constexpr int kAccColumns = 256;  // TMEM columns of each of the two accumulators
 constexpr int kRaster = 16;   // row tiles that share a sweep over the columns
 
 struct RowsArgs {
@@ -15,6 +19,7 @@ struct RowsArgs {
   int sum;  // length of the summed index
   Epilogue epi;
   uint32_t* err;
+  const float* a_sf;  // [rows][sum / 128]: scales of A, applied to the sums; null: none
 };
 
 struct Tile {
@@ -46,6 +51,57 @@ struct Tiles {
   }
 };
 
+// ---- scaled sums -----------------------------------------------------------------------
+//
+// FP8 rows with fp32 scales: the codes are exact in bf16, their products with 128 columns of B are
+// summed in TMEM, and that sum times the row's scale is added to the thread's sums in
+// registers, out = sum_g sf[r][g] * (sum over the 128 columns of g), so that nothing is
+// rounded to bf16 before the end (1.7e-3 of the result's norm, its own rounding; 2.8e-3 with rows
+// rounded after scaling). A warp holds 32 rows and two chunks of 32 columns of the tile:
+// chunk h = its place among the four of its quarter, and chunk h + 4 (gated: h of the other half).
+
+__device__ __forceinline__ void add_scaled(uint32_t at, float scale, float (&sum)[32]) {
+#pragma unroll
+  for (int i = 0; i < 32; i += 16) {
+    float t[16];
+    tmem_ld16(at + i, t);
+    tmem_ld_wait();
+#pragma unroll
+    for (int j = 0; j < 16; ++j) sum[i + j] = fmaf(scale, t[j], sum[i + j]);
+  }
+}
+
+// Takes `n` accumulators in turn, the first being number `acc`: v += scale * columns c0 on, u those
+// from c1 on (negative: none). `lanes`: TMEM address of column 0 in the warp's lanes; `sf`: the
+// row's first scale (null: the row does not count). arrive(b) hands accumulator b back.
+// False if a wait gave up.
+template <class Arrive>
+__device__ __forceinline__ bool sum_scaled(uint64_t* full, uint32_t lanes, int c0, int c1, const float* sf, int n,
+                                           uint32_t& acc, float (&v)[32], float (&u)[32], const volatile int* abort,
+                                           Arrive arrive) {
+#pragma unroll
+  for (int j = 0; j < 32; ++j) v[j] = u[j] = 0.f;
+  const bool live = __any_sync(kFullMask, sf != nullptr);
+  float next = sf != nullptr && n > 0 ? __ldg(sf) : 0.f;
+  for (int g = 0; g < n; ++g, ++acc) {
+    const float scale = next;
+    if (sf != nullptr && g + 1 < n) next = __ldg(sf + g + 1);
+    const uint32_t b = acc & 1u;
+    const bool ok = *abort == 0 && mbar_wait_timed<false>(smem_addr(&full[b]), acc >> 1 & 1u);
+    if (!__all_sync(kFullMask, ok)) return false;
+    tc_fence_after();
+    const uint32_t d = lanes + b * kAccColumns;
+    if (live) {
+      if (c0 >= 0) add_scaled(d + c0, scale, v);
+      if (c1 >= 0) add_scaled(d + c1, scale, u);
+    }
+    tc_fence_before();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) arrive(b);
+  }
+  return true;
+}
+
 // Tensor maps of A (boxes of `a_rows` rows) and B: K-major boxes of `b_rows` of the output
 // index, or MN-major panels of 64.
 template <bool kBMn>
@@ -74,20 +130,22 @@ struct SplitPlan {
   bool narrow;  // tiles of 128 rows of B instead of 256
   int64_t tiles;
 };
-SplitPlan plan_rows_split(const RowsArgs& a, bool gated);
+SplitPlan plan_rows_split(const RowsArgs& a, bool gated);  // with scales, parts are whole scales
 
 // The three kernels: a CTA per tile of 128 rows, CTA pairs on tiles of 256 rows (both with
 // tiles of `bn` rows of B), and clusters that split the summed index of a few tiles.
 // The first also sums by parts of `part` blocks (0: all at once), on tiles of 128 rows of B at most.
-template <int kAct, bool kBMn>
+template <int kAct, bool kBMn, bool kScaled>
 cudaError_t launch_rows_single(const uint16_t* A, const uint16_t* B, const RowsArgs& a, int bn, int part, int num_sms,
                                cudaStream_t stream);
-template <int kAct, bool kBMn>
+template <int kAct, bool kBMn, bool kScaled>
 cudaError_t launch_rows_pair(const uint16_t* A, const uint16_t* B, const RowsArgs& a, int bn, int num_sms, cudaStream_t stream);
-template <int kAct, bool kBMn>
+template <int kAct, bool kBMn, bool kScaled>
 cudaError_t launch_rows_split(const uint16_t* A, const uint16_t* B, const RowsArgs& a, const SplitPlan& plan, cudaStream_t stream);
 
-#define EP_ROWS_INSTANCES(X) \
-  X(EP_ACT_NONE, false) X(EP_ACT_RELU, false) X(EP_ACT_SILU, false) X(EP_ACT_GELU, false) X(EP_ACT_SWIGLU, false) X(EP_ACT_NONE, true)
+#define EP_ROWS_INSTANCES(X)                                                                                      \
+  X(EP_ACT_NONE, false, false) X(EP_ACT_RELU, false, false) X(EP_ACT_SILU, false, false) X(EP_ACT_GELU, false, false) \
+  X(EP_ACT_SWIGLU, false, false) X(EP_ACT_NONE, true, false) X(EP_ACT_NONE, false, true) X(EP_ACT_RELU, false, true) \
+  X(EP_ACT_SILU, false, true) X(EP_ACT_GELU, false, true) X(EP_ACT_SWIGLU, false, true)
 
 }  // namespace ep

@@ -17,28 +17,34 @@ namespace ep {
 
 namespace {
 
-constexpr int kThreads = kRowsThreadsTc;
 constexpr int kBM = kTileRows;
 // Clusters of S CTAs that fit on the GPU this is written for at one CTA per SM (152 SMs in
 // processing clusters of unequal size); one more would run after the others.
 constexpr int resident_clusters(int S) { return S == 8 ? 15 : S == 4 ? 36 : 76; }
 
-template <int kBN>
+template <int kBN, bool kScaled>
 struct Shape {
   static constexpr int kABytes = kBM * kBK * 2, kBBytes = kBN * kBK * 2, kStageBytes = kABytes + kBBytes;
-  static constexpr int kStages = 196608 / kStageBytes;
+  static constexpr int kStages = (kScaled ? 180224 : 196608) / kStageBytes;  // the more warps, the more patches
+  // the exchanged sums of 8 CTAs fit where the stages were
+  static_assert(8 * kBM * (kBN / 8 + 4) * 4 <= kStages * kStageBytes, "");
 };
 
-template <int kAct, bool kBMn, int kBN>
-__global__ void __launch_bounds__(kThreads, 1)
+// kScaled: scaled sums (product_rows.cuh), an accumulator per scale; a CTA's sums stay in its
+// threads' registers until they are exchanged.
+template <int kAct, bool kBMn, bool kScaled, int kBN>
+__global__ void __launch_bounds__(rows_threads(kScaled), 1)
     rows_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, RowsArgs a,
-                      int S, int a_rows) {
+                      int S, int per, int a_rows) {
   constexpr bool kGated = kAct == EP_ACT_SWIGLU;
+  constexpr int kThreads = rows_threads(kScaled), kEpilogueWarps = epilogue_warps(kScaled);
   constexpr int kCols = kGated ? kBN / 2 : kBN;
   constexpr int kHalves = kGated ? 2 : 1;
-  constexpr int kStages = Shape<kBN>::kStages, kStageBytes = Shape<kBN>::kStageBytes, kABytes = Shape<kBN>::kABytes;
+  using Sizes = Shape<kBN, kScaled>;
+  constexpr int kStages = Sizes::kStages, kStageBytes = Sizes::kStageBytes, kABytes = Sizes::kABytes;
+  constexpr int kTmem = kScaled ? 2 * kAccColumns : kBN;
   extern __shared__ uint8_t s_raw[];
-  __shared__ __align__(8) uint64_t s_full[kStages], s_empty[kStages], s_acc_full;
+  __shared__ __align__(8) uint64_t s_full[kStages], s_empty[kStages], s_acc_full, s_sum_full[2], s_sum_empty[2];
   __shared__ uint32_t s_tmem;
   __shared__ volatile int s_abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -53,13 +59,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init_count(smem_addr(&s_empty[s]), 1);
     }
     mbar_init_count(smem_addr(&s_acc_full), 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init_count(smem_addr(&s_sum_full[i]), 1);
+      mbar_init_count(smem_addr(&s_sum_empty[i]), kEpilogueWarps);
+    }
     s_abort = 0;
     fence_barrier_init();
     tma_prefetch_map(&map_a);
     tma_prefetch_map(&map_b);
   }
   if (warp == 2) {
-    tmem_alloc(smem_addr(&s_tmem), kBN);
+    tmem_alloc(smem_addr(&s_tmem), kTmem);
     tmem_relinquish();
   }
   pdl_launch_dependents();
@@ -73,7 +83,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tile = blockIdx.x / S;
   const bool work = tile < tiles.total;  // the same for the whole cluster
   const Tile t = work ? tiles.at(tile) : Tile{0, 0, 0, 0};
-  const int blocks = (a.sum + kBK - 1) / kBK, per = (blocks + S - 1) / S;
+  const int blocks = (a.sum + kBK - 1) / kBK;
   const int kb0 = work ? min(blocks, rank * per) : 0, kb1 = work ? min(blocks, kb0 + per) : 0;
   auto give_up = [&] {
     s_abort = 1;
@@ -121,15 +131,46 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         tc_fence_after();
+        uint32_t d = tmem;
+        bool first = n == 0;
+        const uint32_t acc = n / kScaledBlocks, b = acc & 1u;  // scaled: the accumulator
+        if constexpr (kScaled) {
+          first = n % kScaledBlocks == 0;
+          d += b * kAccColumns;
+          if (first && (s_abort || !mbar_wait_timed(smem_addr(&s_sum_empty[b]), (acc >> 1 & 1u) ^ 1u))) {
+            if (!s_abort) give_up();
+            break;
+          }
+          tc_fence_after();
+        }
         const uint32_t sa = stage0 + s * kStageBytes, sb = sa + kABytes;
         const uint64_t da = desc_k_major(sa);
         const uint64_t db = kBMn ? desc_mn_major(sb, kBK * 128) : desc_k_major(sb);
 #pragma unroll
         for (int k = 0; k < kBK / 16; ++k)
-          mma_bf16(tmem, da + k * kStepK, db + k * (kBMn ? kStepMN : kStepK), idesc, n > 0 || k > 0);
+          mma_bf16(d, da + k * kStepK, db + k * (kBMn ? kStepMN : kStepK), idesc, !first || k > 0);
         mma_commit(smem_addr(&s_empty[s]));
+        if constexpr (kScaled)
+          if (n % kScaledBlocks == kScaledBlocks - 1) mma_commit(smem_addr(&s_sum_full[b]));
       }
       mma_commit(smem_addr(&s_acc_full));  // also when it gave up: what was issued has finished
+    }
+  }
+  const int quarter = warp & 3, rows = min(kBM, t.rows);
+  const int row = quarter * 32 + lane;
+  // scaled sums of this thread's row: 32 columns each from column c0 and c0 + 128 of the tile on
+  float own[kScaled ? 2 : 1][32];
+  const int c0 = (warp - 2) / 4 * 32;
+  if constexpr (kScaled) {
+    if (warp >= 2) {
+      const int all = blocks / kScaledBlocks;
+      const float* sf = row < rows ? a.a_sf + (static_cast<int64_t>(t.begin) + row) * all + kb0 / kScaledBlocks : nullptr;
+      uint32_t acc = 0;
+      if (!sum_scaled(s_sum_full, tmem + (static_cast<uint32_t>(quarter * 32) << 16), c0, kBN > 128 ? c0 + 128 : -1, sf,
+                      (kb1 - kb0) / kScaledBlocks, acc, own[0], own[1], &s_abort,
+                      [&](uint32_t b) { mbar_arrive(smem_addr(&s_sum_empty[b])); }) &&
+          lane == 0 && !s_abort)
+        give_up();
     }
   }
   __syncwarp();
@@ -141,35 +182,39 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // partial sums [S][rows][width + 4] floats over the stages; CTA r holds columns r * slice on
   const int slice = kCols / S, width = slice * kHalves, stride = width + 4;
-  const int quarter = warp & 3, rows = min(kBM, t.rows);
-  const int row = quarter * 32 + lane;
+  auto give_out = [&](int c, const float (&v)[32]) {
+    if (row >= rows) return;
+#pragma unroll
+    for (int j = 0; j < 32; j += 4) {
+      const int n = c + j, h = n / kCols, col = n - h * kCols, r = col / slice;
+      const uint32_t at = stage0 + 4u * static_cast<uint32_t>((rank * kBM + row) * stride + h * slice + col - r * slice);
+      st_cluster16(cluster_addr(at, static_cast<uint32_t>(r)), v[j], v[j + 1], v[j + 2], v[j + 3]);
+    }
+  };
   if (warp >= 2 && quarter * 32 < rows) {
-    const int half = (warp - 2) >> 2;
-    const uint32_t d = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-    for (int c = half * (kBN / 2); c < (half + 1) * (kBN / 2); c += 32) {
-      float v[32];
-      if (kb1 > kb0) {
-        tmem_ld32(d + c, v);
-        tmem_ld_wait();
-      } else {
+    if constexpr (kScaled) {
+      give_out(c0, own[0]);
+      if constexpr (kBN > 128) give_out(c0 + 128, own[1]);
+    } else {
+      const int half = (warp - 2) >> 2;
+      const uint32_t d = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+      for (int c = half * (kBN / 2); c < (half + 1) * (kBN / 2); c += 32) {
+        float v[32];
+        if (kb1 > kb0) {
+          tmem_ld32(d + c, v);
+          tmem_ld_wait();
+        } else {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = 0.f;
-      }
-      if (row < rows) {
-#pragma unroll
-        for (int j = 0; j < 32; j += 4) {
-          const int n = c + j, h = n / kCols, col = n - h * kCols, r = col / slice;
-          const uint32_t at = stage0 + 4u * static_cast<uint32_t>((rank * kBM + row) * stride + h * slice + col - r * slice);
-          st_cluster16(cluster_addr(at, static_cast<uint32_t>(r)), v[j], v[j + 1], v[j + 2], v[j + 3]);
+          for (int j = 0; j < 32; ++j) v[j] = 0.f;
         }
+        give_out(c, v);
       }
     }
   }
   cluster_sync_all();  // the partial sums have arrived
   if (warp >= 2 && quarter * 32 < rows) {
-    const int half = (warp - 2) >> 2;
     const uint32_t patch = patch0 + (warp - 2) * kPatchBytes;
-    for (int c = half * 32; c < slice; c += 64) {
+    for (int c = (warp - 2) / 4 * 32; c < slice; c += kEpilogueWarps * 8) {
       const int n0 = t.n0 + rank * slice + c, cols = min(32, slice - c);
       if (n0 >= a.epi.cols) break;
       float v[32], u[kGated ? 32 : 1];
@@ -200,22 +245,25 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 2) tmem_dealloc(tmem, kBN);
+  if (warp == 2) tmem_dealloc(tmem, kTmem);
 }
 
-template <int kAct, bool kBMn, int kBN>
-cudaError_t launch(const uint16_t* A, const uint16_t* B, const RowsArgs& a, int64_t tiles, int S, cudaStream_t stream) {
+template <int kAct, bool kBMn, bool kScaled, int kBN>
+cudaError_t launch(const uint16_t* A, const uint16_t* B, const RowsArgs& a, const SplitPlan& plan, cudaStream_t stream) {
+  using Sizes = Shape<kBN, kScaled>;
+  constexpr int kThreads = rows_threads(kScaled);
+  const int S = plan.S;
   // boxes of A no higher than the rows there are
   const int a_rows = a.groups.rows < kBM ? (a.groups.rows + 7) / 8 * 8 : kBM;
   CUtensorMap map_a, map_b;
   const cudaError_t st = make_rows_maps<kBMn>(&map_a, &map_b, A, B, a, a_rows, kBN / 2);
   if (st != cudaSuccess) return st;
-  auto kern = rows_split_kernel<kAct, kBMn, kBN>;
-  const size_t smem = 1024 + Shape<kBN>::kStages * Shape<kBN>::kStageBytes + kEpilogueWarps * kPatchBytes +
+  auto kern = rows_split_kernel<kAct, kBMn, kScaled, kBN>;
+  const size_t smem = 1024 + Sizes::kStages * Sizes::kStageBytes + epilogue_warps(kScaled) * kPatchBytes +
                       sizeof(int) * (static_cast<size_t>(a.groups.E) + 1);
   if (resident_ctas(reinterpret_cast<const void*>(kern), kThreads, smem) < 1) return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(tiles * S));
+  cfg.gridDim = dim3(static_cast<unsigned>(plan.tiles * S));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
@@ -228,7 +276,7 @@ cudaError_t launch(const uint16_t* A, const uint16_t* B, const RowsArgs& a, int6
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kern, map_a, map_b, a, S, a_rows);
+  return cudaLaunchKernelEx(&cfg, kern, map_a, map_b, a, S, plan.part, a_rows);
 }
 
 }  // namespace
@@ -250,20 +298,21 @@ SplitPlan plan_rows_split(const RowsArgs& a, bool gated) {
   if (blocks < (rows <= 32 ? 16 : 32)) return plan;
   int64_t ctas = 0;
   for (int s = 2; s <= 8 && blocks >= s * 2; s *= 2) {
-    const int part = (blocks + s - 1) / s;
+    int part = (blocks + s - 1) / s;
+    if (a.a_sf != nullptr) part = (part + kScaledBlocks - 1) / kScaledBlocks * kScaledBlocks;
     if (wide <= resident_clusters(s) && wide * s > ctas) plan = {s, part, false, wide}, ctas = wide * s;
     if (narrow <= resident_clusters(s) && narrow * s > ctas) plan = {s, part, true, narrow}, ctas = narrow * s;
   }
   return plan;
 }
 
-template <int kAct, bool kBMn>
+template <int kAct, bool kBMn, bool kScaled>
 cudaError_t launch_rows_split(const uint16_t* A, const uint16_t* B, const RowsArgs& a, const SplitPlan& plan, cudaStream_t stream) {
-  return plan.narrow ? launch<kAct, kBMn, 128>(A, B, a, plan.tiles, plan.S, stream)
-                     : launch<kAct, kBMn, 256>(A, B, a, plan.tiles, plan.S, stream);
+  return plan.narrow ? launch<kAct, kBMn, kScaled, 128>(A, B, a, plan, stream)
+                     : launch<kAct, kBMn, kScaled, 256>(A, B, a, plan, stream);
 }
-#define X(act, mn) \
-  template cudaError_t launch_rows_split<act, mn>(const uint16_t*, const uint16_t*, const RowsArgs&, const SplitPlan&, cudaStream_t);
+#define X(act, mn, scaled) \
+  template cudaError_t launch_rows_split<act, mn, scaled>(const uint16_t*, const uint16_t*, const RowsArgs&, const SplitPlan&, cudaStream_t);
 EP_ROWS_INSTANCES(X)
 #undef X
 

@@ -36,21 +36,30 @@ __device__ __forceinline__ uint64_t global_ns() {
   asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
   return t;
 }
-// the barrier may also be arrived on from the other CTAs of a cluster
+// kCluster: what other CTAs of the cluster wrote before they arrived becomes visible. Without
+// it the wait is for this CTA's copies and products, or for others that publish no memory.
+template <bool kCluster>
 __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
   uint32_t done;
-  asm volatile(
-      "{ .reg .pred p; mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
-      : "=r"(done)
-      : "r"(bar), "r"(parity)
-      : "memory");
+  if constexpr (kCluster)
+    asm volatile(
+        "{ .reg .pred p; mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
+  else
+    asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+                 : "=r"(done)
+                 : "r"(bar), "r"(parity)
+                 : "memory");
   return done != 0;
 }
+template <bool kCluster = true>
 __device__ __forceinline__ bool mbar_wait_timed(uint32_t bar, uint32_t parity) {
-  if (mbar_try(bar, parity)) return true;
+  if (mbar_try<kCluster>(bar, parity)) return true;
   const uint64_t start = global_ns();
   for (uint32_t i = 0; i < kBulkWaitLimit; ++i) {
-    if (mbar_try(bar, parity)) return true;
+    if (mbar_try<kCluster>(bar, parity)) return true;
     if ((i & 15u) == 15u && global_ns() - start > kWaitNs) return false;
   }
   return false;
@@ -154,6 +163,12 @@ __device__ __forceinline__ void cluster_sync_all() {
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+// For handing an accumulator back: the thread's reads of TMEM are complete (tcgen05.wait::ld) and
+// it publishes nothing in memory, so the release need not reach the cluster, which
+// takes about a microsecond.
+__device__ __forceinline__ void mbar_arrive_read(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
 __device__ __forceinline__ void st_cluster16(uint32_t p, float a, float b, float c, float d) {
   asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(p), "f"(a), "f"(b), "f"(c), "f"(d) : "memory");
 }
@@ -213,7 +228,19 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, float (&v)[32]) {
 #pragma unroll
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
-// and the same back
+// the same for 16 columns
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, float (&v)[16]) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(addr));
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+// 32 columns from the registers back to TMEM
 __device__ __forceinline__ void tmem_st32(uint32_t addr, const float (&v)[32]) {
   uint32_t r[32];
 #pragma unroll

@@ -421,7 +421,7 @@ typedef struct ep_product_config {
   int32_t out_features; /* N of out, a multiple of 8, up to 2^20                    */
   int32_t activation;   /* EP_ACT_*                                                 */
   int32_t x_dtype;      /* EP_DTYPE_BF16, or EP_DTYPE_FP8_E4M3: the rows and x_sf of an
-                           FP8 dispatch (each element is taken as bf16_rn(code * scale);
+                           FP8 dispatch (each element is code * scale, not rounded;
                            forward only)                                            */
   int32_t sf_pack;      /* x_sf as ep_config_t.sf_pack                              */
   int32_t num_sms;      /* SMs to use; 0 = all. Results do not depend on it. (d_weight

@@ -1,5 +1,5 @@
 """Matrix gradients that are sums over so many rows that a tile takes seconds: the waits of the
-kernel's other warps last as long (they once gave up after two seconds; this call takes 4.4)."""
+kernel's other warps last as long (here 4.4 seconds)."""
 import pytest
 import torch
 
