@@ -502,6 +502,9 @@ _BF16, _F32, _I32, _I64, _U8 = torch.bfloat16, torch.float32, torch.int32, torch
 
 @dataclasses.dataclass
 class RouteConfig(_KeepsStruct):
+    """ep_route_config_t. Softmax scores with a choice bias or groups: both act on the logits,
+    not on the probabilities."""
+
     num_segments: int
     num_tokens: int  # per segment
     num_experts: int

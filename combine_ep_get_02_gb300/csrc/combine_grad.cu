@@ -13,7 +13,8 @@
 // the row of top-k lane k, and the lowest lane of those that share a row stands for it.
 // Each lane holds 8 columns of g per step and streams the distinct rows past them; the K
 // dot products stay in registers in 32 bits to the end of the token and are summed across
-// the warp once, then over the token's warps in their order.
+// the warp once, then over the token's warps in their order. Up to 16 top-k lanes the rows in
+// flight fit the registers; with 17 to 32 a thread takes 255 of them and spills 240 bytes.
 #include "ep_device.cuh"
 #include "moe_internal.cuh"
 

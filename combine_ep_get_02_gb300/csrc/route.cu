@@ -2,7 +2,8 @@
 // counts and the balance loss; and the gradient of the logits.
 //
 // With l the logits of a token (E of them), s = softmax(l) or sigmoid(l):
-//   choice score c = l + b (softmax; the softmax keeps the order) or s + b (sigmoid);
+//   choice score c = l + b (softmax: single experts rank by l as they do by s; sums of two and
+//   sums with a bias are those of logits) or s + b (sigmoid);
 //   expert groups: a group's score is the sum of its two best c; the best `keep`
 //   groups stay, ties to the lowest group;
 //   the K best c are chosen in order, ties to the lowest expert; -inf is never chosen;
@@ -18,9 +19,10 @@
 // Reading the logits once is what the operator cannot do without; what bounds it is the
 // instructions on them, about 560 a token at 256 experts, top 8, half of them the choice
 // (comparisons run at half rate). Measured: 16 x 4096 tokens, 256 experts, top 8, softmax
-// 45 us (67 MB of logits, 1.6 TB/s; 84 us with sigmoid scores and 8 groups), one segment of
-// 65536 tokens 43 us; 64 tokens 7 us, of which 3.5 are the statistics' chain of one atomic
-// and one load across the CTAs; the gradient of 16 x 4096 tokens 32 us (sigmoid; 141 MB, 4.4 TB/s).
+// 48 us (67 MB of logits, 1.4 TB/s; 88 us with sigmoid scores and 8 groups, 92 with a bias), one
+// segment of 65536 tokens 43 us; 64 tokens 7 us, of which 3.5 are the statistics' chain of one atomic
+// and one load across the CTAs; the gradient of 16 x 4096 tokens
+// 30 us, with sigmoid scores 32 (141 MB, 4.4 TB/s).
 #include <type_traits>
 
 #include "ep_device.cuh"
@@ -800,8 +802,9 @@ cudaError_t launch_bwd(const RouteGradArgs& a, cudaStream_t stream) {
   return launch_chained(kern, dim3(static_cast<unsigned>(a.g.B) * a.g.C), dim3(kRouteThreads), smem, stream, a);
 }
 
-// Registers per lane: the least of 1, 2, 4, 8, 16, 32, 128 that holds E (128 spills; it
-// serves more than 1024 experts only). Rows of a multiple of 4 logits load 4 at a time.
+// Logits per lane: the least of 1, 2, 4, 8, 16, 32, 128 that holds E. 128 serves more than 1024
+// experts only and spills 1 to 5 KB a thread; the forward's 8 spills 12 bytes at the 64 registers that
+// four CTAs an SM leave. Rows of a multiple of 4 logits load 4 at a time.
 template <class Args, class Launch>
 cudaError_t by_size(const Args& a, Launch launch) {
   const int E = a.g.E;

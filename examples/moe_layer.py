@@ -23,7 +23,8 @@ import combine_ep_get_02_gb300 as ep  # noqa: E402
 
 class MoELayer:
     """Router matrix [E][H] and experts' matrices [E][2 inner][H] and [E][H][inner]; ranks x tokens
-    of hidden size H, K experts each."""
+    of hidden size H, K experts each. fp8: rows travel as FP8, which the forward takes; the gradients
+    of the experts' matrices need bf16 rows, so backward() refuses it."""
 
     def __init__(self, ranks, tokens, hidden, inner, experts, topk, seed=0, score=ep.EP_SCORE_SOFTMAX, fp8=False,
                  grad=True):

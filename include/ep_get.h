@@ -361,6 +361,10 @@ size_t ep_route_workspace_bytes(const ep_route_config_t* cfg);
  *   - The K experts of largest choice score in order, ties to the lowest expert;
  *     with groups, among the topk_groups groups whose two best choice scores have the
  *     largest fp32 sum, ties to the lowest group.
+ *   - With softmax scores the choice score is the logit. Without groups and bias that chooses
+ *     the largest probabilities. A bias is added to logits, and groups are ranked by sums
+ *     of logits: a router trained with a bias on probabilities, or with groups ranked by
+ *     sums of probabilities, chooses differently and is not what this computes.
  *   - An expert whose logit or choice score is -inf is never chosen; lanes for which
  *     no expert is left are -1. NaN and +inf are taken as -inf and latch
  *     EP_ERR_NONFINITE.
