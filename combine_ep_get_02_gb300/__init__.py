@@ -9,8 +9,10 @@ is missing, importing the binding raises.
 The entry points keep the C names (``ep_get_dispatch_layout``, ``ep_dispatch``,
 ``ep_combine``, ...). ``Config`` mirrors ``ep_config_t``; ``alloc_layout``,
 ``alloc_recv`` and ``alloc_workspace`` allocate correctly sized tensors.
-Beside them stand the router (``ep_route`` with its balance loss), the experts'
-products (``ep_expert_product``) and their gradients with the combine's.
+Beside them stand the norm in front of the router (``ep_norm``), the router
+(``ep_route`` with its balance loss), the experts' products (``ep_expert_product``),
+their gradients with the combine's, and rows kept in 8 bits for the backward pass
+(``ep_checkpoint``).
 """
 from __future__ import annotations
 
@@ -39,6 +41,9 @@ __all__ = [
     "RouteConfig", "Route", "ProductConfig", "ep_route_workspace_bytes", "ep_product_workspace_bytes",
     "alloc_route", "alloc_route_workspace", "alloc_product_workspace", "ep_route", "ep_route_grad",
     "ep_combine_grad", "ep_expert_product", "ep_expert_product_grad",
+    "NormConfig", "ep_norm_workspace_bytes", "alloc_norm_workspace", "ep_norm", "ep_norm_grad",
+    "CheckpointConfig", "ep_checkpoint_workspace_bytes", "alloc_checkpoint_workspace", "ep_checkpoint",
+    "ep_checkpoint_rows", "ep_checkpoint_grad",
 ]
 
 
@@ -220,6 +225,20 @@ def lib():
         L.ep_expert_product.argtypes = [P, P, P, P, P, P, P, P, P, P, C.c_size_t, P]
         L.ep_expert_product_grad.restype = I
         L.ep_expert_product_grad.argtypes = [P, P, P, P, P, P, P, P, P, P, C.c_size_t, P]
+        L.ep_norm_workspace_bytes.restype = C.c_size_t
+        L.ep_norm_workspace_bytes.argtypes = [P]
+        L.ep_norm.restype = I
+        L.ep_norm.argtypes = [P] * 9
+        L.ep_norm_grad.restype = I
+        L.ep_norm_grad.argtypes = [P, P, P, P, P, P, P, P, P, C.c_size_t, P]
+        L.ep_checkpoint_workspace_bytes.restype = C.c_size_t
+        L.ep_checkpoint_workspace_bytes.argtypes = [P]
+        L.ep_checkpoint.restype = I
+        L.ep_checkpoint.argtypes = [P, P, P, P, P, P, C.c_size_t, P]
+        L.ep_checkpoint_rows.restype = I
+        L.ep_checkpoint_rows.argtypes = [P, P, P, P, P, P, C.c_size_t, P]
+        L.ep_checkpoint_grad.restype = I
+        L.ep_checkpoint_grad.argtypes = [P, P, P, P, P, P, P, P, P, C.c_size_t, P]
         L.ep_check_error.restype = I
         L.ep_check_error.argtypes = [P, P]
         L.ep_status_string.restype = C.c_char_p
@@ -742,3 +761,162 @@ def ep_expert_product_grad(cfg: ProductConfig, layout, x, weight, z, d_out: torc
         None if d_bias is None else _at(d_bias, _F32, n_b, w, "d_bias"), *_space(ws, w), _raw_stream(stream))
     if st:
         raise EpError(st, w)
+
+
+# ---- norm, rows kept in 8 bits ----------------------------------------------------------
+
+
+class _NormConfig(C.Structure):
+    _fields_ = [("rows", C.c_int64), ("hidden", C.c_int32), ("x_dtype", C.c_int32), ("sf_pack", C.c_int32),
+                ("eps", C.c_float)]
+
+
+class _CheckpointConfig(C.Structure):
+    _fields_ = [("num_ranks", C.c_int32), ("num_experts", C.c_int32), ("rows", C.c_int64)] + [
+        (n, C.c_int32) for n in ("features", "activation", "sf_pack")]
+
+
+@dataclasses.dataclass
+class NormConfig(_KeepsStruct):
+    rows: int
+    hidden: int
+    x_dtype: int = EP_DTYPE_BF16  # of x, residual, sum and their gradients (or EP_DTYPE_FP32)
+    sf_pack: int = 0
+    eps: float = 1e-6
+
+    def _needs(self):
+        """(type of x, elements, scales, columns, rows) of a call, kept as the struct is."""
+        G = self.hidden // 128
+        n = (_F32 if self.x_dtype == EP_DTYPE_FP32 else _BF16, self.rows * self.hidden,
+             self.rows * ((G + 3) // 4 if self.sf_pack else G), self.hidden, self.rows)
+        object.__setattr__(self, "_sizes", n)
+        return n
+
+    def _build_struct(self) -> _NormConfig:
+        return _NormConfig(int(self.rows), int(self.hidden), int(self.x_dtype), int(self.sf_pack), float(self.eps))
+
+
+@dataclasses.dataclass
+class CheckpointConfig(_KeepsStruct):
+    num_ranks: int
+    num_experts: int
+    rows: int
+    features: int                  # columns of the kept rows: z_features of their product
+    activation: int = EP_ACT_NONE  # ep_checkpoint_grad only
+    sf_pack: int = 0
+
+    @property
+    def out_features(self) -> int:
+        """Columns after the activation: half of the features when gated."""
+        return self.features // (2 if self.activation == EP_ACT_SWIGLU else 1)
+
+    def _needs(self):
+        """(rows' elements, scales, elements after the activation, d_bias, -, -, blocks' counts, starts,
+        regions) of a call; the last three as in ProductConfig."""
+        G, E = self.features // 128, self.num_experts
+        n = (self.rows * self.features, self.rows * ((G + 3) // 4 if self.sf_pack else G), self.rows * self.out_features,
+             E * self.features, 0, 0, E, E + self.num_ranks, self.num_ranks + 1)
+        object.__setattr__(self, "_sizes", n)
+        return n
+
+    def _build_struct(self) -> _CheckpointConfig:
+        return _CheckpointConfig(*(int(getattr(self, f[0])) for f in _CheckpointConfig._fields_))
+
+
+def ep_norm_workspace_bytes(cfg: NormConfig) -> int:
+    return int(lib().ep_norm_workspace_bytes(cfg._ref()))
+
+
+def ep_checkpoint_workspace_bytes(cfg: CheckpointConfig) -> int:
+    return int(lib().ep_checkpoint_workspace_bytes(cfg._ref()))
+
+
+def _alloc_headed(n: int, where: str, device) -> torch.Tensor:
+    """Workspace of n bytes with a zeroed header."""
+    if n == 0:
+        raise EpError(EP_ERR_INVALID_ARG, where)
+    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    ws[:256].zero_()
+    return ws
+
+
+def alloc_norm_workspace(cfg: NormConfig, device="cuda") -> torch.Tensor:
+    """Workspace of ep_norm_grad: ep_norm_workspace_bytes(cfg) bytes."""
+    return _alloc_headed(ep_norm_workspace_bytes(cfg), "ep_norm_workspace_bytes", device)
+
+
+def alloc_checkpoint_workspace(cfg: CheckpointConfig, device="cuda") -> torch.Tensor:
+    """Workspace of ep_checkpoint_workspace_bytes(cfg) bytes with a zeroed header."""
+    return _alloc_headed(ep_checkpoint_workspace_bytes(cfg), "ep_checkpoint_workspace_bytes", device)
+
+
+def _codes(t, numel: int, where: str, name: str = "codes"):
+    """Address of e4m3 codes: uint8, or torch's own type."""
+    return _at(t, torch.float8_e4m3fn if t is not None and t.dtype is torch.float8_e4m3fn else _U8, numel, where, name)
+
+
+def ep_norm(cfg: NormConfig, x: torch.Tensor, residual, weight, sum, y, codes, sf, stream=None):
+    """y = rms-norm of x + residual, times weight; sum keeps x + residual; codes and sf are y as the
+    FP8 rows that ep_dispatch takes. residual, weight, sum may be None, y or the codes too."""
+    w = "ep_norm"
+    kind, n, n_sf, H, _ = cfg._sizes or cfg._needs()
+    st = (_lib or lib()).ep_norm(
+        cfg._reference or cfg._ref(), _at(x, kind, n, w, "x"),
+        None if residual is None else _at(residual, kind, n, w, "residual"),
+        None if weight is None else _at(weight, _BF16, H, w, "weight"), None if sum is None else _at(sum, kind, n, w, "sum"),
+        None if y is None else _at(y, _BF16, n, w, "y"), None if codes is None else _codes(codes, n, w),
+        None if sf is None else _at(sf, _F32, n_sf, w, "sf"), _raw_stream(stream))
+    if st:
+        raise EpError(st, w)
+
+
+def ep_norm_grad(cfg: NormConfig, sum: torch.Tensor, weight, token_mask, d_y: torch.Tensor, d_sum, d_x, d_weight,
+                 ws: torch.Tensor, stream=None):
+    """Gradients of ep_norm's rows (d_x, of x and the residual alike) and weights; d_sum is what arrives
+    at the kept sum itself (None: zero), and d_x may take its place."""
+    w = "ep_norm_grad"
+    kind, n, _, H, rows = cfg._sizes or cfg._needs()
+    if token_mask is not None:
+        token_mask = _at(token_mask, torch.bool if token_mask.dtype is torch.bool else _U8, rows, w, "token_mask")
+    st = (_lib or lib()).ep_norm_grad(
+        cfg._reference or cfg._ref(), _at(sum, kind, n, w, "sum"), None if weight is None else _at(weight, _BF16, H, w, "weight"),
+        token_mask, _at(d_y, _BF16, n, w, "d_y"), None if d_sum is None else _at(d_sum, kind, n, w, "d_sum"),
+        None if d_x is None else _at(d_x, kind, n, w, "d_x"),
+        None if d_weight is None else _at(d_weight, _F32, H, w, "d_weight"), *_space(ws, w), _raw_stream(stream))
+    if st:
+        raise EpError(st, w)
+
+
+def ep_checkpoint(cfg: CheckpointConfig, layout, x: torch.Tensor, codes: torch.Tensor, sf: torch.Tensor, ws: torch.Tensor,
+                  stream=None):
+    """Keeps the bf16 rows of every expert's block of an expanded layout (layout None: all rows) in 8
+    bits: codes and a scale per 128 columns, as ep_dispatch casts."""
+    w = "ep_checkpoint"
+    needs = cfg._sizes or cfg._needs()
+    _check((_lib or lib()).ep_checkpoint(
+        cfg._reference or cfg._ref(), _blocks_arg(w, needs, layout), _at(x, _BF16, needs[0], w, "x"),
+        _codes(codes, needs[0], w), _at(sf, _F32, needs[1], w, "sf"), *_space(ws, w), _raw_stream(stream)), w)
+
+
+def ep_checkpoint_rows(cfg: CheckpointConfig, layout, codes: torch.Tensor, sf: torch.Tensor, x: torch.Tensor,
+                       ws: torch.Tensor, stream=None):
+    """Kept rows (or rows of an FP8 dispatch) back in bf16."""
+    w = "ep_checkpoint_rows"
+    needs = cfg._sizes or cfg._needs()
+    _check((_lib or lib()).ep_checkpoint_rows(
+        cfg._reference or cfg._ref(), _blocks_arg(w, needs, layout), _codes(codes, needs[0], w),
+        _at(sf, _F32, needs[1], w, "sf"), _at(x, _BF16, needs[0], w, "x"), *_space(ws, w), _raw_stream(stream)), w)
+
+
+def ep_checkpoint_grad(cfg: CheckpointConfig, layout, codes: torch.Tensor, sf: torch.Tensor, d_h: torch.Tensor, h, d_z,
+                       d_bias, ws: torch.Tensor, stream=None):
+    """The backward pass through the activation of kept rows z: h = act(z) again, d_z = d_h act'(z) and
+    the bias gradients d_bias [E][features]; any of the three may be None."""
+    w = "ep_checkpoint_grad"
+    needs = cfg._sizes or cfg._needs()
+    n, n_sf, n_h, n_b = needs[:4]
+    _check((_lib or lib()).ep_checkpoint_grad(
+        cfg._reference or cfg._ref(), _blocks_arg(w, needs, layout), _codes(codes, n, w), _at(sf, _F32, n_sf, w, "sf"),
+        _at(d_h, _BF16, n_h, w, "d_h"), None if h is None else _at(h, _BF16, n_h, w, "h"),
+        None if d_z is None else _at(d_z, _BF16, n, w, "d_z"), None if d_bias is None else _at(d_bias, _F32, n_b, w, "d_bias"),
+        *_space(ws, w), _raw_stream(stream)), w)

@@ -1,0 +1,80 @@
+// Rows of an expanded layout's blocks kept in 8 bits (the dispatch's FP8 rows: e4m3 codes and a scale
+// per 128 columns), and back in bf16. Rows outside the blocks' lanes are neither read nor written.
+#include "dispatch_common.cuh"
+
+#include "block_internal.cuh"
+#include "fp8_rows.cuh"
+#include "product_common.cuh"
+
+namespace ep {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kSpan = 256, kAcross = kSpan / 16, kDown = kThreads / kAcross;  // columns a CTA takes, 16 a thread
+
+// A CTA takes 64 rows of a block and 256 columns: 16 threads across, 16 columns each (8 neighbouring
+// threads share a scale), 16 rows down. Memory bounds it: nothing is read or written twice.
+template <bool kBack>
+__global__ void __launch_bounds__(kThreads) checkpoint_kernel(CheckpointArgs a) {
+  extern __shared__ int prefix[];  // [E + 1]
+  pdl_launch_dependents();
+  pdl_wait();
+  build_prefix<kThreads>(a.groups, kDzRows, prefix, blockIdx.x == 0 ? a.err : nullptr);
+  const int across = threadIdx.x % kAcross, down = threadIdx.x / kAcross;
+  const int spans = (a.F + kSpan - 1) / kSpan, G = a.F >> 7;
+  const int64_t units = static_cast<int64_t>(prefix[a.groups.E]) * spans;
+  for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+    const int tile = static_cast<int>(u / spans), col = static_cast<int>(u - static_cast<int64_t>(tile) * spans) * kSpan + across * 16;
+    const int g = group_of_tile(prefix, a.groups.E, tile);
+    const GroupRows rows = group_rows(a.groups, g);
+    const int m0 = (tile - prefix[g]) * kDzRows, n = min(kDzRows, rows.count - m0);
+    const bool in = col < a.F;  // the same for the 8 threads of a scale
+#pragma unroll
+    for (int i = 0; i < kDzRows / kDown; ++i) {  // whole warps take part in the maxima
+      const int r = i * kDown + down;
+      const int64_t row = static_cast<int64_t>(rows.begin) + m0 + r, at = row * a.F + col;
+      const bool there = in && r < n;
+      if constexpr (kBack) {
+        if (there) {
+          const uint4 q = ld_stream16(static_cast<const uint8_t*>(a.in) + at);
+          const float s = load_scale(a.sf, row, col >> 7, G, a.sf_pack);
+          float f[16];
+          e4m3x4_to_f32(q.x, f);
+          e4m3x4_to_f32(q.y, f + 4);
+          e4m3x4_to_f32(q.z, f + 8);
+          e4m3x4_to_f32(q.w, f + 12);
+#pragma unroll
+          for (int k = 0; k < 16; ++k) f[k] *= s;
+          st16(static_cast<uint16_t*>(a.out) + at, pack8(f));
+          st16(static_cast<uint16_t*>(a.out) + at + 8, pack8(f + 8));
+        }
+      } else {
+        uint4 lo = make_uint4(0u, 0u, 0u, 0u), hi = lo;
+        if (there) {
+          lo = ld_stream16(static_cast<const uint16_t*>(a.in) + at);
+          hi = ld_stream16(static_cast<const uint16_t*>(a.in) + at + 8);
+        }
+        const CastUnit c = cast_unit(lo, hi, there, a.sf_pack);
+        if (there) {
+          st16(static_cast<uint8_t*>(a.out) + at, c.q);
+          if ((across & 7) == 0) store_scale(a.sf, row, col >> 7, G, RowScale{0.f, c.sf, c.sf_byte}, a.sf_pack);
+        }
+      }
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_checkpoint(const CheckpointArgs& a, bool back, int num_sms, cudaStream_t stream) {
+  auto kern = back ? checkpoint_kernel<true> : checkpoint_kernel<false>;
+  const size_t smem = sizeof(int) * (static_cast<size_t>(a.groups.E) + 1);
+  const int per_sm = resident_ctas(reinterpret_cast<const void*>(kern), kThreads, smem);
+  if (per_sm < 1) return cudaErrorInvalidConfiguration;
+  const int64_t most = max_row_tiles(a.groups, kDzRows) * ((a.F + kSpan - 1) / kSpan);
+  const int64_t ctas = static_cast<int64_t>(num_sms) * per_sm;
+  return launch_chained(kern, dim3(static_cast<unsigned>(most < ctas ? most : ctas)), dim3(kThreads), smem, stream, a);
+}
+
+}  // namespace ep

@@ -1,5 +1,7 @@
 // What the products need around the tensor cores: the tensor maps, FP8 rows as bf16,
 // and the gradient through the activation with the bias gradient's sums.
+#include "block_internal.cuh"
+#include "fp8_rows.cuh"
 #include "product_common.cuh"
 
 namespace ep {
@@ -7,6 +9,12 @@ namespace ep {
 namespace {
 
 constexpr int kThreads = 256;
+
+__device__ __forceinline__ uint2 ld_stream8(const void* p) {
+  uint2 v;
+  asm("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  return v;
+}
 
 __device__ __forceinline__ void st32(void* p, const uint4& a, const uint4& b) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w),
@@ -78,9 +86,28 @@ struct DzArgs {
   float* d_bias;
   uint32_t* done;  // [E][spans]: tiles finished (returns to 0); null: the sums stay in part
   uint32_t* err;
+  const uint8_t* codes = nullptr;  // z kept in 8 bits, in its place ...
+  const float* z_sf = nullptr;     // ... with its scales
+  int sf_pack = 0;
+  uint16_t* h = nullptr;           // act(z) again; may be null
 };
 
-template <int kAct>
+// Eight columns c.. of row `row` of z: bf16, or kept in 8 bits (G scales a row).
+template <bool kKept>
+__device__ __forceinline__ void load_z(const DzArgs& a, int64_t row, int c, float (&f)[8]) {
+  if constexpr (kKept) {
+    const uint2 q = ld_stream8(a.codes + row * a.Z + c);
+    const float s = load_scale(a.z_sf, row, c >> 7, a.Z >> 7, a.sf_pack);
+    e4m3x4_to_f32(q.x, f);
+    e4m3x4_to_f32(q.y, f + 4);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] *= s;
+  } else {
+    unpack8(ld_stream16(a.z + row * a.Z + c), f);
+  }
+}
+
+template <int kAct, bool kKept = false>
 __global__ void __launch_bounds__(kThreads) dz_kernel(DzArgs a) {
   constexpr bool kGated = kAct == EP_ACT_SWIGLU;
   constexpr int kHalves = kGated ? 2 : 1;
@@ -114,21 +141,27 @@ __global__ void __launch_bounds__(kThreads) dz_kernel(DzArgs a) {
         unpack8(ld_stream16(a.d_out + row * a.N + col), d);
         if constexpr (kGated) {
           float zg[8], zu[8];
-          unpack8(ld_stream16(a.z + row * a.Z + col), zg);
-          unpack8(ld_stream16(a.z + row * a.Z + a.N + col), zu);
+          load_z<kKept>(a, row, col, zg);
+          load_z<kKept>(a, row, a.N + col, zu);
+          float again[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
+            const float v = activate<kAct>(zg[i]);
+            again[i] = v * zu[i];
             t[i] = d[i] * zu[i] * activate_grad<kAct>(zg[i]);
-            t[8 + i] = d[i] * activate<kAct>(zg[i]);
+            t[8 + i] = d[i] * v;
           }
-        } else if constexpr (kAct == EP_ACT_NONE) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) t[i] = d[i];
+          if (kKept && a.h != nullptr) st16(a.h + row * a.N + col, pack8(again));
         } else {
           float zv[8];
-          unpack8(ld_stream16(a.z + row * a.Z + col), zv);
+          if (kAct != EP_ACT_NONE || (kKept && a.h != nullptr)) load_z<kKept>(a, row, col, zv);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) t[i] = d[i] * activate_grad<kAct>(zv[i]);
+          for (int i = 0; i < 8; ++i) t[i] = kAct == EP_ACT_NONE ? d[i] : d[i] * activate_grad<kAct>(zv[i]);
+          if (kKept && a.h != nullptr) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) zv[i] = activate<kAct>(zv[i]);
+            st16(a.h + row * a.N + col, pack8(zv));
+          }
         }
         if (a.dz != nullptr) {
 #pragma unroll
@@ -223,9 +256,9 @@ __global__ void __launch_bounds__(kThreads) bias_sum_kernel(Groups q, int Z, con
   }
 }
 
-template <int kAct>
+template <int kAct, bool kKept = false>
 cudaError_t launch_dz(DzArgs a, int num_sms, cudaStream_t stream) {
-  auto kern = dz_kernel<kAct>;
+  auto kern = dz_kernel<kAct, kKept>;
   const size_t smem = sizeof(int) * (static_cast<size_t>(a.groups.E) + 1);
   const int per_sm = resident_ctas(reinterpret_cast<const void*>(kern), kThreads, smem);
   if (per_sm < 1) return cudaErrorInvalidConfiguration;
@@ -294,6 +327,21 @@ cudaError_t launch_product_dz(const ProductGradArgs& p, int num_sms, cudaStream_
     case EP_ACT_GELU: return launch_dz<EP_ACT_GELU>(a, num_sms, stream);
     case EP_ACT_SWIGLU: return launch_dz<EP_ACT_SWIGLU>(a, num_sms, stream);
     default: return launch_dz<EP_ACT_NONE>(a, num_sms, stream);
+  }
+}
+
+cudaError_t launch_checkpoint_grad(const CheckpointGradArgs& p, int num_sms, cudaStream_t stream) {
+  DzArgs a = {p.groups, p.N, p.Z, nullptr, p.d_h, p.d_z, p.part, p.d_bias, p.done, p.err};
+  a.codes = p.codes;
+  a.z_sf = p.sf;
+  a.sf_pack = p.sf_pack;
+  a.h = p.h;
+  switch (p.act) {
+    case EP_ACT_RELU: return launch_dz<EP_ACT_RELU, true>(a, num_sms, stream);
+    case EP_ACT_SILU: return launch_dz<EP_ACT_SILU, true>(a, num_sms, stream);
+    case EP_ACT_GELU: return launch_dz<EP_ACT_GELU, true>(a, num_sms, stream);
+    case EP_ACT_SWIGLU: return launch_dz<EP_ACT_SWIGLU, true>(a, num_sms, stream);
+    default: return launch_dz<EP_ACT_NONE, true>(a, num_sms, stream);
   }
 }
 

@@ -70,7 +70,7 @@ extern "C" {
 /* ---- element types ------------------------------------------------------- */
 #define EP_DTYPE_BF16 0
 #define EP_DTYPE_FP8_E4M3 1 /* OCP E4M3 ("FN"), fp32 scale per 128 columns */
-#define EP_DTYPE_FP32 2     /* router logits only                          */
+#define EP_DTYPE_FP32 2     /* router logits, and the rows in front of the norm */
 
 /* ---- configuration --------------------------------------------------------
  * Ranks: R = num_scaleout_ranks * num_scaleup_ranks; global rank
@@ -459,6 +459,89 @@ int ep_expert_product_grad(const ep_product_config_t* cfg, const ep_layout_t* la
                            const uint16_t* x, const uint16_t* weight, const uint16_t* z,
                            const uint16_t* d_out, uint16_t* d_x, uint16_t* d_weight,
                            float* d_bias, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---- norm in front of the router ----------------------------------------------------
+ * (No counterpart on the DeepEP pages.) The residual's addition and the root-mean-square
+ * norm, in bf16 for the router and the experts, and as the FP8 rows with scales that
+ * ep_dispatch takes (x_dtype EP_DTYPE_FP8_E4M3):
+ *   s = x + residual,   y = s / sqrt(mean of s^2 over the row + eps) * weight
+ */
+typedef struct ep_norm_config {
+  int64_t rows;    /* 0..2^31-1                                                       */
+  int32_t hidden;  /* H, a multiple of 8 (of 128 with codes), up to 16384             */
+  int32_t x_dtype; /* of x, residual, sum, d_sum and d_x: EP_DTYPE_BF16 or EP_DTYPE_FP32 */
+  int32_t sf_pack; /* the scales' format, as ep_config_t.sf_pack                      */
+  float eps;       /* finite, 1e-20 or more                                           */
+} ep_norm_config_t;
+
+/* Forward. Device pointers, rows dense and 16-byte aligned: x [rows][H]; residual the same or
+ * NULL; weight bf16 [H] or NULL (ones); sum [rows][H] or NULL: s, rounded to x's type (it
+ * may be x or residual itself); y bf16 [rows][H] or NULL; codes uint8 [rows][H] and sf
+ * (fp32 [rows][H/128], or [rows][ceil(H/512)] packed words) or both NULL; y or codes is
+ * there. The norm is taken of s in fp32, before it is rounded; codes are made of y before it is
+ * rounded, as the dispatch's cast makes them of bf16. Sums of squares past fp32's range
+ * are taken of smaller values. A NaN makes its row NaN, an infinity too (zeros beside it). */
+int ep_norm(const ep_norm_config_t* cfg, const void* x, const void* residual, const uint16_t* weight, void* sum,
+            uint16_t* y, uint8_t* codes, float* sf, void* stream);
+
+/* Workspace bytes of ep_norm_grad (0 for an invalid configuration); nothing in it has to be
+ * initialised. One stream at a time. */
+size_t ep_norm_workspace_bytes(const ep_norm_config_t* cfg);
+
+/* Gradients for d_y (bf16 [rows][H]), from the kept sum: with q = 1 / sqrt(mean s^2 + eps),
+ * n = s q and t = d_y weight,
+ *   d_x = q (t - n mean(t n)) + d_sum   (also the residual's gradient),
+ *   d_weight = sum over the rows of d_y n (fp32 [H]).
+ * d_sum: what arrives at the sum itself, [rows][H] of x's type, or NULL (zero); d_x may take its
+ * place. d_x or d_weight may be NULL. token_mask: uint8 [rows] or NULL; 0 = padding: d_x is
+ * zero there, its other tensors are not read. Codes pass gradients on as if they were not
+ * rounded. Bitwise reproducible. */
+int ep_norm_grad(const ep_norm_config_t* cfg, const void* sum, const uint16_t* weight, const uint8_t* token_mask,
+                 const uint16_t* d_y, const void* d_sum, void* d_x, float* d_weight, void* workspace,
+                 size_t workspace_bytes, void* stream);
+
+/* ---- rows kept in 8 bits for the backward pass ----------------------------------------
+ * (No counterpart on the DeepEP pages.) The rows of an expanded layout's blocks in the form of the
+ * dispatch's FP8 rows, half of bf16's bytes: z of the experts' products, or the rows that were
+ * dispatched as FP8 (those are in this form already). Rows outside the blocks' lanes are
+ * neither read for a result nor written. layout = NULL: one group of all rows, with
+ * num_ranks = num_experts = 1; blocks that leave the rows or overlap are cut as in the products
+ * and latch EP_ERR_OVERFLOW. Each kept value is off by at most 2^-4 of itself, or of the
+ * least step of its 128 columns (2^-10 of their scale).
+ */
+typedef struct ep_checkpoint_config {
+  int32_t num_ranks;   /* R of the layout                                              */
+  int32_t num_experts; /* E, a multiple of R, 1..4096                                  */
+  int64_t rows;        /* 0..2^31-257                                                  */
+  int32_t features;    /* F, columns of the kept rows (Z of the product), a multiple of
+                          128, up to 2^21                                              */
+  int32_t activation;  /* EP_ACT_*, ep_checkpoint_grad only (gated: F = 2 N)           */
+  int32_t sf_pack;     /* the scales' format, as ep_config_t.sf_pack                   */
+} ep_checkpoint_config_t;
+
+/* Workspace bytes of the three calls (0 for an invalid configuration). Its 256-byte header is
+ * zero-filled once before first use (every call leaves its counters zero); one stream at a
+ * time; errors are read by ep_check_error. */
+size_t ep_checkpoint_workspace_bytes(const ep_checkpoint_config_t* cfg);
+
+/* x bf16 [rows][F] -> codes uint8 [rows][F], sf fp32 [rows][F/128] or packed words
+ * [rows][ceil(F/512)]: the codes and scales of ep_dispatch's cast, bit for bit. */
+int ep_checkpoint(const ep_checkpoint_config_t* cfg, const ep_layout_t* layout, const uint16_t* x, uint8_t* codes, float* sf,
+                  void* workspace, size_t workspace_bytes, void* stream);
+
+/* Back: x = bf16_rn(code * scale), exact with packed scales (down to bf16's least numbers), such as
+ * the x that ep_expert_product_grad needs for d_weight. */
+int ep_checkpoint_rows(const ep_checkpoint_config_t* cfg, const ep_layout_t* layout, const uint8_t* codes, const float* sf,
+                       uint16_t* x, void* workspace, size_t workspace_bytes, void* stream);
+
+/* The backward pass through the activation, from kept z = code * scale (fp32, not rounded) and
+ * d_h (bf16 [rows][N]): h = act(z) (bf16 [rows][N]: x of the next product's d_weight, so that it
+ * need not be kept), d_z = d_h act'(z) (bf16 [rows][F]: d_out of the product's own gradient
+ * with EP_ACT_NONE), d_bias_g = column sums of the unrounded d_z over the block (fp32
+ * [E][F], zeros for an empty block). Any of the three may be NULL. Bitwise reproducible. */
+int ep_checkpoint_grad(const ep_checkpoint_config_t* cfg, const ep_layout_t* layout, const uint8_t* codes, const float* sf,
+                       const uint16_t* d_h, uint16_t* h, uint16_t* d_z, float* d_bias, void* workspace,
+                       size_t workspace_bytes, void* stream);
 
 /* Synchronises `stream`, returns the first device-detected error latched in
  * the workspace since the last call (EP_OK if none) and clears it. The
