@@ -11,8 +11,8 @@ The entry points keep the C names (``ep_get_dispatch_layout``, ``ep_dispatch``,
 ``alloc_recv`` and ``alloc_workspace`` allocate correctly sized tensors.
 Beside them stand the norm in front of the router (``ep_norm``), the router
 (``ep_route`` with its balance loss), the experts' products (``ep_expert_product``),
-their gradients with the combine's, and rows kept in 8 bits for the backward pass
-(``ep_checkpoint``).
+their gradients with the combine's, rows kept in 8 bits for the backward pass
+(``ep_checkpoint``), and the experts' layer of a few tokens (``ep_expert_layer``).
 """
 from __future__ import annotations
 
@@ -44,6 +44,7 @@ __all__ = [
     "NormConfig", "ep_norm_workspace_bytes", "alloc_norm_workspace", "ep_norm", "ep_norm_grad",
     "CheckpointConfig", "ep_checkpoint_workspace_bytes", "alloc_checkpoint_workspace", "ep_checkpoint",
     "ep_checkpoint_rows", "ep_checkpoint_grad",
+    "LayerConfig", "ep_layer_workspace_bytes", "alloc_layer_workspace", "ep_expert_layer",
 ]
 
 
@@ -239,6 +240,10 @@ def lib():
         L.ep_checkpoint_rows.argtypes = [P, P, P, P, P, P, C.c_size_t, P]
         L.ep_checkpoint_grad.restype = I
         L.ep_checkpoint_grad.argtypes = [P, P, P, P, P, P, P, P, P, C.c_size_t, P]
+        L.ep_layer_workspace_bytes.restype = C.c_size_t
+        L.ep_layer_workspace_bytes.argtypes = [P]
+        L.ep_expert_layer.restype = I
+        L.ep_expert_layer.argtypes = [P] * 13 + [C.c_size_t, P]
         L.ep_check_error.restype = I
         L.ep_check_error.argtypes = [P, P]
         L.ep_status_string.restype = C.c_char_p
@@ -920,3 +925,74 @@ def ep_checkpoint_grad(cfg: CheckpointConfig, layout, codes: torch.Tensor, sf: t
         _at(d_h, _BF16, n_h, w, "d_h"), None if h is None else _at(h, _BF16, n_h, w, "h"),
         None if d_z is None else _at(d_z, _BF16, n, w, "d_z"), None if d_bias is None else _at(d_bias, _F32, n_b, w, "d_bias"),
         *_space(ws, w), _raw_stream(stream)), w)
+
+
+# ---- the experts' layer of a few tokens ---------------------------------------------------
+
+
+class _LayerConfig(C.Structure):
+    _fields_ = [(n, C.c_int32) for n in (
+        "num_tokens", "num_experts", "num_topk", "hidden", "inner", "activation", "weight_dtype", "num_sms")]
+
+
+@dataclasses.dataclass
+class LayerConfig(_KeepsStruct):
+    num_tokens: int  # up to 64
+    num_experts: int
+    num_topk: int
+    hidden: int
+    inner: int
+    activation: int = EP_ACT_SWIGLU
+    weight_dtype: int = EP_DTYPE_BF16  # or EP_DTYPE_FP8_E4M3: codes, a scale for every 128 x 128
+    num_sms: int = 0
+
+    @property
+    def z_features(self) -> int:
+        """Rows of each expert's up matrix: twice inner when gated."""
+        return self.inner * (2 if self.activation == EP_ACT_SWIGLU else 1)
+
+    def _needs(self):
+        """(tokens' elements, lanes, up, its scales, its biases, down, its scales, its biases) of a call."""
+        T, E, H, I, Z = self.num_tokens, self.num_experts, self.hidden, self.inner, self.z_features
+        n = (T * H, T * self.num_topk, E * Z * H, E * ((Z + 127) // 128) * (H // 128), E * Z, E * H * I,
+             E * (H // 128) * (I // 128), E * H)
+        object.__setattr__(self, "_sizes", n)
+        return n
+
+    def _build_struct(self) -> _LayerConfig:
+        return _LayerConfig(*(int(getattr(self, f[0])) for f in _LayerConfig._fields_))
+
+
+def ep_layer_workspace_bytes(cfg: LayerConfig) -> int:
+    return int(lib().ep_layer_workspace_bytes(cfg._ref()))
+
+
+def alloc_layer_workspace(cfg: LayerConfig, device="cuda") -> torch.Tensor:
+    """Zero-filled workspace of ep_layer_workspace_bytes(cfg) bytes."""
+    n = ep_layer_workspace_bytes(cfg)
+    if n == 0:
+        raise EpError(EP_ERR_INVALID_ARG, "ep_layer_workspace_bytes")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def ep_expert_layer(cfg: LayerConfig, x: torch.Tensor, topk_idx: torch.Tensor, topk_weights: torch.Tensor, up: torch.Tensor,
+                    up_sf, up_bias, down: torch.Tensor, down_sf, down_bias, residual, out: torch.Tensor, ws: torch.Tensor,
+                    stream=None):
+    """out = sum over each token's lanes of topk_weights * expert(x), plus residual: dispatch, both products
+    of every chosen expert and combine of up to 64 tokens in two kernels."""
+    w = "ep_expert_layer"
+    n_x, n_k, n_up, n_us, n_ub, n_down, n_ds, n_db = cfg._sizes or cfg._needs()
+    if cfg.weight_dtype == EP_DTYPE_FP8_E4M3:
+        up, down = _codes(up, n_up, w, "up"), _codes(down, n_down, w, "down")
+        up_sf, down_sf = _at(up_sf, _F32, n_us, w, "up_sf"), _at(down_sf, _F32, n_ds, w, "down_sf")
+    else:
+        up, down = _at(up, _BF16, n_up, w, "up"), _at(down, _BF16, n_down, w, "down")
+        up_sf, down_sf = _maybe(up_sf, _F32, 0, w, "up_sf"), _maybe(down_sf, _F32, 0, w, "down_sf")
+    st = (_lib or lib()).ep_expert_layer(
+        cfg._reference or cfg._ref(), _at(x, _BF16, n_x, w, "x"), _at(topk_idx, _I64, n_k, w, "topk_idx"),
+        _at(topk_weights, _F32, n_k, w, "topk_weights"), up, up_sf, None if up_bias is None else _at(up_bias, _BF16, n_ub, w, "up_bias"),
+        down, down_sf, None if down_bias is None else _at(down_bias, _BF16, n_db, w, "down_bias"),
+        None if residual is None else _at(residual, _BF16, n_x, w, "residual"), _at(out, _BF16, n_x, w, "out"),
+        *_space(ws, w), _raw_stream(stream))
+    if st:
+        raise EpError(st, w)

@@ -87,6 +87,32 @@ int checkpoint(const ep_checkpoint_config_t* cfg, const ep_layout_t* layout, con
   return cuda_status(launch_checkpoint(a, back, sms, static_cast<cudaStream_t>(stream)));
 }
 
+int check_layer(const ep_layer_config_t* c) {
+  if (c == nullptr) return EP_ERR_INVALID_ARG;
+  if (c->num_tokens < 0 || c->num_experts < 1 || c->num_topk < 1 || c->num_sms < 0) return EP_ERR_INVALID_ARG;
+  if (c->num_tokens > kLayerMaxTokens || c->num_experts > kMaxExperts || c->num_topk > kMaxTopk) return EP_ERR_UNSUPPORTED;
+  if (c->activation < EP_ACT_NONE || c->activation > EP_ACT_SWIGLU) return EP_ERR_INVALID_ARG;
+  if (c->weight_dtype != EP_DTYPE_BF16 && c->weight_dtype != EP_DTYPE_FP8_E4M3) return EP_ERR_INVALID_ARG;
+  const int unit = c->weight_dtype == EP_DTYPE_FP8_E4M3 ? 128 : 8;
+  if (c->hidden < unit || c->hidden % unit != 0 || c->inner < unit || c->inner % unit != 0) return EP_ERR_INVALID_ARG;
+  if (c->hidden > 1 << 20 || c->inner > 1 << 20) return EP_ERR_UNSUPPORTED;
+  return EP_OK;
+}
+
+struct LayerWorkspace {
+  size_t done, h, part, total;
+};
+
+LayerWorkspace layer_workspace(const ep_layer_config_t* c) {
+  LayerWorkspace w;
+  const size_t T = static_cast<size_t>(c->num_tokens);
+  w.done = 256;
+  w.h = w.done + round256(sizeof(uint32_t) * ((c->hidden + 15) / 16));
+  w.part = w.h + round256(2 * T * c->num_topk * c->inner);
+  w.total = w.part + round256(sizeof(float) * kLayerMaxSplit * T * c->hidden);
+  return w;
+}
+
 }  // namespace
 
 }  // namespace ep
@@ -184,6 +210,56 @@ int ep_checkpoint_grad(const ep_checkpoint_config_t* cfg, const ep_layout_t* lay
   a.d_bias = d_bias;
   a.err = at<uint32_t>(workspace, 0);
   return cuda_status(launch_checkpoint_grad(a, sms, s));
+}
+
+size_t ep_layer_workspace_bytes(const ep_layer_config_t* cfg) {
+  return check_layer(cfg) == EP_OK ? layer_workspace(cfg).total : 0;
+}
+
+int ep_expert_layer(const ep_layer_config_t* cfg, const uint16_t* x, const int64_t* topk_idx, const float* topk_weights,
+                    const void* up, const float* up_sf, const uint16_t* up_bias, const void* down, const float* down_sf,
+                    const uint16_t* down_bias, const uint16_t* residual, uint16_t* out, void* workspace,
+                    size_t workspace_bytes, void* stream) {
+  int st = check_layer(cfg);
+  if (st != EP_OK) return st;
+  const LayerWorkspace w = layer_workspace(cfg);
+  if ((st = check_workspace(workspace, workspace_bytes, w.total)) != EP_OK) return st;
+  if (cfg->num_tokens == 0) return EP_OK;
+  if (x == nullptr || topk_idx == nullptr || topk_weights == nullptr || up == nullptr || down == nullptr || out == nullptr)
+    return EP_ERR_INVALID_ARG;
+  const bool fp8 = cfg->weight_dtype == EP_DTYPE_FP8_E4M3;
+  if (fp8 != (up_sf != nullptr) || fp8 != (down_sf != nullptr)) return EP_ERR_INVALID_ARG;
+  if (!aligned(x, 16) || !aligned(topk_idx, 8) || !aligned(topk_weights, 4) || !aligned(up, 16) || !aligned(up_sf, 4) ||
+      !aligned(up_bias, 16) || !aligned(down, 16) || !aligned(down_sf, 4) || !aligned(down_bias, 16) ||
+      !aligned(residual, 16) || !aligned(out, 16))
+    return EP_ERR_INVALID_ARG;
+  LayerArgs a;
+  a.device_sms = device_sm_count();
+  if (a.device_sms <= 0) return EP_ERR_CUDA;
+  const int sms = cfg->num_sms > 0 && cfg->num_sms < a.device_sms ? cfg->num_sms : a.device_sms;
+  a.x = x;
+  a.idx = topk_idx;
+  a.w = topk_weights;
+  a.up = up;
+  a.up_sf = up_sf;
+  a.up_bias = up_bias;
+  a.down = down;
+  a.down_sf = down_sf;
+  a.down_bias = down_bias;
+  a.residual = residual;
+  a.out = out;
+  a.h = at<uint16_t>(workspace, w.h);
+  a.part = at<float>(workspace, w.part);
+  a.done = at<uint32_t>(workspace, w.done);
+  a.err = at<uint32_t>(workspace, 0);
+  a.T = cfg->num_tokens;
+  a.E = cfg->num_experts;
+  a.K = cfg->num_topk;
+  a.H = cfg->hidden;
+  a.I = cfg->inner;
+  a.Z = cfg->activation == EP_ACT_SWIGLU ? 2 * cfg->inner : cfg->inner;
+  a.act = cfg->activation;
+  return cuda_status(launch_layer(a, fp8, sms, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -72,4 +72,31 @@ struct CheckpointGradArgs {
 cudaError_t launch_checkpoint(const CheckpointArgs& a, bool back, int num_sms, cudaStream_t stream);
 cudaError_t launch_checkpoint_grad(const CheckpointGradArgs& a, int num_sms, cudaStream_t stream);
 
+// ---- the experts' layer of a few tokens -----------------------------------------------
+
+constexpr int kLayerMaxTokens = 64;
+constexpr int kLayerMaxSplit = 8;  // parts that an output tile's sum over experts is taken in at most
+
+struct LayerArgs {
+  const uint16_t* x;          // [T][H]
+  const int64_t* idx;         // [T][K]
+  const float* w;             // [T][K]
+  const void* up;             // [E][Z][H] bf16 or codes
+  const float* up_sf;         // [E][ceil(Z / 128)][H / 128] or null
+  const uint16_t* up_bias;    // [E][Z] or null
+  const void* down;           // [E][H][I]
+  const float* down_sf;       // [E][H / 128][I / 128] or null
+  const uint16_t* down_bias;  // [E][H] or null
+  const uint16_t* residual;   // [T][H] or null
+  uint16_t* out;              // [T][H]
+  uint16_t* h;                // workspace [lanes][I]
+  float* part;                // workspace [kLayerMaxSplit][T][H]
+  uint32_t* done;             // workspace [H / 16]: parts of a tile that are there (return to 0)
+  uint32_t* err;
+  int T, E, K, H, I, Z, act;
+  int device_sms;
+};
+
+cudaError_t launch_layer(const LayerArgs& a, bool fp8, int num_sms, cudaStream_t stream);
+
 }  // namespace ep

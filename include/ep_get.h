@@ -543,6 +543,44 @@ int ep_checkpoint_grad(const ep_checkpoint_config_t* cfg, const ep_layout_t* lay
                        const uint16_t* d_h, uint16_t* h, uint16_t* d_z, float* d_bias, void* workspace,
                        size_t workspace_bytes, void* stream);
 
+/* ---- the experts' layer of a few tokens ------------------------------------------------
+ * (No counterpart on the DeepEP pages.) What dispatch, both products of each expert and combine
+ * compute for a serving step of up to 64 tokens on one rank, straight from the router's choice, in
+ * two kernels that read each chosen expert's matrices once:
+ *   h = act(x_t W_up[e]^T + b_up[e]),   out_t = sum over the lanes k of topk_weights[t][k] *
+ *   (h W_down[e]^T + b_down[e]) + residual_t          with e = topk_idx[t][k]
+ * Sums are fp32; h is rounded to bf16 (as between the products), out once; the lanes' results
+ * are not rounded. (ep_dispatch and ep_expert_product take any number of tokens.)
+ */
+typedef struct ep_layer_config {
+  int32_t num_tokens;   /* T, 0..64                                                      */
+  int32_t num_experts;  /* E, 1..4096                                                    */
+  int32_t num_topk;     /* K, 1..32                                                      */
+  int32_t hidden;       /* H, a multiple of 8 (of 128 with FP8 matrices), up to 2^20     */
+  int32_t inner;        /* I, a multiple of 8 (of 128 with FP8 matrices), up to 2^20     */
+  int32_t activation;   /* EP_ACT_*; gated: up has Z = 2 I rows, the I gate rows first   */
+  int32_t weight_dtype; /* EP_DTYPE_BF16, or EP_DTYPE_FP8_E4M3: codes with an fp32 scale
+                           for every 128 x 128 of a matrix                               */
+  int32_t num_sms;      /* SMs to use; 0 = all. Results do not depend on it.             */
+} ep_layer_config_t;
+
+/* Workspace bytes (0 for an invalid configuration). Zero-filled once before first use (every call
+ * leaves its counters zero); one stream at a time; errors are read by ep_check_error. */
+size_t ep_layer_workspace_bytes(const ep_layer_config_t* cfg);
+
+/* Device pointers, rows dense and 16-byte aligned: x bf16 [T][H], topk_idx int64 [T][K] and
+ * topk_weights fp32 [T][K] as ep_route writes them (-1: no expert; other values outside [0, E)
+ * latch EP_ERR_BAD_TOPK and count as -1; a weight where there is no expert is not used; an
+ * expert twice counts with both weights), up [E][Z][H] and down [E][H][I] bf16, or codes with
+ * up_sf fp32 [E][ceil(Z/128)][H/128] and down_sf [E][H/128][I/128] (else NULL), up_bias bf16
+ * [E][Z], down_bias bf16 [E][H], residual bf16 [T][H] or NULL each (residual may be out itself,
+ * and out may be x), out bf16 [T][H]. Matrices of experts that no token chose are not read.
+ * A token without an expert gets its residual, or 0. Bitwise reproducible. */
+int ep_expert_layer(const ep_layer_config_t* cfg, const uint16_t* x, const int64_t* topk_idx, const float* topk_weights,
+                    const void* up, const float* up_sf, const uint16_t* up_bias, const void* down, const float* down_sf,
+                    const uint16_t* down_bias, const uint16_t* residual, uint16_t* out, void* workspace,
+                    size_t workspace_bytes, void* stream);
+
 /* Synchronises `stream`, returns the first device-detected error latched in
  * the workspace since the last call (EP_OK if none) and clears it. The
  * library's own convention (the pages print and continue on a device error;

@@ -70,3 +70,43 @@ def checkpoint_grad(blocks, z, d_h, kind):
         (d,) = torch.autograd.grad(v, t, d_h[a:a + c])
         h[a:a + c], d_z[a:a + c], d_bias[g] = v.detach(), d, d.sum(0)
     return h, d_z, d_bias
+
+
+def unscale(codes, sf):
+    """Matrices of e4m3 codes [E][rows][columns] with a scale for every 128 x 128, in 64 bits."""
+    v = codes.view(torch.float8_e4m3fn).double()
+    return v * sf.double().repeat_interleave(128, 1)[:, :v.shape[1]].repeat_interleave(128, 2)
+
+
+def layer(x, idx, w, up, up_bias, down, down_bias, residual, kind, fun):
+    """The experts' layer with h rounded to bf16 -> (out, bound of its error before the last rounding).
+
+    Products are exact; a sum of n of them passes through at most n / 128 + 24 additions, of 2^-22 of the sum of
+    magnitudes each (the tensor cores cut what they add at 2^-23 of the largest). h of fp32 sums
+    lies within such an error, and `fun` for the activation, of h of 64 bits, so its rounding lies
+    between the roundings of both ends."""
+    T, H = x.shape
+    out, bound = (torch.zeros(T, H, dtype=torch.float64, device=x.device) for _ in range(2))
+    if residual is not None:
+        out += residual.double()
+        bound += residual.double().abs() * 2.0 ** -22
+    x = x.double()
+    for e in torch.unique(idx[(idx >= 0) & (idx < len(up))]).tolist():
+        t, k = torch.nonzero(idx == e, as_tuple=True)
+        u, d, xe, we = up[e].double(), down[e].double(), x[t], w[t, k].double()[:, None]
+        z = xe @ u.T + (0 if up_bias is None else up_bias[e].double())
+        ez = (xe.abs() @ u.abs().T) * ((x.shape[1] / 128 + 24) * 2.0 ** -22) + z.abs() * 2.0 ** -23
+        h = act(z, kind)
+        if kind == "swiglu":
+            (a, b), (ea, eb) = z.chunk(2, -1), ez.chunk(2, -1)
+            eh = 1.11 * ea * (b.abs() + eb) + torch.nn.functional.silu(a).abs() * eb + a.abs() * b.abs() * fun
+        else:
+            eh = 1.13 * ez + z.abs() * fun
+        low, high = (h - eh).bfloat16().double(), (h + eh).bfloat16().double()
+        mid = (low + high) / 2
+        y = mid @ d.T + (0 if down_bias is None else down_bias[e].double())
+        size = mid.abs() @ d.abs().T
+        ey = (high - low) / 2 @ d.abs().T + size * ((d.shape[1] / 128 + 24) * 2.0 ** -22) + y.abs() * 2.0 ** -23
+        out.index_add_(0, t, we * y)
+        bound.index_add_(0, t, we.abs() * (ey + y.abs() * (idx.shape[1] + 8) * 2.0 ** -22))
+    return out, bound

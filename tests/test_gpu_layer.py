@@ -1,0 +1,291 @@
+"""The experts' layer of a few tokens against 64 bits (h rounded to bf16 as defined; bounds in
+_block_reference.layer, and half a step of bf16 for the output)."""
+import math
+
+import pytest
+import torch
+
+import _block_reference as ref
+from test_gpu_checkpoint import FUN
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def ep():
+    import combine_ep_get_02_gb300 as ep
+    ep.lib()
+    return ep
+
+
+class Case:
+    def __init__(self, ep, T, E, K, H, I, act="swiglu", fp8=False, bias=False, residual=False, masked=0.0, seed=0, num_sms=0):
+        g = torch.Generator(device="cuda").manual_seed(seed + 7 * T + H)
+        rnd = lambda *s, scale=1.0: (torch.randn(*s, generator=g, device="cuda") * scale).bfloat16()  # noqa: E731
+        self.ep, self.act, self.fp8 = ep, act, fp8
+        self.cfg = ep.LayerConfig(T, E, K, H, I, getattr(ep, f"EP_ACT_{act.upper()}"),
+                                  ep.EP_DTYPE_FP8_E4M3 if fp8 else ep.EP_DTYPE_BF16, num_sms)
+        Z = self.cfg.z_features
+        self.x = rnd(T, H)
+        self.idx = torch.rand(T, E, generator=g, device="cuda").topk(min(K, E)).indices
+        if K > E:
+            self.idx = self.idx.repeat(1, K)[:, :K].contiguous()
+        self.w = torch.rand(T, K, generator=g, device="cuda")
+        if masked:
+            self.idx[torch.rand(T, K, generator=g, device="cuda") < masked] = -1
+        self.mats = {}
+        for name, rows, columns in (("up", Z, H), ("down", H, I)):
+            m, sf = rnd(E, rows, columns, scale=columns ** -0.5), None
+            if fp8:
+                m = torch.randint(0, 255, (E, rows, columns), generator=g, device="cuda").to(torch.uint8)
+                m[(m & 0x7F) == 0x7F] = 0x40
+                sf = torch.exp(torch.randn(E, (rows + 127) // 128, columns // 128, generator=g, device="cuda")) * 0.02 * columns ** -0.5
+            self.mats[name] = (m, sf, rnd(E, rows, scale=0.5) if bias else None)
+        self.residual = rnd(T, H) if residual else None
+        self.ws = ep.alloc_layer_workspace(self.cfg)
+
+    def poison(self):
+        """NaN wherever nothing may depend on: other experts' matrices, weights of absent lanes, tokens without
+        an expert, and the workspace behind the counters."""
+        T, E = self.x.shape[0], self.mats["up"][0].shape[0]
+        used = torch.zeros(E, dtype=torch.bool, device="cuda")
+        live = (self.idx >= 0) & (self.idx < E)
+        used[self.idx[live]] = True
+        for m, sf, b in self.mats.values():
+            m[~used] = 0x7F if self.fp8 else math.nan
+            for t in (sf, b):
+                if t is not None:
+                    t[~used] = math.nan
+        self.w[~live] = math.nan
+        self.x[~live.any(1)] = math.nan
+        at = 256 + (4 * ((self.cfg.hidden + 15) // 16) + 255) // 256 * 256
+        self.ws[at:] = 0xFF
+
+    def run(self, out=None, x=None, residual=None, cfg=None):
+        (up, up_sf, up_b), (down, down_sf, down_b) = self.mats["up"], self.mats["down"]
+        if out is None:
+            out = torch.full(self.x.shape, 33.0, device="cuda").bfloat16()
+        self.ep.ep_expert_layer(cfg or self.cfg, self.x if x is None else x, self.idx, self.w, up, up_sf, up_b, down, down_sf,
+                                down_b, self.residual if residual is None else residual, out, self.ws)
+        return out
+
+    def check(self, status=0):
+        self.poison()
+        out = self.run()
+        assert self.ep.ep_check_error(self.ws) == status
+        n = 256 + 4 * ((self.cfg.hidden + 15) // 16)
+        assert not self.ws[:n].any()
+        (up, up_sf, up_b), (down, down_sf, down_b) = self.mats["up"], self.mats["down"]
+        if self.fp8:
+            up, down = ref.unscale(up, up_sf), ref.unscale(down, down_sf)
+        want, bound = ref.layer(self.x, self.idx, self.w, up, up_b, down, down_b, self.residual, self.act, FUN)
+        err = (out.double() - want).abs()
+        assert (err <= want.abs() * 2.0 ** -8 + bound * (1 + 2.0 ** -7)).all(), (err - want.abs() * 2.0 ** -8 - bound).max()
+        again = self.run()
+        assert torch.equal(again, out)
+        return out
+
+
+SMALL = [(1, 1, 1, 8, 8), (1, 8, 2, 64, 24), (2, 4, 4, 520, 72), (3, 16, 3, 1000, 136), (4, 32, 8, 1032, 40), (5, 8, 2, 2056, 104),
+         (8, 64, 6, 512, 520), (9, 8, 2, 264, 264), (16, 16, 4, 1024, 512), (33, 16, 2, 776, 96), (64, 8, 2, 1024, 256),
+         (64, 64, 8, 640, 128), (17, 300, 5, 200, 88)]
+
+
+@pytest.mark.parametrize("act", ["swiglu", "gelu"])
+@pytest.mark.parametrize("T,E,K,H,I", SMALL)
+def test_sizes(ep, T, E, K, H, I, act):
+    Case(ep, T, E, K, H, I, act, bias=T % 2 == 0, residual=T % 3 == 0, masked=0.1 if T > 4 else 0.0).check()
+
+
+@pytest.mark.parametrize("act", ["none", "relu", "silu", "gelu", "swiglu"])
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
+def test_activations(ep, act, fp8):
+    Case(ep, 6, 8, 3, 640, 384, act, fp8, bias=True, residual=True).check()
+    Case(ep, 1, 8, 3, 640, 384, act, fp8).check()
+
+
+@pytest.mark.parametrize("T,E,K,H,I", [(1, 1, 1, 128, 128), (1, 16, 4, 1152, 384), (4, 8, 2, 640, 128), (7, 8, 4, 512, 640),
+                                       (16, 32, 4, 384, 256), (33, 4, 2, 1024, 128), (64, 8, 4, 640, 384), (64, 64, 8, 256, 256)])
+def test_fp8_matrices(ep, T, E, K, H, I):
+    Case(ep, T, E, K, H, I, fp8=True, bias=T % 2 == 1, residual=T % 2 == 0, masked=0.1 if T > 4 else 0.0).check()
+
+
+def test_every_code(ep):
+    """Each of the 256 codes as a matrix element meets a token that picks it out."""
+    H = I = 128
+    up = torch.zeros(1, 2 * I, H, dtype=torch.uint8, device="cuda")
+    down = torch.zeros(1, H, I, dtype=torch.uint8, device="cuda")
+    codes = torch.arange(256, device="cuda").to(torch.uint8)
+    one, cfg = 0x38, ep.LayerConfig(2, 1, 1, H, I, ep.EP_ACT_NONE, ep.EP_DTYPE_FP8_E4M3)
+    up = torch.zeros(1, I, H, dtype=torch.uint8, device="cuda")
+    up[0, :, 0], up[0, :, 1] = codes[:128], codes[128:]
+    down[0].fill_diagonal_(one)
+    x = torch.zeros(2, H, device="cuda", dtype=torch.bfloat16)
+    x[0, 0] = x[1, 1] = 1.0
+    ones = torch.ones(1, 1, 1, device="cuda")
+    out, idx, w = torch.empty_like(x), torch.zeros(2, 1, dtype=torch.int64, device="cuda"), torch.ones(2, 1, device="cuda")
+    up_of = lambda c: c.view(torch.float8_e4m3fn).float()  # noqa: E731
+    ok = ~up_of(codes).isnan()
+    for bad in (False, True):  # without the codes for NaN, which make their whole row NaN, then with them
+        if not bad:
+            up[0][up[0] == 0x7F] = 0
+            up[0][up[0] == 0xFF] = 0
+        else:
+            up[0, 127, 0], up[0, 127, 1] = 0x7F, 0xFF
+        down[0, 127, 127] = one
+        if bad:
+            down[0, :, 127] = 0
+            down[0, 127, 127] = one
+        ep.ep_expert_layer(cfg, x, idx, w, up, ones, None, down, ones, None, None, out, ep.alloc_layer_workspace(cfg))
+        got = torch.cat([out[0], out[1]])
+        if bad:
+            assert got.isnan().all()  # 0 x NaN counts in a sum
+        else:
+            assert torch.equal(got[ok].float(), up_of(codes)[ok])
+
+
+def test_choices_at_the_ends(ep):
+    for T, E, K in ((64, 1, 1), (64, 4, 1), (40, 3, 3), (64, 100, 32), (12, 4096, 4), (64, 4096, 32), (1, 4096, 32), (1, 3, 2)):
+        c = Case(ep, T, E, K, 72, 40, masked=0.2)
+        if T == 40:
+            c.idx[:] = torch.tensor([2, 0, 2], device="cuda")  # an expert twice
+            c.idx[7] = 1
+        c.check()
+    # no lane at all, with and without a residual
+    for residual in (True, False):
+        for T in (1, 40):
+            c = Case(ep, T, 8, 3, 136, 24, residual=residual)
+            c.idx[:] = -1
+            out = c.check()
+            assert torch.equal(out, c.residual if residual else torch.zeros_like(out))
+    # every token to one expert, others with nothing
+    c = Case(ep, 64, 16, 4, 264, 72, residual=True)
+    c.idx[:] = -1
+    c.idx[:, 2] = 11
+    c.idx[5:9] = -1
+    c.check()
+
+
+def test_repeated_experts(ep):
+    """The same expert in several lanes of a token counts with the sum of their weights."""
+    for T, K in ((4, 6), (30, 8)):
+        c = Case(ep, T, 5, K, 264, 136)
+        c.idx = torch.randint(-1, 5, (T, K), device="cuda", generator=torch.Generator(device="cuda").manual_seed(2))
+        c.idx[0] = 3
+        c.check()
+
+
+def test_bad_choices_are_reported(ep):
+    for T in (4, 40):
+        c = Case(ep, T, 8, 4, 136, 72)
+        c.idx[1, 0], c.idx[2, 1], c.idx[3, 3] = 8, -2, 1 << 40
+        c.check(ep.EP_ERR_BAD_TOPK)
+
+
+@pytest.mark.parametrize("T,E,K,H,I,fp8", [(1, 16, 4, 1024, 512, False), (12, 16, 4, 1000, 264, False), (64, 16, 4, 640, 384, True)])
+def test_independent_of_the_grid(ep, T, E, K, H, I, fp8):
+    c = Case(ep, T, E, K, H, I, fp8=fp8, residual=True)
+    want = c.check()
+    for sms in (1, 3, 100, 1000):
+        cfg = ep.LayerConfig(**{**{f: getattr(c.cfg, f) for f in c.cfg.__dataclass_fields__}, "num_sms": sms})
+        assert torch.equal(c.run(cfg=cfg), want)
+
+
+def test_output_in_place(ep):
+    c = Case(ep, 9, 8, 2, 520, 136, residual=True)
+    want = c.check()
+    r = c.residual.clone()
+    assert torch.equal(c.run(out=r, residual=r), want)
+    x = c.x.clone()
+    assert torch.equal(c.run(out=x, x=x), want)
+
+
+def test_a_tokens_result_is_its_own(ep):
+    """Infinities and NaN in one token stay there; a token computed alone has the same bits up to its sums'
+    order (the same kernels' tiles), so it is compared with 64 bits instead."""
+    c = Case(ep, 8, 4, 2, 264, 72)
+    c.poison()
+    want = c.run()
+    c.x[3, 5] = math.inf
+    c.x[6, 100] = math.nan
+    out = c.run()
+    keep = [0, 1, 2, 4, 5, 7]
+    assert torch.equal(out[keep], want[keep]) and out[6].isnan().all() and not out[3].isfinite().any()
+
+
+def test_same_as_the_long_way(ep):
+    """Against layout, dispatch, both products and combine, which round each lane's result to bf16 too."""
+    T, E, K, H, I = 24, 16, 4, 512, 256
+    c = Case(ep, T, E, K, H, I)
+    out = c.run()
+    cfg = ep.Config(1, 1, E, K, T, T, H, expand=1)
+    lay, recv, ws = ep.alloc_layout(cfg), ep.alloc_recv(cfg, sidecars=False), ep.alloc_workspace(cfg)
+    idx, w, x = c.idx[None], c.w[None], c.x[None]
+    ep.ep_get_dispatch_layout(cfg, idx, lay, ws)
+    ep.ep_dispatch(cfg, lay, x, None, idx, w, recv, ws)
+    rows = recv.recv_x.shape[0]
+    up, down = ep.ProductConfig(1, E, rows, H, I, ep.EP_ACT_SWIGLU), ep.ProductConfig(1, E, rows, I, H)
+    h, y = (torch.empty(rows, n, dtype=torch.bfloat16, device="cuda") for n in (I, H))
+    pws = ep.alloc_product_workspace(up)
+    ep.ep_expert_product(up, lay, recv.recv_x, None, c.mats["up"][0], None, None, None, h, pws)
+    ep.ep_expert_product(down, lay, h, None, c.mats["down"][0], None, None, None, y, ep.alloc_product_workspace(down))
+    far = torch.empty_like(x)
+    ep.ep_combine(cfg, lay, y, idx, w, far, ws)
+    want, bound = ref.layer(c.x, c.idx, c.w, c.mats["up"][0], None, c.mats["down"][0], None, None, "swiglu", FUN)
+    assert ((far[0].double() - want).norm() / want.norm()) < 2.0 ** -8
+    assert ((out.double() - want).norm() / want.norm()) <= (far[0].double() - want).norm() / want.norm()
+
+
+def test_matrices_past_2_31_elements(ep):
+    E, H, I = 72, 4096, 4096
+    g = torch.Generator(device="cuda").manual_seed(1)
+    up = torch.empty(E, 2 * I, H, dtype=torch.bfloat16, device="cuda")
+    down = torch.empty(E, H, I, dtype=torch.bfloat16, device="cuda")
+    for e in (70, 71):
+        up[e] = torch.randn(2 * I, H, generator=g, device="cuda") * H ** -0.5
+        down[e] = torch.randn(H, I, generator=g, device="cuda") * I ** -0.5
+    cfg = ep.LayerConfig(3, E, 2, H, I)
+    x = torch.randn(3, H, generator=g, device="cuda").bfloat16()
+    idx = torch.tensor([[71, -1], [70, 71], [-1, 70]], device="cuda")
+    w, out = torch.rand(3, 2, generator=g, device="cuda"), torch.empty_like(x)
+    ep.ep_expert_layer(cfg, x, idx, w, up, None, None, down, None, None, None, out, ep.alloc_layer_workspace(cfg))
+    want, bound = ref.layer(x, idx, w, up, None, down, None, None, "swiglu", FUN)
+    assert ((out.double() - want).abs() <= want.abs() * 2.0 ** -8 + bound * (1 + 2.0 ** -7)).all()
+
+
+def test_streams_and_graphs(ep):
+    """Two calls captured on one workspace, replayed in turn; and on a stream of its own."""
+    a, b = (Case(ep, 8, 16, 4, 512, 264, seed=s, residual=True) for s in (1, 2))
+    b.ws = a.ws
+    want = [a.run(), b.run()]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = [a.run(), b.run()]
+    side.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(got, want))
+    outs, graphs = [torch.empty_like(a.x) for _ in range(2)], []
+    for c, o in zip((a, b), outs):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            c.run(out=o)
+    for _ in range(4):
+        for o in outs:
+            o.fill_(math.nan)
+        for gr in graphs:
+            gr.replay()
+        assert all(torch.equal(x, y) for x, y in zip(outs, want))
+
+
+def test_many_calls_back_to_back(ep):
+    """The second kernel of a call starts while the first still runs, and the next call's first behind it."""
+    c = Case(ep, 2, 16, 4, 1024, 512)
+    want = c.check()
+    outs = [c.run() for _ in range(300)]
+    assert all(torch.equal(o, want) for o in outs)
+    # the input of each call is the output of the one before
+    xs = [c.x]
+    for _ in range(6):
+        xs.append(c.run(x=xs[-1]))
+    for x, y in zip(xs, xs[1:]):
+        assert torch.equal(c.run(x=x.clone()), y)
