@@ -4,13 +4,13 @@
 //   down  out_t = sum_k w_tk (h_l W_down[e]^T + b_down[e]) + residual_t
 //
 // Reading the chosen experts' matrices once is what it costs, so both kernels are one stream of
-// matrix rows through shared memory: a producer warp keeps a ring of stages full with bulk copies, eight
-// warps multiply. A work item is a strip of 16 or 32 matrix rows times all tokens of that expert
-// (a group; tokens past kTokens are another group): the matrix rows are the 16 rows of mma.sync's
-// A operand, the tokens its 8 columns, and the eight warps share the summed index. With at most
-// 32 tokens to a matrix the tensor cores are far from being the limit, so the products go where their
-// operands need least preparation: the fragments are read straight from rows as they lie in
-// memory (the summed index is permuted alike for both), and FP8 codes become bf16 on the way.
+// matrix rows through shared memory: a warp keeps a ring of stages full of them (TMA) and eight warps
+// multiply, which fetch their pieces of the tokens' rows (small, in L2) a stage ahead. A work item is a strip of 16 or 32 matrix rows times all tokens
+// of that expert (a group; tokens past kTokens are another group): the matrix rows are the 16 rows
+// of mma.sync's A operand, the tokens its 8 columns, and the eight warps share the summed index.
+// With at most 32 tokens to a matrix the tensor cores are far from being the limit, so the products go
+// where their operands need least preparation: the fragments are read straight from rows as they
+// lie in memory (the summed index is permuted alike for both), and FP8 codes become bf16 on the way.
 #include "block_internal.cuh"
 #include "fp8_rows.cuh"
 #include "product_common.cuh"
@@ -20,7 +20,7 @@ namespace ep {
 namespace {
 
 constexpr int kWarps = 8;                        // that multiply
-constexpr int kThreads = (kWarps + 1) * 32;      // and the producer's
+constexpr int kThreads = (kWarps + 1) * 32;      // with the one that loads
 constexpr int kMaxStages = 16;
 constexpr int kMaxLanes = kLayerMaxTokens * kMaxTopk;
 
@@ -183,10 +183,21 @@ __device__ __forceinline__ void codes_to_bf16(uint32_t w, uint32_t& lo, uint32_t
 
 __device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory"); }
 
-__device__ __forceinline__ void bulk_row(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-               "l"(src), "r"(bytes), "r"(bar)
-               : "memory");
+// A place in the ring: the stage, and the parity of its barriers' phase.
+struct Place {
+  int stage = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next(int stages) {
+    if (++stage == stages) stage = 0, phase ^= 1u;
+  }
+};
+
+// As mbar_wait_timed, which looks at the clock after its first try; here most waits end within a few.
+__device__ __forceinline__ bool wait_stage(uint32_t bar, uint32_t parity) {
+#pragma unroll 1
+  for (int i = 0; i < 64; ++i)
+    if (mbar_try<false>(bar, parity)) return true;
+  return mbar_wait_timed<false>(bar, parity);
 }
 
 __device__ __forceinline__ float act_any(float z, int act) {
@@ -201,26 +212,23 @@ __device__ __forceinline__ float act_any(float z, int act) {
 
 // Shared memory of a kernel, in bytes from the start of its dynamic part.
 struct Plan {
-  uint32_t token, weight, groups, sums, acc, ring, stage, stages, total;
+  uint32_t token, weight, groups, sums, acc, ring, stages, total;
 };
 
-// A stage: kRowBytes of each matrix row of the strip and as many values of each token's row, at pitches that put
-// the 16-byte pieces which eight threads read at once in different banks; with FP8 the
-// scales of 8 rows x 128 columns each.
+// A stage: 16 KB of matrix rows in columns of 128 bytes a row, as TMA writes them with the 128-byte swizzle.
+constexpr int kStageBytes = 16384;
 template <bool kFp8, int kRows, int kTokens>
 struct Stage {
-  static constexpr int kRowBytes = kFp8 || kTokens == 32 ? 512 : 1024;
-  static constexpr int kPitch = kRowBytes + 64;
-  static constexpr int kColumns = kFp8 ? kRowBytes : kRowBytes / 2;  // of the summed index
-  static constexpr int kXPitch = kFp8 ? 2 * kRowBytes + 16 : kPitch;
-  static constexpr int kXAt = kRows * kPitch;
-  static constexpr int kScaleAt = kXAt + kTokens * kXPitch;
-  static constexpr int kGroups = kColumns / 128;  // of columns with a scale
-  static constexpr int kBytes = (kScaleAt + (kFp8 ? kRows / 8 * kGroups * 4 : 0) + 127) / 128 * 128;
+  static constexpr int kBoxes = kStageBytes / (kRows * 128);   // columns of 128 bytes
+  static constexpr int kColumns = kBoxes * (kFp8 ? 128 : 64);  // of the summed index
+  // Few tokens: both kernels' CTAs fit an SM together, so that the second has its lists and first stages ready
+  // when the first ends. With more there is more to do, and the ring gets the whole SM.
+  static constexpr int kCtas = kTokens <= 8 ? 2 : 1;
 };
 
 template <bool kFp8, int kRows, int kTokens>
 Plan plan_of(int T, int K, int E) {
+  using S = Stage<kFp8, kRows, kTokens>;
   const uint32_t lanes = static_cast<uint32_t>(T) * K;
   auto up = [](uint32_t n) { return (n + 127u) & ~127u; };
   Plan p;
@@ -228,13 +236,12 @@ Plan plan_of(int T, int K, int E) {
   p.weight = up(lanes * 2);
   p.groups = p.weight + up(lanes * 4);
   p.sums = p.groups + up(lanes * 4);
-  p.acc = p.sums + kWarps * kRows * kTokens * 4;
-  p.ring = p.acc + up(static_cast<uint32_t>(T) * kRows * 4);
-  p.stage = Stage<kFp8, kRows, kTokens>::kBytes;
-  const uint32_t room = 220u * 1024u;
-  p.stages = (room - p.ring) / p.stage;
+  p.acc = p.sums + 2 * kWarps * kRows * kTokens * 4;
+  p.ring = (p.acc + static_cast<uint32_t>(T) * kRows * 4 + 1023u) & ~1023u;
+  const uint32_t room = (S::kCtas == 2 ? 111u : 224u) * 1024u;  // of 113 or 227 KB, static memory among it
+  p.stages = room > p.ring ? (room - p.ring) / kStageBytes : 0;
   if (p.stages > kMaxStages) p.stages = kMaxStages;
-  uint32_t ring = p.stages * p.stage;
+  uint32_t ring = p.stages * kStageBytes;
   const uint32_t scratch = (2 * lanes + 2 * static_cast<uint32_t>(E)) * 4;  // of the lists, before the ring is used
   if (ring < scratch) ring = scratch;
   p.total = p.ring + ring;
@@ -243,12 +250,14 @@ Plan plan_of(int T, int K, int E) {
 
 // kDown: the second kernel. kRows: matrix rows of a strip, kTokens: of a group at most.
 template <bool kFp8, bool kDown, int kRows, int kTokens>
-__global__ void __launch_bounds__(kThreads, 1) layer_kernel(LayerArgs a, Plan p) {
-  constexpr int kM = kRows / 16, kN = kTokens / 8;
+__global__ void __launch_bounds__(kThreads, Stage<kFp8, kRows, kTokens>::kCtas)
+    layer_kernel(const __grid_constant__ CUtensorMap matrices, LayerArgs a, Plan p, int whole) {
   using S = Stage<kFp8, kRows, kTokens>;
-  constexpr int kColumns = S::kColumns, kPitch = S::kPitch, kXPitch = S::kXPitch, kXAt = S::kXAt, kScaleAt = S::kScaleAt;
-  constexpr int kPiece = kFp8 ? 64 : 32;  // columns that a warp takes at once: 64 bytes of a matrix row
-  extern __shared__ __align__(128) uint8_t smem[];
+  constexpr int kM = kRows / 16, kN = kTokens / 8;
+  constexpr int kColumns = S::kColumns;
+  constexpr int kPiece = kFp8 ? 64 : 32;           // columns that a warp takes at once: 64 bytes of a matrix row
+  constexpr int kPieces = 2 * S::kBoxes / kWarps;  // of a stage, for each warp
+  extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ __align__(8) uint64_t s_full[kMaxStages], s_empty[kMaxStages];
   __shared__ volatile int s_abort;
   __shared__ bool s_last;
@@ -256,15 +265,16 @@ __global__ void __launch_bounds__(kThreads, 1) layer_kernel(LayerArgs a, Plan p)
   const int stages = static_cast<int>(p.stages);
   if (threadIdx.x == 0) {
     for (int i = 0; i < stages; ++i) {
-      mbar_init_count(smem_addr(&s_full[i]), kFp8 ? 33 : 1);  // with scales, every lane of the producer
+      mbar_init_count(smem_addr(&s_full[i]), 1);
       mbar_init_count(smem_addr(&s_empty[i]), kWarps);
     }
     s_abort = 0;
     fence_barrier_init();
+    tma_prefetch_map(&matrices);
   }
   if constexpr (!kDown) pdl_wait();
-  // The second kernel may be placed as soon as what ran before the first is done: only h, which
-  // its producer waits for, comes from the first.
+  // The second kernel may be placed as soon as what ran before the first is done: only h, which the warps
+  // that multiply wait for, comes from the first.
   pdl_launch_dependents();
   const Lists lists = {reinterpret_cast<uint16_t*>(smem + p.token), reinterpret_cast<float*>(smem + p.weight),
                        reinterpret_cast<uint32_t*>(smem + p.groups)};
@@ -295,111 +305,136 @@ __global__ void __launch_bounds__(kThreads, 1) layer_kernel(LayerArgs a, Plan p)
   }
   const int64_t units = static_cast<int64_t>(tiles) * (kDown ? split : groups);
 
-  // Every strip of this CTA in order: f(group, tile, part) until it says false.
-  auto walk = [&](auto f) {
-    for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
-      const int part = static_cast<int>(u / tiles), tile = static_cast<int>(u - static_cast<int64_t>(part) * tiles);
-      const int g0 = kDown ? groups * part / split : part, g1 = kDown ? groups * (part + 1) / split : part + 1;
-      for (int g = g0; g < g1; ++g)
-        if (!f(g, tile)) return;
-    }
+  // The stages of this CTA in order: all of the summed index of a strip, the strips of a tile's groups, the tiles.
+  struct Cursor {
+    int64_t u;
+    int tile, part, g, end, step;
   };
+  auto enter = [&](Cursor& c) {
+    if (c.u >= units) return;
+    c.part = static_cast<int>(c.u / tiles);
+    c.tile = static_cast<int>(c.u - static_cast<int64_t>(c.part) * tiles);
+    c.g = kDown ? groups * c.part / split : c.part;
+    c.end = kDown ? groups * (c.part + 1) / split : c.part + 1;
+    c.step = 0;
+  };
+  auto advance = [&](Cursor& c) {
+    if (++c.step < steps) return;
+    c.step = 0;
+    if (++c.g < c.end) return;
+    c.u += gridDim.x;
+    enter(c);
+  };
+  Cursor cur = {blockIdx.x, 0, 0, 0, 0, 0};
+  // no group, no stage: there is still the output
+  if (groups > 0) enter(cur);
+  const uint8_t* const ring = smem + p.ring;
+  Place at;
 
-  if (warp == kWarps) {
-    const uint32_t ring = smem_addr(smem + p.ring);
-    const uint8_t* matrices = static_cast<const uint8_t*>(kDown ? a.down : a.up);
-    const float* scales = kDown ? a.down_sf : a.up_sf;
-    const uint16_t* x = kDown ? a.h : a.x;
-    const int bytes_a = kFp8 ? 1 : 2;
-    const int scale_rows = (z_rows + 127) >> 7, scale_columns = sum >> 7;
-    // matrix rows (and their scales) and token rows of one stage
-    auto issue = [&](uint32_t n, int g, int tile, int step, bool rows, bool tokens) {
-      const Group q = unpack_group(lists.groups[g]);
-      const uint32_t s = n % stages, bar = smem_addr(&s_full[s]), at = ring + s * p.stage;
-      const int c0 = step * kColumns, columns = min(kColumns, sum - c0);
-      const uint32_t row_bytes = columns * bytes_a, x_bytes = columns * 2;
-      // row i of the strip: gated, 8 rows of the gate, then the same 8 of the other half
-      const int first = gated ? tile * strip : tile * kRows;
-      auto row_of = [&](int i) { return gated ? (i & 8 ? a.I : 0) + first + (i >> 4) * 8 + (i & 7) : first + i; };
-      auto there = [&](int i) { return gated ? first + (i >> 4) * 8 + (i & 7) < a.I : first + i < z_rows; };
-      if (rows) {
-        const bool mine = lane < kRows && there(lane);
-        const unsigned all = __ballot_sync(kFullMask, mine);
-        if (lane == 0) mbar_expect(bar, __popc(all) * row_bytes + q.n * x_bytes);
-        __syncwarp();
-        if (mine)
-          bulk_row(at + lane * kPitch, matrices + ((static_cast<int64_t>(q.expert) * z_rows + row_of(lane)) * sum + c0) * bytes_a,
-                   row_bytes, bar);
-        if constexpr (kFp8) {  // scale [i / 8][column / 128] of the strip's rows
-          constexpr int kGroups = S::kGroups;
-          static_assert(kRows / 8 * kGroups <= 32, "a lane a scale");
-          const int i = lane / kGroups * 8, c = (c0 >> 7) + lane % kGroups;
-          if (i < kRows && there(i) && c < scale_columns) {
-            const float* src = scales + (static_cast<int64_t>(q.expert) * scale_rows + (row_of(i) >> 7)) * scale_columns + c;
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(at + kScaleAt + lane * 4), "l"(src) : "memory");
-          }
-          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+  if (warp == kWarps) {  // matrix rows: one thread, one copy a stage; what lies outside a matrix reads as zero
+    if (elect_one() && groups > 0) {
+      uint32_t n = 0;
+      for (; cur.u < units; advance(cur), at.next(stages), ++n) {
+        if (s_abort != 0 || !wait_stage(smem_addr(&s_empty[at.stage]), at.phase ^ 1u)) {
+          if (s_abort == 0) atomicOr(a.err, kErrTimeout);
+          s_abort = 1;  // the copies in flight end before the CTA does
+          for (uint32_t m = n - min(n, p.stages); m < n; ++m)
+            mbar_wait_timed<false>(smem_addr(&s_full[m % p.stages]), m / p.stages & 1u);
+          break;
         }
-      }
-      if (tokens && lane < q.n) {
-        const int64_t row = kDown ? q.start + lane : lists.token[q.start + lane];
-        bulk_row(at + kXAt + lane * kXPitch, x + row * sum + c0, x_bytes, bar);
-      }
-    };
-    uint32_t early = 0;
-    if constexpr (kDown) {  // the first stages' matrix rows do not wait for h
-      walk([&](int g, int tile) {
-        for (int step = 0; step < steps; ++step) {
-          if (early == static_cast<uint32_t>(stages)) return false;
-          issue(early++, g, tile, step, true, false);
+        const Group q = unpack_group(lists.groups[cur.g]);
+        const int plane = gated ? 2 * q.expert : q.expert, row = cur.tile * strip;
+        const uint32_t bar = smem_addr(&s_full[at.stage]), to = smem_addr(ring + at.stage * kStageBytes);
+        if (whole) {
+          mbar_expect(bar, kStageBytes);
+          tma_load_4d(to, &matrices, 0, row, plane, cur.step * S::kBoxes, bar);
+        } else {  // columns that are no multiple of 128 bytes: box by box
+          const int boxes = min(S::kBoxes, (sum - cur.step * kColumns + 63) / 64);
+          mbar_expect(bar, boxes * kRows * 128);
+          for (int i = 0; i < boxes; ++i) tma_load_3d(to + i * kRows * 128, &matrices, cur.step * kColumns + i * 64, row, plane, bar);
         }
-        return true;
-      });
-      pdl_wait();
-    }
-    uint32_t n = 0;
-    bool ok = true;
-    walk([&](int g, int tile) {
-      for (int step = 0; step < steps; ++step, ++n) {
-        bool free = true;
-        if (lane == 0) {
-          free = s_abort == 0 && mbar_wait_timed<false>(smem_addr(&s_empty[n % stages]), (n / stages & 1u) ^ 1u);
-          if (!free && s_abort == 0) atomicOr(a.err, kErrTimeout);
-        }
-        if (!__shfl_sync(kFullMask, free, 0)) {
-          s_abort = 1;
-          ok = false;
-          return false;
-        }
-        issue(n, g, tile, step, n >= early, true);
-      }
-      return true;
-    });
-    if (!ok) {  // the copies in flight end before the CTA does
-      if (n < early) {  // matrix rows whose tokens' rows were not asked for: their barriers do not complete
-        const uint64_t t0 = global_ns();
-        while (global_ns() - t0 < 10000000ull) __nanosleep(1000);
-      }
-      for (uint32_t back = min(n, static_cast<uint32_t>(stages)); back > 0; --back) {
-        const uint32_t m = n - back;
-        mbar_wait_timed<false>(smem_addr(&s_full[m % stages]), m / stages & 1u);
       }
     }
+    if constexpr (kDown) pdl_wait();  // no CTA of this kernel ends before the first kernel
     return;
   }
 
   // ---- the eight warps that multiply
   const int t = lane & 3, r8 = lane >> 2;
-  const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
-  float4* sums = reinterpret_cast<float4*>(smem + p.sums);  // [warp][kM * kN][lane]
-  uint32_t n = 0;
-  int64_t u = blockIdx.x;
-  for (; u < units; u += gridDim.x) {
+  // The matrix rows of threads r8 = 2 i and 2 i + 1 are 4 apart, so that with the swizzle the eight 16-byte
+  // pieces that 8 threads read at once lie in different banks.
+  const int row8 = r8 >> 1 | (r8 & 1) << 2;
+  // [turn][warp][kM * kN][lane]: two buffers, so that one barrier a strip is enough
+  float4* all_sums = reinterpret_cast<float4*>(smem + p.sums);
+  const int lo_step = gated ? 8 : 16, hi_at = gated ? kRows / 2 : 8;  // rows of the strip: lo_step m + (0 or hi_at) + row8
+
+  // What a warp's pieces of a stage meet: the tokens' values and the scales.
+  struct Beside {
+    uint4 x[kPieces][kN][kFp8 ? 2 : 1];
+    float scale[kFp8 ? kPieces : 1][kFp8 ? kM : 1][2];
+  };
+  const uint16_t* const x = kDown ? a.h : a.x;
+  const float* const scales = kDown ? a.down_sf : a.up_sf;
+  const int scale_rows = (z_rows + 127) >> 7, scale_columns = sum >> 7;
+  const uint16_t* from[kN];  // of the strip that is fetched: this thread's tokens' rows (past the last token: the last's)
+  const float* scale_at[kFp8 ? kM : 1][2];
+  auto fetch_strip = [&](const Cursor& c) {
+    const Group q = unpack_group(lists.groups[c.g]);
+#pragma unroll
+    for (int j = 0; j < kN; ++j) {
+      const int i = q.start + min(j * 8 + r8, q.n - 1);
+      from[j] = x + static_cast<int64_t>(kDown ? i : lists.token[i]) * sum + t * (kFp8 ? 16 : 8);
+    }
+    if constexpr (kFp8) {
+#pragma unroll
+      for (int m = 0; m < kM; ++m)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int row = c.tile * strip + (gated ? m * 8 + h * a.I : m * 16 + h * 8);
+          scale_at[m][h] = scales + (static_cast<int64_t>(q.expert) * scale_rows + (row >> 7)) * scale_columns;
+        }
+    }
+  };
+  auto fetch = [&](const Cursor& c, Beside& b) {
+    const int c0 = c.step * kColumns;
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      const int column = c0 + (i * kWarps + warp) * kPiece;
+      const bool in = kFp8 ? column < sum : column + t * 8 < sum;
+#pragma unroll
+      for (int j = 0; j < kN; ++j)
+#pragma unroll
+        for (int h = 0; h < (kFp8 ? 2 : 1); ++h) {
+          b.x[i][j][h] = make_uint4(0u, 0u, 0u, 0u);
+          if (in) b.x[i][j][h] = kDown ? __ldcg(reinterpret_cast<const uint4*>(from[j] + column + h * 8))
+                                       : *reinterpret_cast<const uint4*>(from[j] + column + h * 8);
+        }
+      if constexpr (kFp8) {
+#pragma unroll
+        for (int m = 0; m < kM; ++m)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) b.scale[i][m][h] = in ? __ldg(scale_at[m][h] + (column >> 7)) : 0.f;
+      }
+    }
+  };
+
+  if constexpr (kDown) pdl_wait();
+  uint32_t strips = 0;
+  Cursor ahead = cur;
+  Beside now, next;
+  if (groups > 0 && cur.u < units) {
+    fetch_strip(ahead);
+    fetch(ahead, now);
+    advance(ahead);
+  }
+  for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
     const int part = static_cast<int>(u / tiles), tile = static_cast<int>(u - static_cast<int64_t>(part) * tiles);
     const int g0 = kDown ? groups * part / split : part, g1 = kDown ? groups * (part + 1) / split : part + 1;
-    for (int g = g0; g < g1; ++g) {
+    for (int g = g0; g < g1; ++g, ++strips) {
       const Group q = unpack_group(lists.groups[g]);
-      const int used = (q.n + 7) >> 3;  // tiles of 8 tokens
+      float4* sums = all_sums + (strips & 1u) * (kWarps * kM * kN * 32);
+      // tiles of 8 tokens; of two both are computed, as that costs less than asking
+      const int used = kN > 2 ? (q.n + 15) >> 4 << 1 : kN;
       float d[kM][kN][4];
 #pragma unroll
       for (int m = 0; m < kM; ++m)
@@ -407,41 +442,33 @@ __global__ void __launch_bounds__(kThreads, 1) layer_kernel(LayerArgs a, Plan p)
         for (int j = 0; j < kN; ++j)
 #pragma unroll
           for (int i = 0; i < 4; ++i) d[m][j][i] = 0.f;
-      for (int step = 0; step < steps; ++step, ++n) {
-        const uint32_t s = n % stages;
-        if (!s_abort && !mbar_wait_timed<false>(smem_addr(&s_full[s]), n / stages & 1u)) {
-          if (!s_abort && lane == 0) atomicOr(a.err, kErrTimeout);
-          s_abort = 1;  // what follows is not waited for: outputs are incomplete
+      for (int step = 0; step < steps; ++step) {
+        if (ahead.u < units) {
+          if (ahead.step == 0) fetch_strip(ahead);
+          fetch(ahead, next);
+          advance(ahead);
+        }
+        // a wait that gives up is the last one: what follows is computed without, and reported
+        const uint32_t bar = smem_addr(&s_full[at.stage]);
+        if (!mbar_try<false>(bar, at.phase) && s_abort == 0 && !wait_stage(bar, at.phase)) {
+          if (s_abort == 0) atomicOr(a.err, kErrTimeout);
+          s_abort = 1;
         }
         __syncwarp();
-        const uint8_t* stage = smem + p.ring + s * p.stage;
-        const int columns = min(kColumns, sum - step * kColumns);
+        const uint8_t* stage = ring + at.stage * kStageBytes;
+        const int columns = sum - step * kColumns;
 #pragma unroll
-        for (int b = 0; b < S::kRowBytes / 64 / kWarps; ++b) {
-          const int piece = b * kWarps + warp, c = piece * kPiece;
-          if (c >= columns) break;
-          const bool in = kFp8 || c + t * 8 < columns;  // 16 bytes of a row are all there, or none is
-          const uint8_t* rows = stage + r8 * kPitch + piece * 64 + t * 16;
-          const uint8_t* xs = stage + kXAt + r8 * kXPitch + c * 2 + t * (kFp8 ? 32 : 16);
-          uint4 xv[kN][kFp8 ? 2 : 1];
-#pragma unroll
-          for (int j = 0; j < kN; ++j)
-#pragma unroll
-            for (int h = 0; h < (kFp8 ? 2 : 1); ++h) {
-              xv[j][h] = make_uint4(0u, 0u, 0u, 0u);
-              if (j < used && in) xv[j][h] = *reinterpret_cast<const uint4*>(xs + j * 8 * kXPitch + h * 16);
-            }
+        for (int b = 0; b < kPieces; ++b) {
+          const int piece = b * kWarps + warp;
+          if (piece * kPiece >= columns) break;
+          const uint8_t* rows = stage + (piece >> 1) * (kRows * 128) + row8 * 128 + ((((piece & 1) << 2) + t) ^ row8) * 16;
 #pragma unroll
           for (int m = 0; m < kM; ++m) {
-            uint4 lo = make_uint4(0u, 0u, 0u, 0u), hi = lo;
-            if (in) {
-              lo = *reinterpret_cast<const uint4*>(rows + m * 16 * kPitch);
-              hi = *reinterpret_cast<const uint4*>(rows + (m * 16 + 8) * kPitch);
-            }
+            const uint4 lo = *reinterpret_cast<const uint4*>(rows + m * lo_step * 128);
+            const uint4 hi = *reinterpret_cast<const uint4*>(rows + (m * lo_step + hi_at) * 128);
             if constexpr (kFp8) {
               const uint32_t l[4] = {lo.x, lo.y, lo.z, lo.w}, u4[4] = {hi.x, hi.y, hi.z, hi.w};
-              const float* sf = reinterpret_cast<const float*>(stage + kScaleAt) + m * 2 * S::kGroups + (c >> 7);
-              const float s0 = sf[0], s1 = sf[S::kGroups];
+              const float s0 = now.scale[b][m][0], s1 = now.scale[b][m][1];
               float e[kN][4];
 #pragma unroll
               for (int j = 0; j < kN; ++j)
@@ -455,7 +482,7 @@ __global__ void __launch_bounds__(kThreads, 1) layer_kernel(LayerArgs a, Plan p)
 #pragma unroll
                 for (int j = 0; j < kN; ++j)
                   if (j < used) {
-                    const uint4 v = xv[j][k >> 1];
+                    const uint4 v = now.x[b][j][k >> 1];
                     mma_16x8(e[j], a0, a1, a2, a3, k & 1 ? v.z : v.x, k & 1 ? v.w : v.y);
                   }
               }
@@ -470,14 +497,17 @@ __global__ void __launch_bounds__(kThreads, 1) layer_kernel(LayerArgs a, Plan p)
 #pragma unroll
               for (int j = 0; j < kN; ++j)
                 if (j < used) {
-                  mma_16x8(d[m][j], lo.x, hi.x, lo.y, hi.y, xv[j][0].x, xv[j][0].y);
-                  mma_16x8(d[m][j], lo.z, hi.z, lo.w, hi.w, xv[j][0].z, xv[j][0].w);
+                  const uint4 v = now.x[b][j][0];
+                  mma_16x8(d[m][j], lo.x, hi.x, lo.y, hi.y, v.x, v.y);
+                  mma_16x8(d[m][j], lo.z, hi.z, lo.w, hi.w, v.z, v.w);
                 }
             }
           }
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_addr(&s_empty[s]));
+        if (lane == 0) mbar_arrive(smem_addr(&s_empty[at.stage]));
+        at.next(stages);
+        now = next;
       }
       // the eight warps' sums, in their order: a warp takes a tile of 16 x 8 of them
 #pragma unroll
@@ -487,19 +517,19 @@ __global__ void __launch_bounds__(kThreads, 1) layer_kernel(LayerArgs a, Plan p)
           if (j < used) sums[(warp * kM * kN + m * kN + j) * 32 + lane] = make_float4(d[m][j][0], d[m][j][1], d[m][j][2], d[m][j][3]);
       consumers_sync();
 #pragma unroll
-      for (int i = warp; i < kM * kN; i += kWarps) {
+      for (int i = static_cast<int>((warp - strips) & (kWarps - 1)); i < kM * kN; i += kWarps) {  // the warps take turns
         const int m = i / kN, j = i - m * kN;
         if (j >= used) continue;
-        float4 v = none;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
           const float4 o = sums[(w * kM * kN + i) * 32 + lane];
           v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
         }
-        // v: results of rows r8 and r8 + 8 for tokens 2 t and 2 t + 1 of the tile
+        // v: results of rows row8 and row8 + 8 for tokens 2 t and 2 t + 1 of the tile
         const float got[2][2] = {{v.x, v.y}, {v.z, v.w}};
         if (gated) {
-          const int c = tile * strip + m * 8 + r8;
+          const int c = tile * strip + m * 8 + row8;
           if (c < a.I) {
             float b0 = 0.f, b1 = 0.f;
             if (a.up_bias != nullptr) {
@@ -517,7 +547,7 @@ __global__ void __launch_bounds__(kThreads, 1) layer_kernel(LayerArgs a, Plan p)
         } else {
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
-            const int in_strip = m * 16 + half * 8 + r8, c = tile * kRows + in_strip;
+            const int in_strip = m * 16 + half * 8 + row8, c = tile * kRows + in_strip;
             if (c >= out_rows) continue;
             const uint16_t* bias = kDown ? a.down_bias : a.up_bias;
             float b = 0.f;
@@ -537,9 +567,9 @@ __global__ void __launch_bounds__(kThreads, 1) layer_kernel(LayerArgs a, Plan p)
           }
         }
       }
-      consumers_sync();
     }
     if constexpr (kDown) {  // the tile's tokens: 8 results a thread
+      consumers_sync();
       constexpr int kEights = kRows / 8;
       bool finish = split == 1;
       if (split > 1) {
@@ -598,9 +628,28 @@ __global__ void __launch_bounds__(kThreads, 1) layer_kernel(LayerArgs a, Plan p)
 template <bool kFp8, bool kDown, int kRows, int kTokens>
 cudaError_t launch_one(const LayerArgs& a, int num_sms, cudaStream_t stream) {
   auto kern = layer_kernel<kFp8, kDown, kRows, kTokens>;
+  using S = Stage<kFp8, kRows, kTokens>;
   const Plan p = plan_of<kFp8, kRows, kTokens>(a.T, a.K, a.E);
   if (p.stages < 2 || resident_ctas(reinterpret_cast<const void*>(kern), kThreads, p.total) < 1) return cudaErrorInvalidConfiguration;
-  return launch_chained(kern, dim3(num_sms), dim3(kThreads), p.total, stream, a, p);
+  // 16-bit elements (two codes each); gated, the gate rows and the others of an expert are planes of their own
+  const bool gated = !kDown && a.act == EP_ACT_SWIGLU;
+  const uint64_t columns = static_cast<uint64_t>(kDown ? a.I : a.H) / (kFp8 ? 2 : 1), rows = kDown ? a.H : a.I;
+  const uint64_t planes = static_cast<uint64_t>(a.E) * (gated ? 2 : 1);
+  const uint32_t box_rows = gated ? kRows / 2 : kRows, box_planes = gated ? 2 : 1;
+  const int whole = columns % 64 == 0;  // then one copy brings all columns of a stage
+  CUtensorMap map;
+  cudaError_t st;
+  if (whole) {
+    const uint64_t size[4] = {64, rows, planes, columns / 64}, stride[3] = {2 * columns, 2 * columns * rows, 128};
+    const uint32_t box[4] = {64, box_rows, box_planes, S::kBoxes};
+    st = make_strided_map(&map, kDown ? a.down : a.up, 4, size, stride, box);
+  } else {
+    const uint64_t size[3] = {columns, rows, planes};
+    const uint32_t box[3] = {64, box_rows, box_planes};
+    st = make_tensor_map(&map, kDown ? a.down : a.up, 3, size, box);
+  }
+  if (st != cudaSuccess) return st;
+  return launch_chained(kern, dim3(num_sms), dim3(kThreads), p.total, stream, map, a, p, whole);
 }
 
 template <bool kFp8, int kRows, int kTokens>
@@ -611,8 +660,7 @@ cudaError_t launch_both(const LayerArgs& a, int num_sms, cudaStream_t stream) {
 
 template <bool kFp8>
 cudaError_t launch_typed(const LayerArgs& a, int num_sms, cudaStream_t stream) {
-  if (a.T <= 4) return launch_both<kFp8, 16, 8>(a, num_sms, stream);
-  if (a.T <= 8) return launch_both<kFp8, 32, 8>(a, num_sms, stream);
+  if (a.T <= 8) return launch_both<kFp8, 16, 8>(a, num_sms, stream);
   // tokens to a group: most experts' tokens are one group
   return 2 * a.T * a.K <= 21 * a.E ? launch_both<kFp8, 32, 16>(a, num_sms, stream) : launch_both<kFp8, 32, 32>(a, num_sms, stream);
 }

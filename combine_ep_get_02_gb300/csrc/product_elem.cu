@@ -277,7 +277,8 @@ cudaError_t launch_dz(DzArgs a, int num_sms, cudaStream_t stream) {
 
 }  // namespace
 
-cudaError_t make_tensor_map(CUtensorMap* map, const void* base, int dims, const uint64_t* size, const uint32_t* box) {
+cudaError_t make_strided_map(CUtensorMap* map, const void* base, int dims, const uint64_t* size, const uint64_t* stride,
+                             const uint32_t* box) {
   using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                               const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                               CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -291,21 +292,25 @@ cudaError_t make_tensor_map(CUtensorMap* map, const void* base, int dims, const 
     return reinterpret_cast<Encode>(fn);
   }();
   if (encode == nullptr) return cudaErrorNotSupported;
-  cuuint64_t sizes[3], strides[2];
-  cuuint32_t boxes[3], steps[3];
-  cuuint64_t stride = 2;
+  cuuint64_t sizes[4], strides[3];
+  cuuint32_t boxes[4], steps[4];
   for (int i = 0; i < dims; ++i) {
     sizes[i] = size[i];
     boxes[i] = box[i];
     steps[i] = 1;
-    stride *= size[i];
-    if (i + 1 < dims) strides[i] = stride;
+    if (i + 1 < dims) strides[i] = stride[i];
   }
   const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<cuuint32_t>(dims), const_cast<void*>(base),
                             sizes, strides, boxes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
                             box[0] == 32 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
                             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+cudaError_t make_tensor_map(CUtensorMap* map, const void* base, int dims, const uint64_t* size, const uint32_t* box) {
+  uint64_t stride[3], bytes = 2;
+  for (int i = 0; i + 1 < dims; ++i) stride[i] = bytes *= size[i];
+  return make_strided_map(map, base, dims, size, stride, box);
 }
 
 cudaError_t launch_dequant(const ProductGeometry& g, const uint8_t* x, const float* x_sf, uint16_t* out, int num_sms,

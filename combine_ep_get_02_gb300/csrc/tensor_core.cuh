@@ -96,6 +96,13 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
       "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
       : "memory");
 }
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+      "[%6];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+      : "memory");
+}
 // stores of tiles in shared memory; the issuing thread's groups as for bulk copies
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, int x, int y, uint32_t src) {
   asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(map), "r"(x), "r"(y),
@@ -293,5 +300,8 @@ constexpr uint32_t idesc_bf16(int m, int n, bool a_mn, bool b_mn) {
 // are 128 bytes with the 128-byte swizzle, or 64 with the 64-byte one; elements outside
 // read as zero and are not written.
 cudaError_t make_tensor_map(CUtensorMap* map, const void* base, int dims, const uint64_t* size, const uint32_t* box);
+// The same with the outer dimensions (4 in all at most) `stride` bytes apart.
+cudaError_t make_strided_map(CUtensorMap* map, const void* base, int dims, const uint64_t* size, const uint64_t* stride,
+                             const uint32_t* box);
 
 }  // namespace ep
