@@ -5,7 +5,7 @@
 //
 // Reading the chosen experts' matrices once is what it costs, so both kernels are one stream of
 // matrix rows through shared memory: a warp keeps a ring of stages full of them (TMA) and eight warps
-// multiply, which fetch their pieces of the tokens' rows (small, in L2) a stage ahead. A work item is a strip of 16 or 32 matrix rows times all tokens
+// multiply, whose threads fetch their own pieces of the tokens' rows (small, in L2) a few stages ahead. A work item is a strip of 16 or 32 matrix rows times all tokens
 // of that expert (a group; tokens past kTokens are another group): the matrix rows are the 16 rows
 // of mma.sync's A operand, the tokens its 8 columns, and the eight warps share the summed index.
 // With at most 32 tokens to a matrix the tensor cores are far from being the limit, so the products go
@@ -212,7 +212,7 @@ __device__ __forceinline__ float act_any(float z, int act) {
 
 // Shared memory of a kernel, in bytes from the start of its dynamic part.
 struct Plan {
-  uint32_t token, weight, groups, sums, acc, ring, stages, total;
+  uint32_t token, weight, groups, sums, beside, acc, ring, stages, total;
 };
 
 // A stage: 16 KB of matrix rows in columns of 128 bytes a row, as TMA writes them with the 128-byte swizzle.
@@ -221,9 +221,16 @@ template <bool kFp8, int kRows, int kTokens>
 struct Stage {
   static constexpr int kBoxes = kStageBytes / (kRows * 128);   // columns of 128 bytes
   static constexpr int kColumns = kBoxes * (kFp8 ? 128 : 64);  // of the summed index
+  static constexpr int kPieces = 2 * kBoxes / kWarps;          // of 64 bytes a row, for each warp
+  // What a warp's pieces meet: for each thread (of 4 tokens' in (16, 4)) 16 bytes of each token tile's row, twice
+  // with FP8, and then the scales. Fetched kAhead stages ahead.
+  static constexpr int kM = kRows / 16, kN = (kTokens + 7) / 8;
+  static constexpr int kLanes = kTokens < 8 ? 4 * kTokens : 32;
+  static constexpr int kBesideBytes = kPieces * kN * (kFp8 ? 2 : 1) * kLanes * 16 + (kFp8 ? kPieces * kM * 8 : 0);
+  static constexpr int kAhead = kFp8 && kTokens > 16 ? 2 : 4;
   // Few tokens: both kernels' CTAs fit an SM together, so that the second has its lists and first stages ready
   // when the first ends. With more there is more to do, and the ring gets the whole SM.
-  static constexpr int kCtas = kTokens <= 8 ? 2 : 1;
+  static constexpr int kCtas = kTokens <= (kFp8 ? 4 : 8) ? 2 : 1;
 };
 
 template <bool kFp8, int kRows, int kTokens>
@@ -236,7 +243,8 @@ Plan plan_of(int T, int K, int E) {
   p.weight = up(lanes * 2);
   p.groups = p.weight + up(lanes * 4);
   p.sums = p.groups + up(lanes * 4);
-  p.acc = p.sums + 2 * kWarps * kRows * kTokens * 4;
+  p.beside = p.sums + 2 * kWarps * kRows * S::kN * 8 * 4;
+  p.acc = p.beside + up(kWarps * S::kAhead * S::kBesideBytes);
   p.ring = (p.acc + static_cast<uint32_t>(T) * kRows * 4 + 1023u) & ~1023u;
   const uint32_t room = (S::kCtas == 2 ? 111u : 224u) * 1024u;  // of 113 or 227 KB, static memory among it
   p.stages = room > p.ring ? (room - p.ring) / kStageBytes : 0;
@@ -253,10 +261,9 @@ template <bool kFp8, bool kDown, int kRows, int kTokens>
 __global__ void __launch_bounds__(kThreads, Stage<kFp8, kRows, kTokens>::kCtas)
     layer_kernel(const __grid_constant__ CUtensorMap matrices, LayerArgs a, Plan p, int whole) {
   using S = Stage<kFp8, kRows, kTokens>;
-  constexpr int kM = kRows / 16, kN = kTokens / 8;
-  constexpr int kColumns = S::kColumns;
+  constexpr int kM = S::kM, kN = S::kN, kHalves = kFp8 ? 2 : 1, kAhead = S::kAhead;
+  constexpr int kColumns = S::kColumns, kPieces = S::kPieces;
   constexpr int kPiece = kFp8 ? 64 : 32;           // columns that a warp takes at once: 64 bytes of a matrix row
-  constexpr int kPieces = 2 * S::kBoxes / kWarps;  // of a stage, for each warp
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ __align__(8) uint64_t s_full[kMaxStages], s_empty[kMaxStages];
   __shared__ volatile int s_abort;
@@ -368,65 +375,66 @@ __global__ void __launch_bounds__(kThreads, Stage<kFp8, kRows, kTokens>::kCtas)
   float4* all_sums = reinterpret_cast<float4*>(smem + p.sums);
   const int lo_step = gated ? 8 : 16, hi_at = gated ? kRows / 2 : 8;  // rows of the strip: lo_step m + (0 or hi_at) + row8
 
-  // What a warp's pieces of a stage meet: the tokens' values and the scales.
-  struct Beside {
-    uint4 x[kPieces][kN][kFp8 ? 2 : 1];
-    float scale[kFp8 ? kPieces : 1][kFp8 ? kM : 1][2];
-  };
+  // The pieces of a stage that is `kAhead` ahead, by each thread for itself (so no barrier stands between
+  // them and their use, but a warp's for the scales): zeros behind the last column.
   const uint16_t* const x = kDown ? a.h : a.x;
   const float* const scales = kDown ? a.down_sf : a.up_sf;
   const int scale_rows = (z_rows + 127) >> 7, scale_columns = sum >> 7;
-  const uint16_t* from[kN];  // of the strip that is fetched: this thread's tokens' rows (past the last token: the last's)
-  const float* scale_at[kFp8 ? kM : 1][2];
-  auto fetch_strip = [&](const Cursor& c) {
-    const Group q = unpack_group(lists.groups[c.g]);
+  uint8_t* const beside = smem + p.beside + warp * (kAhead * S::kBesideBytes);
+  const int slot = (kTokens < 8 ? lane & (S::kLanes - 1) : lane) * 16;
+  const uint16_t* from[kN];         // of the strip that is fetched: this thread's tokens' rows
+  const float* scale_at = nullptr;  // this lane's, of [kPieces][kM][2]
+  Cursor ahead = cur;
+  int place = 0;  // of kAhead
+  auto fetch = [&] {
+    if (ahead.u < units) {
+      if (ahead.step == 0) {
+        const Group q = unpack_group(lists.groups[ahead.g]);
 #pragma unroll
-    for (int j = 0; j < kN; ++j) {
-      const int i = q.start + min(j * 8 + r8, q.n - 1);
-      from[j] = x + static_cast<int64_t>(kDown ? i : lists.token[i]) * sum + t * (kFp8 ? 16 : 8);
-    }
-    if constexpr (kFp8) {
-#pragma unroll
-      for (int m = 0; m < kM; ++m)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int row = c.tile * strip + (gated ? m * 8 + h * a.I : m * 16 + h * 8);
-          scale_at[m][h] = scales + (static_cast<int64_t>(q.expert) * scale_rows + (row >> 7)) * scale_columns;
+        for (int j = 0; j < kN; ++j) {
+          const int i = q.start + j * 8 + r8;
+          from[j] = j * 8 + r8 < q.n ? x + static_cast<int64_t>(kDown ? i : lists.token[i]) * sum + t * (kFp8 ? 16 : 8) : nullptr;
         }
-    }
-  };
-  auto fetch = [&](const Cursor& c, Beside& b) {
-    const int c0 = c.step * kColumns;
-#pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-      const int column = c0 + (i * kWarps + warp) * kPiece;
-      const bool in = kFp8 ? column < sum : column + t * 8 < sum;
-#pragma unroll
-      for (int j = 0; j < kN; ++j)
-#pragma unroll
-        for (int h = 0; h < (kFp8 ? 2 : 1); ++h) {
-          b.x[i][j][h] = make_uint4(0u, 0u, 0u, 0u);
-          if (in) b.x[i][j][h] = kDown ? __ldcg(reinterpret_cast<const uint4*>(from[j] + column + h * 8))
-                                       : *reinterpret_cast<const uint4*>(from[j] + column + h * 8);
+        if constexpr (kFp8) {
+          const int h = lane & 1, m = (lane >> 1) % kM;
+          const int row = ahead.tile * strip + (gated ? m * 8 + h * a.I : m * 16 + h * 8);
+          scale_at = scales + (static_cast<int64_t>(q.expert) * scale_rows + (row >> 7)) * scale_columns;
         }
-      if constexpr (kFp8) {
-#pragma unroll
-        for (int m = 0; m < kM; ++m)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) b.scale[i][m][h] = in ? __ldg(scale_at[m][h] + (column >> 7)) : 0.f;
       }
+      const uint32_t to = smem_addr(beside + place * S::kBesideBytes);
+      const int c0 = ahead.step * kColumns;
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i) {
+        const int column = c0 + (i * kWarps + warp) * kPiece;
+        const int bytes = (kFp8 ? column < sum : column + t * 8 < sum) ? 16 : 0;
+#pragma unroll
+        for (int j = 0; j < kN; ++j)
+#pragma unroll
+          for (int h = 0; h < kHalves; ++h)
+            if (from[j] != nullptr)  // columns without a token are nobody's
+              asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                               to + ((i * kN + j) * kHalves + h) * (S::kLanes * 16) + slot),
+                           "l"(from[j] + (bytes ? column + h * 8 : 0)), "r"(bytes)
+                           : "memory");
+      }
+      if constexpr (kFp8) {
+        const int column = c0 + (lane / (2 * kM) * kWarps + warp) * kPiece;
+        if (lane < kPieces * kM * 2 && column < sum)
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to + kPieces * kN * kHalves * (S::kLanes * 16) + lane * 4),
+                       "l"(scale_at + (column >> 7))
+                       : "memory");
+      }
+      advance(ahead);
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    if (++place == kAhead) place = 0;
   };
 
   if constexpr (kDown) pdl_wait();
   uint32_t strips = 0;
-  Cursor ahead = cur;
-  Beside now, next;
-  if (groups > 0 && cur.u < units) {
-    fetch_strip(ahead);
-    fetch(ahead, now);
-    advance(ahead);
-  }
+  if (groups == 0) ahead.u = units;
+#pragma unroll 1
+  for (int i = 0; i < kAhead - 1; ++i) fetch();
   for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
     const int part = static_cast<int>(u / tiles), tile = static_cast<int>(u - static_cast<int64_t>(part) * tiles);
     const int g0 = kDown ? groups * part / split : part, g1 = kDown ? groups * (part + 1) / split : part + 1;
@@ -443,11 +451,10 @@ __global__ void __launch_bounds__(kThreads, Stage<kFp8, kRows, kTokens>::kCtas)
 #pragma unroll
           for (int i = 0; i < 4; ++i) d[m][j][i] = 0.f;
       for (int step = 0; step < steps; ++step) {
-        if (ahead.u < units) {
-          if (ahead.step == 0) fetch_strip(ahead);
-          fetch(ahead, next);
-          advance(ahead);
-        }
+        const uint8_t* here = beside + (place + 1 == kAhead ? 0 : place + 1) * S::kBesideBytes + slot;
+        const float* sf = reinterpret_cast<const float*>(here - slot + kPieces * kN * kHalves * (S::kLanes * 16));
+        fetch();
+        asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
         // a wait that gives up is the last one: what follows is computed without, and reported
         const uint32_t bar = smem_addr(&s_full[at.stage]);
         if (!mbar_try<false>(bar, at.phase) && s_abort == 0 && !wait_stage(bar, at.phase)) {
@@ -462,13 +469,19 @@ __global__ void __launch_bounds__(kThreads, Stage<kFp8, kRows, kTokens>::kCtas)
           const int piece = b * kWarps + warp;
           if (piece * kPiece >= columns) break;
           const uint8_t* rows = stage + (piece >> 1) * (kRows * 128) + row8 * 128 + ((((piece & 1) << 2) + t) ^ row8) * 16;
+          uint4 xv[kN][kHalves];
+#pragma unroll
+          for (int j = 0; j < kN; ++j)
+#pragma unroll
+            for (int h = 0; h < kHalves; ++h)
+              xv[j][h] = *reinterpret_cast<const uint4*>(here + ((b * kN + j) * kHalves + h) * (S::kLanes * 16));
 #pragma unroll
           for (int m = 0; m < kM; ++m) {
             const uint4 lo = *reinterpret_cast<const uint4*>(rows + m * lo_step * 128);
             const uint4 hi = *reinterpret_cast<const uint4*>(rows + (m * lo_step + hi_at) * 128);
             if constexpr (kFp8) {
               const uint32_t l[4] = {lo.x, lo.y, lo.z, lo.w}, u4[4] = {hi.x, hi.y, hi.z, hi.w};
-              const float s0 = now.scale[b][m][0], s1 = now.scale[b][m][1];
+              const float s0 = sf[(b * kM + m) * 2], s1 = sf[(b * kM + m) * 2 + 1];
               float e[kN][4];
 #pragma unroll
               for (int j = 0; j < kN; ++j)
@@ -482,7 +495,7 @@ __global__ void __launch_bounds__(kThreads, Stage<kFp8, kRows, kTokens>::kCtas)
 #pragma unroll
                 for (int j = 0; j < kN; ++j)
                   if (j < used) {
-                    const uint4 v = now.x[b][j][k >> 1];
+                    const uint4 v = xv[j][k >> 1];
                     mma_16x8(e[j], a0, a1, a2, a3, k & 1 ? v.z : v.x, k & 1 ? v.w : v.y);
                   }
               }
@@ -497,7 +510,7 @@ __global__ void __launch_bounds__(kThreads, Stage<kFp8, kRows, kTokens>::kCtas)
 #pragma unroll
               for (int j = 0; j < kN; ++j)
                 if (j < used) {
-                  const uint4 v = now.x[b][j][0];
+                  const uint4 v = xv[j][0];
                   mma_16x8(d[m][j], lo.x, hi.x, lo.y, hi.y, v.x, v.y);
                   mma_16x8(d[m][j], lo.z, hi.z, lo.w, hi.w, v.z, v.w);
                 }
@@ -507,7 +520,6 @@ __global__ void __launch_bounds__(kThreads, Stage<kFp8, kRows, kTokens>::kCtas)
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_addr(&s_empty[at.stage]));
         at.next(stages);
-        now = next;
       }
       // the eight warps' sums, in their order: a warp takes a tile of 16 x 8 of them
 #pragma unroll
@@ -660,6 +672,7 @@ cudaError_t launch_both(const LayerArgs& a, int num_sms, cudaStream_t stream) {
 
 template <bool kFp8>
 cudaError_t launch_typed(const LayerArgs& a, int num_sms, cudaStream_t stream) {
+  if (a.T <= 4) return launch_both<kFp8, 16, 4>(a, num_sms, stream);
   if (a.T <= 8) return launch_both<kFp8, 16, 8>(a, num_sms, stream);
   // tokens to a group: most experts' tokens are one group
   return 2 * a.T * a.K <= 21 * a.E ? launch_both<kFp8, 32, 16>(a, num_sms, stream) : launch_both<kFp8, 32, 32>(a, num_sms, stream);
