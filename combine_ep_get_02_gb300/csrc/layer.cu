@@ -22,8 +22,7 @@ namespace ep {
 
 namespace {
 
-constexpr int kWorkers = 8;
-constexpr int kMaxStages = 32;
+constexpr int kMaxStages = 48;
 constexpr int kMaxLanes = kLayerMaxTokens * kMaxTopk;
 
 // A group: the tokens (at most kTokens) that go to one expert, `n` of them at `start` in the lists.
@@ -216,26 +215,31 @@ struct Plan {
   uint32_t token, weight, groups, sums, acc, ring, stages, total;
 };
 
-// A stage: matrix rows in columns of 128 bytes a row, as TMA writes them with the 128-byte swizzle. Its size
-// bounds the tokens' values that a worker's threads hold beside it (at most 64 registers).
-template <bool kFp8, int kRows, int kTokens>
-struct Stage {
-  static constexpr int kBytes = kRows == 16 || (kFp8 && kTokens == 32) ? 4096 : 8192;
+// A kernel's shape. kSmall: for little work, with both kernels' CTAs on an SM together, so that the second has its
+// lists and first stages ready when the first ends (64 experts' strips of 1024 x 512 a token: 12.2 instead
+// of 13.5 us); with more work the ring gets the whole SM (8 experts of 7168 x 2048: 110 instead of 123 us).
+// A stage is matrix rows in columns of 128 bytes a row, as TMA writes them with the 128-byte swizzle. Its size
+// bounds the tokens' values that a worker's threads hold beside it; a loader takes about 330 cycles for
+// a copy, most of them for its wait, so that 4 KB ones would take four loaders (one: 207 us instead of 127).
+template <bool kFp8_, int kRows_, int kTokens_, bool kSmall>
+struct Shape {
+  static constexpr bool kFp8 = kFp8_;
+  static constexpr int kRows = kRows_, kTokens = kTokens_;     // of a strip, of a group at most
+  static constexpr int kWorkers = kFp8 && kRows == 16 && !kSmall ? 12 : 8;
+  static constexpr int kLoaders = kFp8 && kRows == 16 && !kSmall ? 3 : 2;  // that take the stages in turn
+  static constexpr int kEpilogue = kSmall || kTokens == 32 || (kFp8 && kRows == 16) ? 1 : 2;  // warps that take the units in turn
+  static constexpr int kBytes = kFp8 && kSmall ? 4096 : 8192;
   static constexpr int kBoxes = kBytes / (kRows * 128);        // columns of 128 bytes
   static constexpr int kColumns = kBoxes * (kFp8 ? 128 : 64);  // of the summed index
   static constexpr int kPieces = 2 * kBoxes;                   // of 64 bytes a row
   static constexpr int kM = kRows / 16, kN = kTokens / 8;
-  // Few tokens: both kernels' CTAs fit an SM together, so that the second has its lists and first stages ready
-  // when the first ends. With more there is more to do, and the ring gets the whole SM.
-  static constexpr int kCtas = kTokens <= 8 ? 2 : 1;
-  static constexpr int kEpilogue = kRows == 16 ? 1 : 4;        // warps
-  static constexpr int kSlots = kTokens == 32 ? 2 : 4;          // strips whose sums may wait for them
-  static constexpr int kThreads = (kWorkers + 1 + kEpilogue) * 32;
+  static constexpr int kCtas = kSmall ? 2 : 1;
+  static constexpr int kSlots = kRows == 32 ? 2 : 4;           // strips whose sums may wait for each of them
+  static constexpr int kThreads = (kWorkers + kLoaders + kEpilogue) * 32;
 };
 
-template <bool kFp8, int kRows, int kTokens>
+template <class S>
 Plan plan_of(int T, int K, int E) {
-  using S = Stage<kFp8, kRows, kTokens>;
   const uint32_t lanes = static_cast<uint32_t>(T) * K;
   auto up = [](uint32_t n) { return (n + 127u) & ~127u; };
   Plan p;
@@ -243,13 +247,13 @@ Plan plan_of(int T, int K, int E) {
   p.weight = up(lanes * 2);
   p.groups = p.weight + up(lanes * 4);
   p.sums = p.groups + up(lanes * 4);
-  p.acc = p.sums + S::kSlots * kWorkers * S::kM * S::kN * 512;
-  p.ring = (p.acc + static_cast<uint32_t>(T) * kRows * 4 + 1023u) & ~1023u;
+  p.acc = p.sums + S::kEpilogue * S::kSlots * S::kWorkers * S::kM * S::kN * 512;
+  p.ring = (p.acc + static_cast<uint32_t>(T) * S::kRows * S::kEpilogue * 4 + 1023u) & ~1023u;
   const uint32_t room = (S::kCtas == 2 ? 111u : 224u) * 1024u;  // of 113 or 227 KB, static memory among it
   // As many to each worker, so that it is always the same one's: a worker that waits for a stage has then
   // itself emptied it before, and a barrier is never two phases behind what is waited for.
-  p.stages = room > p.ring ? (room - p.ring) / S::kBytes / kWorkers * kWorkers : 0;
-  if (p.stages > kMaxStages) p.stages = kMaxStages;
+  p.stages = room > p.ring ? (room - p.ring) / S::kBytes / S::kWorkers * S::kWorkers : 0;
+  if (p.stages > kMaxStages) p.stages = kMaxStages / S::kWorkers * S::kWorkers;
   uint32_t ring = p.stages * S::kBytes;
   const uint32_t scratch = (2 * lanes + 2 * static_cast<uint32_t>(E)) * 4;  // of the lists, before the ring is used
   if (ring < scratch) ring = scratch;
@@ -257,20 +261,22 @@ Plan plan_of(int T, int K, int E) {
   return p;
 }
 
-// kDown: the second kernel. kRows: matrix rows of a strip, kTokens: of a group at most.
-template <bool kFp8, bool kDown, int kRows, int kTokens>
-__global__ void __launch_bounds__((Stage<kFp8, kRows, kTokens>::kThreads), (Stage<kFp8, kRows, kTokens>::kCtas))
+// kDown: the second kernel.
+template <class S, bool kDown>
+__global__ void __launch_bounds__(S::kThreads, S::kCtas)
     layer_kernel(const __grid_constant__ CUtensorMap matrices, LayerArgs a, Plan p, int whole) {
-  using S = Stage<kFp8, kRows, kTokens>;
+  constexpr bool kFp8 = S::kFp8;
+  constexpr int kRows = S::kRows, kTokens = S::kTokens;
   constexpr int kM = S::kM, kN = S::kN, kHalves = kFp8 ? 2 : 1;
   constexpr int kColumns = S::kColumns, kPieces = S::kPieces, kStageBytes = S::kBytes, kSlots = S::kSlots;
   constexpr int kPiece = kFp8 ? 64 : 32;  // columns of 64 bytes of a matrix row
-  constexpr int kThreads = S::kThreads;
+  constexpr int kThreads = S::kThreads, kWorkers = S::kWorkers, kLoaders = S::kLoaders;
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ __align__(8) uint64_t s_full[kMaxStages], s_empty[kMaxStages];     // of the stages
-  __shared__ __align__(8) uint64_t s_strip_full[kSlots], s_strip_empty[kSlots];  // of the strips' sums
+  // of the strips' sums: every epilogue warp has its own, so that each barrier has one that waits for it, in order
+  constexpr int kEpilogue = S::kEpilogue;
+  __shared__ __align__(8) uint64_t s_strip_full[kEpilogue * kSlots], s_strip_empty[kEpilogue * kSlots];
   __shared__ volatile int s_abort;
-  __shared__ bool s_last;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int stages = static_cast<int>(p.stages);
 
@@ -288,9 +294,9 @@ __global__ void __launch_bounds__((Stage<kFp8, kRows, kTokens>::kThreads), (Stag
       mbar_init_count(smem_addr(&s_full[i]), 1);
       mbar_init_count(smem_addr(&s_empty[i]), 1);
     }
-    for (int i = 0; i < kSlots; ++i) {
+    for (int i = 0; i < kEpilogue * kSlots; ++i) {
       mbar_init_count(smem_addr(&s_strip_full[i]), kWorkers);
-      mbar_init_count(smem_addr(&s_strip_empty[i]), S::kEpilogue);
+      mbar_init_count(smem_addr(&s_strip_empty[i]), 1);
     }
     s_abort = 0;
     fence_barrier_init();
@@ -302,21 +308,22 @@ __global__ void __launch_bounds__((Stage<kFp8, kRows, kTokens>::kThreads), (Stag
   pdl_launch_dependents();
   const Lists lists = {reinterpret_cast<uint16_t*>(smem + p.token), reinterpret_cast<float*>(smem + p.weight),
                        reinterpret_cast<uint32_t*>(smem + p.groups)};
-  float* acc_out = reinterpret_cast<float*>(smem + p.acc);  // [T][kRows]
   if constexpr (kDown)
-    for (int i = threadIdx.x; i < a.T * kRows; i += kThreads) acc_out[i] = 0.f;
+    for (int i = threadIdx.x; i < a.T * kRows * S::kEpilogue; i += kThreads) reinterpret_cast<float*>(smem + p.acc)[i] = 0.f;
   const int groups = build_lists<kThreads>(a, kTokens, lists, reinterpret_cast<uint32_t*>(smem + p.ring),
                                            !kDown && blockIdx.x == 0 ? a.err : nullptr);
   fence_async_shared();  // the lists' scratch was where the ring is
   __syncthreads();
 
   // Down: a tile's groups are split in `split` parts where that evens the SMs' work out; the parts'
-  // sums are added by the last to finish. By the device's SMs, so that results do not depend on num_sms.
+  // sums are added by the last to finish. In bytes of matrices, with what a unit's end costs beside them: a
+  // part's, with its fence and atomic, about 20 KB; by the device's SMs, so that results do not depend on num_sms.
   int split = 1;
   if constexpr (kDown) {
-    int best = (tiles + a.device_sms - 1) / a.device_sms * groups;
+    const int64_t bytes = static_cast<int64_t>(kRows) * sum * (kFp8 ? 1 : 2);
+    int64_t best = (tiles + a.device_sms - 1) / a.device_sms * (groups * bytes + 4096);
     for (int s = 2; s <= min(kLayerMaxSplit, groups); ++s) {
-      const int cost = (tiles * s + a.device_sms - 1) / a.device_sms * ((groups + s - 1) / s);
+      const int64_t cost = (static_cast<int64_t>(tiles) * s + a.device_sms - 1) / a.device_sms * ((groups + s - 1) / s * bytes + 20480);
       if (cost < best) best = cost, split = s;
     }
   }
@@ -326,6 +333,7 @@ __global__ void __launch_bounds__((Stage<kFp8, kRows, kTokens>::kThreads), (Stag
   struct Cursor {
     int64_t u;
     int tile, part, g, end;
+    int turn = 0;  // the unit's epilogue warp
   };
   auto enter = [&](Cursor& c) {
     if (c.u >= units) return;
@@ -337,8 +345,10 @@ __global__ void __launch_bounds__((Stage<kFp8, kRows, kTokens>::kThreads), (Stag
   auto advance = [&](Cursor& c) {
     if (++c.g < c.end) return;
     c.u += gridDim.x;
+    if (kEpilogue > 1) c.turn ^= 1;
     enter(c);
   };
+  static_assert(kEpilogue <= 2, "turns");
   auto give_up = [&] {
     if (s_abort == 0) atomicOr(a.err, kErrTimeout);
     s_abort = 1;
@@ -355,7 +365,9 @@ __global__ void __launch_bounds__((Stage<kFp8, kRows, kTokens>::kThreads), (Stag
   // pieces that 8 threads read at once lie in different banks.
   const int t = lane & 3, r8 = lane >> 2, row8 = r8 >> 1 | (r8 & 1) << 2;
 
-  if (warp == kWorkers) {  // matrix rows: one thread, one copy a stage; what lies outside a matrix reads as zero
+  // Matrix rows: one thread of a loader warp, one copy a stage (of every kLoaders-th stage); what lies outside
+  // a matrix reads as zero. A copy takes this thread about 330 cycles, most of them for the wait.
+  if (warp >= kWorkers && warp < kWorkers + kLoaders) {
     if (elect_one() && groups > 0) {
       Place at;
       uint32_t n = 0;
@@ -364,7 +376,8 @@ __global__ void __launch_bounds__((Stage<kFp8, kRows, kTokens>::kThreads), (Stag
         const Group q = unpack_group(lists.groups[cur.g]);
         const int plane = gated ? 2 * q.expert : q.expert, row = cur.tile * strip;
         for (int step = 0; step < steps; ++step, at.next(stages), ++n) {
-          if (s_abort != 0 || !wait_stage(smem_addr(&s_empty[at.stage]), at.phase ^ 1u)) {
+          if (kLoaders > 1 && n % kLoaders != static_cast<uint32_t>(warp - kWorkers)) continue;
+          if (!wait_stage(smem_addr(&s_empty[at.stage]), at.phase ^ 1u)) {
             give_up();
             ok = false;
             break;
@@ -382,7 +395,8 @@ __global__ void __launch_bounds__((Stage<kFp8, kRows, kTokens>::kThreads), (Stag
       }
       if (!ok)  // the copies in flight end before the CTA does
         for (uint32_t m = n - min(n, p.stages); m < n; ++m)
-          mbar_wait_timed<false>(smem_addr(&s_full[m % p.stages]), m / p.stages & 1u);
+          if (kLoaders == 1 || m % kLoaders == static_cast<uint32_t>(warp - kWorkers))
+            mbar_wait_timed<false>(smem_addr(&s_full[m % p.stages]), m / p.stages & 1u);
     }
     if constexpr (kDown) pdl_wait();  // no CTA of this kernel ends before the first kernel
     return;
@@ -395,148 +409,179 @@ __global__ void __launch_bounds__((Stage<kFp8, kRows, kTokens>::kThreads), (Stag
     const float* const scales = kDown ? a.down_sf : a.up_sf;
     const int scale_rows = (z_rows + 127) >> 7, scale_columns = sum >> 7;
     const int lo_step = gated ? 8 : 16, hi_at = gated ? kRows / 2 : 8;  // rows of the strip: lo_step m + (0 or hi_at) + row8
-    int step = warp, stage = warp;
-    uint32_t phase = 0, strips = 0;
-    for (; cur.u < units; advance(cur), ++strips, step -= steps) {
-      const uint32_t slot = strips % kSlots;
-      if (step >= steps) {  // none of this strip's stages; every worker keeps pace with the strips' barriers all the same
-        wait_for(&s_strip_empty[slot], (strips / kSlots & 1u) ^ 1u);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_addr(&s_strip_full[slot]));
-        continue;
-      }
-      const int first = step;
-      const Group q = unpack_group(lists.groups[cur.g]);
-      // tiles of 8 tokens; of two both are computed, as that costs less than asking
-      const int used = kN > 2 ? (q.n + 15) >> 4 << 1 : kN;
-      const uint16_t* from[kN];  // this thread's tokens' rows (past the last token: the last's; nobody's results)
+    // What a stage's pieces meet: this thread's tokens' values (zeros behind the last column), and the scales.
+    struct Beside {
+      uint4 x[kPieces][kN][kHalves];
+      float scale[kFp8 ? kPieces / 2 : 1][kFp8 ? kM : 1][2];
+    };
+    const uint16_t* from[kN];  // of the strip that is fetched: this thread's tokens' rows (past the last token: the last's)
+    auto enter_strip = [&](const Cursor& c) {
+      const Group q = unpack_group(lists.groups[c.g]);
 #pragma unroll
       for (int j = 0; j < kN; ++j) {
         const int i = q.start + min(j * 8 + r8, q.n - 1);
         from[j] = x + static_cast<int64_t>(kDown ? i : lists.token[i]) * sum + t * (kFp8 ? 16 : 8);
       }
-      float d[kM][kN][4];
+    };
+    auto fetch = [&](const Cursor& c, int step, Beside& b) {
+      const int c0 = step * kColumns;
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i) {
+        const int column = c0 + i * kPiece;
+        const bool in = kFp8 ? column < sum : column + t * 8 < sum;
+#pragma unroll
+        for (int j = 0; j < kN; ++j)
+#pragma unroll
+          for (int h = 0; h < kHalves; ++h) {
+            b.x[i][j][h] = make_uint4(0u, 0u, 0u, 0u);
+            if (in) b.x[i][j][h] = __ldcg(reinterpret_cast<const uint4*>(from[j] + column + h * 8));
+          }
+      }
+      if constexpr (kFp8) {
+        const int expert = unpack_group(lists.groups[c.g]).expert;
+#pragma unroll
+        for (int m = 0; m < kM; ++m)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int row = c.tile * strip + (gated ? m * 8 + h * a.I : m * 16 + h * 8);
+            const float* sf = scales + (static_cast<int64_t>(expert) * scale_rows + (row >> 7)) * scale_columns;
+#pragma unroll
+            for (int i = 0; i < kPieces / 2; ++i) {
+              const int k = (c0 >> 7) + i;
+              b.scale[i][m][h] = k < scale_columns ? __ldg(sf + k) : 0.f;
+            }
+          }
+      }
+    };
+    int step = warp, stage = warp;
+    uint32_t phase = 0, strips[2] = {0, 0};  // for each epilogue warp
+    // This worker's share of a strip's sums, if it has one; every worker keeps pace with the strips' barriers.
+    auto leave_strip = [&](int turn, auto put) {
+      const uint32_t count = turn ? strips[1] : strips[0], slot = turn * kSlots + count % kSlots;
+      wait_for(&s_strip_empty[slot], (count / kSlots & 1u) ^ 1u);
+      put(all_sums + slot * kWorkers * (kM * kN * 32) + lane);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(&s_strip_full[slot]));
+      if (turn) ++strips[1];
+      else ++strips[0];
+    };
+    const auto nothing = [](float4*) {};
+    for (; cur.u < units && step >= steps; step -= steps, advance(cur)) leave_strip(cur.turn, nothing);
+    if (cur.u >= units) return;
+    int first = step;
+    float d[kM][kN][4];
+    auto clear = [&] {
 #pragma unroll
       for (int m = 0; m < kM; ++m)
 #pragma unroll
         for (int j = 0; j < kN; ++j)
 #pragma unroll
           for (int i = 0; i < 4; ++i) d[m][j][i] = 0.f;
-      for (; step < steps; step += kWorkers) {
-        // the tokens' values (and scales) of the stage, while its matrix rows are on their way
-        const int c0 = step * kColumns;
-        uint4 xv[kPieces][kN][kHalves];
-        float sf[kFp8 ? kPieces / 2 : 1][kFp8 ? kM : 1][2];
+    };
+    clear();
+    enter_strip(cur);
+    while (cur.u < units) {
+      const Group q = unpack_group(lists.groups[cur.g]);
+      // tiles of 8 tokens; of two both are computed, as that costs less than asking
+      const int used = kN > 2 ? (q.n + 15) >> 4 << 1 : kN;
+      const int c0 = step * kColumns;
+      Beside b;
+      fetch(cur, step, b);  // while the matrix rows are on their way
+      Cursor then = cur;
+      int passed = 0;
+      for (step += kWorkers; step >= steps && then.u < units; step -= steps, ++passed) advance(then);
+      wait_for(&s_full[stage], phase);
+      __syncwarp();
+      const uint8_t* rows = ring + stage * kStageBytes + row8 * 128;
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i) {
-          const int column = c0 + i * kPiece;
-          const bool in = kFp8 ? column < sum : column + t * 8 < sum;
+      for (int i = 0; i < kPieces; ++i) {
+        if (c0 + i * kPiece >= sum) break;
+        const uint8_t* piece = rows + (i >> 1) * (kRows * 128) + ((((i & 1) << 2) + t) ^ row8) * 16;
 #pragma unroll
-          for (int j = 0; j < kN; ++j)
+        for (int m = 0; m < kM; ++m) {
+          const uint4 lo = *reinterpret_cast<const uint4*>(piece + m * lo_step * 128);
+          const uint4 hi = *reinterpret_cast<const uint4*>(piece + (m * lo_step + hi_at) * 128);
+          if constexpr (kFp8) {
+            const uint32_t l[4] = {lo.x, lo.y, lo.z, lo.w}, u4[4] = {hi.x, hi.y, hi.z, hi.w};
+            float e[kN][4];
 #pragma unroll
-            for (int h = 0; h < kHalves; ++h) {
-              xv[i][j][h] = make_uint4(0u, 0u, 0u, 0u);
-              if (j < used && in) xv[i][j][h] = __ldcg(reinterpret_cast<const uint4*>(from[j] + column + h * 8));
-            }
-        }
-        if constexpr (kFp8) {
+            for (int j = 0; j < kN; ++j)
 #pragma unroll
-          for (int i = 0; i < kPieces / 2; ++i)
+              for (int k = 0; k < 4; ++k) e[j][k] = 0.f;
 #pragma unroll
-            for (int m = 0; m < kM; ++m)
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const int row = cur.tile * strip + (gated ? m * 8 + h * a.I : m * 16 + h * 8), c = (c0 >> 7) + i;
-                sf[i][m][h] = c < scale_columns
-                                  ? __ldg(scales + (static_cast<int64_t>(q.expert) * scale_rows + (row >> 7)) * scale_columns + c)
-                                  : 0.f;
-              }
-        }
-        wait_for(&s_full[stage], phase);
-        __syncwarp();
-        const uint8_t* rows = ring + stage * kStageBytes + row8 * 128;
-#pragma unroll
-        for (int i = 0; i < kPieces; ++i) {
-          if (c0 + i * kPiece >= sum) break;
-          const uint8_t* piece = rows + (i >> 1) * (kRows * 128) + ((((i & 1) << 2) + t) ^ row8) * 16;
-#pragma unroll
-          for (int m = 0; m < kM; ++m) {
-            const uint4 lo = *reinterpret_cast<const uint4*>(piece + m * lo_step * 128);
-            const uint4 hi = *reinterpret_cast<const uint4*>(piece + (m * lo_step + hi_at) * 128);
-            if constexpr (kFp8) {
-              const uint32_t l[4] = {lo.x, lo.y, lo.z, lo.w}, u4[4] = {hi.x, hi.y, hi.z, hi.w};
-              float e[kN][4];
-#pragma unroll
-              for (int j = 0; j < kN; ++j)
-#pragma unroll
-                for (int k = 0; k < 4; ++k) e[j][k] = 0.f;
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                uint32_t a0, a1, a2, a3;
-                codes_to_bf16(l[k], a0, a2);
-                codes_to_bf16(u4[k], a1, a3);
-#pragma unroll
-                for (int j = 0; j < kN; ++j)
-                  if (j < used) {
-                    const uint4 v = xv[i][j][k >> 1];
-                    mma_16x8(e[j], a0, a1, a2, a3, k & 1 ? v.z : v.x, k & 1 ? v.w : v.y);
-                  }
-              }
-              const float s0 = sf[i >> 1][m][0], s1 = sf[i >> 1][m][1];
-#pragma unroll
-              for (int j = 0; j < kN; ++j) {
-                d[m][j][0] = fmaf(s0, e[j][0], d[m][j][0]);
-                d[m][j][1] = fmaf(s0, e[j][1], d[m][j][1]);
-                d[m][j][2] = fmaf(s1, e[j][2], d[m][j][2]);
-                d[m][j][3] = fmaf(s1, e[j][3], d[m][j][3]);
-              }
-            } else {
+            for (int k = 0; k < 4; ++k) {
+              uint32_t a0, a1, a2, a3;
+              codes_to_bf16(l[k], a0, a2);
+              codes_to_bf16(u4[k], a1, a3);
 #pragma unroll
               for (int j = 0; j < kN; ++j)
                 if (j < used) {
-                  const uint4 v = xv[i][j][0];
-                  mma_16x8(d[m][j], lo.x, hi.x, lo.y, hi.y, v.x, v.y);
-                  mma_16x8(d[m][j], lo.z, hi.z, lo.w, hi.w, v.z, v.w);
+                  const uint4 v = b.x[i][j][k >> 1];
+                  mma_16x8(e[j], a0, a1, a2, a3, k & 1 ? v.z : v.x, k & 1 ? v.w : v.y);
                 }
             }
+            const float s0 = b.scale[i >> 1][m][0], s1 = b.scale[i >> 1][m][1];
+#pragma unroll
+            for (int j = 0; j < kN; ++j) {
+              d[m][j][0] = fmaf(s0, e[j][0], d[m][j][0]);
+              d[m][j][1] = fmaf(s0, e[j][1], d[m][j][1]);
+              d[m][j][2] = fmaf(s1, e[j][2], d[m][j][2]);
+              d[m][j][3] = fmaf(s1, e[j][3], d[m][j][3]);
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < kN; ++j)
+              if (j < used) {
+                const uint4 v = b.x[i][j][0];
+                mma_16x8(d[m][j], lo.x, hi.x, lo.y, hi.y, v.x, v.y);
+                mma_16x8(d[m][j], lo.z, hi.z, lo.w, hi.w, v.z, v.w);
+              }
           }
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_addr(&s_empty[stage]));
-        if ((stage += kWorkers) >= stages) stage -= stages, phase ^= 1u;
       }
-      // this worker's share of the strip's sums
-      wait_for(&s_strip_empty[slot], (strips / kSlots & 1u) ^ 1u);
-      float4* sums = all_sums + (slot * kWorkers + first) * (kM * kN * 32) + lane;
-#pragma unroll
-      for (int m = 0; m < kM; ++m)
-#pragma unroll
-        for (int j = 0; j < kN; ++j)
-          if (j < used) sums[(m * kN + j) * 32] = make_float4(d[m][j][0], d[m][j][1], d[m][j][2], d[m][j][3]);
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_addr(&s_strip_full[slot]));
+      if (lane == 0) mbar_arrive(smem_addr(&s_empty[stage]));
+      if ((stage += kWorkers) >= stages) stage -= stages, phase ^= 1u;
+      if (passed > 0) {
+        leave_strip(cur.turn, [&](float4* sums) {
+#pragma unroll
+          for (int m = 0; m < kM; ++m)
+#pragma unroll
+            for (int j = 0; j < kN; ++j)
+              if (j < used)
+                sums[(first * kM * kN + m * kN + j) * 32] = make_float4(d[m][j][0], d[m][j][1], d[m][j][2], d[m][j][3]);
+        });
+        for (advance(cur); passed > 1; --passed, advance(cur)) leave_strip(cur.turn, nothing);
+        first = step;
+        clear();
+        if (then.u < units) enter_strip(then);
+      }
+      cur = then;
     }
     return;
   }
 
-  // ---- the epilogue warps: a strip's shares added in their order, 16 x 8 results a warp at a time
-  const int index = warp - kWorkers - 1, thread = index * 32 + lane;
-  auto epilogue_sync = [] {
-    if constexpr (S::kEpilogue == 1) __syncwarp();
-    else asm volatile("bar.sync 1, %0;" ::"n"(S::kEpilogue * 32) : "memory");
-  };
+  // ---- the epilogue warps: a strip's shares added in their order, 16 x 8 results at a time. They take the
+  // units (tiles) in turn, so that one ends a tile while another begins the next.
+  const int index = warp - kWorkers - kLoaders;
+  float* const acc_out = reinterpret_cast<float*>(smem + p.acc) + index * a.T * kRows;  // [T][kRows]
   if constexpr (kDown) pdl_wait();  // `out` may be what the first kernel reads
   uint32_t strips = 0;
-  while (cur.u < units) {
+  for (int turn = 0; cur.u < units; turn = turn + 1 == kEpilogue ? 0 : turn + 1) {
     const Cursor unit = cur;
+    if (turn != index) {
+      cur.u += gridDim.x;
+      enter(cur);
+      continue;
+    }
     for (; cur.u == unit.u && groups > 0; advance(cur), ++strips) {
       const Group q = unpack_group(lists.groups[cur.g]);
-      const uint32_t slot = strips % kSlots;
+      const uint32_t slot = index * kSlots + strips % kSlots;
       const float4* sums = all_sums + slot * kWorkers * (kM * kN * 32) + lane;
       wait_for(&s_strip_full[slot], strips / kSlots & 1u);
       __syncwarp();
 #pragma unroll
-      for (int i = index; i < kM * kN; i += S::kEpilogue) {
+      for (int i = 0; i < kM * kN; ++i) {
         const int m = i / kN, j = i - m * kN;
         if (j * 8 >= q.n) continue;
         float4 v = sums[i * 32];
@@ -587,16 +632,12 @@ __global__ void __launch_bounds__((Stage<kFp8, kRows, kTokens>::kThreads), (Stag
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_addr(&s_strip_empty[slot]));
-      if constexpr (kDown && S::kEpilogue > 1) epilogue_sync();  // a token's results pass from warp to warp
     }
-    if constexpr (!kDown) {
-      if (groups == 0) return;
-    } else {  // the tile's tokens: 8 results a thread
+    if constexpr (kDown) {  // the tile's tokens: 8 results a thread
       constexpr int kEights = kRows / 8;
-      epilogue_sync();
       bool finish = split == 1;
       if (split > 1) {
-        for (int i = thread; i < a.T * kEights; i += S::kEpilogue * 32) {
+        for (int i = lane; i < a.T * kEights; i += 32) {
           const int token = i / kEights, c = (i - token * kEights) * 8;
           if (unit.tile * kRows + c >= a.H) continue;
           const float* v = acc_out + token * kRows + c;
@@ -605,17 +646,15 @@ __global__ void __launch_bounds__((Stage<kFp8, kRows, kTokens>::kThreads), (Stag
           *reinterpret_cast<float4*>(to + 4) = *reinterpret_cast<const float4*>(v + 4);
         }
         __threadfence();
-        epilogue_sync();
-        if (thread == 0) {
-          s_last = atomicAdd(a.done + unit.tile, 1u) == static_cast<uint32_t>(split) - 1u;
-          if (s_last) a.done[unit.tile] = 0u;
-        }
-        epilogue_sync();
-        finish = s_last;
+        __syncwarp();
+        uint32_t before = 0;
+        if (lane == 0) before = atomicAdd(a.done + unit.tile, 1u);
+        finish = __shfl_sync(kFullMask, before, 0) == static_cast<uint32_t>(split) - 1u;
+        if (finish && lane == 0) a.done[unit.tile] = 0u;
         __threadfence();
       }
       if (finish) {
-        for (int i = thread; i < a.T * kEights; i += S::kEpilogue * 32) {
+        for (int i = lane; i < a.T * kEights; i += 32) {
           const int token = i / kEights, c = (i - token * kEights) * 8;
           if (unit.tile * kRows + c >= a.H) continue;
           float v[8];
@@ -625,6 +664,7 @@ __global__ void __launch_bounds__((Stage<kFp8, kRows, kTokens>::kThreads), (Stag
           } else {
 #pragma unroll
             for (int k = 0; k < 8; ++k) v[k] = 0.f;
+#pragma unroll 4
             for (int s = 0; s < split; ++s) {
               const float* from = a.part + (static_cast<int64_t>(s) * a.T + token) * a.H + unit.tile * kRows + c;
               const float4 l = __ldcg(reinterpret_cast<const float4*>(from)), h = __ldcg(reinterpret_cast<const float4*>(from + 4));
@@ -641,9 +681,9 @@ __global__ void __launch_bounds__((Stage<kFp8, kRows, kTokens>::kThreads), (Stag
           st16(a.out + at, pack8(v));
         }
       }
-      epilogue_sync();
-      for (int i = thread; i < a.T * kRows; i += S::kEpilogue * 32) acc_out[i] = 0.f;
-      epilogue_sync();
+      __syncwarp();
+      for (int i = lane; i < a.T * kRows; i += 32) acc_out[i] = 0.f;
+      __syncwarp();
       if (groups == 0) {
         cur.u += gridDim.x;
         enter(cur);
@@ -652,12 +692,14 @@ __global__ void __launch_bounds__((Stage<kFp8, kRows, kTokens>::kThreads), (Stag
   }
 }
 
-template <bool kFp8, bool kDown, int kRows, int kTokens>
+template <class S, bool kDown>
 cudaError_t launch_one(const LayerArgs& a, int num_sms, cudaStream_t stream) {
-  auto kern = layer_kernel<kFp8, kDown, kRows, kTokens>;
-  using S = Stage<kFp8, kRows, kTokens>;
-  const Plan p = plan_of<kFp8, kRows, kTokens>(a.T, a.K, a.E);
-  if (p.stages < kWorkers || resident_ctas(reinterpret_cast<const void*>(kern), S::kThreads, p.total) < 1) return cudaErrorInvalidConfiguration;
+  constexpr bool kFp8 = S::kFp8;
+  constexpr int kRows = S::kRows;
+  auto kern = layer_kernel<S, kDown>;
+  const Plan p = plan_of<S>(a.T, a.K, a.E);
+  if (p.stages < S::kWorkers || resident_ctas(reinterpret_cast<const void*>(kern), S::kThreads, p.total) < 1)
+    return cudaErrorInvalidConfiguration;
   // 16-bit elements (two codes each); gated, the gate rows and the others of an expert are planes of their own
   const bool gated = !kDown && a.act == EP_ACT_SWIGLU;
   const uint64_t columns = static_cast<uint64_t>(kDown ? a.I : a.H) / (kFp8 ? 2 : 1), rows = kDown ? a.H : a.I;
@@ -679,17 +721,26 @@ cudaError_t launch_one(const LayerArgs& a, int num_sms, cudaStream_t stream) {
   return launch_chained(kern, dim3(num_sms), dim3(S::kThreads), p.total, stream, map, a, p, whole);
 }
 
-template <bool kFp8, int kRows, int kTokens>
+template <class S>
 cudaError_t launch_both(const LayerArgs& a, int num_sms, cudaStream_t stream) {
-  const cudaError_t st = launch_one<kFp8, false, kRows, kTokens>(a, num_sms, stream);
-  return st != cudaSuccess ? st : launch_one<kFp8, true, kRows, kTokens>(a, num_sms, stream);
+  const cudaError_t st = launch_one<S, false>(a, num_sms, stream);
+  return st != cudaSuccess ? st : launch_one<S, true>(a, num_sms, stream);
 }
 
 template <bool kFp8>
 cudaError_t launch_typed(const LayerArgs& a, int num_sms, cudaStream_t stream) {
-  if (a.T <= 8) return launch_both<kFp8, 16, 8>(a, num_sms, stream);
-  // tokens to a group: most experts' tokens are one group
-  return 2 * a.T * a.K <= 21 * a.E ? launch_both<kFp8, 32, 16>(a, num_sms, stream) : launch_both<kFp8, 32, 32>(a, num_sms, stream);
+  if (a.T <= 8) {
+    // matrices that are read, at most: 600 KB an SM is where both shapes take as long
+    const int64_t lanes = static_cast<int64_t>(a.T) * a.K, experts = lanes < a.E ? lanes : a.E;
+    const int64_t bytes = experts * (static_cast<int64_t>(a.Z) + a.I) * a.H * (kFp8 ? 1 : 2);
+    if (bytes <= 614400ll * a.device_sms && plan_of<Shape<kFp8, 16, 8, true>>(a.T, a.K, a.E).stages >= 8)
+      return launch_both<Shape<kFp8, 16, 8, true>>(a, num_sms, stream);
+    return launch_both<Shape<kFp8, 16, 8, false>>(a, num_sms, stream);
+  }
+  // tokens to a group: most experts' tokens are one group (another group reads the matrix from L2 again)
+  if constexpr (!kFp8)
+    if (2 * a.T * a.K > 21 * a.E) return launch_both<Shape<kFp8, 32, 32, false>>(a, num_sms, stream);
+  return launch_both<Shape<kFp8, 32, 16, false>>(a, num_sms, stream);
 }
 
 }  // namespace
