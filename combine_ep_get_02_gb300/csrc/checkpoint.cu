@@ -21,6 +21,7 @@ __global__ void __launch_bounds__(kThreads) checkpoint_kernel(CheckpointArgs a) 
   pdl_launch_dependents();
   pdl_wait();
   build_prefix<kThreads>(a.groups, kDzRows, prefix, blockIdx.x == 0 ? a.err : nullptr);
+  const bool sectors = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;  // rows are whole ones, the tensor may begin inside one
   const int across = threadIdx.x % kAcross, down = threadIdx.x / kAcross;
   const int spans = (a.F + kSpan - 1) / kSpan, G = a.F >> 7;
   const int64_t units = static_cast<int64_t>(prefix[a.groups.E]) * spans;
@@ -30,35 +31,49 @@ __global__ void __launch_bounds__(kThreads) checkpoint_kernel(CheckpointArgs a) 
     const GroupRows rows = group_rows(a.groups, g);
     const int m0 = (tile - prefix[g]) * kDzRows, n = min(kDzRows, rows.count - m0);
     const bool in = col < a.F;  // the same for the 8 threads of a scale
+    constexpr int kRows = kDzRows / kDown;  // of a thread: all on their way before the first is used
+    const int64_t row0 = static_cast<int64_t>(rows.begin) + m0 + down, at0 = row0 * a.F + col;
+    const int64_t step = static_cast<int64_t>(kDown) * a.F;
+    if constexpr (kBack) {
+      uint4 q[kRows];
+      float s[kRows];
 #pragma unroll
-    for (int i = 0; i < kDzRows / kDown; ++i) {  // whole warps take part in the maxima
-      const int r = i * kDown + down;
-      const int64_t row = static_cast<int64_t>(rows.begin) + m0 + r, at = row * a.F + col;
-      const bool there = in && r < n;
-      if constexpr (kBack) {
-        if (there) {
-          const uint4 q = ld_stream16(static_cast<const uint8_t*>(a.in) + at);
-          const float s = load_scale(a.sf, row, col >> 7, G, a.sf_pack);
+      for (int i = 0; i < kRows; ++i)
+        if (in && i * kDown + down < n) {
+          q[i] = ld_stream16(static_cast<const uint8_t*>(a.in) + at0 + i * step);
+          s[i] = load_scale(a.sf, row0 + i * kDown, col >> 7, G, a.sf_pack);
+        }
+#pragma unroll
+      for (int i = 0; i < kRows; ++i)
+        if (in && i * kDown + down < n) {
           float f[16];
-          e4m3x4_to_f32(q.x, f);
-          e4m3x4_to_f32(q.y, f + 4);
-          e4m3x4_to_f32(q.z, f + 8);
-          e4m3x4_to_f32(q.w, f + 12);
+          e4m3x4_to_f32(q[i].x, f);
+          e4m3x4_to_f32(q[i].y, f + 4);
+          e4m3x4_to_f32(q[i].z, f + 8);
+          e4m3x4_to_f32(q[i].w, f + 12);
 #pragma unroll
-          for (int k = 0; k < 16; ++k) f[k] *= s;
-          st16(static_cast<uint16_t*>(a.out) + at, pack8(f));
-          st16(static_cast<uint16_t*>(a.out) + at + 8, pack8(f + 8));
+          for (int k = 0; k < 16; ++k) f[k] *= s[i];
+          uint16_t* to = static_cast<uint16_t*>(a.out) + at0 + i * step;
+          if (sectors) st32(to, pack8(f), pack8(f + 8));
+          else st16(to, pack8(f)), st16(to + 8, pack8(f + 8));
         }
-      } else {
-        uint4 lo = make_uint4(0u, 0u, 0u, 0u), hi = lo;
-        if (there) {
-          lo = ld_stream16(static_cast<const uint16_t*>(a.in) + at);
-          hi = ld_stream16(static_cast<const uint16_t*>(a.in) + at + 8);
+    } else {
+      uint4 lo[kRows], hi[kRows];
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        lo[i] = hi[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (in && i * kDown + down < n) {
+          lo[i] = ld_stream16(static_cast<const uint16_t*>(a.in) + at0 + i * step);
+          hi[i] = ld_stream16(static_cast<const uint16_t*>(a.in) + at0 + i * step + 8);
         }
-        const CastUnit c = cast_unit(lo, hi, there, a.sf_pack);
+      }
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {  // whole warps take part in the maxima
+        const bool there = in && i * kDown + down < n;
+        const CastUnit c = cast_unit(lo[i], hi[i], there, a.sf_pack);
         if (there) {
-          st16(static_cast<uint8_t*>(a.out) + at, c.q);
-          if ((across & 7) == 0) store_scale(a.sf, row, col >> 7, G, RowScale{0.f, c.sf, c.sf_byte}, a.sf_pack);
+          st16(static_cast<uint8_t*>(a.out) + at0 + i * step, c.q);
+          if ((across & 7) == 0) store_scale(a.sf, row0 + i * kDown, col >> 7, G, RowScale{0.f, c.sf, c.sf_byte}, a.sf_pack);
         }
       }
     }

@@ -50,6 +50,13 @@ __device__ __forceinline__ float load_scale(const float* sf, int64_t row, int g,
   return e ? __uint_as_float(e << 23) : __uint_as_float(0x00400000u);  // 2^(e - 127)
 }
 
+// 32 bytes, 32-byte aligned: a whole sector, which two 16-byte stores write in two.
+__device__ __forceinline__ void st32(void* p, const uint4& a, const uint4& b) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w),
+               "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+               : "memory");
+}
+
 // Four codes -> four floats; exact.
 __device__ __forceinline__ void e4m3x4_to_f32(uint32_t w, float* f) {
 #pragma unroll
