@@ -846,7 +846,7 @@ def _alloc_headed(n: int, where: str, device) -> torch.Tensor:
 
 
 def alloc_norm_workspace(cfg: NormConfig, device="cuda") -> torch.Tensor:
-    """Workspace of ep_norm_grad: ep_norm_workspace_bytes(cfg) bytes."""
+    """Workspace of ep_norm_grad: ep_norm_workspace_bytes(cfg) bytes with a zeroed header."""
     return _alloc_headed(ep_norm_workspace_bytes(cfg), "ep_norm_workspace_bytes", device)
 
 

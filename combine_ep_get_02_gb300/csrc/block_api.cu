@@ -157,7 +157,7 @@ int ep_norm_grad(const ep_norm_config_t* cfg, const void* sum, const uint16_t* w
   const int sms = device_sm_count();
   if (sms <= 0) return EP_ERR_CUDA;
   const NormGradArgs a = {sum, weight, token_mask, d_y, d_sum, d_x, d_weight,
-                          d_weight == nullptr ? nullptr : at<float>(workspace, 256), cfg->rows, cfg->hidden, cfg->eps};
+                          d_weight == nullptr ? nullptr : at<float>(workspace, 256), at<uint32_t>(workspace, 0), cfg->rows, cfg->hidden, cfg->eps};
   return cuda_status(launch_norm_grad(a, cfg->x_dtype == EP_DTYPE_FP32, sms, s));
 }
 

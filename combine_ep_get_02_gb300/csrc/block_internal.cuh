@@ -33,6 +33,7 @@ struct NormGradArgs {
   void* d_x;                // may be null
   float* d_weight;          // may be null
   float* part;              // workspace [CTAs][H]
+  uint32_t* err;
   int64_t rows;
   int H;
   float eps;

@@ -9,6 +9,7 @@
 #include "block_internal.cuh"
 #include "fp8_rows.cuh"
 #include "product_common.cuh"
+#include "tensor_core.cuh"
 
 namespace ep {
 
@@ -293,6 +294,176 @@ __global__ void __launch_bounds__(threads_of<kV, kWarpRow, true>) norm_grad_kern
   }
 }
 
+// The same for many rows of more than 512 columns: one CTA to an SM takes its rows from a ring in shared
+// memory, which bulk copies of whole rows keep full, so that the next rows arrive while this one is added
+// up (65536 x 7168 with d_sum: REPLACE3 instead of 853 us for the kernel above, whose CTAs load and
+// add in turn). The one barrier of a row, for its sums, also says that the row before it is
+// used up, and the thread that sends for rows does so behind it.
+constexpr int kRingThreads = 512, kRingMax = 8;
+
+template <bool kFp32, int kV>
+__global__ void __launch_bounds__(kRingThreads, 1) norm_grad_ring_kernel(NormGradArgs a, int stages, uint32_t stage_bytes) {
+  extern __shared__ __align__(128) uint8_t ring[];
+  __shared__ float2 s_sum[2][kRingThreads / 32];
+  __shared__ float s_more[2][32];
+  __shared__ __align__(8) uint64_t s_full[kRingMax];
+  __shared__ volatile int s_abort;
+  constexpr uint32_t kSize = kFp32 ? 4 : 2;
+  const int at = threadIdx.x, lane = at & 31, warp = at >> 5, chunks = a.H >> 3;
+  const uint32_t row_bytes = a.H * kSize, y_bytes = a.H * 2;
+  const bool through = a.d_sum != nullptr && a.d_x != nullptr;
+  if (at == 0) {
+    for (int i = 0; i < stages; ++i) mbar_init_count(smem_addr(&s_full[i]), 1);
+    s_abort = 0;
+    fence_barrier_init();
+  }
+  pdl_launch_dependents();
+  pdl_wait();
+  __syncthreads();
+  // row, d_y, d_sum of one row; of a padding row nothing (but the barrier's phase passes)
+  auto send = [&](int64_t row, int stage) {
+    const uint32_t bar = smem_addr(&s_full[stage]), to = smem_addr(ring + stage * stage_bytes);
+    if (a.mask != nullptr && __ldg(a.mask + row) == 0) {
+      mbar_arrive(bar);
+      return;
+    }
+    mbar_expect(bar, row_bytes + y_bytes + (through ? row_bytes : 0));
+    auto copy = [&](uint32_t dst, const void* src, uint32_t bytes) {
+      asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                   "l"(src), "r"(bytes), "r"(bar)
+                   : "memory");
+    };
+    copy(to, static_cast<const uint8_t*>(a.sum) + row * row_bytes, row_bytes);
+    copy(to + row_bytes, a.d_y + row * a.H, y_bytes);
+    if (through) copy(to + row_bytes + y_bytes, static_cast<const uint8_t*>(a.d_sum) + row * row_bytes, row_bytes);
+  };
+  uint4 w[kV];
+  float dw[kV][8];
+#pragma unroll
+  for (int v = 0; v < kV; ++v) {
+    const int c = v * kRingThreads + at;
+    w[v] = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
+    if (c < chunks && a.weight != nullptr) w[v] = __ldg(reinterpret_cast<const uint4*>(a.weight + c * 8));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) dw[v][i] = 0.f;
+  }
+  if (at == 0)
+    for (int i = 0; i + 1 < stages; ++i)
+      if (const int64_t row = blockIdx.x + static_cast<int64_t>(i) * gridDim.x; row < a.rows) send(row, i);
+  int stage = 0, turn = 0;
+  uint32_t phase = 0;
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    const bool live = a.mask == nullptr || __ldg(a.mask + row) != 0;
+    // a wait that gives up is the last one: the results are incomplete, and reported
+    if (!mbar_try<false>(smem_addr(&s_full[stage]), phase) && s_abort == 0 && !mbar_wait_timed<false>(smem_addr(&s_full[stage]), phase)) {
+      if (s_abort == 0) atomicOr(a.err, kErrTimeout);
+      s_abort = 1;
+    }
+    const uint8_t* from = ring + stage * stage_bytes;
+    auto chunk = [&](const uint8_t* p, int c, float (&f)[8]) {
+      if constexpr (kFp32) {
+        const float4 l = *reinterpret_cast<const float4*>(p + c * 32), h = *reinterpret_cast<const float4*>(p + c * 32 + 16);
+        f[0] = l.x, f[1] = l.y, f[2] = l.z, f[3] = l.w, f[4] = h.x, f[5] = h.y, f[6] = h.z, f[7] = h.w;
+      } else {
+        unpack8(*reinterpret_cast<const uint4*>(p + c * 16), f);
+      }
+    };
+    auto y_chunk = [&](int c, float (&f)[8]) { unpack8(*reinterpret_cast<const uint4*>(from + row_bytes + c * 16), f); };
+    float ss = 0.f, ts = 0.f;
+    if (live) {
+#pragma unroll
+      for (int v = 0; v < kV; ++v) {
+        const int c = v * kRingThreads + at;
+        if (c >= chunks) break;
+        float s[8], y[8], g[8];
+        chunk(from, c, s);
+        y_chunk(c, y);
+        unpack8(w[v], g);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          ss = fmaf(s[i], s[i], ss);
+          ts = fmaf(y[i] * g[i], s[i], ts);
+        }
+      }
+    }
+    ss = warp_sum(ss);
+    ts = warp_sum(ts);
+    if (lane == 0) s_sum[turn][warp] = make_float2(ss, ts);
+    __syncthreads();
+    // the row before is used up by all: its stage may be filled again
+    if (at == 0) {
+      const int64_t next = row + static_cast<int64_t>(stages - 1) * gridDim.x;
+      if (next < a.rows && s_abort == 0) send(next, stage == 0 ? stages - 1 : stage - 1);
+    }
+    const float2 part = lane < kRingThreads / 32 ? s_sum[turn][lane] : make_float2(0.f, 0.f);
+    turn ^= 1;
+    ss = warp_sum(part.x);
+    ts = warp_sum(part.y);
+    float q = __frsqrt_rn(ss / a.H + a.eps), mean = ts * q / a.H;
+    if (live && (!(fabsf(ts) < INFINITY) || ss == INFINITY)) {  // the same for the whole CTA
+      if (ss == INFINITY) {
+        float small = 0.f;
+        for (int v = 0; v < kV; ++v) {
+          const int c = v * kRingThreads + at;
+          if (c >= chunks) break;
+          float s[8];
+          chunk(from, c, s);
+          for (int i = 0; i < 8; ++i) small = fmaf(s[i] * kShrink, s[i] * kShrink, small);
+        }
+        q = __frsqrt_rn(row_sum<false>(small, s_more[0]) / a.H) * kShrink;
+      }
+      float tn = 0.f;
+      for (int v = 0; v < kV; ++v) {
+        const int c = v * kRingThreads + at;
+        if (c >= chunks) break;
+        float s[8], y[8], g[8];
+        chunk(from, c, s);
+        y_chunk(c, y);
+        unpack8(w[v], g);
+        for (int i = 0; i < 8; ++i) tn = fmaf(y[i] * g[i], s[i] * q, tn);
+      }
+      mean = row_sum<false>(tn, s_more[1]) / a.H;
+      __syncthreads();  // before the next row that comes here writes there
+    }
+#pragma unroll
+    for (int v = 0; v < kV; ++v) {
+      const int c = v * kRingThreads + at;
+      if (c >= chunks) break;
+      float d[8] = {};
+      if (live) {
+        float s[8], y[8], g[8];
+        chunk(from, c, s);
+        y_chunk(c, y);
+        unpack8(w[v], g);
+        if (through) chunk(from + row_bytes + y_bytes, c, d);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float n = s[i] * q;
+          dw[v][i] = fmaf(y[i], n, dw[v][i]);
+          d[i] = fmaf(q, fmaf(-n, mean, y[i] * g[i]), d[i]);
+        }
+      }
+      if (a.d_x != nullptr) Eight<kFp32>::store(a.d_x, row * a.H + c * 8, d);
+    }
+    if (++stage == stages) stage = 0, phase ^= 1u;
+  }
+  if (at == 0 && s_abort != 0)  // copies in flight end before the CTA does
+    for (int i = 0; i < stages; ++i) {
+      mbar_wait_timed<false>(smem_addr(&s_full[i]), 0);
+      mbar_wait_timed<false>(smem_addr(&s_full[i]), 1);
+    }
+  if (a.part == nullptr) return;
+#pragma unroll
+  for (int v = 0; v < kV; ++v) {
+    const int c = v * kRingThreads + at;
+    if (c < chunks) {
+      float* to = a.part + static_cast<int64_t>(blockIdx.x) * a.H + c * 8;
+      *reinterpret_cast<float4*>(to) = make_float4(dw[v][0], dw[v][1], dw[v][2], dw[v][3]);
+      *reinterpret_cast<float4*>(to + 4) = make_float4(dw[v][4], dw[v][5], dw[v][6], dw[v][7]);
+    }
+  }
+}
+
 // d_weight: a CTA takes 32 columns; each of its 8 warps every 8th partial sum, then the warps in order.
 __global__ void __launch_bounds__(256) norm_weight_kernel(const float* part, int parts, int H, float* d_weight) {
   __shared__ float s_sum[8][32];
@@ -359,7 +530,19 @@ cudaError_t launch_norm_grad_typed(const NormGradArgs& a, int num_sms, cudaStrea
     return launch_rows(kernel, a, s, kNormGradCtas / s.rows, num_sms, &n, stream);
   };
   cudaError_t st;
-  if (s.warp_row) st = s.v == 1 ? go(norm_grad_kernel<kFp32, 1, true>) : go(norm_grad_kernel<kFp32, 2, true>);
+  const uint32_t stage_bytes = (static_cast<uint32_t>(a.H) * ((kFp32 ? 4 : 2) * (a.d_sum != nullptr ? 2 : 1) + 2) + 127u) & ~127u;
+  const int stages = static_cast<int>(min(216u * 1024u / stage_bytes, static_cast<uint32_t>(kRingMax)));
+  if (!s.warp_row && a.rows >= 2 * num_sms && stages >= 3) {
+    n = num_sms < kNormGradCtas ? num_sms : kNormGradCtas;
+    auto ring = [&](void (*kernel)(NormGradArgs, int, uint32_t)) {
+      const size_t smem = static_cast<size_t>(stages) * stage_bytes;
+      if (resident_ctas(reinterpret_cast<const void*>(kernel), kRingThreads, smem) < 1) return cudaErrorInvalidConfiguration;
+      return launch_chained(kernel, dim3(n), dim3(kRingThreads), smem, stream, a, stages, stage_bytes);
+    };
+    const int v = (a.H / 8 + kRingThreads - 1) / kRingThreads;
+    st = v <= 1 ? ring(norm_grad_ring_kernel<kFp32, 1>) : v <= 2 ? ring(norm_grad_ring_kernel<kFp32, 2>)
+                                                                 : ring(norm_grad_ring_kernel<kFp32, 4>);
+  } else if (s.warp_row) st = s.v == 1 ? go(norm_grad_kernel<kFp32, 1, true>) : go(norm_grad_kernel<kFp32, 2, true>);
   else if (s.v == 1) st = go(norm_grad_kernel<kFp32, 1, false>);
   else st = s.v == 2 ? go(norm_grad_kernel<kFp32, 2, false>) : go(norm_grad_kernel<kFp32, 4, false>);
   if (st != cudaSuccess || a.part == nullptr) return st;

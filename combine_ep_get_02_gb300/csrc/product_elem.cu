@@ -68,6 +68,9 @@ __global__ void __launch_bounds__(kThreads)
 // few thousand rows already occupy every SM evenly. Memory bounds it, with GELU the arithmetic:
 // 4096 x 4096 GELU 30 us (100 MB), 16384 x 1024 gated 29 us (168 MB, 5.8 TB/s).
 constexpr int kSpan = kDzColumns, kAcross = kSpan / 8, kDown = kThreads / kAcross;
+// Kept rows in a tile where there are so many that every CTA has several: a tile's column sums cost
+// about as much as the rows of half a small tile (65536 x 2 x 2048: 272 us with 64 rows, REPLACE2 with 256).
+constexpr int kKeptRows = 256;
 constexpr int kBiasWays = 8;  // orders the bias gradients' sums, here and in bias_sum_kernel
 
 struct DzArgs {
@@ -84,6 +87,7 @@ struct DzArgs {
   const float* z_sf = nullptr;     // ... with its scales
   int sf_pack = 0;
   uint16_t* h = nullptr;           // act(z) again; may be null
+  int tile_rows = kDzRows;         // of a tile; kept rows: kDzRows or kKeptRows
 };
 
 // Eight columns of a kept row as they lie in memory, with their scale.
@@ -173,7 +177,8 @@ __global__ void __launch_bounds__(kThreads, kKept ? 2 : 0) dz_kernel(DzArgs a) {
   __shared__ float s_sum[kDown][kHalves * kSpan];
   pdl_launch_dependents();
   pdl_wait();
-  build_prefix<kThreads>(a.groups, kDzRows, prefix, blockIdx.x == 0 ? a.err : nullptr);
+  const int tile_rows = kKept ? a.tile_rows : kDzRows;
+  build_prefix<kThreads>(a.groups, tile_rows, prefix, blockIdx.x == 0 ? a.err : nullptr);
   __shared__ bool s_last;
   const int across = threadIdx.x % kAcross, down = threadIdx.x / kAcross;
   const int spans = (a.N + kSpan - 1) / kSpan;
@@ -186,7 +191,7 @@ __global__ void __launch_bounds__(kThreads, kKept ? 2 : 0) dz_kernel(DzArgs a) {
     const int tile = static_cast<int>(u / spans), col = static_cast<int>(u - static_cast<int64_t>(tile) * spans) * kSpan + across * 8;
     const int g = group_of_tile(prefix, a.groups.E, tile);
     const GroupRows rows = group_rows(a.groups, g);
-    const int m0 = (tile - prefix[g]) * kDzRows, n = min(kDzRows, rows.count - m0);
+    const int m0 = (tile - prefix[g]) * tile_rows, n = min(tile_rows, rows.count - m0);
     const int64_t first = static_cast<int64_t>(rows.begin) + m0;
     float sum[kHalves * 8];
 #pragma unroll
@@ -199,53 +204,56 @@ __global__ void __launch_bounds__(kThreads, kKept ? 2 : 0) dz_kernel(DzArgs a) {
         // a thread's rows of the tile are all on their way before the first is used (one after the other: 385 us
         // instead of 281 for 65536 x 2 x 2048 gated)
         constexpr int kRows = kDzRows / kDown;
-        KeptEight zg[kRows], zu[kGated ? kRows : 1];
-        uint4 dv[kRows];
         const bool needs_z = kAct != EP_ACT_NONE || a.h != nullptr;
+#pragma unroll 1
+        for (int r0 = 0; r0 < n; r0 += kDzRows) {
+          KeptEight zg[kRows], zu[kGated ? kRows : 1];
+          uint4 dv[kRows];
 #pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-          const int r = i * kDown + down;
-          if (r >= n) break;
-          dv[i] = ld_stream16(a.d_out + (first + r) * a.N + col);
-          if (needs_z) zg[i].load(a, first + r, col);
-          if constexpr (kGated) zu[i].load(a, first + r, a.N + col);
-        }
-#pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-          const int64_t row = first + i * kDown + down;
-          if (i * kDown + down >= n) break;
-          const uint32_t dw[4] = {dv[i].x, dv[i].y, dv[i].z, dv[i].w};
-          uint32_t again[4], t[kHalves][4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const Two d = two_of_bf16(dw[k]);
-            if constexpr (kGated) {
-              Two v, g;
-              act_two<kAct>(two_of_kept(zg[i], k, two(zg[i].s, zg[i].s)), v, g);
-              const Two u = two_of_kept(zu[i], k, two(zu[i].s, zu[i].s));
-              const Two t0 = d * u * g, t1 = d * v;
-              again[k] = pack_two(v * u);
-              t[0][k] = pack_two(t0);
-              t[1][k] = pack_two(t1);
-              sum2[k] = sum2[k] + t0;
-              sum2[4 + k] = sum2[4 + k] + t1;
-            } else {
-              Two v = two(0.f, 0.f), t0 = d;
-              if (needs_z) {
-                Two g;
-                act_two<kAct>(two_of_kept(zg[i], k, two(zg[i].s, zg[i].s)), v, g);
-                if constexpr (kAct != EP_ACT_NONE) t0 = d * g;
-              }
-              again[k] = pack_two(v);
-              t[0][k] = pack_two(t0);
-              sum2[k] = sum2[k] + t0;
-            }
+          for (int i = 0; i < kRows; ++i) {
+            const int r = r0 + i * kDown + down;
+            if (r >= n) break;
+            dv[i] = ld_stream16(a.d_out + (first + r) * a.N + col);
+            if (needs_z) zg[i].load(a, first + r, col);
+            if constexpr (kGated) zu[i].load(a, first + r, a.N + col);
           }
-          if (a.h != nullptr) st16(a.h + row * a.N + col, make_uint4(again[0], again[1], again[2], again[3]));
-          if (a.dz != nullptr) {
 #pragma unroll
-            for (int h = 0; h < kHalves; ++h)
-              st16(a.dz + row * a.Z + h * a.N + col, make_uint4(t[h][0], t[h][1], t[h][2], t[h][3]));
+          for (int i = 0; i < kRows; ++i) {
+            const int64_t row = first + r0 + i * kDown + down;
+            if (r0 + i * kDown + down >= n) break;
+            const uint32_t dw[4] = {dv[i].x, dv[i].y, dv[i].z, dv[i].w};
+            uint32_t again[4], t[kHalves][4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const Two d = two_of_bf16(dw[k]);
+              if constexpr (kGated) {
+                Two v, g;
+                act_two<kAct>(two_of_kept(zg[i], k, two(zg[i].s, zg[i].s)), v, g);
+                const Two u = two_of_kept(zu[i], k, two(zu[i].s, zu[i].s));
+                const Two t0 = d * u * g, t1 = d * v;
+                again[k] = pack_two(v * u);
+                t[0][k] = pack_two(t0);
+                t[1][k] = pack_two(t1);
+                sum2[k] = sum2[k] + t0;
+                sum2[4 + k] = sum2[4 + k] + t1;
+              } else {
+                Two v = two(0.f, 0.f), t0 = d;
+                if (needs_z) {
+                  Two g;
+                  act_two<kAct>(two_of_kept(zg[i], k, two(zg[i].s, zg[i].s)), v, g);
+                  if constexpr (kAct != EP_ACT_NONE) t0 = d * g;
+                }
+                again[k] = pack_two(v);
+                t[0][k] = pack_two(t0);
+                sum2[k] = sum2[k] + t0;
+              }
+            }
+            if (a.h != nullptr) st16(a.h + row * a.N + col, make_uint4(again[0], again[1], again[2], again[3]));
+            if (a.dz != nullptr) {
+#pragma unroll
+              for (int h = 0; h < kHalves; ++h)
+                st16(a.dz + row * a.Z + h * a.N + col, make_uint4(t[h][0], t[h][1], t[h][2], t[h][3]));
+            }
           }
         }
 #pragma unroll
@@ -343,14 +351,14 @@ __global__ void __launch_bounds__(kThreads, kKept ? 2 : 0) dz_kernel(DzArgs a) {
 
 // d_bias_g = the sum over the group's row tiles: 32 columns a CTA, 8 ways of every 8th tile,
 // then the ways in order. (A thread for all tiles of a column took 18 us at 4096 rows.)
-__global__ void __launch_bounds__(kThreads) bias_sum_kernel(Groups q, int Z, const float* part, float* d_bias) {
+__global__ void __launch_bounds__(kThreads) bias_sum_kernel(Groups q, int tile_rows, int Z, const float* part, float* d_bias) {
   constexpr int kWays = kBiasWays;
   static_assert(kWays == kThreads / 32, "a warp a way");
   extern __shared__ int prefix[];
   __shared__ float s_sum[kWays][32];
   pdl_launch_dependents();
   pdl_wait();
-  build_prefix<kThreads>(q, kDzRows, prefix, nullptr);
+  build_prefix<kThreads>(q, tile_rows, prefix, nullptr);
   const int way = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int spans = (Z + 31) / 32;
   const int64_t units = static_cast<int64_t>(q.E) * spans;
@@ -378,8 +386,9 @@ cudaError_t launch_dz(DzArgs a, int num_sms, cudaStream_t stream) {
   const size_t smem = sizeof(int) * (static_cast<size_t>(a.groups.E) + 1);
   const int per_sm = resident_ctas(reinterpret_cast<const void*>(kern), kThreads, smem);
   if (per_sm < 1) return cudaErrorInvalidConfiguration;
-  const int64_t most = max_row_tiles(a.groups, kDzRows) * ((a.N + kSpan - 1) / kSpan);
-  const int64_t ctas = static_cast<int64_t>(num_sms) * per_sm;
+  const int64_t ctas = static_cast<int64_t>(num_sms) * per_sm, spans = (a.N + kSpan - 1) / kSpan;
+  if (kKept && max_row_tiles(a.groups, kKeptRows) * spans >= 8 * ctas) a.tile_rows = kKeptRows;
+  const int64_t most = max_row_tiles(a.groups, a.tile_rows) * spans;
   if (a.part == nullptr || most > ctas || a.groups.E * ((a.N + kSpan - 1) / kSpan) > kDzCounters) a.done = nullptr;
   const cudaError_t st = launch_chained(kern, dim3(static_cast<unsigned>(most < ctas ? most : ctas)), dim3(kThreads), smem, stream, a);
   if (st != cudaSuccess || a.part == nullptr || a.done != nullptr) return st;
@@ -388,7 +397,7 @@ cudaError_t launch_dz(DzArgs a, int num_sms, cudaStream_t stream) {
   const int64_t need = static_cast<int64_t>(a.groups.E) * ((a.Z + 31) / 32);
   const int64_t sum_ctas = static_cast<int64_t>(num_sms) * sum_per_sm;
   return launch_chained(bias_sum_kernel, dim3(static_cast<unsigned>(need < sum_ctas ? need : sum_ctas)), dim3(kThreads),
-                        smem, stream, a.groups, a.Z, static_cast<const float*>(a.part), a.d_bias);
+                        smem, stream, a.groups, a.tile_rows, a.Z, static_cast<const float*>(a.part), a.d_bias);
 }
 
 }  // namespace

@@ -484,8 +484,9 @@ typedef struct ep_norm_config {
 int ep_norm(const ep_norm_config_t* cfg, const void* x, const void* residual, const uint16_t* weight, void* sum,
             uint16_t* y, uint8_t* codes, float* sf, void* stream);
 
-/* Workspace bytes of ep_norm_grad (0 for an invalid configuration); nothing in it has to be
- * initialised. One stream at a time. */
+/* Workspace bytes of ep_norm_grad (0 for an invalid configuration). Its 256-byte header is zero-filled
+ * once before first use; one stream at a time; errors (a bounded wait that gave up) are read by
+ * ep_check_error. */
 size_t ep_norm_workspace_bytes(const ep_norm_config_t* cfg);
 
 /* Gradients for d_y (bf16 [rows][H]), from the kept sum: with q = 1 / sqrt(mean s^2 + eps),
