@@ -294,7 +294,7 @@ __global__ void __launch_bounds__(threads_of<kV, kWarpRow, true>) norm_grad_kern
   }
 }
 
-// The same for many rows of more than 512 columns: one CTA to an SM takes its rows from a ring in shared
+// The same for many rows of more than 512 columns: the CTAs, 512 threads of them to an SM, take their rows from rings in shared
 // memory, which bulk copies of whole rows keep full, so that the next rows arrive while this one is added
 // up (65536 x 7168 with d_sum: REPLACE3 instead of 853 us for the kernel above, whose CTAs load and
 // add in turn). The one barrier of a row, for its sums, also says that the row before it is
@@ -309,7 +309,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) norm_grad_ring_kernel(NormGra
   __shared__ __align__(8) uint64_t s_full[kRingMax];
   __shared__ volatile int s_abort;
   constexpr uint32_t kSize = kFp32 ? 4 : 2;
-  const int at = threadIdx.x, lane = at & 31, warp = at >> 5, chunks = a.H >> 3;
+  const int at = threadIdx.x, across = blockDim.x, lane = at & 31, warp = at >> 5, chunks = a.H >> 3;
   const uint32_t row_bytes = a.H * kSize, y_bytes = a.H * 2;
   const bool through = a.d_sum != nullptr && a.d_x != nullptr;
   if (at == 0) {
@@ -341,7 +341,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) norm_grad_ring_kernel(NormGra
   float dw[kV][8];
 #pragma unroll
   for (int v = 0; v < kV; ++v) {
-    const int c = v * kRingThreads + at;
+    const int c = v * across + at;
     w[v] = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
     if (c < chunks && a.weight != nullptr) w[v] = __ldg(reinterpret_cast<const uint4*>(a.weight + c * 8));
 #pragma unroll
@@ -373,7 +373,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) norm_grad_ring_kernel(NormGra
     if (live) {
 #pragma unroll
       for (int v = 0; v < kV; ++v) {
-        const int c = v * kRingThreads + at;
+        const int c = v * across + at;
         if (c >= chunks) break;
         float s[8], y[8], g[8];
         chunk(from, c, s);
@@ -395,7 +395,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) norm_grad_ring_kernel(NormGra
       const int64_t next = row + static_cast<int64_t>(stages - 1) * gridDim.x;
       if (next < a.rows && s_abort == 0) send(next, stage == 0 ? stages - 1 : stage - 1);
     }
-    const float2 part = lane < kRingThreads / 32 ? s_sum[turn][lane] : make_float2(0.f, 0.f);
+    const float2 part = lane < across >> 5 ? s_sum[turn][lane] : make_float2(0.f, 0.f);
     turn ^= 1;
     ss = warp_sum(part.x);
     ts = warp_sum(part.y);
@@ -404,7 +404,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) norm_grad_ring_kernel(NormGra
       if (ss == INFINITY) {
         float small = 0.f;
         for (int v = 0; v < kV; ++v) {
-          const int c = v * kRingThreads + at;
+          const int c = v * across + at;
           if (c >= chunks) break;
           float s[8];
           chunk(from, c, s);
@@ -414,7 +414,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) norm_grad_ring_kernel(NormGra
       }
       float tn = 0.f;
       for (int v = 0; v < kV; ++v) {
-        const int c = v * kRingThreads + at;
+        const int c = v * across + at;
         if (c >= chunks) break;
         float s[8], y[8], g[8];
         chunk(from, c, s);
@@ -427,7 +427,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) norm_grad_ring_kernel(NormGra
     }
 #pragma unroll
     for (int v = 0; v < kV; ++v) {
-      const int c = v * kRingThreads + at;
+      const int c = v * across + at;
       if (c >= chunks) break;
       float d[8] = {};
       if (live) {
@@ -455,7 +455,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) norm_grad_ring_kernel(NormGra
   if (a.part == nullptr) return;
 #pragma unroll
   for (int v = 0; v < kV; ++v) {
-    const int c = v * kRingThreads + at;
+    const int c = v * across + at;
     if (c < chunks) {
       float* to = a.part + static_cast<int64_t>(blockIdx.x) * a.H + c * 8;
       *reinterpret_cast<float4*>(to) = make_float4(dw[v][0], dw[v][1], dw[v][2], dw[v][3]);
@@ -530,16 +530,19 @@ cudaError_t launch_norm_grad_typed(const NormGradArgs& a, int num_sms, cudaStrea
     return launch_rows(kernel, a, s, kNormGradCtas / s.rows, num_sms, &n, stream);
   };
   cudaError_t st;
+  // threads of a CTA of the ring's: a chunk of 8 columns each in rows of up to 4096
+  const int threads = a.H <= 1024 ? 128 : a.H <= 2048 ? 256 : kRingThreads, per_sm = kRingThreads / threads;
   const uint32_t stage_bytes = (static_cast<uint32_t>(a.H) * ((kFp32 ? 4 : 2) * (a.d_sum != nullptr ? 2 : 1) + 2) + 127u) & ~127u;
-  const int stages = static_cast<int>(min(216u * 1024u / stage_bytes, static_cast<uint32_t>(kRingMax)));
+  const int stages = static_cast<int>(min(216u / per_sm * 1024u / stage_bytes, static_cast<uint32_t>(kRingMax)));
   if (!s.warp_row && a.rows >= 2 * num_sms && stages >= 3) {
-    n = num_sms < kNormGradCtas ? num_sms : kNormGradCtas;
+    n = num_sms * per_sm < kNormGradCtas ? num_sms * per_sm : kNormGradCtas;
+    if (n > a.rows) n = static_cast<int>(a.rows);
     auto ring = [&](void (*kernel)(NormGradArgs, int, uint32_t)) {
       const size_t smem = static_cast<size_t>(stages) * stage_bytes;
-      if (resident_ctas(reinterpret_cast<const void*>(kernel), kRingThreads, smem) < 1) return cudaErrorInvalidConfiguration;
-      return launch_chained(kernel, dim3(n), dim3(kRingThreads), smem, stream, a, stages, stage_bytes);
+      if (resident_ctas(reinterpret_cast<const void*>(kernel), threads, smem) < 1) return cudaErrorInvalidConfiguration;
+      return launch_chained(kernel, dim3(n), dim3(threads), smem, stream, a, stages, stage_bytes);
     };
-    const int v = (a.H / 8 + kRingThreads - 1) / kRingThreads;
+    const int v = (a.H / 8 + threads - 1) / threads;
     st = v <= 1 ? ring(norm_grad_ring_kernel<kFp32, 1>) : v <= 2 ? ring(norm_grad_ring_kernel<kFp32, 2>)
                                                                  : ring(norm_grad_ring_kernel<kFp32, 4>);
   } else if (s.warp_row) st = s.v == 1 ? go(norm_grad_kernel<kFp32, 1, true>) : go(norm_grad_kernel<kFp32, 2, true>);
