@@ -12,8 +12,11 @@
 // With at most 32 tokens to a matrix the tensor cores are far from being the limit, so the products go
 // where their operands need least preparation: the fragments are read straight from rows as they
 // lie in memory (the summed index is permuted alike for both), and FP8 codes become bf16 on the way.
-// (Sharing each stage among the workers took 165 us where this takes REPLACE: a stage's bookkeeping then
+// (Sharing each stage among the workers took 165 us where this takes 136: a stage's bookkeeping then
 // comes eight times, and every stage waits for its slowest warp.)
+// Memory bounds it with bf16 matrices: 16 tokens on 16 experts of 4096 x 2048 136 us (805 MB, 5.9 TB/s), one token on 8
+// experts of 7168 x 2048 107 us (705 MB, 6.6 TB/s); with FP8 ones the codes' way to bf16, two instructions a code
+// and thread: 70 us (5.0 TB/s; 60 without the products).
 #include "block_internal.cuh"
 #include "fp8_rows.cuh"
 #include "product_common.cuh"
@@ -493,6 +496,9 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
       wait_for(&s_full[stage], phase);
       __syncwarp();
       const uint8_t* rows = ring + stage * kStageBytes + row8 * 128;
+      // Sums before their scale: of its 128 columns (two pieces) where the registers hold them, else of a piece.
+      constexpr bool kPair = kM == 1;
+      float e[kFp8 ? (kPair ? kM : 1) : 1][kFp8 ? kN : 1][4];
 #pragma unroll
       for (int i = 0; i < kPieces; ++i) {
         if (c0 + i * kPiece >= sum) break;
@@ -503,11 +509,12 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
           const uint4 hi = *reinterpret_cast<const uint4*>(piece + (m * lo_step + hi_at) * 128);
           if constexpr (kFp8) {
             const uint32_t l[4] = {lo.x, lo.y, lo.z, lo.w}, u4[4] = {hi.x, hi.y, hi.z, hi.w};
-            float e[kN][4];
+            if (!kPair || (i & 1) == 0) {
 #pragma unroll
-            for (int j = 0; j < kN; ++j)
+              for (int j = 0; j < kN; ++j)
 #pragma unroll
-              for (int k = 0; k < 4; ++k) e[j][k] = 0.f;
+                for (int k = 0; k < 4; ++k) e[kPair ? m : 0][j][k] = 0.f;
+            }
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               uint32_t a0, a1, a2, a3;
@@ -517,16 +524,18 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
               for (int j = 0; j < kN; ++j)
                 if (j < used) {
                   const uint4 v = b.x[i][j][k >> 1];
-                  mma_16x8(e[j], a0, a1, a2, a3, k & 1 ? v.z : v.x, k & 1 ? v.w : v.y);
+                  mma_16x8(e[kPair ? m : 0][j], a0, a1, a2, a3, k & 1 ? v.z : v.x, k & 1 ? v.w : v.y);
                 }
             }
-            const float s0 = b.scale[i >> 1][m][0], s1 = b.scale[i >> 1][m][1];
+            if (!kPair || (i & 1)) {  // columns come in whole 128s
+              const float s0 = b.scale[i >> 1][m][0], s1 = b.scale[i >> 1][m][1];
 #pragma unroll
-            for (int j = 0; j < kN; ++j) {
-              d[m][j][0] = fmaf(s0, e[j][0], d[m][j][0]);
-              d[m][j][1] = fmaf(s0, e[j][1], d[m][j][1]);
-              d[m][j][2] = fmaf(s1, e[j][2], d[m][j][2]);
-              d[m][j][3] = fmaf(s1, e[j][3], d[m][j][3]);
+              for (int j = 0; j < kN; ++j) {
+                d[m][j][0] = fmaf(s0, e[kPair ? m : 0][j][0], d[m][j][0]);
+                d[m][j][1] = fmaf(s0, e[kPair ? m : 0][j][1], d[m][j][1]);
+                d[m][j][2] = fmaf(s1, e[kPair ? m : 0][j][2], d[m][j][2]);
+                d[m][j][3] = fmaf(s1, e[kPair ? m : 0][j][3], d[m][j][3]);
+              }
             }
           } else {
 #pragma unroll

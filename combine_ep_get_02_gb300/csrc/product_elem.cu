@@ -69,7 +69,7 @@ __global__ void __launch_bounds__(kThreads)
 // 4096 x 4096 GELU 30 us (100 MB), 16384 x 1024 gated 29 us (168 MB, 5.8 TB/s).
 constexpr int kSpan = kDzColumns, kAcross = kSpan / 8, kDown = kThreads / kAcross;
 // Kept rows in a tile where there are so many that every CTA has several: a tile's column sums cost
-// about as much as the rows of half a small tile (65536 x 2 x 2048: 272 us with 64 rows, REPLACE2 with 256).
+// about as much as the rows of half a small tile (65536 x 2 x 2048: 272 us with 64 rows, 246 with 256).
 constexpr int kKeptRows = 256;
 constexpr int kBiasWays = 8;  // orders the bias gradients' sums, here and in bias_sum_kernel
 

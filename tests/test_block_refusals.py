@@ -139,3 +139,60 @@ def test_configs_copy_and_pickle(ep):
         cfg.rows = 64  # what was kept goes with the field
         assert cfg._sizes is None and cfg._c().rows == 64
     assert checkpoint_cfg(ep, activation=ep.EP_ACT_SWIGLU).out_features == 128
+
+
+def layer_cfg(ep, **kw):
+    return ep.LayerConfig(**{**dict(num_tokens=4, num_experts=8, num_topk=2, hidden=256, inner=128), **kw})
+
+
+@pytest.mark.parametrize("bad,code", [
+    (dict(num_tokens=-1), -1), (dict(num_tokens=65), -2), (dict(num_experts=0), -1), (dict(num_experts=4097), -2),
+    (dict(num_topk=0), -1), (dict(num_topk=33), -2), (dict(hidden=0), -1), (dict(hidden=12), -1), (dict(inner=4), -1),
+    (dict(hidden=1 << 21), -2), (dict(inner=1 << 21), -2), (dict(activation=5), -1), (dict(activation=-1), -1),
+    (dict(weight_dtype=2), -1), (dict(weight_dtype=1, hidden=136), -1), (dict(weight_dtype=1, inner=64), -1),
+    (dict(num_sms=-1), -1),
+])
+def test_layer_configs(ep, bad, code):
+    cfg = layer_cfg(ep, **bad)
+    assert ep.ep_layer_workspace_bytes(cfg) == 0
+    assert ep.lib().ep_expert_layer(C.byref(cfg._c()), *[None] * 12, 0, None) == code
+    with pytest.raises(ep.EpError):
+        ep.alloc_layer_workspace(cfg)
+
+
+def test_layer_arguments(ep):
+    L, cfg = ep.lib(), layer_cfg(ep)
+    n, c = ep.ep_layer_workspace_bytes(cfg), cfg._c()
+    assert n == 256 + up(4 * 16) + up(2 * 4 * 2 * 128) + up(4 * 8 * 4 * 256)
+    bad, odd, off = ep.EP_ERR_INVALID_ARG, P(0x40008), P(0x40002)
+
+    def call(x=A, idx=A, w=A, u=A, us=None, ub=None, d=A, ds=None, db=None, r=None, out=A, ws=WS, size=n, cc=c):
+        return L.ep_expert_layer(C.byref(cc), x, idx, w, u, us, ub, d, ds, db, r, out, ws, size, None)
+
+    assert call(ws=None) == call(size=n - 1) == call(ws=P(0x10010)) == ep.EP_ERR_WORKSPACE
+    assert call(x=None) == call(idx=None) == call(w=None) == call(u=None) == call(d=None) == call(out=None) == bad
+    assert call(us=A) == call(ds=A) == call(us=A, ds=A) == bad  # scales of bf16 matrices
+    fp8 = layer_cfg(ep, weight_dtype=1)._c()
+    assert call(cc=fp8, size=1 << 30) == call(us=A, cc=fp8, size=1 << 30) == call(ds=A, cc=fp8, size=1 << 30) == bad
+    for name in ("x", "u", "ub", "d", "db", "r", "out"):
+        assert call(**{name: odd}) == bad
+    assert call(idx=P(0x40004)) == call(w=off) == bad
+    assert call(us=off, ds=A, cc=fp8, size=1 << 30) == call(us=A, ds=off, cc=fp8, size=1 << 30) == bad
+    assert call(x=None, cc=layer_cfg(ep, num_tokens=0)._c()) == ep.EP_OK
+    assert L.ep_expert_layer(None, *[A] * 12, n, None) == bad
+
+
+def test_layer_tensors(ep):
+    """The binding refuses each tensor by name before the library is called."""
+    bf, cfg = torch.bfloat16, layer_cfg(ep)
+    x, idx, w = torch.empty(4, 256, dtype=bf), torch.zeros(4, 2, dtype=torch.int64), torch.empty(4, 2)
+    up_, down = torch.empty(8, 256, 256, dtype=bf), torch.empty(8, 256, 128, dtype=bf)
+    for bad, why in ((up_.float(), "float32"), (up_[:7], "elements"), (up_.transpose(1, 2), "contiguous"), (up_, "GPU"), (None, "missing")):
+        with pytest.raises(ep.EpError, match=f"ep_expert_layer: up .*{why}"):
+            ep.ep_expert_layer(cfg, x, idx, w, bad, None, None, down, None, None, None, x, None)
+    fp8 = layer_cfg(ep, weight_dtype=ep.EP_DTYPE_FP8_E4M3)
+    with pytest.raises(ep.EpError, match="up is torch.bfloat16"):
+        ep.ep_expert_layer(fp8, x, idx, w, up_, None, None, down, None, None, None, x, None)
+    assert fp8._needs()[3] == 8 * 2 * 2 and fp8.z_features == 256
+    cfg._ref(), cfg._needs()
+    assert pickle.loads(pickle.dumps(cfg)) == cfg and copy.copy(cfg)._sizes is None

@@ -139,7 +139,8 @@ def test_values_at_the_ends(ep, h):
 
 @pytest.mark.parametrize("kind", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
 @pytest.mark.parametrize("n,h", [(1, 8), (5, 256), (153, 264), (609, 512), (9, 520), (1, 4096), (700, 2048), (2, 4104),
-                                 (620, 7168), (3, 8192), (160, 8200), (1, 16384), (170, 16384)])
+                                 (620, 7168), (3, 8192), (160, 8200), (1, 16384), (170, 16384), (305, 520), (1300, 1024),
+                                 (2000, 1032), (306, 8200), (310, 16384)])
 def test_gradients(ep, n, h, kind):
     """d_x: two sums over the row (each ROW of the sum of its terms' magnitudes) and five roundings of
     terms: 2 ROW of their magnitudes, and its own rounding. d_weight: every term off by ROW, at most
@@ -189,6 +190,31 @@ def test_gradients_against_differences(ep):
         assert abs((d_x.double() * v).sum() - along) <= (size * v.abs()).sum() * 4 * ROW + 1e-6 * abs(along) + 1e-5
         along = (f(s, w.double() + step * u) - f(s, w.double() - step * u)) / (2 * step)
         assert abs((d_w.double() * u).sum() - along) <= (size_w * u.abs()).sum() * (ROW + 72 * 2.0 ** -24) + 1e-5
+
+
+@pytest.mark.parametrize("kind", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
+def test_values_at_the_ends_among_many_rows(ep, kind):
+    """The same through the rows' ring: large values, NaN and infinities stay in their rows; a padding row
+    between them is not read."""
+    n, h = 700, 2048
+    x = torch.randn(n, h, generator=gen(15), device="cuda")
+    x[5::16] *= 1e25
+    x[6::16] = 0
+    x = x.to(kind)
+    x[3::16, 9], x[4::16, 11] = torch.nan, torch.inf
+    mask = torch.ones(n, dtype=torch.bool, device="cuda")
+    mask[7::16] = False
+    x[7::16] = torch.nan
+    d_y = torch.randn(n, h, generator=gen(16), device="cuda").bfloat16()
+    cfg = config(ep, n, h, kind)
+    d_x, ws = torch.full_like(x, 7.0), ep.alloc_norm_workspace(cfg)
+    ep.ep_norm_grad(cfg, x, None, mask, d_y, None, d_x, None, ws)
+    i = torch.arange(n, device="cuda") % 16
+    sure = (i != 3) & (i != 4) & (i != 7)
+    want, _, size, _ = ref.norm_grad(x[sure], None, None, d_y[sure], None, EPS)
+    assert ((d_x[sure].double() - want).abs() <= want.abs() * ref.HALF[kind] + size * 4 * ROW + 2.0 ** -133).all()
+    assert d_x[3::16].isnan().all() and (d_x[7::16] == 0).all()
+    assert ep.ep_check_error(ws) == ep.EP_OK
 
 
 def test_no_rows(ep):
