@@ -66,16 +66,18 @@ int resident_ctas(const void* kernel, int threads, size_t smem) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return -1;
   std::lock_guard<std::mutex> lock(mu);
-  if (smem > 48 * 1024) {  // raise the kernel's limit when this launch needs more; never lower it
+  // Raise the kernel's limit when this launch needs more; never lower it. Without one the dynamic and the
+  // kernel's static memory (16 KB at most) share 48 KB.
+  if (const size_t limit = smem > 48 * 1024 ? smem : 48 * 1024; smem > 32 * 1024) {
     Limit* lim = nullptr;
     for (Limit& l : limits)
       if (l.kernel == kernel && l.device == dev) lim = &l;
-    if (lim == nullptr || lim->smem < smem) {
-      if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) !=
+    if (lim == nullptr || lim->smem < limit) {
+      if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(limit)) !=
           cudaSuccess)
         return -1;
-      if (lim == nullptr) limits.push_back({kernel, dev, smem});
-      else lim->smem = smem;
+      if (lim == nullptr) limits.push_back({kernel, dev, limit});
+      else lim->smem = limit;
     }
   }
   for (const Known& e : known)

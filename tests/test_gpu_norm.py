@@ -4,6 +4,10 @@ Error bounds. A sum over a row is taken in a thread's chain of at most 32 terms 
 pairwise steps: of squares (all positive) it is off by 42 * 2^-24 of itself, so q by 21 * 2^-24, with its
 own rounding, eps' addition, s and the two products below 40 * 2^-24: ROW. A rounding to a type adds half
 a step of it."""
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -299,3 +303,19 @@ def test_rows_travel_through_the_dispatch(ep):
         token = torch.arange(R * T, device="cuda").view(R, T, 1).expand(R, T, K)
         assert torch.equal(recv.recv_x[row.reshape(-1)], codes[token.reshape(-1)])
         assert torch.equal(recv.recv_sf.view(torch.int32)[row.reshape(-1)], sf.view(torch.int32)[token.reshape(-1)])
+
+
+@pytest.mark.parametrize("n,h,kind", [(1024, 1024, 0), (700, 1640, 0), (800, 784, 2)])
+def test_the_first_call_of_a_process(n, h, kind):
+    """Rings of just below and just above 48 KB of shared memory, before any other call has raised a limit."""
+    code = f"""
+import torch, combine_ep_get_02_gb300 as ep
+t = torch.bfloat16 if {kind} == 0 else torch.float32
+cfg = ep.NormConfig({n}, {h}, x_dtype={kind})
+s, d = (torch.randn({n}, {h}, device="cuda").to(t) for _ in range(2))
+y = torch.randn({n}, {h}, device="cuda").bfloat16()
+ep.ep_norm_grad(cfg, s, None, None, y, d, d, None, ep.alloc_norm_workspace(cfg))
+torch.cuda.synchronize()
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    subprocess.run([sys.executable, "-c", code], check=True, cwd=root, timeout=300)
