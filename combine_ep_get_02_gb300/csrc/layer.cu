@@ -228,9 +228,9 @@ template <bool kFp8_, int kRows_, int kTokens_, bool kSmall>
 struct Shape {
   static constexpr bool kFp8 = kFp8_;
   static constexpr int kRows = kRows_, kTokens = kTokens_;     // of a strip, of a group at most
-  static constexpr int kWorkers = kFp8 && kRows == 16 && !kSmall ? 12 : 8;
-  static constexpr int kLoaders = kFp8 && kRows == 16 && !kSmall ? 3 : 2;  // that take the stages in turn
-  static constexpr int kEpilogue = kSmall || kTokens == 32 || (kFp8 && kRows == 16) ? 1 : 2;  // warps that take the units in turn
+  static constexpr int kWorkers = kFp8 && kTokens == 8 && !kSmall ? 12 : 8;
+  static constexpr int kLoaders = kFp8 && kTokens == 8 && !kSmall ? 3 : 2;  // that take the stages in turn
+  static constexpr int kEpilogue = kSmall || kTokens == 32 || (kFp8 && kTokens == 8) ? 1 : 2;  // warps that take the units in turn
   static constexpr int kBytes = kFp8 && kSmall ? 4096 : 8192;
   static constexpr int kBoxes = kBytes / (kRows * 128);        // columns of 128 bytes
   static constexpr int kColumns = kBoxes * (kFp8 ? 128 : 64);  // of the summed index
@@ -239,6 +239,8 @@ struct Shape {
   static constexpr int kCtas = kSmall ? 2 : 1;
   static constexpr int kSlots = kRows == 32 ? 2 : 4;           // strips whose sums may wait for each of them
   static constexpr int kThreads = (kWorkers + kLoaders + kEpilogue) * 32;
+  // stages are as many to each worker, so with this a stage is always the same loader's too
+  static_assert(kWorkers % kLoaders == 0, "a loader that waits for a stage has itself sent for it before");
 };
 
 template <class S>
@@ -497,7 +499,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
       __syncwarp();
       const uint8_t* rows = ring + stage * kStageBytes + row8 * 128;
       // Sums before their scale: of its 128 columns (two pieces) where the registers hold them, else of a piece.
-      constexpr bool kPair = kM == 1;
+      constexpr bool kPair = kM * kN <= 2;
       float e[kFp8 ? (kPair ? kM : 1) : 1][kFp8 ? kN : 1][4];
 #pragma unroll
       for (int i = 0; i < kPieces; ++i) {
@@ -744,6 +746,9 @@ cudaError_t launch_typed(const LayerArgs& a, int num_sms, cudaStream_t stream) {
     const int64_t bytes = experts * (static_cast<int64_t>(a.Z) + a.I) * a.H * (kFp8 ? 1 : 2);
     if (bytes <= 614400ll * a.device_sms && plan_of<Shape<kFp8, 16, 8, true>>(a.T, a.K, a.E).stages >= 8)
       return launch_both<Shape<kFp8, 16, 8, true>>(a, num_sms, stream);
+    // FP8, 7168 x 2048 and 4096 x 2048: one token 70 us with strips of 16 rows and 73 with 32, eight tokens 92 and 83
+    if constexpr (kFp8)
+      if (a.T > 2) return launch_both<Shape<kFp8, 32, 8, false>>(a, num_sms, stream);
     return launch_both<Shape<kFp8, 16, 8, false>>(a, num_sms, stream);
   }
   // tokens to a group: another group of the same expert reads its matrix from L2 again, and groups of 32 have
