@@ -110,6 +110,18 @@ def test_fp8_matrices(ep, T, E, K, H, I):
     Case(ep, T, E, K, H, I, fp8=True, bias=T % 2 == 1, residual=T % 2 == 0, masked=0.1 if T > 4 else 0.0).check()
 
 
+@pytest.mark.parametrize("T,E,K,H,I,act,fp8", [
+    (1, 40, 32, 1000, 520, "swiglu", False), (2, 64, 32, 1032, 584, "gelu", False), (5, 64, 16, 1024, 520, "swiglu", False),
+    (8, 64, 8, 1096, 640, "swiglu", False), (1, 40, 32, 1152, 1024, "swiglu", True), (2, 64, 20, 1408, 1024, "silu", True),
+    (3, 64, 16, 1152, 896, "swiglu", True), (8, 64, 8, 1152, 640, "swiglu", True), (8, 48, 8, 384, 5376, "swiglu", True)])
+def test_more_work_than_two_ctas_share_an_sm_for(ep, T, E, K, H, I, act, fp8):
+    """Few tokens on matrices of more than 600 KB an SM, where the kernels take other shapes."""
+    c = Case(ep, T, E, K, H, I, act, fp8, bias=T % 2 == 0, residual=T % 2 == 1, masked=0.05)
+    up, down = (c.mats[k][0] for k in ("up", "down"))
+    assert min(T * K, E) * (up[0].nbytes + down[0].nbytes) > 614400 * 152
+    c.check()
+
+
 def test_every_code(ep):
     """Each of the 256 codes as a matrix element meets a token that picks it out."""
     H = I = 128
