@@ -9,7 +9,7 @@
 // 32 matrix rows times all tokens of that expert (a group; tokens past kTokens are another group): the
 // matrix rows are the 16 rows of mma.sync's A operand, the tokens its 8 columns, and a stage
 // is a part of the summed index, so the strip's stages go to different workers.
-// With at most 32 tokens to a matrix the tensor cores are far from being the limit, so the products go
+// With at most 16 tokens to a matrix the tensor cores are far from being the limit, so the products go
 // where their operands need least preparation: the fragments are read straight from rows as they
 // lie in memory (the summed index is permuted alike for both), and FP8 codes become bf16 on the way.
 // (Sharing each stage among the workers took 165 us where this takes 136: a stage's bookkeeping then
@@ -230,7 +230,7 @@ struct Shape {
   static constexpr int kRows = kRows_, kTokens = kTokens_;     // of a strip, of a group at most
   static constexpr int kWorkers = kFp8 && kTokens == 8 && !kSmall ? 12 : 8;
   static constexpr int kLoaders = kFp8 && kTokens == 8 && !kSmall ? 3 : 2;  // that take the stages in turn
-  static constexpr int kEpilogue = kSmall || kTokens == 32 || (kFp8 && kTokens == 8) ? 1 : 2;  // warps that take the units in turn
+  static constexpr int kEpilogue = kSmall || (kFp8 && kTokens == 8) ? 1 : 2;  // warps that take the units in turn
   static constexpr int kBytes = kFp8 && kSmall ? 4096 : 8192;
   static constexpr int kBoxes = kBytes / (kRows * 128);        // columns of 128 bytes
   static constexpr int kColumns = kBoxes * (kFp8 ? 128 : 64);  // of the summed index
@@ -322,13 +322,15 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
 
   // Down: a tile's groups are split in `split` parts where that evens the SMs' work out; the parts'
   // sums are added by the last to finish. In bytes of matrices, with what a unit's end costs beside them: a
-  // part's, with its fence and atomic, about 20 KB; by the device's SMs, so that results do not depend on num_sms.
+  // part's, with its fence and atomic, about 20 KB and 32 bytes for each of its sums (64 tokens, top 4 of 16 experts: 8 parts
+  // where this takes 1 made the second kernel 103 us long); by the device's SMs, so that results do not depend
+  // on num_sms.
   int split = 1;
   if constexpr (kDown) {
     const int64_t bytes = static_cast<int64_t>(kRows) * sum * (kFp8 ? 1 : 2);
-    int64_t best = (tiles + a.device_sms - 1) / a.device_sms * (groups * bytes + 4096);
+    int64_t best = (tiles + a.device_sms - 1) / a.device_sms * (groups * bytes + 4096 + a.T * kRows * 8);
     for (int s = 2; s <= min(kLayerMaxSplit, groups); ++s) {
-      const int64_t cost = (static_cast<int64_t>(tiles) * s + a.device_sms - 1) / a.device_sms * ((groups + s - 1) / s * bytes + 20480);
+      const int64_t cost = (static_cast<int64_t>(tiles) * s + a.device_sms - 1) / a.device_sms * ((groups + s - 1) / s * bytes + 20480 + a.T * kRows * 32);
       if (cost < best) best = cost, split = s;
     }
   }
@@ -486,9 +488,6 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
     clear();
     enter_strip(cur);
     while (cur.u < units) {
-      const Group q = unpack_group(lists.groups[cur.g]);
-      // tiles of 8 tokens; of two both are computed, as that costs less than asking
-      const int used = kN > 2 ? (q.n + 15) >> 4 << 1 : kN;
       const int c0 = step * kColumns;
       Beside b;
       fetch(cur, step, b);  // while the matrix rows are on their way
@@ -523,11 +522,10 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
               codes_to_bf16(l[k], a0, a2);
               codes_to_bf16(u4[k], a1, a3);
 #pragma unroll
-              for (int j = 0; j < kN; ++j)
-                if (j < used) {
-                  const uint4 v = b.x[i][j][k >> 1];
-                  mma_16x8(e[kPair ? m : 0][j], a0, a1, a2, a3, k & 1 ? v.z : v.x, k & 1 ? v.w : v.y);
-                }
+              for (int j = 0; j < kN; ++j) {  // both tiles of 8 tokens: that costs less than asking
+                const uint4 v = b.x[i][j][k >> 1];
+                mma_16x8(e[kPair ? m : 0][j], a0, a1, a2, a3, k & 1 ? v.z : v.x, k & 1 ? v.w : v.y);
+              }
             }
             if (!kPair || (i & 1)) {  // columns come in whole 128s
               const float s0 = b.scale[i >> 1][m][0], s1 = b.scale[i >> 1][m][1];
@@ -541,12 +539,11 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
             }
           } else {
 #pragma unroll
-            for (int j = 0; j < kN; ++j)
-              if (j < used) {
-                const uint4 v = b.x[i][j][0];
-                mma_16x8(d[m][j], lo.x, hi.x, lo.y, hi.y, v.x, v.y);
-                mma_16x8(d[m][j], lo.z, hi.z, lo.w, hi.w, v.z, v.w);
-              }
+            for (int j = 0; j < kN; ++j) {
+              const uint4 v = b.x[i][j][0];
+              mma_16x8(d[m][j], lo.x, hi.x, lo.y, hi.y, v.x, v.y);
+              mma_16x8(d[m][j], lo.z, hi.z, lo.w, hi.w, v.z, v.w);
+            }
           }
         }
       }
@@ -559,8 +556,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
           for (int m = 0; m < kM; ++m)
 #pragma unroll
             for (int j = 0; j < kN; ++j)
-              if (j < used)
-                sums[(first * kM * kN + m * kN + j) * 32] = make_float4(d[m][j][0], d[m][j][1], d[m][j][2], d[m][j][3]);
+              sums[(first * kM * kN + m * kN + j) * 32] = make_float4(d[m][j][0], d[m][j][1], d[m][j][2], d[m][j][3]);
         });
         for (advance(cur); passed > 1; --passed, advance(cur)) leave_strip(cur.turn, nothing);
         first = step;
@@ -751,11 +747,8 @@ cudaError_t launch_typed(const LayerArgs& a, int num_sms, cudaStream_t stream) {
       if (a.T > 2) return launch_both<Shape<kFp8, 32, 8, false>>(a, num_sms, stream);
     return launch_both<Shape<kFp8, 16, 8, false>>(a, num_sms, stream);
   }
-  // tokens to a group: another group of the same expert reads its matrix from L2 again, and groups of 32 have
-  // fewer strips whose sums wait for the epilogue. With 16 tokens an expert the two are about even (16 experts:
-  // 177 us with groups of 16, 215 with 32; 8 experts: 118 and 105). FP8 would take too many registers for 32.
-  if constexpr (!kFp8)
-    if (a.T * a.K > 20 * a.E) return launch_both<Shape<kFp8, 32, 32, false>>(a, num_sms, stream);
+  // Another group of the same expert reads its matrix from L2 again; groups of 32 instead took as long or longer
+  // (64 tokens, top 2 of 8 experts: 105 us instead of 108, of 4: 92 instead of 86; top 8 of 16: 282 and 285).
   return launch_both<Shape<kFp8, 32, 16, false>>(a, num_sms, stream);
 }
 
