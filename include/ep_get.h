@@ -551,7 +551,8 @@ int ep_checkpoint_grad(const ep_checkpoint_config_t* cfg, const ep_layout_t* lay
  *   h = act(x_t W_up[e]^T + b_up[e]),   out_t = sum over the lanes k of topk_weights[t][k] *
  *   (h W_down[e]^T + b_down[e]) + residual_t          with e = topk_idx[t][k]
  * Sums are fp32; h is rounded to bf16 (as between the products), out once; the lanes' results
- * are not rounded. (ep_dispatch and ep_expert_product take any number of tokens.)
+ * are not rounded. ep_dispatch and ep_expert_product take any number of tokens, and are faster
+ * from about 8 tokens an expert on.
  */
 typedef struct ep_layer_config {
   int32_t num_tokens;   /* T, 0..64                                                      */
