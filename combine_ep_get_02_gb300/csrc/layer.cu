@@ -4,8 +4,8 @@
 //   down  out_t = sum_k w_tk (h_l W_down[e]^T + b_down[e]) + residual_t
 //
 // Reading the chosen experts' matrices once is what it costs, so both kernels are one stream of
-// matrix rows through shared memory: a warp keeps a ring of stages full of them (TMA), eight worker warps
-// take a stage each in turn and multiply it, and epilogue warps add their sums up. A strip is 16 or
+// matrix rows through shared memory: loader warps keep a ring of stages full of them (TMA), eight or twelve
+// worker warps take a stage each in turn and multiply it, and epilogue warps add their sums up. A strip is 16 or
 // 32 matrix rows times all tokens of that expert (a group; tokens past kTokens are another group): the
 // matrix rows are the 16 rows of mma.sync's A operand, the tokens its 8 columns, and a stage
 // is a part of the summed index, so the strip's stages go to different workers.
@@ -219,8 +219,8 @@ struct Plan {
 };
 
 // A kernel's shape. kSmall: for little work, with both kernels' CTAs on an SM together, so that the second has its
-// lists and first stages ready when the first ends (64 experts' strips of 1024 x 512 a token: 12.2 instead
-// of 13.5 us); with more work the ring gets the whole SM (8 experts of 7168 x 2048: 110 instead of 123 us).
+// lists and first stages ready when the first ends (one token on 4 experts of 1024 x 512: 12.2 instead
+// of 13.5 us); with more work the ring gets the whole SM (on 8 of 7168 x 2048: 110 instead of 123 us).
 // A stage is matrix rows in columns of 128 bytes a row, as TMA writes them with the 128-byte swizzle. Its size
 // bounds the tokens' values that a worker's threads hold beside it; a loader takes about 330 cycles for
 // a copy, most of them for its wait, so that 4 KB ones would take four loaders (one: 207 us instead of 127).
@@ -322,15 +322,16 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
 
   // Down: a tile's groups are split in `split` parts where that evens the SMs' work out; the parts'
   // sums are added by the last to finish. In bytes of matrices, with what a unit's end costs beside them: a
-  // part's, with its fence and atomic, about 20 KB and 32 bytes for each of its sums (64 tokens, top 4 of 16 experts: 8 parts
-  // where this takes 1 made the second kernel 103 us long); by the device's SMs, so that results do not depend
+  // part's, with its fence and atomic, about 20 KB and 32 bytes for each of its sums (without the latter 64 tokens,
+  // top 4 of 16 experts, were 8 parts: 217 instead of 180 us); by the device's SMs, so that results do not depend
   // on num_sms.
   int split = 1;
   if constexpr (kDown) {
     const int64_t bytes = static_cast<int64_t>(kRows) * sum * (kFp8 ? 1 : 2);
     int64_t best = (tiles + a.device_sms - 1) / a.device_sms * (groups * bytes + 4096 + a.T * kRows * 8);
     for (int s = 2; s <= min(kLayerMaxSplit, groups); ++s) {
-      const int64_t cost = (static_cast<int64_t>(tiles) * s + a.device_sms - 1) / a.device_sms * ((groups + s - 1) / s * bytes + 20480 + a.T * kRows * 32);
+      const int64_t rounds = (static_cast<int64_t>(tiles) * s + a.device_sms - 1) / a.device_sms;
+      const int64_t cost = rounds * ((groups + s - 1) / s * bytes + 20480 + a.T * kRows * 32);
       if (cost < best) best = cost, split = s;
     }
   }
@@ -400,10 +401,10 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
           }
         }
       }
-      if (!ok)  // the copies in flight end before the CTA does
-        for (uint32_t m = n - min(n, p.stages); m < n; ++m)
-          if (kLoaders == 1 || m % kLoaders == static_cast<uint32_t>(warp - kWorkers))
-            mbar_wait_timed<false>(smem_addr(&s_full[m % p.stages]), m / p.stages & 1u);
+      // the last copies end before the CTA does, also when a wait gave up, here or in a worker
+      for (uint32_t m = n - min(n, p.stages); m < n; ++m)
+        if (kLoaders == 1 || m % kLoaders == static_cast<uint32_t>(warp - kWorkers))
+          mbar_wait_timed<false>(smem_addr(&s_full[m % p.stages]), m / p.stages & 1u);
     }
     if constexpr (kDown) pdl_wait();  // no CTA of this kernel ends before the first kernel
     return;
