@@ -108,7 +108,7 @@ LayerWorkspace layer_workspace(const ep_layer_config_t* c) {
   const size_t T = static_cast<size_t>(c->num_tokens);
   w.done = 256;
   w.h = w.done + round256(sizeof(uint32_t) * ((c->hidden + 15) / 16));
-  w.part = w.h + round256(2 * T * c->num_topk * c->inner);
+  w.part = w.h + round256((c->num_tokens <= kLayerPairTokens ? 4 : 2) * T * c->num_topk * c->inner);
   w.total = w.part + round256(sizeof(float) * kLayerMaxSplit * T * c->hidden);
   return w;
 }

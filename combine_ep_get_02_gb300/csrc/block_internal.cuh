@@ -76,6 +76,8 @@ cudaError_t launch_checkpoint_grad(const CheckpointGradArgs& a, int num_sms, cud
 // ---- the experts' layer of a few tokens -----------------------------------------------
 
 constexpr int kLayerMaxTokens = 64;
+// Up to as many tokens h is kept as the sum of two bf16: the 8 columns of a product then have room for both terms.
+constexpr int kLayerPairTokens = 4;
 constexpr int kLayerMaxSplit = 8;  // parts that an output tile's sum over experts is taken in at most
 
 struct LayerArgs {
@@ -90,7 +92,7 @@ struct LayerArgs {
   const uint16_t* down_bias;  // [E][H] or null
   const uint16_t* residual;   // [T][H] or null
   uint16_t* out;              // [T][H]
-  uint16_t* h;                // workspace [lanes][I]
+  uint16_t* h;                // workspace [lanes][I], up to kLayerPairTokens tokens [2][lanes][I]
   float* part;                // workspace [kLayerMaxSplit][T][H]
   uint32_t* done;             // workspace [H / 16]: parts of a tile that are there (return to 0)
   uint32_t* err;

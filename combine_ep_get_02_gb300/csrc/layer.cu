@@ -9,6 +9,8 @@
 // 32 matrix rows times all tokens of that expert (a group; tokens past kTokens are another group): the
 // matrix rows are the 16 rows of mma.sync's A operand, the tokens its 8 columns, and a stage
 // is a part of the summed index, so the strip's stages go to different workers.
+// Up to 4 tokens h goes from one kernel to the other as two bf16 terms, the second kernel's products have
+// columns for both, and the layer's error is that of its last rounding (1.6e-3 of its norm; with one term 2.4e-3).
 // With at most 16 tokens to a matrix the tensor cores are far from being the limit, so the products go
 // where their operands need least preparation: the fragments are read straight from rows as they
 // lie in memory (the summed index is permuted alike for both), and FP8 codes become bf16 on the way.
@@ -293,6 +295,9 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
   const int tiles = (out_rows + strip - 1) / strip;
   const int steps = (sum + kColumns - 1) / kColumns;            // stages of a strip
   const int parts = min(steps, kWorkers);                       // workers that share it
+  const int lanes = a.T * a.K;
+  static_assert(kN == 1 || kTokens > 2 * kLayerPairTokens, "two terms for each token fit 8 columns");
+  const bool pairs = kDown && kN == 1 && a.T <= kLayerPairTokens;  // columns 0 to 3 are the first terms of h, 4 to 7 the second
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < stages; ++i) {
@@ -427,8 +432,9 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
       const Group q = unpack_group(lists.groups[c.g]);
 #pragma unroll
       for (int j = 0; j < kN; ++j) {
-        const int i = q.start + min(j * 8 + r8, q.n - 1);
-        from[j] = x + static_cast<int64_t>(kDown ? i : lists.token[i]) * sum + t * (kFp8 ? 16 : 8);
+        const int i = q.start + min(pairs ? r8 & 3 : j * 8 + r8, q.n - 1);
+        const int64_t row = kDown ? i + (pairs && r8 > 3 ? lanes : 0) : lists.token[i];
+        from[j] = x + row * sum + t * (kFp8 ? 16 : 8);
       }
     };
     auto fetch = [&](const Cursor& c, int step, Beside& b) {
@@ -574,6 +580,13 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
   const int index = warp - kWorkers - kLoaders;
   float* const acc_out = reinterpret_cast<float*>(smem + p.acc) + index * a.T * kRows;  // [T][kRows]
   if constexpr (kDown) pdl_wait();  // `out` may be what the first kernel reads
+  auto put_h = [&](int lane_at, int c, float h) {
+    uint16_t* to = a.h + static_cast<int64_t>(lane_at) * a.I + c;
+    const uint32_t first = f32x2_to_bf16x2(h, 0.f) & 0xFFFFu;
+    *to = static_cast<uint16_t>(first);
+    if (kN == 1 && a.T <= kLayerPairTokens)
+      to[static_cast<int64_t>(lanes) * a.I] = static_cast<uint16_t>(f32x2_to_bf16x2(h - __uint_as_float(first << 16), 0.f));
+  };
   uint32_t strips = 0;
   for (int turn = 0; cur.u < units; turn = turn + 1 == kEpilogue ? 0 : turn + 1) {
     const Cursor unit = cur;
@@ -597,6 +610,13 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
           const float4 o = sums[(w * (kM * kN) + i) * 32];
           v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
         }
+        if (pairs) {  // both terms' products: the second's is four columns, two threads on
+          auto add_second = [](float& first) {  // an infinity of h or of the matrix stays what the first term makes it
+            const float second = __shfl_xor_sync(kFullMask, first, 2);
+            if (fabsf(first) < INFINITY) first += second;
+          };
+          add_second(v.x), add_second(v.y), add_second(v.z), add_second(v.w);
+        }
         // v: results of rows row8 and row8 + 8 for tokens 2 t and 2 t + 1 of the tile
         const float got[2][2] = {{v.x, v.y}, {v.z, v.w}};
         if (gated) {
@@ -612,7 +632,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
             for (int o = 0; o < 2; ++o) {
               const int token = j * 8 + 2 * t + o;
               const float h = activate<EP_ACT_SWIGLU>(got[0][o] + b0) * (got[1][o] + b1);
-              if (token < q.n) a.h[static_cast<int64_t>(q.start + token) * a.I + c] = static_cast<uint16_t>(f32x2_to_bf16x2(h, 0.f));
+              if (token < q.n) put_h(q.start + token, c, h);
             }
           }
         } else {
@@ -631,8 +651,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
                 float& to = acc_out[lists.token[q.start + token] * kRows + in_strip];
                 to = fmaf(lists.weight[q.start + token], got[half][o] + b, to);
               } else {
-                a.h[static_cast<int64_t>(q.start + token) * a.I + c] =
-                    static_cast<uint16_t>(f32x2_to_bf16x2(act_any(got[half][o] + b, a.act), 0.f));
+                put_h(q.start + token, c, act_any(got[half][o] + b, a.act));
               }
             }
           }

@@ -550,8 +550,8 @@ int ep_checkpoint_grad(const ep_checkpoint_config_t* cfg, const ep_layout_t* lay
  * two kernels that read each chosen expert's matrices once:
  *   h = act(x_t W_up[e]^T + b_up[e]),   out_t = sum over the lanes k of topk_weights[t][k] *
  *   (h W_down[e]^T + b_down[e]) + residual_t          with e = topk_idx[t][k]
- * Sums are fp32; h is rounded to bf16 (as between the products), out once; the lanes' results
- * are not rounded. ep_dispatch and ep_expert_product take any number of tokens, and are faster
+ * Sums are fp32; h is rounded to bf16 as between the products (for up to 4 tokens to the sum of
+ * two bf16, off by 2^-16 of itself at most), out once; the lanes' results are not rounded. ep_dispatch and ep_expert_product take any number of tokens, and are faster
  * from about 8 tokens an expert on.
  */
 typedef struct ep_layer_config {

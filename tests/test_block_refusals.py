@@ -163,7 +163,9 @@ def test_layer_configs(ep, bad, code):
 def test_layer_arguments(ep):
     L, cfg = ep.lib(), layer_cfg(ep)
     n, c = ep.ep_layer_workspace_bytes(cfg), cfg._c()
-    assert n == 256 + up(4 * 16) + up(2 * 4 * 2 * 128) + up(4 * 8 * 4 * 256)
+    assert n == 256 + up(4 * 16) + up(4 * 4 * 2 * 128) + up(4 * 8 * 4 * 256)  # h as two terms
+    five = ep.ep_layer_workspace_bytes(layer_cfg(ep, num_tokens=5))
+    assert five == 256 + up(4 * 16) + up(2 * 5 * 2 * 128) + up(4 * 8 * 5 * 256)
     bad, odd, off = ep.EP_ERR_INVALID_ARG, P(0x40008), P(0x40002)
 
     def call(x=A, idx=A, w=A, u=A, us=None, ub=None, d=A, ds=None, db=None, r=None, out=A, ws=WS, size=n, cc=c):

@@ -1,4 +1,4 @@
-"""The experts' layer of a few tokens against 64 bits (h rounded to bf16 as defined; bounds in
+"""The experts' layer of a few tokens against 64 bits (h rounded to bf16, up to 4 tokens to two, as defined; bounds in
 _block_reference.layer, and half a step of bf16 for the output)."""
 import math
 
@@ -301,3 +301,34 @@ def test_many_calls_back_to_back(ep):
         xs.append(c.run(x=xs[-1]))
     for x, y in zip(xs, xs[1:]):
         assert torch.equal(c.run(x=x.clone()), y)
+
+
+def test_two_terms_of_h_up_to_four_tokens(ep):
+    """Of the error only the last rounding is left: up to 2^-8 of a value in [1, 2), evenly spread, a mean square of
+    2^-16 / 3, over the values' own mean square of 3 / (2 ln 2): 1.53e-3 of the norm. 2^-9 is 1.95e-3; with one term
+    it was 2.4e-3."""
+    for T in (1, 4):
+        for fp8, size in ((False, (64, 8, 1024, 512)), (False, (32, 8, 2048, 1536)), (True, (64, 8, 1024, 512)), (True, (16, 16, 2048, 2048))):
+            E, K, H, I = size
+            c = Case(ep, T, E, min(K, E), H, I, fp8=fp8, seed=5)
+            out = c.check()
+            mats = [c.mats[k][0] if not fp8 else ref.unscale(c.mats[k][0], c.mats[k][1]) for k in ("up", "down")]
+            want, _ = ref.layer(c.x, c.idx, c.w, mats[0], None, mats[1], None, None, "swiglu", FUN)
+            assert (out.double() - want).norm() / want.norm() <= 2.0 ** -9
+
+
+@pytest.mark.parametrize("T", [1, 3, 4, 5])
+def test_infinities_of_the_second_matrix_keep_their_sign(ep, T):
+    """A row of the second matrix with one infinity: each token's result is that infinity times its h."""
+    c = Case(ep, T, 4, 4, 512, 256, seed=11)
+    up, down = c.mats["up"][0], c.mats["down"][0]
+    c.idx[:] = torch.arange(4, device="cuda")
+    down[2, 7::16, 100] = math.inf
+    out = c.run()
+    z = c.x.double() @ up[2].double().T
+    want, _ = ref.layer(c.x, c.idx, c.w, up, None, down, None, None, "swiglu", FUN)
+    rows = torch.zeros(512, dtype=torch.bool, device="cuda")
+    rows[7::16] = True
+    assert z.isfinite().all() and want[:, ~rows].isfinite().all() and out[:, ~rows].isfinite().all()
+    assert want[:, rows].isinf().all()  # no h is so small that its sign is in doubt, nor its product zero
+    assert torch.equal(out[:, rows].double(), want[:, rows])
