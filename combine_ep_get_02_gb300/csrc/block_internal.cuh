@@ -94,7 +94,7 @@ struct LayerArgs {
   uint16_t* out;              // [T][H]
   uint16_t* h;                // workspace [lanes][I], up to kLayerPairTokens tokens [2][lanes][I]
   float* part;                // workspace [kLayerMaxSplit][T][H]
-  uint32_t* done;             // workspace [H / 16]: parts of a tile that are there (return to 0)
+  uint32_t* done;             // workspace [H / 16]: parts of a tile that are there (the first kernel zeroes them)
   uint32_t* err;
   int T, E, K, H, I, Z, act;
   int device_sms;

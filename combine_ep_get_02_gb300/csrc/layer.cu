@@ -312,7 +312,11 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
     fence_barrier_init();
     tma_prefetch_map(&matrices);
   }
-  if constexpr (!kDown) pdl_wait();
+  if constexpr (!kDown) {
+    pdl_wait();
+    // What another size's call, or another operator, left in the workspace is no count of the second kernel's tiles.
+    for (int i = blockIdx.x * kThreads + threadIdx.x; i < (a.H + 15) / 16; i += gridDim.x * kThreads) a.done[i] = 0u;
+  }
   // The second kernel may be placed as soon as what ran before the first is done: only h, which its
   // workers wait for, comes from the first.
   pdl_launch_dependents();

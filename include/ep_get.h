@@ -566,8 +566,9 @@ typedef struct ep_layer_config {
   int32_t num_sms;      /* SMs to use; 0 = all. Results do not depend on it.             */
 } ep_layer_config_t;
 
-/* Workspace bytes (0 for an invalid configuration). Zero-filled once before first use (every call
- * leaves its counters zero); one stream at a time; errors are read by ep_check_error. */
+/* Workspace bytes (0 for an invalid configuration). Its 256-byte header is zero-filled once before first
+ * use, and it may then serve any configuration that fits it; one stream at a time; errors are read by
+ * ep_check_error. */
 size_t ep_layer_workspace_bytes(const ep_layer_config_t* cfg);
 
 /* Device pointers, rows dense and 16-byte aligned: x bf16 [T][H], topk_idx int64 [T][K] and
