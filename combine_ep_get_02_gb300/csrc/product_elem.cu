@@ -150,7 +150,8 @@ __device__ __forceinline__ void act_two(Two z, Two& v, Two& g) {
   if constexpr (kAct == EP_ACT_SILU || kAct == EP_ACT_SWIGLU) {
     const Two s = sigmoid_two(z);
     v = z * s;
-    g = fma_two(v, s * two(-1.f, -1.f), v + s);  // s + v (1 - s)
+    // s (1 + z (1 - s)); s + v (1 - s) from v + s is (z + 1) - z where s is 1: nothing is left of it from 2^24 on
+    g = s * fma_two(z, fma_two(s, two(-1.f, -1.f), two(1.f, 1.f)), two(1.f, 1.f));
   } else {
     const float2 f = both(z);
     v = two(activate<kAct>(f.x), activate<kAct>(f.y));
