@@ -394,6 +394,9 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
         const int plane = gated ? 2 * q.expert : q.expert, row = cur.tile * strip;
         for (int step = 0; step < steps; ++step, at.next(stages), ++n) {
           if (kLoaders > 1 && n % kLoaders != static_cast<uint32_t>(warp - kWorkers)) continue;
+          // The first kernel may take its time: a full ring is emptied only behind it, and no wait is timed before.
+          if constexpr (kDown)
+            if (n >= p.stages && n < p.stages + kLoaders) pdl_wait();
           // After a wait that gave up, workers hand on stages that they did not wait for: their copies may still be on the
           // way, and a second one must not be announced beside them.
           if (!wait_stage(smem_addr(&s_empty[at.stage]), at.phase ^ 1u)) give_up();
