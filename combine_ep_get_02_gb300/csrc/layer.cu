@@ -318,8 +318,9 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
     for (int i = blockIdx.x * kThreads + threadIdx.x; i < (a.H + 15) / 16; i += gridDim.x * kThreads) a.done[i] = 0u;
   }
   // The second kernel may be placed as soon as what ran before the first is done: only h, which its
-  // workers wait for, comes from the first.
-  pdl_launch_dependents();
+  // workers wait for, comes from the first. On a part of the SMs its CTAs would wait on those that are not the
+  // call's, so they (and what comes behind the second) are placed as this kernel's CTAs end.
+  if (static_cast<int>(gridDim.x) >= a.device_sms) pdl_launch_dependents();
   const Lists lists = {reinterpret_cast<uint16_t*>(smem + p.token), reinterpret_cast<float*>(smem + p.weight),
                        reinterpret_cast<uint32_t*>(smem + p.groups)};
   if constexpr (kDown)
