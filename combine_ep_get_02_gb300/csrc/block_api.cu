@@ -1,8 +1,6 @@
 // C ABI of the norm, of activations kept in 8 bits and of the experts' layer of a few tokens: argument
 // checks, workspace layout, launches. Every host-detectable problem is reported before anything
 // is enqueued.
-#include <math.h>
-
 #include "block_internal.cuh"
 
 namespace ep {
@@ -30,7 +28,7 @@ int check_norm(const ep_norm_config_t* c) {
   if (c->rows > INT32_MAX || c->hidden > kNormMaxHidden) return EP_ERR_UNSUPPORTED;
   if (c->x_dtype != EP_DTYPE_BF16 && c->x_dtype != EP_DTYPE_FP32) return EP_ERR_INVALID_ARG;
   if (c->sf_pack != 0 && c->sf_pack != 1) return EP_ERR_INVALID_ARG;
-  if (!isfinite(c->eps) || !(c->eps >= kNormMinEps)) return EP_ERR_INVALID_ARG;
+  if (!(c->eps >= kNormMinEps && c->eps <= kNormMaxEps)) return EP_ERR_INVALID_ARG;
   return EP_OK;
 }
 

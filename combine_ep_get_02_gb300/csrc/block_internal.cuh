@@ -9,7 +9,7 @@ namespace ep {
 // ---- norm -----------------------------------------------------------------------
 
 constexpr int kNormMaxHidden = 16384;
-constexpr float kNormMinEps = 1e-20f;
+constexpr float kNormMinEps = 1e-20f, kNormMaxEps = 1e38f;  // the largest mean of squares, 2^125, and eps stay in fp32
 
 struct NormArgs {
   const void* x;            // [rows][H] bf16 or fp32

@@ -83,6 +83,11 @@ __device__ __forceinline__ float row_sum(float v, float* s) {
 // the largest of them, and what is below that does not count beside them.
 constexpr float kShrink = 8.271806125530277e-25f;  // 2^-80
 
+// 1 / sqrt(mean s^2 + eps) of the sum of squares so taken; eps counts where it is as large as they are
+__device__ __forceinline__ float root_of_small(float small, int H, float eps) {
+  return __frsqrt_rn(small / H + eps * kShrink * kShrink) * kShrink;
+}
+
 // Threads of a CTA at most: as many as the registers of kV chunks each leave room for.
 template <int kV, bool kWarpRow, bool kGrad>
 constexpr int threads_of = kWarpRow ? 128 : kV == 1 && !kGrad ? 1024 : 512;
@@ -134,7 +139,7 @@ __global__ void __launch_bounds__(threads_of<kV, kWarpRow, false>) norm_kernel(N
         for (int i = 0; i < 8; ++i) small = fmaf(f[v][i] * kShrink, f[v][i] * kShrink, small);
       small = row_sum<kWarpRow>(small, s_sum[turn]);
       turn ^= 1;
-      q = __frsqrt_rn(small / a.H) * kShrink;
+      q = root_of_small(small, a.H, a.eps);
     }
 #pragma unroll
     for (int v = 0; v < kV; ++v) {
@@ -249,7 +254,7 @@ __global__ void __launch_bounds__(threads_of<kV, kWarpRow, true>) norm_grad_kern
 #pragma unroll
           for (int i = 0; i < 8; ++i) small = fmaf(s[i] * kShrink, s[i] * kShrink, small);
         }
-        q = __frsqrt_rn(row_sum<kWarpRow>(small, s_sum[turn]) / a.H) * kShrink;
+        q = root_of_small(row_sum<kWarpRow>(small, s_sum[turn]), a.H, a.eps);
       }
       float tn = 0.f;
 #pragma unroll
@@ -410,7 +415,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) norm_grad_ring_kernel(NormGra
           chunk(from, c, s);
           for (int i = 0; i < 8; ++i) small = fmaf(s[i] * kShrink, s[i] * kShrink, small);
         }
-        q = __frsqrt_rn(row_sum<false>(small, s_more[0]) / a.H) * kShrink;
+        q = root_of_small(row_sum<false>(small, s_more[0]), a.H, a.eps);
       }
       float tn = 0.f;
       for (int v = 0; v < kV; ++v) {

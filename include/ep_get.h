@@ -471,7 +471,7 @@ typedef struct ep_norm_config {
   int32_t hidden;  /* H, a multiple of 8 (of 128 with codes), up to 16384             */
   int32_t x_dtype; /* of x, residual, sum, d_sum and d_x: EP_DTYPE_BF16 or EP_DTYPE_FP32 */
   int32_t sf_pack; /* the scales' format, as ep_config_t.sf_pack                      */
-  float eps;       /* finite, 1e-20 or more                                           */
+  float eps;       /* 1e-20 to 1e38                                                   */
 } ep_norm_config_t;
 
 /* Forward. Device pointers, rows dense and 16-byte aligned: x [rows][H]; residual the same or
