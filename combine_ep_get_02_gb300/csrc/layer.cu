@@ -3,7 +3,7 @@
 //   up    h_l = act(x_t W_up[e]^T + b_up[e])                      for every lane l = (t, k), e its expert
 //   down  out_t = sum_k w_tk (h_l W_down[e]^T + b_down[e]) + residual_t
 //
-// Reading the chosen experts' matrices once is what it costs, so both kernels are one stream of
+// Reading the chosen experts' matrices is what it costs (once for every 16 tokens of an expert), so both kernels are one stream of
 // matrix rows through shared memory: loader warps keep a ring of stages full of them (TMA), eight or twelve
 // worker warps take a stage each in turn and multiply it, and epilogue warps add their sums up. A strip is 16 or
 // 32 matrix rows times all tokens of that expert (a group; tokens past kTokens are another group): the
@@ -11,13 +11,15 @@
 // is a part of the summed index, so the strip's stages go to different workers.
 // Up to 4 tokens h goes from one kernel to the other as two bf16 terms, the second kernel's products have
 // columns for both, and the layer's error is that of its last rounding (1.6e-3 of its norm; with one term 2.4e-3).
+// With more tokens the columns are taken, and h is rounded once, as ep_expert_product rounds it between the products: a
+// second term would be a product of its own, and as many bytes of h again for every matrix row.
 // With at most 16 tokens to a matrix the tensor cores are far from being the limit, so the products go
 // where their operands need least preparation: the fragments are read straight from rows as they
 // lie in memory (the summed index is permuted alike for both), and FP8 codes become bf16 on the way.
 // (Sharing each stage among the workers took 165 us where this takes 136: a stage's bookkeeping then
 // comes eight times, and every stage waits for its slowest warp.)
 // Memory bounds it with bf16 matrices: 16 tokens on 16 experts of 4096 x 2048 136 us (805 MB, 5.9 TB/s), one token on 8
-// experts of 7168 x 2048 107 us (705 MB, 6.6 TB/s); with FP8 ones the codes' way to bf16, two instructions a code
+// experts of 7168 x 2048 106 us (705 MB, 6.6 TB/s); with FP8 ones the codes' way to bf16, two instructions a code
 // and thread: 70 us (5.0 TB/s; 60 without the products).
 #include "block_internal.cuh"
 #include "fp8_rows.cuh"
@@ -221,8 +223,9 @@ struct Plan {
 };
 
 // A kernel's shape. kSmall: for little work, with both kernels' CTAs on an SM together, so that the second has its
-// lists and first stages ready when the first ends (one token on 4 experts of 1024 x 512: 12.2 instead
-// of 13.5 us); with more work the ring gets the whole SM (on 8 of 7168 x 2048: 110 instead of 123 us).
+// lists and first stages ready when the first ends (one token on 4 experts of 1024 x 512: 11.3 instead
+// of 13.1 us, of 2048 x 1024: 16.6 and 17.3); with more work the ring gets the whole SM (on 8 of 4096 x 1024: 41
+// instead of 44 us, of 7168 x 2048: 110 instead of 125).
 // A stage is matrix rows in columns of 128 bytes a row, as TMA writes them with the 128-byte swizzle. Its size
 // bounds the tokens' values that a worker's threads hold beside it; a loader takes about 330 cycles for
 // a copy, most of them for its wait, so that 4 KB ones would take four loaders (one: 207 us instead of 127).
@@ -767,17 +770,21 @@ cudaError_t launch_both(const LayerArgs& a, int num_sms, cudaStream_t stream) {
 template <bool kFp8>
 cudaError_t launch_typed(const LayerArgs& a, int num_sms, cudaStream_t stream) {
   if (a.T <= 8) {
-    // matrices that are read, at most: 600 KB an SM is where both shapes take as long
+    // Matrices that are read, at most: 600 KB an SM lies between where the small shape is the faster one (0.33 MB: 16.6 and
+    // 17.3 us) and where the other is (FP8, 0.66 MB: 37.4 and 34.0 us; bf16, 1.3 MB: 44.1 and 41.4).
     const int64_t lanes = static_cast<int64_t>(a.T) * a.K, experts = lanes < a.E ? lanes : a.E;
     const int64_t bytes = experts * (static_cast<int64_t>(a.Z) + a.I) * a.H * (kFp8 ? 1 : 2);
     if (bytes <= 614400ll * a.device_sms && plan_of<Shape<kFp8, 16, 8, true>>(a.T, a.K, a.E).stages >= 8)
       return launch_both<Shape<kFp8, 16, 8, true>>(a, num_sms, stream);
-    // FP8, 7168 x 2048 and 4096 x 2048: one token 70 us with strips of 16 rows and 73 with 32, eight tokens 92 and 83
+    // FP8, strips of 16 rows and of 32: 7168 x 2048 with 1, 2, 3, 4, 8 tokens 70, 97, 111, 127, 134 and 75, 104, 115, 130,
+    // 135 us; 4096 x 2048 48, 65, 75, 84, 89 and 48, 63, 72, 80, 86. So up to two tokens those of 16 rows are as good or
+    // better by up to 7%; from three on it is 1 to 4% either way, with the tiles that a size leaves for the last round.
     if constexpr (kFp8)
       if (a.T > 2) return launch_both<Shape<kFp8, 32, 8, false>>(a, num_sms, stream);
     return launch_both<Shape<kFp8, 16, 8, false>>(a, num_sms, stream);
   }
-  // Another group of the same expert reads its matrix from L2 again; groups of 32 instead took as long or longer
+  // Another group of the same expert reads its matrix again, from L2 as far as that holds it (the first kernel takes all
+  // tiles of a group before the next group's, the second a tile's groups in turn); groups of 32 instead took as long or longer
   // (64 tokens, top 2 of 8 experts: 105 us instead of 108, of 4: 92 instead of 86; top 8 of 16: 282 and 285).
   return launch_both<Shape<kFp8, 32, 16, false>>(a, num_sms, stream);
 }

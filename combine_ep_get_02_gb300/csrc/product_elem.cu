@@ -69,7 +69,7 @@ __global__ void __launch_bounds__(kThreads)
 // 4096 x 4096 GELU 30 us (100 MB), 16384 x 1024 gated 29 us (168 MB, 5.8 TB/s).
 constexpr int kSpan = kDzColumns, kAcross = kSpan / 8, kDown = kThreads / kAcross;
 // Kept rows in a tile where there are so many that every CTA has several: a tile's column sums cost
-// about as much as the rows of half a small tile (65536 x 2 x 2048: 272 us with 64 rows, 246 with 256).
+// about as much as the rows of half a small tile (65536 x 2 x 2048: 272 us with 64 rows, 248 with 256).
 constexpr int kKeptRows = 256;
 constexpr int kBiasWays = 8;  // orders the bias gradients' sums, here and in bias_sum_kernel
 
@@ -202,8 +202,8 @@ __global__ void __launch_bounds__(kThreads, kKept ? 2 : 0) dz_kernel(DzArgs a) {
     for (int i = 0; i < (kKept ? kHalves * 4 : 1); ++i) sum2[i] = two(0.f, 0.f);
     if (col < a.N) {
       if constexpr (kKept) {
-        // a thread's rows of the tile are all on their way before the first is used (one after the other: 385 us
-        // instead of 281 for 65536 x 2 x 2048 gated)
+        // a thread's rows of the tile are all on their way before the first is used (65536 x 2 x 2048 gated: 281 us
+        // instead of 385 with one after the other, and 272 once pairs of floats went through one instruction)
         constexpr int kRows = kDzRows / kDown;
         const bool needs_z = kAct != EP_ACT_NONE || a.h != nullptr;
 #pragma unroll 1

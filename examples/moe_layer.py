@@ -103,8 +103,9 @@ class MoELayer:
 
 class KeptBlock(MoELayer):
     """The layer with the norm in front of it and the residual stream around it, in FP8 where rows travel
-    or wait: the norm makes the rows that the dispatch sends, they stay as they were received, and of
-    z only 8 bits are kept (a quarter of what MoELayer keeps a row); h is computed again.
+    or wait: the norm makes the rows that the dispatch sends, they stay as they were received, of z only 8 bits
+    are kept, and h is computed again. A row of an expert keeps 3 hidden + 2 inner bytes and the scales (x, y in bf16,
+    z) where MoELayer keeps 4 hidden + 6 inner: 4/7 with inner = hidden / 2, half with inner = hidden.
 
     forward(x, residual) -> (sum, out): sum = x + residual, and out, which the next block adds to sum."""
 

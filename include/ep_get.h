@@ -547,12 +547,13 @@ int ep_checkpoint_grad(const ep_checkpoint_config_t* cfg, const ep_layout_t* lay
 /* ---- the experts' layer of a few tokens ------------------------------------------------
  * (No counterpart on the DeepEP pages.) What dispatch, both products of each expert and combine
  * compute for a serving step of up to 64 tokens on one rank, straight from the router's choice, in
- * two kernels that read each chosen expert's matrices once:
+ * two kernels that read each chosen expert's matrices once for every 16 of its tokens:
  *   h = act(x_t W_up[e]^T + b_up[e]),   out_t = sum over the lanes k of topk_weights[t][k] *
  *   (h W_down[e]^T + b_down[e]) + residual_t          with e = topk_idx[t][k]
  * Sums are fp32; h is rounded to bf16 as between the products (for up to 4 tokens to the sum of
- * two bf16, off by 2^-16 of itself at most), out once; the lanes' results are not rounded. ep_dispatch and ep_expert_product take any number of tokens, and are faster
- * from about 8 tokens an expert on.
+ * two bf16, off by 2^-16 of itself at most), out once; the lanes' results are not rounded.
+ * ep_dispatch and ep_expert_product take any number of tokens, and are faster from about 8 tokens
+ * an expert on.
  */
 typedef struct ep_layer_config {
   int32_t num_tokens;   /* T, 0..64                                                      */
