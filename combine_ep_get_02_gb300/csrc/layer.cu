@@ -199,11 +199,14 @@ struct Place {
   }
 };
 
-// As mbar_wait_timed, which looks at the clock after its first try; here most waits end within a few.
+// As mbar_wait_timed, which looks at the clock after its first try; here most waits end within a few. kBehind: the kernel
+// in front, which may take its time, comes first: the wait is timed from its end.
+template <bool kBehind = false>
 __device__ __forceinline__ bool wait_stage(uint32_t bar, uint32_t parity) {
 #pragma unroll 1
   for (int i = 0; i < 64; ++i)
     if (mbar_try<false>(bar, parity)) return true;
+  if constexpr (kBehind) pdl_wait();
   return mbar_wait_timed<false>(bar, parity);
 }
 
@@ -322,7 +325,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
   }
   // The second kernel may be placed as soon as what ran before the first is done: only h, which its
   // workers wait for, comes from the first. On a part of the SMs its CTAs would wait on those that are not the
-  // call's, so they (and what comes behind the second) are placed as this kernel's CTAs end.
+  // call's, so they (and what comes behind the second) are placed once every CTA has sent for its last rows.
   if (static_cast<int>(gridDim.x) >= a.device_sms) pdl_launch_dependents();
   const Lists lists = {reinterpret_cast<uint16_t*>(smem + p.token), reinterpret_cast<float*>(smem + p.weight),
                        reinterpret_cast<uint32_t*>(smem + p.groups)};
@@ -374,9 +377,14 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
     if (s_abort == 0) atomicOr(a.err, kErrTimeout);
     s_abort = 1;
   };
-  // A wait that gives up is the CTA's last one: what follows is computed without, and reported.
+  // A wait that gives up is the CTA's last one: what follows is computed without, and reported. Returns whether what it is
+  // for is there.
   auto wait_for = [&](uint64_t* bar, uint32_t parity) {
-    if (!mbar_try<false>(smem_addr(bar), parity) && s_abort == 0 && !wait_stage(smem_addr(bar), parity)) give_up();
+    if (mbar_try<false>(smem_addr(bar), parity)) return true;
+    if (s_abort != 0) return false;
+    if (wait_stage(smem_addr(bar), parity)) return true;
+    give_up();
+    return false;
   };
   Cursor cur = {static_cast<int64_t>(blockIdx.x), 0, 0, 0, 0};
   enter(cur);
@@ -398,13 +406,9 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
         const int plane = gated ? 2 * q.expert : q.expert, row = cur.tile * strip;
         for (int step = 0; step < steps; ++step, at.next(stages), ++n) {
           if (kLoaders > 1 && n % kLoaders != static_cast<uint32_t>(warp - kWorkers)) continue;
-          // The first kernel may take its time: a full ring is emptied only behind it, and no wait is timed before.
-          if constexpr (kDown)
-            if (n >= p.stages && n < p.stages + kLoaders) pdl_wait();
-          // After a wait that gave up, workers hand on stages that they did not wait for: their copies may still be on the
-          // way, and a second one must not be announced beside them.
-          if (!wait_stage(smem_addr(&s_empty[at.stage]), at.phase ^ 1u)) give_up();
-          if (s_abort != 0) {
+          // down: a full ring is emptied only behind the first kernel
+          if (!wait_stage<kDown>(smem_addr(&s_empty[at.stage]), at.phase ^ 1u)) {
+            give_up();
             ok = false;
             break;
           }
@@ -419,6 +423,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
           }
         }
       }
+      pdl_launch_dependents();
       // the last copies end before the CTA does, also when a wait gave up, here or in a worker
       for (uint32_t m = n - min(n, p.stages); m < n; ++m)
         if (kLoaders == 1 || m % kLoaders == static_cast<uint32_t>(warp - kWorkers))
@@ -514,7 +519,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
       Cursor then = cur;
       int passed = 0;
       for (step += kWorkers; step >= steps && then.u < units; step -= steps, ++passed) advance(then);
-      wait_for(&s_full[stage], phase);
+      const bool landed = wait_for(&s_full[stage], phase);
       __syncwarp();
       const uint8_t* rows = ring + stage * kStageBytes + row8 * 128;
       // Sums before their scale: of its 128 columns (two pieces) where the registers hold them, else of a piece.
@@ -568,7 +573,10 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
         }
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_addr(&s_empty[stage]));
+      // A stage that was not waited for is not handed on: its copy may still be on the way, and a loader that has not given
+      // up must not announce a second one beside it. (Loaders that look at s_abort took 10% longer where few SMs are
+      // used and each is fast: 64 tokens, top 8 of 64 experts on 20 SMs 2.80 instead of 2.54 ms.)
+      if (lane == 0 && landed) mbar_arrive(smem_addr(&s_empty[stage]));
       if ((stage += kWorkers) >= stages) stage -= stages, phase ^= 1u;
       if (passed > 0) {
         leave_strip(cur.turn, [&](float4* sums) {
