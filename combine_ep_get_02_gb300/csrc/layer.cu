@@ -786,7 +786,7 @@ cudaError_t launch_typed(const LayerArgs& a, int num_sms, cudaStream_t stream) {
       return launch_both<Shape<kFp8, 16, 8, true>>(a, num_sms, stream);
     // FP8, strips of 16 rows and of 32: 7168 x 2048 with 1, 2, 3, 4, 8 tokens 70, 97, 111, 127, 134 and 75, 104, 115, 130,
     // 135 us; 4096 x 2048 48, 65, 75, 84, 89 and 48, 63, 72, 80, 86. So up to two tokens those of 16 rows are as good or
-    // better by up to 7%; from three on it is 1 to 4% either way, with the tiles that a size leaves for the last round.
+    // better by up to 7%; from three on it is 1 to 4% either way, with how evenly the tiles of a size fill the SMs.
     if constexpr (kFp8)
       if (a.T > 2) return launch_both<Shape<kFp8, 32, 8, false>>(a, num_sms, stream);
     return launch_both<Shape<kFp8, 16, 8, false>>(a, num_sms, stream);
